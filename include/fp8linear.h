@@ -495,6 +495,128 @@ fp8_status fp8_multi_amax_scales(const uint16_t *const *w, const int64_t *numel,
                                  float *amax, float *scale, float *scale_inv, cudaStream_t s);
 
 /* ------------------------------------------------------------------------ */
+/* Layer norm                                                                */
+/* ------------------------------------------------------------------------ */
+/* The calls from here to the status section also take fp32 rows, any number
+ * of columns and rows that lie apart: a row stride (ldx, lddy, ldr, ldg) counts
+ * elements, is at least 0 and needs no alignment, and their tensors need only
+ * the alignment of their elements (16 bytes and multiples of 16 bytes are
+ * faster: rows then move 16 bytes at a time).  Their outputs are contiguous.
+ * Sums, means and weights are fp32. */
+typedef enum { FP8_DT_BF16 = 0, FP8_DT_F32 = 1 } fp8_dtype;
+
+/* y = (x - mean) * rstd * weight + bias for each row of x [rows, cols] (type
+ * xt), mean = sum(x)/cols, rstd = 1/sqrt(sum((x - mean)^2)/cols + eps).
+ * weight, bias [cols] (type wt) are nullable (1 and 0).  Outputs, each
+ * nullable but y and yq not both: y [rows, cols] in x's type; yq [rows, cols]
+ * = e4m3(fl32(y * scale_inv)) of the fp32 y before its rounding to x's type,
+ * rounded to nearest even and saturating (scale_inv [1] is read: delayed
+ * scaling, as in fp8_quantize); amax_out [1] = max |y| of that fp32 y (NaN if
+ * any is), overwritten; mean, rstd [rows], which the backward call takes.
+ * rows >= 0, 0 <= cols < 2^31 (FP8_ERR_SHAPE); eps >= 0. */
+fp8_status fp8_layer_norm(const void *x, int64_t ldx, fp8_dtype xt, const void *weight,
+                          const void *bias, fp8_dtype wt, int64_t rows, int64_t cols, float eps,
+                          void *y, uint8_t *yq, const float *scale_inv, float *amax_out,
+                          float *mean, float *rstd, cudaStream_t s);
+
+/* The gradient of y above: with xhat = (x - mean) * rstd,
+ *   dx = rstd * (weight*dy - mean_c(weight*dy) - xhat * mean_c(weight*dy*xhat)),
+ *   dweight = sum over rows of dy*xhat, dbias = sum over rows of dy.
+ * dy, x, dx have type xt; weight, dweight, dbias type wt.  dx, dweight, dbias
+ * are nullable (not all).  The column sums are formed per block of the launch,
+ * then over the blocks in order: the same call gives the same bits.
+ * workspace: fp8_layer_norm_workspace_bytes(rows, cols) bytes, 16-byte
+ * aligned, overwritten; needed with dweight or dbias.  rows = 0 gives
+ * dweight = dbias = 0. */
+size_t fp8_layer_norm_workspace_bytes(int64_t rows, int64_t cols);
+fp8_status fp8_layer_norm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                                   fp8_dtype xt, const void *weight, fp8_dtype wt,
+                                   const float *mean, const float *rstd, int64_t rows,
+                                   int64_t cols, void *dx, void *dweight, void *dbias,
+                                   void *workspace, cudaStream_t s);
+
+/* ------------------------------------------------------------------------ */
+/* Tokens sorted by expert and back                                          */
+/* ------------------------------------------------------------------------ */
+/* For linears split over `experts` experts: token t has topk assignments
+ * (t, j), each to an expert, and expert e's rows are rows offsets[e] to
+ * offsets[e] + counts[e] - 1 of the sorted order, in the order of t * topk + j.
+ * Segments start at multiples of `multiple` (16 for the tensorwise GEMMs, 128
+ * for the block recipe, 1 for none), so each is an M of fp8_linear_fprop as
+ * it is.  An id below 0 or from `experts` up drops its assignment. */
+
+/* Rows that the sorted order of n assignments takes at most: n plus
+ * multiple - 1 for each of min(n, experts) experts.  Host only; -1 for bad
+ * arguments. */
+int64_t fp8_moe_capacity(int64_t n, int64_t experts, int64_t multiple);
+
+/* ids [n] (int32, or int64 with ids_64 != 0), n = tokens * topk.  Outputs:
+ * row_of [n]: the row of each assignment, -1 when dropped; source [capacity]:
+ * the assignment of each row, -1 for padding and past the last segment;
+ * offsets [experts + 1]; counts [experts].  1 <= experts <= 1024 (else
+ * FP8_ERR_UNSUPPORTED), multiple >= 1, fp8_moe_capacity(...) <= capacity <
+ * 2^31.  workspace: fp8_moe_sort_workspace_bytes(n, experts) bytes (nullable
+ * when 0), overwritten. */
+size_t fp8_moe_sort_workspace_bytes(int64_t n, int64_t experts);
+fp8_status fp8_moe_sort(const void *ids, int32_t ids_64, int64_t n, int64_t experts,
+                        int64_t multiple, int64_t capacity, int32_t *row_of, int32_t *source,
+                        int32_t *offsets, int32_t *counts, void *workspace, cudaStream_t s);
+
+/* rows [capacity, hidden]: row row_of[t, j] = x[t] for x [tokens, hidden] (type
+ * xt), rows without a source zero.  Give `rows` (type xt), or rows_q and
+ * scale_inv for e4m3(fl32(x * scale_inv)) as fp8_quantize makes it; amax_out
+ * (nullable, with rows_q) = max |x| over all tokens, overwritten.  A row_of
+ * entry outside 0..capacity-1 counts as dropped. */
+fp8_status fp8_moe_dispatch(const void *x, int64_t ldx, fp8_dtype xt, int64_t tokens,
+                            int64_t topk, int64_t hidden, const int32_t *row_of,
+                            const int32_t *source, int64_t capacity, void *rows, uint8_t *rows_q,
+                            const float *scale_inv, float *amax_out, cudaStream_t s);
+
+/* dx[t] = sum over j of drows[row_of[t, j]] (the gradient of fp8_moe_dispatch's
+ * x), added in fp32 in the order of j; zero for a token without rows. */
+fp8_status fp8_moe_dispatch_backward(const void *drows, int64_t ldr, fp8_dtype xt, int64_t tokens,
+                                     int64_t topk, int64_t hidden, const int32_t *row_of,
+                                     int64_t capacity, void *dx, cudaStream_t s);
+
+/* y[t] = sum over j of weights[t, j] * rows[row_of[t, j]]; weights fp32
+ * [tokens, topk], nullable (1).  Dropped assignments add nothing, whatever
+ * their weight. */
+fp8_status fp8_moe_combine(const void *rows, int64_t ldr, fp8_dtype xt, int64_t tokens,
+                           int64_t topk, int64_t hidden, const int32_t *row_of, int64_t capacity,
+                           const float *weights, void *y, cudaStream_t s);
+
+/* Its gradients: drows[row_of[t, j]] = weights[t, j] * dy[t] with zero rows
+ * where source is -1, dweights[t, j] = <dy[t], rows[row_of[t, j]]> (fp32,
+ * nullable; 0 when dropped). */
+fp8_status fp8_moe_combine_backward(const void *dy, int64_t lddy, const void *rows, int64_t ldr,
+                                    fp8_dtype xt, int64_t tokens, int64_t topk, int64_t hidden,
+                                    const int32_t *row_of, const int32_t *source, int64_t capacity,
+                                    const float *weights, void *drows, float *dweights,
+                                    cudaStream_t s);
+
+/* ------------------------------------------------------------------------ */
+/* Orthogonalised updates                                                    */
+/* ------------------------------------------------------------------------ */
+/* out [batch, rows, cols] (bf16, contiguous) = scale * X after `steps` steps of
+ *   A = X Xᵀ, B = b A + c A A, X <- a X + B X   (tall matrices: on Xᵀ)
+ * from X = g / (|g|_F + eps), each matrix of the batch by itself; step i takes
+ * (a, b, c) = coefficients[3 i .. 3 i + 2] (host).  g has type gt, row stride
+ * ldg >= 0 and batch stride bsg >= 0 elements.  The products run on the tensor
+ * cores with fp16 operands and fp32 accumulation; singular values must stay
+ * below 4 throughout (the usual coefficients keep them below 1.3), beyond
+ * which fp16 overflows and the result is not finite.  1 <= steps <= 64,
+ * rows and cols <= 65536, batch * ceil(rows/128) * ceil(cols/128) < 2^31
+ * (FP8_ERR_SHAPE); eps >= 0.  workspace:
+ * fp8_orthogonalize_workspace_bytes(batch, rows, cols) bytes (8 a matrix
+ * element and 4 an element of A; 0 for bad arguments), 16-byte aligned,
+ * overwritten; calls that may overlap need their own. */
+size_t fp8_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
+fp8_status fp8_orthogonalize(const void *g, int64_t ldg, int64_t bsg, fp8_dtype gt, int64_t batch,
+                             int64_t rows, int64_t cols, int32_t steps, const float *coefficients,
+                             float eps, float scale, uint16_t *out, void *workspace,
+                             cudaStream_t s);
+
+/* ------------------------------------------------------------------------ */
 /* Status                                                                    */
 /* ------------------------------------------------------------------------ */
 

@@ -47,10 +47,13 @@ class fp8_block_step_scales(ctypes.Structure):
                  "g_scale", "g_scale_inv", "g_scale_t", "g_scale_inv_t")]
 
 
+DT_BF16, DT_F32 = 0, 1
+
 FP8_STEP_NEVENTS = 8
 FP8_STEP_SAVE_XQ_FWD = 1
 
 P, I64, I32, U32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32
+F32 = ctypes.c_float
 S = ctypes.c_int  # fp8_status / enums
 
 SIGNATURES = {
@@ -86,6 +89,19 @@ SIGNATURES = {
     "fp8_multi_amax_scales": (S, [ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(I64), I32, P,
                                   P, P, P]),
     "fp8_pad_tokens": (S, [P, I64, I64, I64, P, ctypes.POINTER(I64), P]),
+    "fp8_layer_norm": (S, [P, I64, S, P, P, S, I64, I64, F32, P, P, P, P, P, P, P]),
+    "fp8_layer_norm_workspace_bytes": (ctypes.c_size_t, [I64, I64]),
+    "fp8_layer_norm_backward": (S, [P, I64, P, I64, S, P, S, P, P, I64, I64, P, P, P, P, P]),
+    "fp8_moe_capacity": (I64, [I64, I64, I64]),
+    "fp8_moe_sort_workspace_bytes": (ctypes.c_size_t, [I64, I64]),
+    "fp8_moe_sort": (S, [P, I32, I64, I64, I64, I64, P, P, P, P, P, P]),
+    "fp8_moe_dispatch": (S, [P, I64, S, I64, I64, I64, P, P, I64, P, P, P, P, P]),
+    "fp8_moe_dispatch_backward": (S, [P, I64, S, I64, I64, I64, P, I64, P, P]),
+    "fp8_moe_combine": (S, [P, I64, S, I64, I64, I64, P, I64, P, P, P]),
+    "fp8_moe_combine_backward": (S, [P, I64, P, I64, S, I64, I64, I64, P, P, I64, P, P, P, P]),
+    "fp8_orthogonalize_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64]),
+    "fp8_orthogonalize": (S, [P, I64, I64, S, I64, I64, I64, I32, ctypes.POINTER(F32), F32, F32,
+                              P, P, P]),
     "fp8_check_device_status": (S, [P]),
     "fp8_inject_launch_failures": (S, [I32]),
     "fp8_selftest_wait_timeout": (S, [U32, P]),

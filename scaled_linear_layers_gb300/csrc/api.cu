@@ -997,6 +997,304 @@ fp8_status fp8_inject_launch_failures(int32_t n) {
     return FP8_OK;
 }
 
+// ------------------------------------------- norm, expert rows, updates ---
+
+namespace {
+
+fp8_status check_dtype(const char *who, fp8_dtype t) {
+    if (t != FP8_DT_BF16 && t != FP8_DT_F32)
+        return fail(FP8_ERR_SHAPE, "%s: unknown element type %d", who, (int)t);
+    return FP8_OK;
+}
+
+fp8_status check_elem(const char *who, const char *name, const void *p, fp8_dtype t) {
+    if ((reinterpret_cast<uintptr_t>(p) & (t == FP8_DT_F32 ? 3u : 1u)) != 0)
+        return fail(FP8_ERR_ALIGNMENT, "%s: %s is not aligned to its elements", who, name);
+    return FP8_OK;
+}
+
+#define FP8_ELEM(ptr, t, who) FP8_TRY(check_elem(who, #ptr, ptr, t))
+
+// tokens, topk, hidden, capacity and the row stride of an expert-row call.
+fp8_status check_moe(const char *who, fp8_dtype t, int64_t tokens, int64_t topk, int64_t hidden,
+                     int64_t capacity, int64_t ld) {
+    FP8_TRY(check_dtype(who, t));
+    if (tokens < 0 || topk < 1 || hidden < 0 || capacity < 0 || ld < 0)
+        return fail(FP8_ERR_SHAPE,
+                    "%s: tokens=%lld topk=%lld hidden=%lld capacity=%lld row stride=%lld", who,
+                    (long long)tokens, (long long)topk, (long long)hidden, (long long)capacity,
+                    (long long)ld);
+    if (topk > 0x7FFFFFFF || capacity > 0x7FFFFFFF || tokens > 0x7FFFFFFF / topk)
+        return fail(FP8_ERR_SHAPE, "%s: rows and assignments must be below 2^31", who);
+    return FP8_OK;
+}
+
+}  // namespace
+
+fp8_status fp8_layer_norm(const void *x, int64_t ldx, fp8_dtype xt, const void *weight,
+                          const void *bias, fp8_dtype wt, int64_t rows, int64_t cols, float eps,
+                          void *y, uint8_t *yq, const float *scale_inv, float *amax_out,
+                          float *mean, float *rstd, cudaStream_t s) {
+    const char *who = "fp8_layer_norm";
+    FP8_TRY(check_dtype(who, xt));
+    FP8_TRY(check_dtype(who, wt));
+    if (rows < 0 || cols < 0 || cols > 0x7FFFFFFF || ldx < 0)
+        return fail(FP8_ERR_SHAPE, "%s: shape [%lld, %lld], row stride %lld", who, (long long)rows,
+                    (long long)cols, (long long)ldx);
+    if (!(eps >= 0.f)) return fail(FP8_ERR_SHAPE, "%s: eps must be at least 0", who);
+    if (rows > 0 && cols > 0) {
+        FP8_NEED(x, who);
+        if (y == nullptr) FP8_NEED(yq, who);
+    }
+    if (yq != nullptr) FP8_NEED(scale_inv, who);
+    FP8_ELEM(x, xt, who);
+    FP8_ELEM(y, xt, who);
+    FP8_ELEM(weight, wt, who);
+    FP8_ELEM(bias, wt, who);
+    FP8_ELEM(scale_inv, FP8_DT_F32, who);
+    FP8_ELEM(amax_out, FP8_DT_F32, who);
+    FP8_ELEM(mean, FP8_DT_F32, who);
+    FP8_ELEM(rstd, FP8_DT_F32, who);
+    FP8_TRY(check_device(who));
+    const NormForward n = {x, ldx, xt == FP8_DT_F32, weight, bias, wt == FP8_DT_F32, rows, cols,
+                           eps, y, yq, scale_inv, amax_out, mean, rstd};
+    return cuda_status(launch_layer_norm(n, s), who);
+}
+
+size_t fp8_layer_norm_workspace_bytes(int64_t rows, int64_t cols) {
+    if (rows <= 0 || cols <= 0) return 0;
+    const int64_t parts = rows < kNormMaxPartials ? rows : kNormMaxPartials;
+    return (size_t)(2 * parts * cols) * sizeof(float);
+}
+
+fp8_status fp8_layer_norm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                                   fp8_dtype xt, const void *weight, fp8_dtype wt,
+                                   const float *mean, const float *rstd, int64_t rows,
+                                   int64_t cols, void *dx, void *dweight, void *dbias,
+                                   void *workspace, cudaStream_t s) {
+    const char *who = "fp8_layer_norm_backward";
+    FP8_TRY(check_dtype(who, xt));
+    FP8_TRY(check_dtype(who, wt));
+    if (rows < 0 || cols < 0 || cols > 0x7FFFFFFF || ldx < 0 || lddy < 0)
+        return fail(FP8_ERR_SHAPE, "%s: shape [%lld, %lld], row strides %lld, %lld", who,
+                    (long long)rows, (long long)cols, (long long)lddy, (long long)ldx);
+    if (dx == nullptr && dweight == nullptr && dbias == nullptr)
+        return fail(FP8_ERR_NULL, "%s: dx, dweight and dbias are all NULL", who);
+    if (rows > 0 && cols > 0) {
+        FP8_NEED(dy, who);
+        FP8_NEED(x, who);
+        FP8_NEED(mean, who);
+        FP8_NEED(rstd, who);
+        if (dweight != nullptr || dbias != nullptr) FP8_NEED(workspace, who);
+    }
+    FP8_ELEM(dy, xt, who);
+    FP8_ELEM(x, xt, who);
+    FP8_ELEM(dx, xt, who);
+    FP8_ELEM(weight, wt, who);
+    FP8_ELEM(dweight, wt, who);
+    FP8_ELEM(dbias, wt, who);
+    FP8_ELEM(mean, FP8_DT_F32, who);
+    FP8_ELEM(rstd, FP8_DT_F32, who);
+    FP8_ALIGN(workspace, who);
+    FP8_TRY(check_device(who));
+    const NormBackward n = {dy, x, lddy, ldx, xt == FP8_DT_F32, weight, wt == FP8_DT_F32, rows,
+                            cols, mean, rstd, dx, dweight, dbias,
+                            reinterpret_cast<float *>(workspace)};
+    return cuda_status(launch_layer_norm_backward(n, s), who);
+}
+
+int64_t fp8_moe_capacity(int64_t n, int64_t experts, int64_t multiple) {
+    if (n < 0 || experts < 1 || multiple < 1 || n > 0x7FFFFFFF || experts > 0x7FFFFFFF ||
+        multiple > 0x7FFFFFFF)
+        return -1;
+    const int64_t active = n < experts ? n : experts;
+    return n + active * (multiple - 1);
+}
+
+size_t fp8_moe_sort_workspace_bytes(int64_t n, int64_t experts) {
+    if (n <= kMoeMinChunk || experts < 1) return 0;
+    return (size_t)(kMoeMaxChunks * experts) * sizeof(int32_t);
+}
+
+fp8_status fp8_moe_sort(const void *ids, int32_t ids_64, int64_t n, int64_t experts,
+                        int64_t multiple, int64_t capacity, int32_t *row_of, int32_t *source,
+                        int32_t *offsets, int32_t *counts, void *workspace, cudaStream_t s) {
+    const char *who = "fp8_moe_sort";
+    const int64_t need = fp8_moe_capacity(n, experts, multiple);
+    if (need < 0)
+        return fail(FP8_ERR_SHAPE, "%s: n=%lld experts=%lld multiple=%lld", who, (long long)n,
+                    (long long)experts, (long long)multiple);
+    if (experts > kMoeMaxExperts)
+        return fail(FP8_ERR_UNSUPPORTED, "%s: experts=%lld, at most %d", who, (long long)experts,
+                    kMoeMaxExperts);
+    if (capacity < need || capacity > 0x7FFFFFFF)
+        return fail(FP8_ERR_SHAPE, "%s: capacity=%lld, %lld to 2^31 - 1 rows are needed", who,
+                    (long long)capacity, (long long)need);
+    if (n > 0) {
+        FP8_NEED(ids, who);
+        FP8_NEED(row_of, who);
+    }
+    if (capacity > 0) FP8_NEED(source, who);
+    FP8_NEED(offsets, who);
+    FP8_NEED(counts, who);
+    if (fp8_moe_sort_workspace_bytes(n, experts) > 0) FP8_NEED(workspace, who);
+    if ((reinterpret_cast<uintptr_t>(ids) & (ids_64 ? 7u : 3u)) != 0)
+        return fail(FP8_ERR_ALIGNMENT, "%s: ids is not aligned to its elements", who);
+    FP8_ELEM(row_of, FP8_DT_F32, who);
+    FP8_ELEM(source, FP8_DT_F32, who);
+    FP8_ELEM(offsets, FP8_DT_F32, who);
+    FP8_ELEM(counts, FP8_DT_F32, who);
+    FP8_ELEM(workspace, FP8_DT_F32, who);
+    FP8_TRY(check_device(who));
+    return cuda_status(launch_moe_sort(ids, ids_64 != 0, n, (int)experts, multiple, capacity,
+                                       row_of, source, offsets, counts,
+                                       reinterpret_cast<int32_t *>(workspace), s),
+                       who);
+}
+
+fp8_status fp8_moe_dispatch(const void *x, int64_t ldx, fp8_dtype xt, int64_t tokens,
+                            int64_t topk, int64_t hidden, const int32_t *row_of,
+                            const int32_t *source, int64_t capacity, void *rows, uint8_t *rows_q,
+                            const float *scale_inv, float *amax_out, cudaStream_t s) {
+    const char *who = "fp8_moe_dispatch";
+    FP8_TRY(check_moe(who, xt, tokens, topk, hidden, capacity, ldx));
+    if (rows != nullptr && rows_q != nullptr)
+        return fail(FP8_ERR_UNSUPPORTED, "%s: rows and rows_q are both given", who);
+    if (amax_out != nullptr && rows != nullptr)
+        return fail(FP8_ERR_UNSUPPORTED, "%s: amax_out goes with rows_q", who);
+    if (tokens > 0) {
+        if (hidden > 0) FP8_NEED(x, who);
+        FP8_NEED(row_of, who);
+    }
+    if (capacity > 0) {
+        FP8_NEED(source, who);
+        if (rows == nullptr && hidden > 0) FP8_NEED(rows_q, who);
+    }
+    if (rows_q != nullptr) FP8_NEED(scale_inv, who);
+    FP8_ELEM(x, xt, who);
+    FP8_ELEM(rows, xt, who);
+    FP8_ELEM(row_of, FP8_DT_F32, who);
+    FP8_ELEM(source, FP8_DT_F32, who);
+    FP8_ELEM(scale_inv, FP8_DT_F32, who);
+    FP8_ELEM(amax_out, FP8_DT_F32, who);
+    FP8_TRY(check_device(who));
+    const MoeRows m = {row_of, source, tokens, capacity, hidden, (int)topk, xt == FP8_DT_F32};
+    return cuda_status(launch_moe_dispatch(m, x, ldx, rows, rows_q, scale_inv, amax_out, s), who);
+}
+
+namespace {
+
+fp8_status combine(const char *who, const void *rows, int64_t ldr, fp8_dtype xt, int64_t tokens,
+                   int64_t topk, int64_t hidden, const int32_t *row_of, int64_t capacity,
+                   const float *weights, void *y, cudaStream_t s) {
+    FP8_TRY(check_moe(who, xt, tokens, topk, hidden, capacity, ldr));
+    if (tokens > 0 && hidden > 0) {
+        if (capacity > 0) FP8_NEED(rows, who);
+        FP8_NEED(row_of, who);
+        FP8_NEED(y, who);
+    }
+    FP8_ELEM(rows, xt, who);
+    FP8_ELEM(y, xt, who);
+    FP8_ELEM(row_of, FP8_DT_F32, who);
+    FP8_ELEM(weights, FP8_DT_F32, who);
+    FP8_TRY(check_device(who));
+    const MoeRows m = {row_of, nullptr, tokens, capacity, hidden, (int)topk, xt == FP8_DT_F32};
+    return cuda_status(launch_moe_combine(m, rows, ldr, weights, y, s), who);
+}
+
+}  // namespace
+
+fp8_status fp8_moe_dispatch_backward(const void *drows, int64_t ldr, fp8_dtype xt, int64_t tokens,
+                                     int64_t topk, int64_t hidden, const int32_t *row_of,
+                                     int64_t capacity, void *dx, cudaStream_t s) {
+    return combine("fp8_moe_dispatch_backward", drows, ldr, xt, tokens, topk, hidden, row_of,
+                   capacity, nullptr, dx, s);
+}
+
+fp8_status fp8_moe_combine(const void *rows, int64_t ldr, fp8_dtype xt, int64_t tokens,
+                           int64_t topk, int64_t hidden, const int32_t *row_of, int64_t capacity,
+                           const float *weights, void *y, cudaStream_t s) {
+    return combine("fp8_moe_combine", rows, ldr, xt, tokens, topk, hidden, row_of, capacity,
+                   weights, y, s);
+}
+
+fp8_status fp8_moe_combine_backward(const void *dy, int64_t lddy, const void *rows, int64_t ldr,
+                                    fp8_dtype xt, int64_t tokens, int64_t topk, int64_t hidden,
+                                    const int32_t *row_of, const int32_t *source, int64_t capacity,
+                                    const float *weights, void *drows, float *dweights,
+                                    cudaStream_t s) {
+    const char *who = "fp8_moe_combine_backward";
+    FP8_TRY(check_moe(who, xt, tokens, topk, hidden, capacity, lddy < ldr ? lddy : ldr));
+    if (tokens > 0) {
+        if (hidden > 0) FP8_NEED(dy, who);
+        FP8_NEED(row_of, who);
+    }
+    if (capacity > 0 && hidden > 0) {
+        FP8_NEED(rows, who);
+        FP8_NEED(source, who);
+        FP8_NEED(drows, who);
+    }
+    FP8_ELEM(dy, xt, who);
+    FP8_ELEM(rows, xt, who);
+    FP8_ELEM(drows, xt, who);
+    FP8_ELEM(row_of, FP8_DT_F32, who);
+    FP8_ELEM(source, FP8_DT_F32, who);
+    FP8_ELEM(weights, FP8_DT_F32, who);
+    FP8_ELEM(dweights, FP8_DT_F32, who);
+    FP8_TRY(check_device(who));
+    const MoeRows m = {row_of, source, tokens, capacity, hidden, (int)topk, xt == FP8_DT_F32};
+    return cuda_status(
+        launch_moe_combine_backward(m, dy, lddy, rows, ldr, weights, drows, dweights, s), who);
+}
+
+namespace {
+
+constexpr int64_t kOrthoMaxDim = 65536;
+
+bool orthogonalize_fits(int64_t batch, int64_t rows, int64_t cols) {
+    if (batch < 0 || rows < 0 || cols < 0 || rows > kOrthoMaxDim || cols > kOrthoMaxDim)
+        return false;
+    const int64_t tiles = ((rows + 127) / 128) * ((cols + 127) / 128);
+    return batch == 0 || tiles <= 0x7FFFFFFF / batch;
+}
+
+}  // namespace
+
+size_t fp8_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
+    if (!orthogonalize_fits(batch, rows, cols) || batch == 0 || rows == 0 || cols == 0) return 0;
+    return (size_t)orthogonalize_workspace_bytes(batch, rows, cols);
+}
+
+fp8_status fp8_orthogonalize(const void *g, int64_t ldg, int64_t bsg, fp8_dtype gt, int64_t batch,
+                             int64_t rows, int64_t cols, int32_t steps, const float *coefficients,
+                             float eps, float scale, uint16_t *out, void *workspace,
+                             cudaStream_t s) {
+    const char *who = "fp8_orthogonalize";
+    FP8_TRY(check_dtype(who, gt));
+    if (!orthogonalize_fits(batch, rows, cols) || ldg < 0 || bsg < 0)
+        return fail(FP8_ERR_SHAPE, "%s: shape [%lld, %lld, %lld], strides %lld, %lld", who,
+                    (long long)batch, (long long)rows, (long long)cols, (long long)bsg,
+                    (long long)ldg);
+    if (steps < 1 || steps > 64)
+        return fail(FP8_ERR_SHAPE, "%s: steps=%d, 1 to 64 are possible", who, steps);
+    if (!(eps >= 0.f)) return fail(FP8_ERR_SHAPE, "%s: eps must be at least 0", who);
+    FP8_NEED(coefficients, who);
+    if (batch > 0 && rows > 0 && cols > 0) {
+        FP8_NEED(g, who);
+        FP8_NEED(out, who);
+        FP8_NEED(workspace, who);
+    }
+    FP8_ELEM(g, gt, who);
+    FP8_ELEM(out, FP8_DT_BF16, who);
+    FP8_ALIGN(workspace, who);
+    FP8_TRY(check_device(who));
+    const Orthogonalize o = {g, ldg, bsg, gt == FP8_DT_F32, batch, rows, cols, steps, coefficients,
+                             eps, scale, out, workspace};
+    const char *why = nullptr;
+    const cudaError_t e = launch_orthogonalize(o, s, &why);
+    return cuda_status(e, who, why);
+}
+
 fp8_status fp8_check_device_status(cudaStream_t s) {
     const char *who = "fp8_check_device_status";
     cudaError_t e = cudaStreamSynchronize(s);

@@ -155,6 +155,78 @@ struct BlockScales {
 cudaError_t launch_gemm_block(const uint8_t *A, const uint8_t *B, int64_t M, int64_t N, int64_t K,
                               const BlockScales &sc, uint16_t *D, cudaStream_t s, const char **why);
 
+// Layer norm of rows of x (layer_norm.cu).  x_f32 / param_f32: fp32 instead of
+// bf16; nullable: w, b, y, yq (which needs scale_inv), amax, mean, rstd.
+struct NormForward {
+    const void *x;
+    int64_t ldx;
+    int x_f32;
+    const void *w, *b;
+    int param_f32;
+    int64_t rows, cols;
+    float eps;
+    void *y;
+    uint8_t *yq;
+    const float *scale_inv;
+    float *amax, *mean, *rstd;
+};
+cudaError_t launch_layer_norm(const NormForward &n, cudaStream_t s);
+// Its gradient; nullable: w, dx, dw, db.  workspace: 2 * min(rows,
+// kNormMaxPartials) * cols floats when dw or db is wanted.
+constexpr int kNormMaxPartials = 512;
+struct NormBackward {
+    const void *dy, *x;
+    int64_t lddy, ldx;
+    int x_f32;
+    const void *w;
+    int param_f32;
+    int64_t rows, cols;
+    const float *mean, *rstd;
+    void *dx, *dw, *db;
+    float *workspace;
+};
+cudaError_t launch_layer_norm_backward(const NormBackward &n, cudaStream_t s);
+
+// Tokens sorted by expert and back (moe.cu).
+constexpr int kMoeMaxExperts = 1024, kMoeMaxChunks = 128;
+constexpr int64_t kMoeMinChunk = 4096;  // assignments
+// ids [n] int32 or int64; the outputs as fp8_moe_sort describes them.
+// workspace: kMoeMaxChunks * experts ints when n > kMoeMinChunk.
+cudaError_t launch_moe_sort(const void *ids, int ids_64, int64_t n, int experts, int64_t multiple,
+                            int64_t capacity, int32_t *row_of, int32_t *source, int32_t *offsets,
+                            int32_t *counts, int32_t *workspace, cudaStream_t s);
+struct MoeRows {
+    const int32_t *row_of, *source;  // [tokens, topk], [capacity]
+    int64_t tokens, capacity, hidden;
+    int topk;
+    int f32;  // element type of the rows
+};
+// out (x's type) or, with scale_inv, outq = the tokens' rows at their places.
+cudaError_t launch_moe_dispatch(const MoeRows &m, const void *x, int64_t ldx, void *out,
+                                uint8_t *outq, const float *scale_inv, float *amax, cudaStream_t s);
+// y[t] = sum_j weights[t, j] * rows[row_of[t, j]] (weights nullable: ones).
+cudaError_t launch_moe_combine(const MoeRows &m, const void *rows, int64_t ldr,
+                               const float *weights, void *y, cudaStream_t s);
+cudaError_t launch_moe_combine_backward(const MoeRows &m, const void *dy, int64_t lddy,
+                                        const void *rows, int64_t ldr, const float *weights,
+                                        void *drows, float *dweights, cudaStream_t s);
+
+// Newton-Schulz orthogonalisation of a batch of [rows, cols] matrices
+// (orthogonalize.cu).
+struct Orthogonalize {
+    const void *g;
+    int64_t ldg, bsg;  // row and batch strides in elements
+    int g_f32;
+    int64_t batch, rows, cols;
+    int steps;
+    const float *coefficients;  // [steps][3], host
+    float eps, scale;
+    uint16_t *out;
+    void *workspace;
+};
+int64_t orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
+cudaError_t launch_orthogonalize(const Orthogonalize &o, cudaStream_t s, const char **why);
+
 cudaError_t launch_meta_init(float *dev, int interval, cudaStream_t s);
 cudaError_t launch_meta_copy(float *dst, const float *src, cudaStream_t s);
 cudaError_t launch_meta_lag(float *scale, float *scale_inv, const float *amax, cudaStream_t s);
