@@ -54,8 +54,10 @@ def _ptr(t):
 
 
 def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:
+        # current_stream() without the Stream object around the handle
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _check(status: int):
@@ -412,59 +414,73 @@ def fp8_pad_tokens(x, multiple, out, stream=None) -> int:
 _DTYPES = {torch.bfloat16: _lib.DT_BF16, torch.float32: _lib.DT_F32}
 
 
-def _need(ok, status, message):
-    if not ok:
-        raise Fp8Error(status, message)
+def _refuse(status, message):
+    raise Fp8Error(status, message)
 
 
 def _rows(t, who, name, dtype=None, shape=None):
     """A 2-d tensor of rows on the GPU, each contiguous (any row stride);
     returns (pointer, row stride)."""
-    _need(isinstance(t, torch.Tensor) and t.is_cuda, _lib.FP8_ERR_NULL,
-          f"{who}: {name} is not a CUDA tensor")
-    _need(t.dtype in _DTYPES if dtype is None else t.dtype == dtype, _lib.FP8_ERR_UNSUPPORTED,
-          f"{who}: {name} has type {t.dtype}")
-    _need(t.dim() == 2 and (shape is None or tuple(t.shape) == tuple(shape)),
-          _lib.FP8_ERR_SHAPE, f"{who}: {name} has shape {tuple(t.shape)}")
-    _need(t.shape[1] <= 1 or t.stride(1) == 1, _lib.FP8_ERR_SHAPE,
-          f"{who}: {name}'s rows are not contiguous")
-    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _refuse(_lib.FP8_ERR_NULL, f"{who}: {name} is not a CUDA tensor")
+    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
+        _refuse(_lib.FP8_ERR_UNSUPPORTED, f"{who}: {name} has type {t.dtype}")
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        _refuse(_lib.FP8_ERR_SHAPE, f"{who}: {name} has shape {tuple(t.shape)}")
+    n, width = t.shape
+    if width > 1 and t.stride(1) != 1:
+        _refuse(_lib.FP8_ERR_SHAPE, f"{who}: {name}'s rows are not contiguous")
+    return t.data_ptr(), t.stride(0) if n > 1 else width
 
 
 def _dense(t, who, name, dtypes, shape):
-    """A contiguous CUDA tensor of one of `dtypes` and of `shape`, or None."""
+    """The pointer of a contiguous CUDA tensor of one of `dtypes` and of
+    `shape`, or None for None."""
     if t is None:
         return None
-    _need(isinstance(t, torch.Tensor) and t.is_cuda, _lib.FP8_ERR_NULL,
-          f"{who}: {name} is not a CUDA tensor")
-    _need(t.dtype in dtypes, _lib.FP8_ERR_UNSUPPORTED, f"{who}: {name} has type {t.dtype}")
-    _need(tuple(t.shape) == tuple(shape) and t.is_contiguous(), _lib.FP8_ERR_SHAPE,
-          f"{who}: {name} must be contiguous with shape {tuple(shape)}, not {tuple(t.shape)}")
-    return ctypes.c_void_p(t.data_ptr())
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _refuse(_lib.FP8_ERR_NULL, f"{who}: {name} is not a CUDA tensor")
+    if t.dtype not in dtypes:
+        _refuse(_lib.FP8_ERR_UNSUPPORTED, f"{who}: {name} has type {t.dtype}")
+    if t.shape != shape or not t.is_contiguous():
+        _refuse(_lib.FP8_ERR_SHAPE,
+                f"{who}: {name} must be contiguous with shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def _workspace(t, who, nbytes):
     if t is None:
-        _need(nbytes == 0, _lib.FP8_ERR_NULL, f"{who}: a workspace of {nbytes} bytes is needed")
+        if nbytes > 0:
+            _refuse(_lib.FP8_ERR_NULL, f"{who}: a workspace of {nbytes} bytes is needed")
         return None
-    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous(), _lib.FP8_ERR_NULL,
-          f"{who}: workspace is not a contiguous CUDA tensor")
-    _need(t.numel() * t.element_size() >= nbytes, _lib.FP8_ERR_SHAPE,
-          f"{who}: a workspace of {nbytes} bytes is needed")
-    return ctypes.c_void_p(t.data_ptr())
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+        _refuse(_lib.FP8_ERR_NULL, f"{who}: workspace is not a contiguous CUDA tensor")
+    if t.numel() * t.element_size() < nbytes:
+        _refuse(_lib.FP8_ERR_SHAPE, f"{who}: a workspace of {nbytes} bytes is needed")
+    return t.data_ptr()
 
 
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
 _E4M3 = (torch.uint8, torch.float8_e4m3fn)
+_BF16 = (torch.bfloat16,)
 
 
-def _params(who, cols, **named):
-    """Pointers of nullable [cols] parameter vectors and their common type."""
-    got = [t for t in named.values() if t is not None]
-    dtype = got[0].dtype if got else torch.float32
-    _need(dtype in _DTYPES, _lib.FP8_ERR_UNSUPPORTED, f"{who}: parameters of type {dtype}")
-    return [_dense(t, who, n, (dtype,), (cols,)) for n, t in named.items()], _DTYPES[dtype]
+def _param_type(who, *params):
+    """The common type of nullable parameter vectors, as a one-element tuple."""
+    for t in params:
+        if t is not None:
+            if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES:
+                _refuse(_lib.FP8_ERR_UNSUPPORTED, f"{who}: parameters must be bf16 or fp32 tensors")
+            return (t.dtype,)
+    return _F32
+
+
+def _source(who, source):
+    if not isinstance(source, torch.Tensor) or source.dim() != 1:
+        _refuse(_lib.FP8_ERR_SHAPE, f"{who}: source must be [capacity]")
+    cap = source.shape[0]
+    return _dense(source, who, "source", _I32, (cap,)), cap
 
 
 def fp8_layer_norm(x, weight, bias, eps, y=None, mean=None, rstd=None, yq=None, scale_inv=None,
@@ -474,9 +490,10 @@ def fp8_layer_norm(x, weight, bias, eps, y=None, mean=None, rstd=None, yq=None, 
     who = "fp8_layer_norm"
     xp, ldx = _rows(x, who, "x")
     rows, cols = x.shape
-    (wp, bp), wt = _params(who, cols, weight=weight, bias=bias)
+    pt = _param_type(who, weight, bias)
     _check(_LIB.fp8_layer_norm(
-        xp, ldx, _DTYPES[x.dtype], wp, bp, wt, rows, cols, float(eps),
+        xp, ldx, _DTYPES[x.dtype], _dense(weight, who, "weight", pt, (cols,)),
+        _dense(bias, who, "bias", pt, (cols,)), _DTYPES[pt[0]], rows, cols, eps,
         _dense(y, who, "y", (x.dtype,), x.shape), _dense(yq, who, "yq", _E4M3, x.shape),
         _dense(scale_inv, who, "scale_inv", _F32, (1,)),
         _dense(amax_out, who, "amax_out", _F32, (1,)), _dense(mean, who, "mean", _F32, (rows,)),
@@ -494,13 +511,15 @@ def fp8_layer_norm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, db
     xp, ldx = _rows(x, who, "x")
     rows, cols = x.shape
     gp, lddy = _rows(dy, who, "dy", x.dtype, x.shape)
-    (wp, dwp, dbp), wt = _params(who, cols, weight=weight, dweight=dweight, dbias=dbias)
+    pt = _param_type(who, weight, dweight, dbias)
     sums = dweight is not None or dbias is not None
     ws = _workspace(workspace, who, fp8_layer_norm_workspace_bytes(rows, cols) if sums else 0)
     _check(_LIB.fp8_layer_norm_backward(
-        gp, lddy, xp, ldx, _DTYPES[x.dtype], wp, wt, _dense(mean, who, "mean", _F32, (rows,)),
+        gp, lddy, xp, ldx, _DTYPES[x.dtype], _dense(weight, who, "weight", pt, (cols,)),
+        _DTYPES[pt[0]], _dense(mean, who, "mean", _F32, (rows,)),
         _dense(rstd, who, "rstd", _F32, (rows,)), rows, cols,
-        _dense(dx, who, "dx", (x.dtype,), x.shape), dwp, dbp, ws, _stream(stream)))
+        _dense(dx, who, "dx", (x.dtype,), x.shape), _dense(dweight, who, "dweight", pt, (cols,)),
+        _dense(dbias, who, "dbias", pt, (cols,)), ws, _stream(stream)))
 
 
 def fp8_moe_capacity(assignments: int, experts: int, multiple: int) -> int:
@@ -516,24 +535,22 @@ def fp8_moe_sort(ids, experts, multiple, row_of, source, offsets, counts, worksp
     """Sorts the assignments ids [tokens, topk] (int32 or int64) by expert: see
     the C header for row_of, source, offsets and counts (int32)."""
     who = "fp8_moe_sort"
-    _need(isinstance(ids, torch.Tensor) and ids.dim() == 2, _lib.FP8_ERR_SHAPE,
-          f"{who}: ids must be [tokens, topk]")
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        _refuse(_lib.FP8_ERR_SHAPE, f"{who}: ids must be [tokens, topk]")
     ip = _dense(ids, who, "ids", (torch.int32, torch.int64), ids.shape)
     n = ids.numel()
-    _need(source is not None and source.dim() == 1, _lib.FP8_ERR_SHAPE,
-          f"{who}: source must be [capacity]")
+    sp, cap = _source(who, source)
     ws = _workspace(workspace, who, fp8_moe_sort_workspace_bytes(n, experts))
     _check(_LIB.fp8_moe_sort(
-        ip, ids.dtype == torch.int64, n, experts, multiple, source.shape[0],
-        _dense(row_of, who, "row_of", _I32, ids.shape),
-        _dense(source, who, "source", _I32, source.shape),
+        ip, ids.dtype == torch.int64, n, experts, multiple, cap,
+        _dense(row_of, who, "row_of", _I32, ids.shape), sp,
         _dense(offsets, who, "offsets", _I32, (experts + 1,)),
         _dense(counts, who, "counts", _I32, (experts,)), ws, _stream(stream)))
 
 
 def _route(who, row_of, tokens):
-    _need(isinstance(row_of, torch.Tensor) and row_of.dim() == 2, _lib.FP8_ERR_SHAPE,
-          f"{who}: row_of must be [tokens, topk]")
+    if not isinstance(row_of, torch.Tensor) or row_of.dim() != 2:
+        _refuse(_lib.FP8_ERR_SHAPE, f"{who}: row_of must be [tokens, topk]")
     topk = row_of.shape[1]
     return _dense(row_of, who, "row_of", _I32, (tokens, topk)), topk
 
@@ -545,14 +562,11 @@ def fp8_moe_dispatch(x, row_of, source, rows, scale_inv=None, amax_out=None, str
     xp, ldx = _rows(x, who, "x")
     tokens, hidden = x.shape
     rp, topk = _route(who, row_of, tokens)
-    _need(source is not None and source.dim() == 1, _lib.FP8_ERR_SHAPE,
-          f"{who}: source must be [capacity]")
-    cap = source.shape[0]
+    sp, cap = _source(who, source)
     quant = scale_inv is not None
     out = _dense(rows, who, "rows", _E4M3 if quant else (x.dtype,), (cap, hidden))
     _check(_LIB.fp8_moe_dispatch(
-        xp, ldx, _DTYPES[x.dtype], tokens, topk, hidden, rp,
-        _dense(source, who, "source", _I32, (cap,)), cap, None if quant else out,
+        xp, ldx, _DTYPES[x.dtype], tokens, topk, hidden, rp, sp, cap, None if quant else out,
         out if quant else None, _dense(scale_inv, who, "scale_inv", _F32, (1,)),
         _dense(amax_out, who, "amax_out", _F32, (1,)), _stream(stream)))
 
@@ -561,7 +575,8 @@ def fp8_moe_dispatch_backward(drows, row_of, dx, stream=None):
     """dx [tokens, hidden] = the sum of each token's rows of drows."""
     who = "fp8_moe_dispatch_backward"
     dp, ldr = _rows(drows, who, "drows")
-    _need(dx is not None and dx.dim() == 2, _lib.FP8_ERR_SHAPE, f"{who}: dx must be 2-d")
+    if not isinstance(dx, torch.Tensor) or dx.dim() != 2:
+        _refuse(_lib.FP8_ERR_SHAPE, f"{who}: dx must be [tokens, hidden]")
     tokens, hidden = dx.shape[0], drows.shape[1]
     rp, topk = _route(who, row_of, tokens)
     _check(_LIB.fp8_moe_dispatch_backward(
@@ -574,7 +589,8 @@ def fp8_moe_combine(rows, row_of, weights, y, stream=None):
     fp32 [tokens, topk] or None for ones)."""
     who = "fp8_moe_combine"
     sp, ldr = _rows(rows, who, "rows")
-    _need(y is not None and y.dim() == 2, _lib.FP8_ERR_SHAPE, f"{who}: y must be 2-d")
+    if not isinstance(y, torch.Tensor) or y.dim() != 2:
+        _refuse(_lib.FP8_ERR_SHAPE, f"{who}: y must be [tokens, hidden]")
     tokens, hidden = y.shape[0], rows.shape[1]
     rp, topk = _route(who, row_of, tokens)
     _check(_LIB.fp8_moe_combine(
@@ -591,7 +607,8 @@ def fp8_moe_combine_backward(dy, rows, row_of, source, weights, drows, dweights=
     cap, hidden = rows.shape
     gp, lddy = _rows(dy, who, "dy", rows.dtype)
     tokens = dy.shape[0]
-    _need(dy.shape[1] == hidden, _lib.FP8_ERR_SHAPE, f"{who}: dy and rows differ in width")
+    if dy.shape[1] != hidden:
+        _refuse(_lib.FP8_ERR_SHAPE, f"{who}: dy and rows differ in width")
     rp, topk = _route(who, row_of, tokens)
     _check(_LIB.fp8_moe_combine_backward(
         gp, lddy, sp, ldr, _DTYPES[rows.dtype], tokens, topk, hidden, rp,
@@ -611,24 +628,28 @@ def fp8_orthogonalize(g, out, workspace, steps=5, coefficients=(3.4445, -4.7750,
     cols] or of each matrix of g [batch, rows, cols] (bf16 or fp32).
     ``coefficients`` is (a, b, c) for every step or one such triple a step."""
     who = "fp8_orthogonalize"
-    _need(isinstance(g, torch.Tensor) and g.is_cuda, _lib.FP8_ERR_NULL,
-          f"{who}: g is not a CUDA tensor")
-    _need(g.dtype in _DTYPES, _lib.FP8_ERR_UNSUPPORTED, f"{who}: g has type {g.dtype}")
-    _need(g.dim() in (2, 3), _lib.FP8_ERR_SHAPE, f"{who}: g has shape {tuple(g.shape)}")
+    if not isinstance(g, torch.Tensor) or not g.is_cuda:
+        _refuse(_lib.FP8_ERR_NULL, f"{who}: g is not a CUDA tensor")
+    if g.dtype not in _DTYPES:
+        _refuse(_lib.FP8_ERR_UNSUPPORTED, f"{who}: g has type {g.dtype}")
+    if g.dim() not in (2, 3):
+        _refuse(_lib.FP8_ERR_SHAPE, f"{who}: g has shape {tuple(g.shape)}")
     batch = g.shape[0] if g.dim() == 3 else 1
     rows, cols = g.shape[-2:]
-    _need(cols <= 1 or g.stride(-1) == 1, _lib.FP8_ERR_SHAPE,
-          f"{who}: g's rows are not contiguous")
+    if cols > 1 and g.stride(-1) != 1:
+        _refuse(_lib.FP8_ERR_SHAPE, f"{who}: g's rows are not contiguous")
     triples = [coefficients] * steps if not hasattr(coefficients[0], "__len__") else coefficients
-    _need(len(triples) == steps and all(len(t) == 3 for t in triples), _lib.FP8_ERR_SHAPE,
-          f"{who}: coefficients must be (a, b, c) or {steps} such triples")
+    if len(triples) != steps or any(len(t) != 3 for t in triples):
+        _refuse(_lib.FP8_ERR_SHAPE,
+                f"{who}: coefficients must be (a, b, c) or {steps} such triples")
     flat = [float(v) for t in triples for v in t]
-    _need(out is not None, _lib.FP8_ERR_NULL, f"{who}: out is None")
+    if out is None:
+        _refuse(_lib.FP8_ERR_NULL, f"{who}: out is None")
     _check(_LIB.fp8_orthogonalize(
-        ctypes.c_void_p(g.data_ptr()), g.stride(-2) if rows > 1 else cols,
+        g.data_ptr(), g.stride(-2) if rows > 1 else cols,
         g.stride(0) if batch > 1 and g.dim() == 3 else rows * cols, _DTYPES[g.dtype], batch, rows,
-        cols, steps, (ctypes.c_float * max(1, len(flat)))(*flat), float(eps), float(scale),
-        _dense(out, who, "out", (torch.bfloat16,), g.shape),
+        cols, steps, (ctypes.c_float * max(1, len(flat)))(*flat), eps, scale,
+        _dense(out, who, "out", _BF16, g.shape),
         _workspace(workspace, who, fp8_orthogonalize_workspace_bytes(batch, rows, cols)),
         _stream(stream)))
 

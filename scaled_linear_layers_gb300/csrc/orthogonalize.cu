@@ -160,9 +160,10 @@ struct NsArgs {
     unsigned int *status;
 };
 
-constexpr int NS_THREADS = 192;
+constexpr int NS_EPI_WARPS = 8;                // two to each quarter of the lanes
+constexpr int NS_THREADS = 64 + 32 * NS_EPI_WARPS;
 constexpr int NS_BOX = 2048;                   // a 32 x 32 box of 2-byte outputs
-constexpr int NS_STAGING = 4 * 4 * NS_BOX;     // four per epilogue warp
+constexpr int NS_STAGING = NS_EPI_WARPS * 2 * NS_BOX;  // an output and a second one
 constexpr int NS_OPERAND = 128 * 128;          // 128 rows of 64 fp16
 constexpr int NS_STAGE = 2 * NS_OPERAND;
 constexpr int NS_STAGES = 6;
@@ -254,18 +255,21 @@ __device__ __forceinline__ float2 half2_floats(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
-// D = A·Bᵀ tiles of 128*CG x 128*CG by one CTA (CG = 1) or a pair on two SMs
-// (CG = 2): warp 0 loads, warp 1 issues the MMAs, warps 2-5 write the output
+// D = A·Bᵀ tiles of 128*CG x BN by one CTA (CG = 1) or a pair on two SMs
+// (CG = 2): warp 0 loads, warp 1 issues the MMAs, the others write the output
 // from the other of two accumulators.  A_MN / B_MN: the operand's M (N) dim,
 // not K, is contiguous in memory.
-template <int CG, bool A_MN, bool B_MN, int MODE>
+template <int CG, int BN, bool A_MN, bool B_MN, int MODE>
 __device__ __forceinline__ void ns_gemm_body(const CUtensorMap &tma_a, const CUtensorMap &tma_b,
                                              const CUtensorMap &tma_d, const CUtensorMap &tma_lo,
                                              const NsArgs &p) {
     constexpr bool SYM = MODE != kUpdate;
-    constexpr int BT = 128 * CG;
-    constexpr uint32_t TMEM_COLS = 2 * BT;
-    constexpr uint32_t IDESC = idesc_f16_f32(BT, BT, A_MN, B_MN);
+    constexpr int BM = 128 * CG, BNH = BN / CG;
+    static_assert(!SYM || BM == BN, "a symmetric product takes square tiles");
+    constexpr uint32_t TMEM_COLS = 256 * CG;  // two accumulators
+    constexpr uint32_t IDESC = idesc_f16_f32(BM, BN, A_MN, B_MN);
+    // an N-contiguous B is loaded 128 columns wide whatever BN is
+    constexpr uint32_t STAGE_TX = NS_OPERAND + (B_MN ? NS_OPERAND : BNH * 128);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~uintptr_t(1023));
@@ -288,7 +292,7 @@ __device__ __forceinline__ void ns_gemm_body(const CUtensorMap &tma_a, const CUt
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&tfull[a], 1);
-            mbar_init(&tempty[a], 4 * CG);
+            mbar_init(&tempty[a], NS_EPI_WARPS * CG);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -324,14 +328,14 @@ __device__ __forceinline__ void ns_gemm_body(const CUtensorMap &tma_a, const CUt
             for (int tile = worker; tile < p.tiles && ok; tile += workers) {
                 int z, tm, tn;
                 ns_locate<SYM>(p, tile, z, tm, tn);
-                const int arow = tm * BT + (int)rank * 128, brow = tn * BT + (int)rank * 128;
+                const int arow = tm * BM + (int)rank * 128, brow = tn * BN + (int)rank * BNH;
                 for (int kb = 0; kb < nk; ++kb) {
                     if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, p.wait_limit_ns,
                                            kStatusTimeoutTma, p.status)) {
                         ok = false;
                         break;
                     }
-                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * NS_STAGE);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * STAGE_TX);
                     const uint32_t lead = CG == 2 ? mapa_shared(smem_u32(&full[stage]), 0) : 0u;
                     uint8_t *da = sA + stage * NS_OPERAND, *db = sB + stage * NS_OPERAND;
                     if constexpr (A_MN) {
@@ -380,7 +384,7 @@ __device__ __forceinline__ void ns_gemm_body(const CUtensorMap &tma_a, const CUt
                     break;
                 }
                 tc_fence_after();
-                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BT);
+                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
                 for (int kb = 0; kb < nk; ++kb) {
                     if (!mbar_wait_bounded(&full[stage], phase, abort_flag, p.wait_limit_ns,
                                            kStatusTimeoutMma, p.status)) {
@@ -412,60 +416,76 @@ __device__ __forceinline__ void ns_gemm_body(const CUtensorMap &tma_a, const CUt
             mbar_wait_bounded(drain, 0, &no_abort, p.wait_limit_ns, kStatusTimeoutMma, p.status);
         }
     } else {
-        const int quarter = warp & 3;
-        uint8_t *stg = staging + quarter * 4 * NS_BOX;
-        uint32_t chunk = 0;
+        // Two warps to each quarter of the accumulator's lanes (rows): chunks
+        // of 32 columns go to them in turn.
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        uint8_t *box = staging + (warp - 2) * 2 * NS_BOX, *box2 = box + NS_BOX;
         int it = 0;
         for (int tile = worker; tile < p.tiles; tile += workers, ++it) {
             const int acc = it & 1;
             const uint32_t acc_phase = (it >> 1) & 1;
+            int z, tm, tn;
+            ns_locate<SYM>(p, tile, z, tm, tn);
+            const int row0 = tm * BM + (int)rank * 128 + quarter * 32, row = row0 + lane;
+            const bool mirror = SYM && tm != tn;
+            const int width = row0 < p.M ? min(BN, p.N - tn * BN) : 0;
+            // The added matrix's values of a chunk, 8 columns at a time (rows
+            // are padded to a multiple of 8, so a group that starts inside
+            // the matrix is inside its row), loaded one chunk ahead of the
+            // accumulator: the first before the tile's products are done.
+            const int64_t at = z * p.bse + (int64_t)row * p.lde;
+            const bool add = MODE != kGram && p.e != nullptr && row < p.M;
+            uint4 eh[4], el[4];
+            auto fetch = [&](int c) {
+                if constexpr (MODE != kGram) {
+                    const int col = tn * BN + c * 32;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const bool in = add && c * 32 < BN && col + 8 * q < p.N;
+                        eh[q] = in ? *reinterpret_cast<const uint4 *>(p.e + at + col + 8 * q)
+                                   : make_uint4(0, 0, 0, 0);
+                        if constexpr (MODE == kUpdate)
+                            el[q] = in && p.e_lo != nullptr
+                                        ? *reinterpret_cast<const uint4 *>(p.e_lo + at + col + 8 * q)
+                                        : make_uint4(0, 0, 0, 0);
+                    }
+                }
+            };
+            fetch(half);
             const bool ok = mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, p.wait_limit_ns,
                                               kStatusTimeoutEpilogue, p.status);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             tc_fence_after();
-            int z, tm, tn;
-            ns_locate<SYM>(p, tile, z, tm, tn);
-            const int row0 = tm * BT + (int)rank * 128 + quarter * 32, row = row0 + lane;
-            const bool row_in = row < p.M;
-            const __half *er = p.e != nullptr ? p.e + z * p.bse + (int64_t)row * p.lde : nullptr;
-            const __half *lr = p.e_lo != nullptr ? p.e_lo + z * p.bse + (int64_t)row * p.lde : nullptr;
-            const bool mirror = SYM && tm != tn;
 #pragma unroll 1
-            for (int c = 0; c < BT / 32; ++c) {
-                const int col = tn * BT + c * 32;
-                if (col >= p.N || row0 >= p.M) continue;  // the same for the whole warp
+            for (int c = half; c * 32 < width; c += 2) {
+                const int col = tn * BN + c * 32;
                 uint32_t r[32];
                 tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(quarter * 32) << 16) +
-                                       (uint32_t)(acc * BT + c * 32),
+                                       (uint32_t)(acc * BN + c * 32),
                                    r);
                 tmem_ld_wait();
                 float v[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * p.acc_mul;
                 if constexpr (MODE != kGram) {
-                    if (er != nullptr && row_in) {
-                        // 8 columns at a time: rows are padded to a multiple
-                        // of 8, so a group that starts inside the matrix is
-                        // inside its row
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            if (col + 8 * q >= p.N) continue;
-                            const uint4 h = *reinterpret_cast<const uint4 *>(er + col + 8 * q);
-                            const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
-                            uint32_t lw[4] = {0, 0, 0, 0};
-                            if (lr != nullptr) {
-                                const uint4 l = *reinterpret_cast<const uint4 *>(lr + col + 8 * q);
-                                lw[0] = l.x, lw[1] = l.y, lw[2] = l.z, lw[3] = l.w;
-                            }
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t hw[4] = {eh[q].x, eh[q].y, eh[q].z, eh[q].w};
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float2 hf = half2_floats(hw[i]), lf = half2_floats(lw[i]);
-                                const int j = 8 * q + 2 * i;
-                                v[j] = fmaf(p.e_mul, fmaf(lf.x, 1.f / kLoScale, hf.x), v[j]);
-                                v[j + 1] = fmaf(p.e_mul, fmaf(lf.y, 1.f / kLoScale, hf.y), v[j + 1]);
+                        for (int i = 0; i < 4; ++i) {
+                            const int j = 8 * q + 2 * i;
+                            float2 e = half2_floats(hw[i]);
+                            if constexpr (MODE == kUpdate) {
+                                const uint32_t lw[4] = {el[q].x, el[q].y, el[q].z, el[q].w};
+                                const float2 l = half2_floats(lw[i]);
+                                e.x = fmaf(l.x, 1.f / kLoScale, e.x);
+                                e.y = fmaf(l.y, 1.f / kLoScale, e.y);
                             }
+                            v[j] = fmaf(p.e_mul, e.x, v[j]);
+                            v[j + 1] = fmaf(p.e_mul, e.y, v[j + 1]);
                         }
                     }
+                    fetch(c + 2);
                 }
                 if constexpr (MODE == kPoly) {
 #pragma unroll
@@ -479,9 +499,7 @@ __device__ __forceinline__ void ns_gemm_body(const CUtensorMap &tma_a, const CUt
 #pragma unroll
                     for (int j = 0; j < 16; ++j) packed[j] = pack_half2(v[2 * j], v[2 * j + 1]);
                 }
-                uint8_t *box = stg + (chunk & 1u) * (2 * NS_BOX), *box2 = box + NS_BOX;
-                ++chunk;
-                if (lane == 0) bulk_wait_group_read<1>();  // this box's previous copy has read it
+                if (lane == 0) bulk_wait_group_read<0>();  // the last copies have read the boxes
                 __syncwarp();
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
@@ -559,16 +577,16 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
     ns_gemm_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_constant__ CUtensorMap tma_b,
                    const __grid_constant__ CUtensorMap tma_d,
                    const __grid_constant__ CUtensorMap tma_lo, const NsArgs p) {
-    ns_gemm_body<1, A_MN, B_MN, MODE>(tma_a, tma_b, tma_d, tma_lo, p);
+    ns_gemm_body<1, 128, A_MN, B_MN, MODE>(tma_a, tma_b, tma_d, tma_lo, p);
 }
 
-template <bool A_MN, bool B_MN, int MODE>
+template <int BN, bool A_MN, bool B_MN, int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
     ns_gemm_pair_kernel(const __grid_constant__ CUtensorMap tma_a,
                         const __grid_constant__ CUtensorMap tma_b,
                         const __grid_constant__ CUtensorMap tma_d,
                         const __grid_constant__ CUtensorMap tma_lo, const NsArgs p) {
-    ns_gemm_body<2, A_MN, B_MN, MODE>(tma_a, tma_b, tma_d, tma_lo, p);
+    ns_gemm_body<2, BN, A_MN, B_MN, MODE>(tma_a, tma_b, tma_d, tma_lo, p);
 }
 
 // A batch of row-major 2-byte matrices [rows, cols] in memory, `ld` elements
@@ -591,8 +609,8 @@ bool ns_tmap(CUtensorMap *m, const Mat &a, int64_t batch, int box_cols, int box_
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool ns_operand(CUtensorMap *m, const Mat &a, int64_t batch, bool mn) {
-    return ns_tmap(m, a, batch, 64, mn ? 64 : 128, CU_TENSOR_MAP_SWIZZLE_128B,
+bool ns_operand(CUtensorMap *m, const Mat &a, int64_t batch, bool mn, int box_rows) {
+    return ns_tmap(m, a, batch, 64, mn ? 64 : box_rows, CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
@@ -600,24 +618,24 @@ bool ns_output(CUtensorMap *m, const Mat &a, int64_t batch) {
     return ns_tmap(m, a, batch, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
-int64_t ns_tiles(const NsArgs &p, int bt, bool sym) {
-    const int64_t mt = (p.M + bt - 1) / bt, nt = (p.N + bt - 1) / bt;
+int64_t ns_tiles(const NsArgs &p, int bm, int bn, bool sym) {
+    const int64_t mt = (p.M + bm - 1) / bm, nt = (p.N + bn - 1) / bn;
     return sym ? mt * (mt + 1) / 2 : mt * nt;
 }
 
-template <typename K>
-cudaError_t ns_launch_kernel(K kernel, std::atomic<bool> (&done)[64], int grid, cudaStream_t s,
-                             const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &d,
-                             const CUtensorMap &lo, const NsArgs &p) {
+template <auto KERNEL>
+cudaError_t ns_launch_kernel(int grid, cudaStream_t s, const CUtensorMap &a, const CUtensorMap &b,
+                             const CUtensorMap &d, const CUtensorMap &lo, const NsArgs &p) {
+    static std::atomic<bool> done[64];
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !done[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)NS_SMEM);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) done[dev] = true;
     }
-    return launch_pdl(kernel, grid, NS_THREADS, NS_SMEM, s, a, b, d, lo, p);
+    return launch_pdl(KERNEL, grid, NS_THREADS, NS_SMEM, s, a, b, d, lo, p);
 }
 
 // One product of the whole batch: d [M, N] from a and b (see ns_gemm_body).
@@ -625,40 +643,47 @@ template <bool A_MN, bool B_MN, int MODE>
 cudaError_t ns_gemm(NsArgs p, int64_t batch, const Mat &a, const Mat &b, const Mat &d, const Mat &lo,
                     cudaStream_t s, const char **why) {
     constexpr bool SYM = MODE != kUpdate;
-    // Tiles of 256 by a CTA pair or of 128 by one CTA, whichever needs less
-    // tensor time: waves times the time of a tile (a pair takes twice as long
-    // over four times the work).
-    const int64_t sms = num_sms();
-    const int64_t t2 = ns_tiles(p, 256, SYM) * batch, t1 = ns_tiles(p, 128, SYM) * batch;
-    const int64_t pairs = sms / 2 > 0 ? sms / 2 : 1;
-    const bool pair = 2 * ((t2 + pairs - 1) / pairs) <= (t1 + sms - 1) / sms;
-    const int bt = pair ? 256 : 128;
-    p.m_tiles = (p.M + bt - 1) / bt;
-    p.n_tiles = (p.N + bt - 1) / bt;
-    p.tiles_per = (int)ns_tiles(p, bt, SYM);
-    p.tiles = (int)(pair ? t2 : t1);
+    // Tiles of 256 x bn by a CTA pair or of 128 x 128 by one CTA (bn = 0):
+    // the least waves times a tile's time, which goes by the rows that each
+    // CTA loads for 64 of K, 128 + bn/2 of a pair's tile (375 ns measured at
+    // 256) and, with less to do between two loads, 205 to 256 of the single
+    // CTA's (297 ns).
+    const int64_t sms = num_sms(), pairs = sms / 2 > 0 ? sms / 2 : 1;
+    int bn = 0;
+    int64_t best = ((ns_tiles(p, 128, 128, SYM) * batch + sms - 1) / sms) * 205;
+    for (int c : {256, 224, 192}) {
+        if (SYM && c != 256) break;
+        const int64_t cost = ((ns_tiles(p, 256, c, SYM) * batch + pairs - 1) / pairs) * (128 + c / 2);
+        if (cost < best) best = cost, bn = c;
+    }
+    const int bm = bn ? 256 : 128, bw = bn ? bn : 128;
+    p.m_tiles = (p.M + bm - 1) / bm;
+    p.n_tiles = (p.N + bw - 1) / bw;
+    p.tiles_per = (int)ns_tiles(p, bm, bw, SYM);
+    p.tiles = (int)(p.tiles_per * batch);
     p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
     p.status = device_status_word();
     CUtensorMap ta, tb, td, tl;
-    if (!ns_operand(&ta, a, batch, A_MN) || !ns_operand(&tb, b, batch, B_MN) ||
+    if (!ns_operand(&ta, a, batch, A_MN, 128) || !ns_operand(&tb, b, batch, B_MN, bn ? bn / 2 : 128) ||
         !ns_output(&td, d, batch) || !ns_output(&tl, lo, batch)) {
         *why = "cuTensorMapEncodeTiled failed";
         return cudaErrorInvalidValue;
     }
-    if (pair) {
-        static std::atomic<bool> done[64];
-        return ns_launch_kernel(ns_gemm_pair_kernel<A_MN, B_MN, MODE>, done,
-                                2 * (int)std::min(t2, pairs), s, ta, tb, td, tl, p);
+    const int grid = (int)(bn ? 2 * std::min<int64_t>(p.tiles, pairs) : std::min<int64_t>(p.tiles, sms));
+    if (bn == 0) return ns_launch_kernel<ns_gemm_kernel<A_MN, B_MN, MODE>>(grid, s, ta, tb, td, tl, p);
+    if constexpr (!SYM) {
+        if (bn == 224)
+            return ns_launch_kernel<ns_gemm_pair_kernel<224, A_MN, B_MN, MODE>>(grid, s, ta, tb, td, tl, p);
+        if (bn == 192)
+            return ns_launch_kernel<ns_gemm_pair_kernel<192, A_MN, B_MN, MODE>>(grid, s, ta, tb, td, tl, p);
     }
-    static std::atomic<bool> done[64];
-    return ns_launch_kernel(ns_gemm_kernel<A_MN, B_MN, MODE>, done, (int)std::min(t1, sms), s, ta,
-                            tb, td, tl, p);
+    return ns_launch_kernel<ns_gemm_pair_kernel<256, A_MN, B_MN, MODE>>(grid, s, ta, tb, td, tl, p);
 }
 
 int64_t pad8(int64_t v) { return (v + 7) / 8 * 8; }
 int64_t pad256(int64_t v) { return (v + 255) / 256 * 256; }
 
-constexpr int kPrepParts = 256;  // blocks a matrix's sum of squares is split over, at most
+constexpr int kPrepParts = 1024;  // blocks a matrix's sum of squares is split over, at most
 
 struct NsLayout {
     int64_t ldx, lds, hi0, hi1, lo0, lo1, a, b, sums, bytes;
