@@ -10,13 +10,18 @@
 //   dw = sum_r dy xhat,  db = sum_r dy.
 //
 // Both directions move every element once, so HBM bounds them: 4 (bf16), 3
-// (bf16 -> E4M3) and 6 (bf16 backward) bytes an element.  A row is held in
-// the registers of TPR threads, EPT elements each, so it is read once for the
-// mean, the squares about the mean (a second sum over registers: no
-// cancellation) and the output.  The threads walk over rows with the same
-// columns each time: w and b stay in registers, the backward's column sums
-// too, and the next row's loads are issued before this row's sums are formed.
-// All sums are fp32.
+// (bf16 -> E4M3) and 6 (bf16 backward) bytes an element.  A row is shared by a
+// team of TPR threads, EPT elements each, always the same columns: w and b
+// stay in registers, and the backward's column sums too.  The mean, the squares about
+// the mean (a second sum over registers: no cancellation) and the output need
+// one read of the row.  Many rows (norm_*_ring_kernel) come through a ring of
+// bulk copies in shared memory, several rows ahead of the sums, so the loads
+// in flight do not depend on registers; few rows, and rows that 16-byte copies
+// cannot take, are loaded straight into registers one row ahead.  All sums are
+// fp32; the mean's, whose terms cancel, also carries its rounding errors.
+#include <algorithm>
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "occupancy.h"
@@ -24,11 +29,13 @@
 
 namespace fp8 {
 
+extern std::atomic<uint64_t> g_wait_limit_ns;
+
 namespace {
 
-// Elements of a row held by one thread in the register kernels.
-constexpr int EPT = 16;
-constexpr int kWideThreads = 1024;  // of the kernels for rows too wide for registers
+constexpr int kWideThreads = 1024;  // of the kernels for rows too wide for a team
+constexpr int kMaxStages = 8;
+constexpr size_t kRingBytes = 208 * 1024;  // of an SM's shared memory, for its blocks' rings
 
 struct NormArgs {
     const void *x;
@@ -43,6 +50,9 @@ struct NormArgs {
     const float *scale_inv;  // with yq
     float *amax;             // nullable, zero on entry
     float *mean, *rstd;      // nullable
+    int stages;              // of the ring
+    uint64_t wait_limit_ns;
+    unsigned int *status;
 };
 
 struct NormBwdArgs {
@@ -54,129 +64,330 @@ struct NormBwdArgs {
     int cols;
     const float *mean, *rstd;
     void *dx;        // nullable
-    float *partial;  // [2][ctas][cols]: dw then db of each CTA's rows; nullable
+    float *partial;  // [2][blocks][cols]: dw then db of each block's rows; nullable
+    int stages;
+    uint64_t wait_limit_ns;
+    unsigned int *status;
 };
 
-constexpr int block_threads(int tpr) { return tpr < 128 ? 128 : tpr; }
+// A block is one team, or eight teams of a warp.
+constexpr int block_threads(int tpr) { return tpr == 32 ? 256 : tpr; }
+constexpr int teams(int tpr) { return block_threads(tpr) / tpr; }
+// Blocks an SM should hold, by the registers that a thread needs; the
+// backward's also by the partial sums that each block leaves.
+constexpr int fwd_blocks(int tpr, int ept) {
+    return tpr > 512 ? 1 : (ept > 16 ? 512 : 768) / block_threads(tpr);
+}
+constexpr int bwd_blocks(int tpr) { return tpr > 256 ? 1 : tpr == 128 ? 3 : 2; }
 
-__device__ __forceinline__ void amax_commit(uint32_t m, float *amax) {
-    m = __reduce_max_sync(0xFFFFFFFFu, m);
+__device__ __forceinline__ void amax_commit(float v, float *amax) {
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v));
     if ((threadIdx.x & 31) == 0 && m != 0)
         atomicMax(reinterpret_cast<unsigned int *>(amax), m);
 }
 
-// TPR threads to a row; a block holds block_threads(TPR) / TPR rows at a time.
-template <typename T, bool VECTOR, int TPR>
-__global__ void __launch_bounds__(block_threads(TPR), TPR > 512 ? 1 : 512 / block_threads(TPR))
+// 16-byte-multiple copy global -> shared, counted on `bar`.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes,
+                                          uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+            "r"(smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// A team's ring: `stages` slots of `slot` bytes with a barrier each.  The
+// dynamic shared memory holds all teams' slots, then their barriers, then the
+// block's give-up flag (a wait that runs out is recorded, and the block
+// carries on with what it has: its outputs are invalid).
+struct Ring {
+    uint8_t *data;
+    uint64_t *bars;
+    volatile int *abort;
+    int stages;
+    uint32_t slot;
+
+    template <int TEAMS>
+    __device__ __forceinline__ void init(uint8_t *smem, int n, uint32_t slot_bytes, int team,
+                                         bool leader) {
+        stages = n;
+        slot = slot_bytes;
+        data = smem + (size_t)team * n * slot_bytes;
+        uint64_t *all = reinterpret_cast<uint64_t *>(smem + (size_t)TEAMS * n * slot_bytes);
+        bars = all + team * n;
+        abort = reinterpret_cast<volatile int *>(all + TEAMS * n);
+        if (leader) {
+            for (int i = 0; i < n; ++i) mbar_init(&bars[i], 1);
+            if (team == 0) *abort = 0;
+            fence_mbarrier_init();
+        }
+        __syncthreads();
+    }
+};
+
+size_t ring_bytes(int team_count, int stages, size_t slot) {
+    return (size_t)team_count * stages * (slot + sizeof(uint64_t)) + 16;
+}
+
+// ---------------------------------------------------------------- forward ---
+
+// What a team member does with its elements of one row, two at a time (the
+// instructions, not the bytes, would bound these kernels otherwise: one at a
+// time 16384 x 4096 to E4M3 took 61 us, its loads and stores need 30).
+// FULL: the row has exactly TPR * EPT columns, so no group is past its end
+// (the tests and branches for that are a fifth of the instructions).
+template <typename T, bool VECTOR, int TPR, int EPT, bool FULL>
+struct NormRow {
+    using RV = RowVec<T, VECTOR>;
+    static constexpr int V = RV::V, NV = EPT / V, P = EPT / 2;
+    uint64_t w[P], b[P];
+    float inv_c, si, amax;
+    int t;
+
+    static __device__ __forceinline__ int column(int e) {
+        return ((e / V) * TPR + threadIdx.x % TPR) * V + e % V;
+    }
+
+    static __device__ __forceinline__ bool inside(int cols, int e) {
+        return FULL || column(e) < cols;
+    }
+
+    __device__ __forceinline__ void init(const NormArgs &a) {
+        t = threadIdx.x % TPR;
+        inv_c = 1.f / (float)a.cols;
+        si = a.yq != nullptr ? *a.scale_inv : 0.f;
+        amax = 0.f;
+        auto param = [&](const void *p, float none, uint64_t (&to)[P]) {
+            float f[EPT];
+#pragma unroll
+            for (int e = 0; e < EPT; ++e) f[e] = none;
+            if (p != nullptr) {
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+                    if (inside(a.cols, j * V))
+                        load_params<V>(p, a.param_f32, column(j * V),
+                                       reinterpret_cast<float(&)[V]>(f[j * V]));
+            }
+#pragma unroll
+            for (int i = 0; i < P; ++i) to[i] = pair_of(f[2 * i], f[2 * i + 1]);
+        };
+        param(a.w, 1.f, w);
+        param(a.b, 0.f, b);
+    }
+
+    // mean of f (columns past the row's end hold zero), leaving f - mean
+    __device__ __forceinline__ float centre(const NormArgs &a, uint64_t (&f)[P], float *red) const {
+        float s, e = 0.f;
+        if constexpr (sizeof(T) == 2) {
+            // 8-bit significands: short sums of them rarely round in fp32
+            uint64_t p[P];
+#pragma unroll
+            for (int i = 0; i < P; ++i) p[i] = f[i];
+#pragma unroll
+            for (int h = P / 2; h > 0; h /= 2)
+#pragma unroll
+                for (int i = 0; i < h; ++i) p[i] = pair_add(p[i], p[i + h]);
+            const float2 v = pair_split(p[0]);
+            s = v.x + v.y;
+        } else {
+            s = 0.f;
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const float2 v = pair_split(f[i]);
+                add_exact(s, e, v.x);
+                add_exact(s, e, v.y);
+            }
+        }
+        const float mean = row_sum_split<TPR>(s, e, red) * inv_c;
+        const uint64_t minus = pair_of(-mean, -mean);
+#pragma unroll
+        for (int i = 0; i < P; ++i) f[i] = pair_add(f[i], minus);
+        return mean;
+    }
+
+    __device__ __forceinline__ float spread(const NormArgs &a, const uint64_t (&f)[P],
+                                            float *red) const {
+        uint64_t q = 0;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            uint64_t d = f[i];
+            if constexpr (V == 1) {
+                float2 v = pair_split(d);
+                if (!inside(a.cols, 2 * i)) v.x = 0.f;
+                if (!inside(a.cols, 2 * i + 1)) v.y = 0.f;
+                d = pair_of(v.x, v.y);
+            } else if (!inside(a.cols, 2 * i)) {
+                continue;
+            }
+            q = pair_fma(d, d, q);
+        }
+        const float2 v = pair_split(q);
+        float s[1] = {v.x + v.y};
+        row_sum<TPR, 1>(s, red);
+        return 1.f / sqrtf(fmaf(s[0], inv_c, a.eps));
+    }
+
+    __device__ __forceinline__ void store(const NormArgs &a, int64_t row, const uint64_t (&f)[P],
+                                          float mean, float rstd) {
+        if (t == 0) {
+            if (a.mean != nullptr) a.mean[row] = mean;
+            if (a.rstd != nullptr) a.rstd[row] = rstd;
+        }
+        const uint64_t r2 = pair_of(rstd, rstd), s2 = pair_of(si, si);
+        float o[EPT];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const float2 v = pair_split(pair_fma(pair_mul(f[i], r2), w[i], b[i]));
+            o[2 * i] = v.x, o[2 * i + 1] = v.y;
+        }
+        auto each = [&](auto act) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (inside(a.cols, j * V))
+                    act(row * a.cols + column(j * V), reinterpret_cast<float(&)[V]>(o[j * V]));
+        };
+        if (a.y != nullptr)
+            each([&](int64_t at, float(&u)[V]) { RV::store(reinterpret_cast<T *>(a.y) + at, u); });
+        if (a.amax != nullptr)
+            each([&](int64_t, float(&u)[V]) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) amax = max_abs_nan(amax, u[i]);
+            });
+        if (a.yq != nullptr)
+            each([&](int64_t at, float(&u)[V]) {
+                if constexpr (V == 1) {
+                    u[0] = __fmul_rn(u[0], si);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V; i += 2) {
+                        const float2 v = pair_split(pair_mul(pair_of(u[i], u[i + 1]), s2));
+                        u[i] = v.x, u[i + 1] = v.y;
+                    }
+                }
+                RV::store_e4m3(a.yq + at, u);
+            });
+    }
+
+    // f = the row's elements, from load(j) of each group
+    template <typename L>
+    static __device__ __forceinline__ void unpack(L load, uint64_t (&f)[P]) {
+        float u[EPT];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) RV::unpack(load(j), reinterpret_cast<float(&)[V]>(u[j * V]));
+#pragma unroll
+        for (int i = 0; i < P; ++i) f[i] = pair_of(u[2 * i], u[2 * i + 1]);
+    }
+};
+
+// Every thread of a block makes the same number of turns in the loops below
+// (the sums may be block-wide); a row past the end is computed from zeros and
+// not stored.
+
+template <typename T, bool VECTOR, int TPR, int EPT>
+__global__ void __launch_bounds__(block_threads(TPR), fwd_blocks(TPR, EPT))
     norm_fwd_kernel(const NormArgs a) {
     using RV = RowVec<T, VECTOR>;
-    constexpr int V = RV::V, NV = EPT / V, RPB = block_threads(TPR) / TPR;
-    __shared__ float red[2][TPR > 32 ? TPR / 32 : 1];
-    const int t = threadIdx.x % TPR;
-    const int C = a.cols;
-    const float inv_c = 1.f / (float)C;
+    using Row = NormRow<T, VECTOR, TPR, EPT, false>;
+    __shared__ float red[2][2 * (TPR > 32 ? TPR / 32 : 1)];
     pdl_wait_prior();
     pdl_allow_next();
-
     const T *x = reinterpret_cast<const T *>(a.x);
-    const int64_t step = (int64_t)gridDim.x * RPB;
-    int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
-    typename RV::Raw nxt[NV];
+    const int64_t step = (int64_t)gridDim.x * teams(TPR);
+    int64_t row = (int64_t)blockIdx.x * teams(TPR) + threadIdx.x / TPR;
+    typename RV::Raw nxt[Row::NV];
     auto fetch = [&](int64_t r) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = (j * TPR + t) * V;
-            nxt[j] = r < a.rows && c < C ? RV::load(x + r * a.ldx + c) : RV::zero();
+        for (int j = 0; j < Row::NV; ++j) {
+            const int c = Row::column(j * Row::V);
+            nxt[j] = r < a.rows && c < a.cols ? RV::load(x + r * a.ldx + c) : RV::zero();
         }
     };
     fetch(row);
-    float w[EPT], b[EPT];
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = (j * TPR + t) * V + i;
-            w[j * V + i] = a.w != nullptr && c < C ? load_param(a.w, a.param_f32, c) : 1.f;
-            b[j * V + i] = a.b != nullptr && c < C ? load_param(a.b, a.param_f32, c) : 0.f;
-        }
-    const float si = a.yq != nullptr ? *a.scale_inv : 0.f;
-    uint32_t m = 0;
-
-    // every thread of a block makes the same number of turns (the sums below
-    // are block-wide); a row past the end is computed from zeros, not stored
-    for (int64_t first = (int64_t)blockIdx.x * RPB; first < a.rows; first += step, row += step) {
-        float f[EPT];
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            float u[V];
-            RV::unpack(nxt[j], u);
-#pragma unroll
-            for (int i = 0; i < V; ++i) f[j * V + i] = u[i];
-        }
+    Row n;
+    n.init(a);
+    for (int64_t first = (int64_t)blockIdx.x * teams(TPR); first < a.rows;
+         first += step, row += step) {
+        uint64_t f[Row::P];
+        Row::unpack([&](int j) { return nxt[j]; }, f);
         fetch(row + step);
-        float s[1] = {0.f};
-#pragma unroll
-        for (int e = 0; e < EPT; ++e) s[0] += f[e];  // columns past C hold zero
-        row_sum<TPR, 1>(s, red[0]);
-        const float mean = s[0] * inv_c;
-        float q[1] = {0.f};
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float d = f[j * V + i] - mean;
-                f[j * V + i] = d;
-                if ((j * TPR + t) * V < C) q[0] = fmaf(d, d, q[0]);
-            }
-        row_sum<TPR, 1>(q, red[1]);
-        const float rstd = 1.f / sqrtf(fmaf(q[0], inv_c, a.eps));
-        if (row < a.rows) {
-            if (t == 0) {
-                if (a.mean != nullptr) a.mean[row] = mean;
-                if (a.rstd != nullptr) a.rstd[row] = rstd;
-            }
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = (j * TPR + t) * V;
-                if (c < C) {
-                    float o[V];
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        o[i] = fmaf(f[j * V + i] * rstd, w[j * V + i], b[j * V + i]);
-                    if (a.y != nullptr) RV::store(reinterpret_cast<T *>(a.y) + row * C + c, o);
-                    if (a.amax != nullptr) {
-#pragma unroll
-                        for (int i = 0; i < V; ++i) m = max(m, abs_bits(o[i]));
-                    }
-                    if (a.yq != nullptr) {
-#pragma unroll
-                        for (int i = 0; i < V; ++i) o[i] = __fmul_rn(o[i], si);
-                        RV::store_e4m3(a.yq + row * C + c, o);
-                    }
-                }
-            }
-        }
+        const float mean = n.centre(a, f, red[0]);
+        const float rstd = n.spread(a, f, red[1]);
+        if (row < a.rows) n.store(a, row, f, mean, rstd);
     }
-    if (a.amax != nullptr) amax_commit(m, a.amax);
+    if (a.amax != nullptr) amax_commit(n.amax, a.amax);
 }
 
-// Rows too wide for registers: one block to a row, three passes over it (the
+template <typename T, int TPR, int EPT, bool FULL>
+__global__ void __launch_bounds__(block_threads(TPR), fwd_blocks(TPR, EPT))
+    norm_fwd_ring_kernel(const NormArgs a) {
+    using RV = RowVec<T, true>;
+    using Row = NormRow<T, true, TPR, EPT, FULL>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float red[2][2 * (TPR > 32 ? TPR / 32 : 1)];
+    const int t = threadIdx.x % TPR, team = threadIdx.x / TPR;
+    const uint32_t bytes = (uint32_t)a.cols * sizeof(T);
+    Ring ring = {};
+    ring.init<teams(TPR)>(smem, a.stages, bytes, team, t == 0);
+    pdl_wait_prior();
+    pdl_allow_next();
+    const T *x = reinterpret_cast<const T *>(a.x);
+    const int64_t step = (int64_t)gridDim.x * teams(TPR);
+    int64_t row = (int64_t)blockIdx.x * teams(TPR) + team;
+    auto request = [&](int64_t r, int slot) {
+        if (r < a.rows) {
+            mbar_arrive_expect_tx(&ring.bars[slot], bytes);
+            bulk_load(ring.data + slot * bytes, x + r * a.ldx, bytes, &ring.bars[slot]);
+        }
+    };
+    if (t == 0)
+        for (int i = 0; i < a.stages; ++i) request(row + i * step, i);
+    Row n;
+    n.init(a);
+    int slot = 0;
+    uint32_t phase = 0;
+    for (int64_t first = (int64_t)blockIdx.x * teams(TPR); first < a.rows;
+         first += step, row += step) {
+        const bool in = row < a.rows;
+        if (in)
+            mbar_wait_bounded(&ring.bars[slot], phase, ring.abort, a.wait_limit_ns,
+                              kStatusTimeoutTma, a.status);
+        const T *src = reinterpret_cast<const T *>(ring.data + slot * bytes);
+        uint64_t f[Row::P];
+        Row::unpack(
+            [&](int j) {
+                return in && Row::inside(a.cols, j * Row::V) ? RV::load(src + Row::column(j * Row::V))
+                                                             : RV::zero();
+            },
+            f);
+        const float mean = n.centre(a, f, red[0]);
+        // the sum needed every member's elements, so the slot has been read
+        if (t == 0) request(row + a.stages * step, slot);
+        const float rstd = n.spread(a, f, red[1]);
+        if (in) n.store(a, row, f, mean, rstd);
+        if (++slot == a.stages) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+    if (a.amax != nullptr) amax_commit(n.amax, a.amax);
+}
+
+// Rows too wide for a team: one block to a row, three passes over it (the
 // second and third find it in L2).
 template <typename T>
 __global__ void __launch_bounds__(kWideThreads) norm_fwd_wide_kernel(const NormArgs a) {
-    __shared__ float red[2][kWideThreads / 32];
+    __shared__ float red[2][2 * kWideThreads / 32];
     pdl_wait_prior();
     pdl_allow_next();
     const int C = a.cols;
     const float inv_c = 1.f / (float)C;
     const float si = a.yq != nullptr ? *a.scale_inv : 0.f;
-    uint32_t m = 0;
+    float m = 0.f;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const T *x = reinterpret_cast<const T *>(a.x) + row * a.ldx;
-        float s[1] = {0.f};
-        for (int c = threadIdx.x; c < C; c += kWideThreads) s[0] += elem_to_float(x[c]);
-        row_sum<kWideThreads, 1>(s, red[0]);
-        const float mean = s[0] * inv_c;
+        float s = 0.f, e = 0.f;
+        for (int c = threadIdx.x; c < C; c += kWideThreads) add_exact(s, e, elem_to_float(x[c]));
+        const float mean = row_sum_split<kWideThreads>(s, e, red[0]) * inv_c;
         float q[1] = {0.f};
         for (int c = threadIdx.x; c < C; c += kWideThreads) {
             const float d = elem_to_float(x[c]) - mean;
@@ -193,7 +404,7 @@ __global__ void __launch_bounds__(kWideThreads) norm_fwd_wide_kernel(const NormA
             const float b = a.b != nullptr ? load_param(a.b, a.param_f32, c) : 0.f;
             float o[1] = {fmaf((elem_to_float(x[c]) - mean) * rstd, w, b)};
             if (a.y != nullptr) float_to_elem(reinterpret_cast<T *>(a.y) + row * C + c, o[0]);
-            m = max(m, abs_bits(o[0]));
+            m = max_abs_nan(m, o[0]);
             if (a.yq != nullptr) {
                 o[0] = __fmul_rn(o[0], si);
                 RowVec<T, false>::store_e4m3(a.yq + row * C + c, o);
@@ -203,130 +414,300 @@ __global__ void __launch_bounds__(kWideThreads) norm_fwd_wide_kernel(const NormA
     if (a.amax != nullptr) amax_commit(m, a.amax);
 }
 
-// The same walk for the gradient; a block's column sums stay in registers and
-// leave once, at its end.  With several rows in a block (TPR = 32) its warps'
-// sums meet in shared memory first.
-template <typename T, bool VECTOR, int TPR>
-__global__ void __launch_bounds__(block_threads(TPR), TPR > 256 ? 1 : 512 / block_threads(TPR))
-    norm_bwd_kernel(const NormBwdArgs a) {
+// --------------------------------------------------------------- backward ---
+
+// A team member's part of the gradient: its columns' sums so far.
+template <typename T, bool VECTOR, int TPR, int EPT, bool FULL>
+struct NormBwdRow {
     using RV = RowVec<T, VECTOR>;
-    constexpr int V = RV::V, NV = EPT / V, RPB = block_threads(TPR) / TPR;
+    using Raw = typename RV::Raw;
+    static constexpr int V = RV::V, NV = EPT / V, P = EPT / 2;
+    // pairs of elements come from one group, or from two single elements
+    static constexpr int STEP = V > 1 ? 1 : 2, PAIRS = V > 1 ? V / 2 : 1;
+    // 32 columns' sums leave no registers for their weights: L1 holds them
+    static constexpr bool W_IN_REGISTERS = EPT <= 16;
+    uint64_t w[W_IN_REGISTERS ? P : 1], dw[P], db[P];
+    float inv_c;
+
+    static __device__ __forceinline__ int column(int e) {
+        return ((e / V) * TPR + threadIdx.x % TPR) * V + e % V;
+    }
+
+    static __device__ __forceinline__ bool inside(int cols, int e) {
+        return FULL || column(e) < cols;
+    }
+
+    // the weights of the elements of groups j to j + STEP - 1
+    __device__ __forceinline__ void weights(const NormBwdArgs &a, int j, uint64_t (&p)[PAIRS]) const {
+        if constexpr (W_IN_REGISTERS) {
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i) p[i] = w[j * V / 2 + i];
+        } else {
+            load_weights(a, j, p);
+        }
+    }
+
+    static __device__ __forceinline__ void load_weights(const NormBwdArgs &a, int j,
+                                                        uint64_t (&p)[PAIRS]) {
+        float f[V * STEP];
+#pragma unroll
+        for (int e = 0; e < V * STEP; ++e) f[e] = 1.f;
+        if (a.w != nullptr) {
+            if constexpr (VECTOR) {
+                if (inside(a.cols, j * V)) load_params<V>(a.w, a.param_f32, column(j * V), f);
+            } else {
+#pragma unroll
+                for (int e = 0; e < STEP; ++e)
+                    if (inside(a.cols, j + e)) f[e] = load_param(a.w, a.param_f32, column(j + e));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) p[i] = pair_of(f[2 * i], f[2 * i + 1]);
+    }
+
+    __device__ __forceinline__ void init(const NormBwdArgs &a) {
+        inv_c = 1.f / (float)a.cols;
+#pragma unroll
+        for (int i = 0; i < P; ++i) dw[i] = db[i] = 0;
+        if constexpr (W_IN_REGISTERS) {
+#pragma unroll
+            for (int j = 0; j < NV; j += STEP)
+                load_weights(a, j, reinterpret_cast<uint64_t(&)[PAIRS]>(w[j * V / 2]));
+        }
+    }
+
+    // the elements of groups j to j + STEP - 1, which load() gives
+    template <typename L>
+    static __device__ __forceinline__ void unpack(L load, int j, uint64_t (&p)[PAIRS]) {
+        float f[V * STEP];
+        RV::unpack(load(j), reinterpret_cast<float(&)[V]>(f[0]));
+        if constexpr (STEP == 2) RV::unpack(load(j + 1), reinterpret_cast<float(&)[V]>(f[1]));
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) p[i] = pair_of(f[2 * i], f[2 * i + 1]);
+    }
+
+    // the row's sums of w dy and w dy xhat, and its share of the columns' (a
+    // row or column past the end holds dy = 0)
+    template <typename LX, typename LG>
+    __device__ __forceinline__ void sums(const NormBwdArgs &a, LX load_x, LG load_dy, float mean,
+                                         float rstd, float (&s)[2]) {
+        const uint64_t minus = pair_of(-mean, -mean), r2 = pair_of(rstd, rstd);
+        uint64_t s0 = 0, s1 = 0;
+#pragma unroll
+        for (int j = 0; j < NV; j += STEP) {
+            uint64_t x[PAIRS], g[PAIRS], wt[PAIRS];
+            unpack(load_x, j, x);
+            unpack(load_dy, j, g);
+            weights(a, j, wt);
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i) {
+                const int e = j * V / 2 + i;
+                const uint64_t h = pair_mul(pair_add(x[i], minus), r2);
+                const uint64_t wg = pair_mul(wt[i], g[i]);
+                s0 = pair_add(s0, wg);
+                s1 = pair_fma(wg, h, s1);
+                dw[e] = pair_fma(g[i], h, dw[e]);
+                db[e] = pair_add(db[e], g[i]);
+            }
+        }
+        const float2 u = pair_split(s0), v = pair_split(s1);
+        s[0] = u.x + u.y;
+        s[1] = v.x + v.y;
+    }
+
+    template <typename LX, typename LG>
+    __device__ __forceinline__ void store(const NormBwdArgs &a, int64_t row, LX load_x, LG load_dy,
+                                          float mean, float rstd, const float (&s)[2]) const {
+        const float m1 = -(s[0] * inv_c), m2 = -(s[1] * inv_c);
+        const uint64_t minus = pair_of(-mean, -mean), r2 = pair_of(rstd, rstd);
+        const uint64_t m12 = pair_of(m1, m1), m22 = pair_of(m2, m2);
+#pragma unroll
+        for (int j = 0; j < NV; j += STEP) {
+            uint64_t x[PAIRS], g[PAIRS], wt[PAIRS];
+            unpack(load_x, j, x);
+            unpack(load_dy, j, g);
+            weights(a, j, wt);
+            float o[V * STEP];
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i) {
+                const uint64_t h = pair_mul(pair_add(x[i], minus), r2);
+                const uint64_t d = pair_fma(h, m22, pair_fma(wt[i], g[i], m12));
+                const float2 v = pair_split(pair_mul(r2, d));
+                o[2 * i] = v.x, o[2 * i + 1] = v.y;
+            }
+#pragma unroll
+            for (int k = 0; k < STEP; ++k) {
+                if (inside(a.cols, (j + k) * V))
+                    RV::store(reinterpret_cast<T *>(a.dx) + row * a.cols + column((j + k) * V),
+                              reinterpret_cast<float(&)[V]>(o[k * V]));
+            }
+        }
+    }
+
+    // group j of the sums; 16 bytes at a time (rows of groups of V > 1 have a
+    // multiple of 4 columns and start on 16 bytes, and so do their sums)
+    static __device__ __forceinline__ void put(float *to, const uint64_t (&sum)[P], int j) {
+        if constexpr (V == 1) {
+            const float2 v = pair_split(sum[j / 2]);
+            *to = j % 2 ? v.y : v.x;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+                const float2 u = pair_split(sum[(j * V + i) / 2]);
+                const float2 v = pair_split(sum[(j * V + i) / 2 + 1]);
+                *reinterpret_cast<float4 *>(to + i) = make_float4(u.x, u.y, v.x, v.y);
+            }
+        }
+    }
+
+    // the block's column sums; with several teams in a block theirs meet in
+    // `meet` [teams][TPR * EPT] first
+    __device__ __forceinline__ void commit(const NormBwdArgs &a, float *meet) const {
+        float *pw = a.partial + (int64_t)blockIdx.x * a.cols;
+        float *pb = pw + (int64_t)gridDim.x * a.cols;
+        if constexpr (teams(TPR) == 1) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                if (!inside(a.cols, j * V)) continue;
+                put(pw + column(j * V), dw, j);
+                put(pb + column(j * V), db, j);
+            }
+        } else {
+            constexpr int WIDTH = TPR * EPT;
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+                __syncthreads();
+#pragma unroll
+                for (int e = 0; e < EPT; ++e) {
+                    const float2 v = pair_split(which ? db[e / 2] : dw[e / 2]);
+                    meet[(threadIdx.x / TPR) * WIDTH + column(e)] = e % 2 ? v.y : v.x;
+                }
+                __syncthreads();
+                for (int c = threadIdx.x; c < a.cols; c += block_threads(TPR)) {
+                    float v = 0.f;
+#pragma unroll
+                    for (int r = 0; r < teams(TPR); ++r) v += meet[r * WIDTH + c];
+                    (which ? pb : pw)[c] = v;
+                }
+            }
+        }
+    }
+};
+
+template <typename T, bool VECTOR, int TPR, int EPT>
+__global__ void __launch_bounds__(block_threads(TPR), bwd_blocks(TPR))
+    norm_bwd_kernel(const NormBwdArgs a) {
+    using Row = NormBwdRow<T, VECTOR, TPR, EPT, false>;
+    using RV = typename Row::RV;
+    using Raw = typename Row::Raw;
     __shared__ float red[2][2 * (TPR > 32 ? TPR / 32 : 1)];
-    __shared__ float sums[RPB > 1 ? RPB : 1][RPB > 1 ? TPR * EPT : 1];
-    const int t = threadIdx.x % TPR;
-    const int C = a.cols;
-    const float inv_c = 1.f / (float)C;
+    __shared__ float meet[teams(TPR) > 1 ? teams(TPR) * TPR * EPT : 1];
     pdl_wait_prior();
     pdl_allow_next();
-
+    const int t = threadIdx.x % TPR;
     const T *x = reinterpret_cast<const T *>(a.x), *dy = reinterpret_cast<const T *>(a.dy);
-    const int64_t step = (int64_t)gridDim.x * RPB;
-    int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
-    typename RV::Raw nx[NV], ng[NV];
+    const int64_t step = (int64_t)gridDim.x * teams(TPR);
+    int64_t row = (int64_t)blockIdx.x * teams(TPR) + threadIdx.x / TPR;
+    Raw nx[Row::NV], ng[Row::NV];
     float nmean, nrstd;
     auto fetch = [&](int64_t r) {
         const bool in = r < a.rows;
         nmean = in ? a.mean[r] : 0.f;
         nrstd = in ? a.rstd[r] : 0.f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = (j * TPR + t) * V;
-            nx[j] = in && c < C ? RV::load(x + r * a.ldx + c) : RV::zero();
-            ng[j] = in && c < C ? RV::load(dy + r * a.lddy + c) : RV::zero();
+        for (int j = 0; j < Row::NV; ++j) {
+            const int c = (j * TPR + t) * Row::V;
+            nx[j] = in && c < a.cols ? RV::load(x + r * a.ldx + c) : RV::zero();
+            ng[j] = in && c < a.cols ? RV::load(dy + r * a.lddy + c) : RV::zero();
         }
     };
     fetch(row);
-    float w[EPT], dw[EPT], db[EPT];
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = (j * TPR + t) * V + i;
-            w[j * V + i] = a.w != nullptr && c < C ? load_param(a.w, a.param_f32, c) : 1.f;
-            dw[j * V + i] = db[j * V + i] = 0.f;
-        }
-
+    Row n;
+    n.init(a);
     int turn = 0;
-    for (int64_t first = (int64_t)blockIdx.x * RPB; first < a.rows;
+    for (int64_t first = (int64_t)blockIdx.x * teams(TPR); first < a.rows;
          first += step, row += step, ++turn) {
-        typename RV::Raw cx[NV], cg[NV];
+        Raw cx[Row::NV], cg[Row::NV];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) cx[j] = nx[j], cg[j] = ng[j];
+        for (int j = 0; j < Row::NV; ++j) cx[j] = nx[j], cg[j] = ng[j];
         const float mean = nmean, rstd = nrstd;
         fetch(row + step);
-        float s[2] = {0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const bool in = (j * TPR + t) * V < C;
-            float fx[V], fg[V];
-            RV::unpack(cx[j], fx);
-            RV::unpack(cg[j], fg);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int e = j * V + i;
-                // columns and rows past the end hold dy = 0 and add nothing,
-                // but their xhat is kept finite too
-                const float h = in ? (fx[i] - mean) * rstd : 0.f;
-                const float wg = w[e] * fg[i];
-                s[0] += wg;
-                s[1] = fmaf(wg, h, s[1]);
-                dw[e] = fmaf(fg[i], h, dw[e]);
-                db[e] += fg[i];
-            }
-        }
+        auto lx = [&](int j) { return cx[j]; };
+        auto lg = [&](int j) { return cg[j]; };
+        float s[2];
+        n.sums(a, lx, lg, mean, rstd, s);
         row_sum<TPR, 2>(s, red[turn & 1]);
-        if (a.dx != nullptr && row < a.rows) {
-            const float m1 = s[0] * inv_c, m2 = s[1] * inv_c;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = (j * TPR + t) * V;
-                if (c < C) {
-                    float fx[V], fg[V], o[V];
-                    RV::unpack(cx[j], fx);
-                    RV::unpack(cg[j], fg);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float h = (fx[i] - mean) * rstd;
-                        o[i] = rstd * (fmaf(w[j * V + i], fg[i], -m1) - h * m2);
-                    }
-                    RV::store(reinterpret_cast<T *>(a.dx) + row * C + c, o);
-                }
-            }
-        }
+        if (a.dx != nullptr && row < a.rows) n.store(a, row, lx, lg, mean, rstd, s);
     }
-    if (a.partial == nullptr) return;
-    float *pw = a.partial + (int64_t)blockIdx.x * C;
-    float *pb = pw + (int64_t)gridDim.x * C;
-    if constexpr (RPB == 1) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int c = (j * TPR + t) * V + i;
-                if (c < C) pw[c] = dw[j * V + i], pb[c] = db[j * V + i];
-            }
-    } else {
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    sums[threadIdx.x / TPR][(j * TPR + t) * V + i] =
-                        which ? db[j * V + i] : dw[j * V + i];
-            __syncthreads();
-            for (int c = threadIdx.x; c < C; c += block_threads(TPR)) {
-                float v = 0.f;
-#pragma unroll
-                for (int r = 0; r < RPB; ++r) v += sums[r][c];
-                (which ? pb : pw)[c] = v;
-            }
-        }
-    }
+    if (a.partial != nullptr) n.commit(a, meet);
 }
 
-// Rows too wide for registers: dx with one block to a row (two passes), the
+// A slot holds the row's x, then its dy; it is read twice, for the sums and
+// for dx, and asked to be filled again one turn later, when the next row's
+// sums show that every member is past it.
+template <typename T, int TPR, int EPT, bool FULL>
+__global__ void __launch_bounds__(block_threads(TPR), bwd_blocks(TPR))
+    norm_bwd_ring_kernel(const NormBwdArgs a) {
+    using Row = NormBwdRow<T, true, TPR, EPT, FULL>;
+    using RV = typename Row::RV;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float red[2][2 * (TPR > 32 ? TPR / 32 : 1)];
+    const int t = threadIdx.x % TPR, team = threadIdx.x / TPR;
+    const uint32_t bytes = (uint32_t)a.cols * sizeof(T);
+    Ring ring = {};
+    ring.init<teams(TPR)>(smem, a.stages, 2 * bytes, team, t == 0);
+    pdl_wait_prior();
+    pdl_allow_next();
+    const T *x = reinterpret_cast<const T *>(a.x), *dy = reinterpret_cast<const T *>(a.dy);
+    const int64_t step = (int64_t)gridDim.x * teams(TPR);
+    int64_t row = (int64_t)blockIdx.x * teams(TPR) + team;
+    auto request = [&](int64_t r, int slot) {
+        if (r < a.rows) {
+            uint8_t *to = ring.data + slot * ring.slot;
+            mbar_arrive_expect_tx(&ring.bars[slot], 2 * bytes);
+            bulk_load(to, x + r * a.ldx, bytes, &ring.bars[slot]);
+            bulk_load(to + bytes, dy + r * a.lddy, bytes, &ring.bars[slot]);
+        }
+    };
+    if (t == 0)
+        for (int i = 0; i < a.stages; ++i) request(row + i * step, i);
+    float nmean = row < a.rows ? a.mean[row] : 0.f, nrstd = row < a.rows ? a.rstd[row] : 0.f;
+    Row n;
+    n.init(a);
+    int slot = 0, before = a.stages - 1, turn = 0;
+    uint32_t phase = 0;
+    for (int64_t first = (int64_t)blockIdx.x * teams(TPR); first < a.rows;
+         first += step, row += step, ++turn) {
+        const bool in = row < a.rows;
+        const float mean = nmean, rstd = nrstd;
+        if (row + step < a.rows) nmean = a.mean[row + step], nrstd = a.rstd[row + step];
+        if (in)
+            mbar_wait_bounded(&ring.bars[slot], phase, ring.abort, a.wait_limit_ns,
+                              kStatusTimeoutTma, a.status);
+        const T *sx = reinterpret_cast<const T *>(ring.data + slot * ring.slot);
+        const T *sg = reinterpret_cast<const T *>(ring.data + slot * ring.slot + bytes);
+        auto load = [&](const T *p, int j) {
+            return in && Row::inside(a.cols, j * Row::V) ? RV::load(p + Row::column(j * Row::V))
+                                                         : RV::zero();
+        };
+        auto lx = [&](int j) { return load(sx, j); };
+        auto lg = [&](int j) { return load(sg, j); };
+        float s[2];
+        n.sums(a, lx, lg, in ? mean : 0.f, in ? rstd : 0.f, s);
+        row_sum<TPR, 2>(s, red[turn & 1]);
+        if (t == 0 && turn > 0) request(row + (a.stages - 1) * step, before);
+        if (a.dx != nullptr && in) n.store(a, row, lx, lg, mean, rstd, s);
+        before = slot;
+        if (++slot == a.stages) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+    // every copy has arrived and been read: the teams' sums meet in the ring
+    if (a.partial != nullptr) n.commit(a, reinterpret_cast<float *>(smem));
+}
+
+// Rows too wide for a team: dx with one block to a row (two passes), the
 // column sums by blocks of 256 columns x a share of the rows.
 template <typename T>
 __global__ void __launch_bounds__(kWideThreads) norm_bwd_wide_kernel(const NormBwdArgs a) {
@@ -377,11 +758,12 @@ __global__ void __launch_bounds__(256) norm_colsum_wide_kernel(const NormBwdArgs
 }
 
 // dw, db = the partial sums of `parts` blocks, added in a fixed order: warp w
-// of a block takes partials w, w + 8, ... of 32 columns, then the eight warps'
-// sums are added in order.
-__global__ void __launch_bounds__(256) norm_reduce_kernel(const float *partial, int parts, int cols,
-                                                          void *dw, void *db, int param_f32) {
-    __shared__ float acc[8][33];
+// of a block takes partials w, w + 32, ... of 32 columns, then the warps' sums
+// are added in order.
+__global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *partial, int parts,
+                                                           int cols, void *dw, void *db,
+                                                           int param_f32) {
+    __shared__ float acc[32][33];
     pdl_wait_prior();
     pdl_allow_next();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -390,26 +772,30 @@ __global__ void __launch_bounds__(256) norm_reduce_kernel(const float *partial, 
     if (out == nullptr) return;
     const float *p = partial + (int64_t)blockIdx.y * parts * cols;
     float v = 0.f;
-    if (c < cols)
-        for (int i = warp; i < parts; i += 8) v += p[(int64_t)i * cols + c];
+    if (c < cols) {
+#pragma unroll 8
+        for (int i = warp; i < parts; i += 32) v += p[(int64_t)i * cols + c];
+    }
     acc[warp][lane] = v;
     __syncthreads();
-    if (warp == 0 && c < cols) {
-        v = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v += acc[i][lane];
+    // transposed: warp w sums column w
+    v = warp_sum(acc[lane][warp]);
+    const int col = blockIdx.x * 32 + warp;
+    if (lane == 0 && col < cols) {
         if (param_f32)
-            reinterpret_cast<float *>(out)[c] = v;
+            reinterpret_cast<float *>(out)[col] = v;
         else
-            float_to_elem(reinterpret_cast<uint16_t *>(out) + c, v);
+            float_to_elem(reinterpret_cast<uint16_t *>(out) + col, v);
     }
 }
 
-// Threads to a row: the fewest that hold it (0: none do).  A row of up to 512
-// columns is one warp's, so its sums need no barrier.
-int threads_for(int64_t cols, int most) {
+// ------------------------------------------------------------------- host ---
+
+// Threads to a row: the fewest, up to `most`, that hold it with `ept` elements
+// each (0: none do).  A team of one warp needs no barrier for its sums.
+int threads_for(int64_t cols, int ept, int most) {
     for (int tpr : {32, 128, 256, 512, 1024})
-        if (tpr <= most && cols <= (int64_t)tpr * EPT) return tpr;
+        if (tpr <= most && cols <= (int64_t)tpr * ept) return tpr;
     return 0;
 }
 
@@ -425,23 +811,95 @@ cudaError_t walk_grid(int threads, int64_t units, int *grid) {
     return cudaSuccess;
 }
 
-template <typename T, bool VECTOR, int TPR>
-cudaError_t run_fwd(const NormArgs &a, cudaStream_t s) {
-    constexpr int RPB = block_threads(TPR) / TPR;
-    int grid = 0;
-    cudaError_t e = walk_grid<norm_fwd_kernel<T, VECTOR, TPR>>(block_threads(TPR), (a.rows + RPB - 1) / RPB, &grid);
+struct RingPlan {
+    int grid, stages;  // stages 0: no ring
+    size_t bytes;
+};
+
+// A ring pays once every team has more than one row, and needs room for two
+// slots; blocks that would leave fewer than three are traded for slots.  The
+// dynamic shared memory is at least `least` bytes.
+template <auto KERNEL>
+cudaError_t plan_ring(int threads, int team_count, int64_t rows, size_t slot, RingPlan *r,
+                      size_t least = 0) {
+    r->stages = 0;
+    int blocks = 0;
+    cudaError_t e = blocks_per_sm<KERNEL>(threads, &blocks);
     if (e != cudaSuccess) return e;
-    return launch_pdl(norm_fwd_kernel<T, VECTOR, TPR>, grid, block_threads(TPR), 0, s, a);
+    int64_t stages = 0;
+    for (;; --blocks) {
+        stages = ((int64_t)(kRingBytes / blocks) - 1024) / (int64_t)(team_count * (slot + 8));
+        if (stages >= 3 || blocks == 1) break;
+    }
+    const int64_t units = (rows + team_count - 1) / team_count;
+    const int64_t grid = (int64_t)num_sms() * blocks;
+    if (stages < 2 || units <= grid) return cudaSuccess;
+    r->grid = (int)grid;
+    r->stages = (int)std::min<int64_t>(stages, kMaxStages);
+    r->bytes = std::max(ring_bytes(team_count, r->stages, slot), least);
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64 || !done[dev]) {
+        e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)kRingBytes);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) done[dev] = true;
+    }
+    return cudaSuccess;
+}
+
+template <typename T, int TPR, int EPT, bool FULL = false>
+cudaError_t run_fwd_ring(NormArgs a, cudaStream_t s, bool *done) {
+    if constexpr (!FULL && TPR * EPT % 1024 == 0)
+        if (a.cols == TPR * EPT) return run_fwd_ring<T, TPR, EPT, true>(a, s, done);
+    constexpr auto ring = norm_fwd_ring_kernel<T, TPR, EPT, FULL>;
+    RingPlan r;
+    cudaError_t e =
+        plan_ring<ring>(block_threads(TPR), teams(TPR), a.rows, a.cols * sizeof(T), &r);
+    if (e != cudaSuccess || r.stages == 0) return e;
+    a.stages = r.stages;
+    *done = true;
+    return launch_pdl(ring, r.grid, block_threads(TPR), r.bytes, s, a);
+}
+
+// Many rows: 32 elements to a thread where the row fills them, so that the
+// sums over the team cost less an element (16384 x 4096 to E4M3: TODO).
+template <typename T>
+cudaError_t pick_fwd_ring(const NormArgs &a, cudaStream_t s, bool *done) {
+    if (a.cols <= 512) return run_fwd_ring<T, 32, 16>(a, s, done);
+    if (a.cols <= 1024) return run_fwd_ring<T, 32, 32>(a, s, done);
+    if (a.cols <= 2048) return run_fwd_ring<T, 128, 16>(a, s, done);
+    if (a.cols <= 4096) return run_fwd_ring<T, 128, 32>(a, s, done);
+    if (a.cols <= 8192) return run_fwd_ring<T, 256, 32>(a, s, done);
+    if (a.cols <= 16384) return run_fwd_ring<T, 512, 32>(a, s, done);
+    return cudaSuccess;
+}
+
+template <typename T, bool VECTOR, int TPR, int EPT>
+cudaError_t run_fwd(const NormArgs &a, cudaStream_t s) {
+    constexpr int THREADS = block_threads(TPR);
+    constexpr auto kernel = norm_fwd_kernel<T, VECTOR, TPR, EPT>;
+    int grid = 0;
+    cudaError_t e = walk_grid<kernel>(THREADS, (a.rows + teams(TPR) - 1) / teams(TPR), &grid);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, grid, THREADS, 0, s, a);
 }
 
 template <typename T, bool VECTOR>
 cudaError_t pick_fwd(const NormArgs &a, cudaStream_t s) {
-    switch (threads_for(a.cols, 1024)) {
-    case 32: return run_fwd<T, VECTOR, 32>(a, s);
-    case 128: return run_fwd<T, VECTOR, 128>(a, s);
-    case 256: return run_fwd<T, VECTOR, 256>(a, s);
-    case 512: return run_fwd<T, VECTOR, 512>(a, s);
-    case 1024: return run_fwd<T, VECTOR, 1024>(a, s);
+    constexpr int EPT = VECTOR ? 16 : 8;
+    if constexpr (VECTOR) {
+        bool done = false;
+        cudaError_t e = pick_fwd_ring<T>(a, s, &done);
+        if (e != cudaSuccess || done) return e;
+    }
+    switch (threads_for(a.cols, EPT, 1024)) {
+    case 32: return run_fwd<T, VECTOR, 32, EPT>(a, s);
+    case 128: return run_fwd<T, VECTOR, 128, EPT>(a, s);
+    case 256: return run_fwd<T, VECTOR, 256, EPT>(a, s);
+    case 512: return run_fwd<T, VECTOR, 512, EPT>(a, s);
+    case 1024: return run_fwd<T, VECTOR, 1024, EPT>(a, s);
     }
     int grid = 0;
     cudaError_t e = walk_grid<norm_fwd_wide_kernel<T>>(kWideThreads, a.rows, &grid);
@@ -449,25 +907,61 @@ cudaError_t pick_fwd(const NormArgs &a, cudaStream_t s) {
     return launch_pdl(norm_fwd_wide_kernel<T>, grid, kWideThreads, 0, s, a);
 }
 
-template <typename T, bool VECTOR, int TPR>
+template <typename T, int TPR, int EPT, bool FULL = false>
+cudaError_t run_bwd_ring(NormBwdArgs a, int *parts, cudaStream_t s, bool *done) {
+    if constexpr (!FULL && TPR * EPT % 1024 == 0)
+        if (a.cols == TPR * EPT) return run_bwd_ring<T, TPR, EPT, true>(a, parts, s, done);
+    constexpr auto ring = norm_bwd_ring_kernel<T, TPR, EPT, FULL>;
+    RingPlan r;
+    cudaError_t e =
+        plan_ring<ring>(block_threads(TPR), teams(TPR), a.rows, 2 * a.cols * sizeof(T), &r,
+                        teams(TPR) > 1 ? teams(TPR) * TPR * EPT * sizeof(float) : 0);
+    if (e != cudaSuccess || r.stages == 0) return e;
+    a.stages = r.stages;
+    *parts = r.grid = std::min(r.grid, kNormMaxPartials);
+    *done = true;
+    return launch_pdl(ring, r.grid, block_threads(TPR), r.bytes, s, a);
+}
+
+template <typename T>
+cudaError_t pick_bwd_ring(const NormBwdArgs &a, int *parts, cudaStream_t s, bool *done) {
+    if (a.cols <= 512) return run_bwd_ring<T, 32, 16>(a, parts, s, done);
+    if (a.cols <= 1024) {
+        if constexpr (sizeof(T) == 2) return run_bwd_ring<T, 32, 32>(a, parts, s, done);
+        else return run_bwd_ring<T, 128, 8>(a, parts, s, done);
+    }
+    if (a.cols <= 2048) return run_bwd_ring<T, 128, 16>(a, parts, s, done);
+    if (a.cols <= 4096) return run_bwd_ring<T, 256, 16>(a, parts, s, done);
+    if (a.cols <= 8192) return run_bwd_ring<T, 512, 16>(a, parts, s, done);
+    if (a.cols <= 16384) return run_bwd_ring<T, 512, 32>(a, parts, s, done);
+    return cudaSuccess;
+}
+
+template <typename T, bool VECTOR, int TPR, int EPT>
 cudaError_t run_bwd(const NormBwdArgs &a, int *parts, cudaStream_t s) {
-    constexpr int RPB = block_threads(TPR) / TPR;
+    constexpr int THREADS = block_threads(TPR);
+    constexpr auto kernel = norm_bwd_kernel<T, VECTOR, TPR, EPT>;
     int grid = 0;
-    cudaError_t e = walk_grid<norm_bwd_kernel<T, VECTOR, TPR>>(block_threads(TPR), (a.rows + RPB - 1) / RPB, &grid);
+    cudaError_t e = walk_grid<kernel>(THREADS, (a.rows + teams(TPR) - 1) / teams(TPR), &grid);
     if (e != cudaSuccess) return e;
-    if (grid > kNormMaxPartials) grid = kNormMaxPartials;
-    *parts = grid;
-    return launch_pdl(norm_bwd_kernel<T, VECTOR, TPR>, grid, block_threads(TPR), 0, s, a);
+    *parts = grid = std::min(grid, kNormMaxPartials);
+    return launch_pdl(kernel, grid, THREADS, 0, s, a);
 }
 
 template <typename T, bool VECTOR>
 cudaError_t pick_bwd(const NormBwdArgs &a, int *parts, cudaStream_t s) {
+    constexpr int EPT = VECTOR ? 16 : 8;
+    if constexpr (VECTOR) {
+        bool done = false;
+        cudaError_t e = pick_bwd_ring<T>(a, parts, s, &done);
+        if (e != cudaSuccess || done) return e;
+    }
     // 1024 threads leave 64 registers each, too few for the column sums
-    switch (threads_for(a.cols, 512)) {
-    case 32: return run_bwd<T, VECTOR, 32>(a, parts, s);
-    case 128: return run_bwd<T, VECTOR, 128>(a, parts, s);
-    case 256: return run_bwd<T, VECTOR, 256>(a, parts, s);
-    case 512: return run_bwd<T, VECTOR, 512>(a, parts, s);
+    switch (threads_for(a.cols, EPT, 512)) {
+    case 32: return run_bwd<T, VECTOR, 32, EPT>(a, parts, s);
+    case 128: return run_bwd<T, VECTOR, 128, EPT>(a, parts, s);
+    case 256: return run_bwd<T, VECTOR, 256, EPT>(a, parts, s);
+    case 512: return run_bwd<T, VECTOR, 512, EPT>(a, parts, s);
     }
     int grid = 0;
     cudaError_t e = cudaSuccess;
@@ -490,7 +984,8 @@ bool row_vectors(const void *p, int64_t ld, int64_t cols) {
 
 template <typename T>
 cudaError_t norm_fwd_type(const NormArgs &a, cudaStream_t s) {
-    const bool vec = row_vectors<T>(a.x, a.ldx, a.cols) &&
+    const bool vec = row_vectors<T>(a.x, a.ldx, a.cols) && aligned_to(a.w, 16) &&
+                     aligned_to(a.b, 16) &&
                      (a.y == nullptr || aligned_to(a.y, 16)) &&
                      (a.yq == nullptr || aligned_to(a.yq, RowVec<T, true>::V));
     return vec ? pick_fwd<T, true>(a, s) : pick_fwd<T, false>(a, s);
@@ -499,7 +994,7 @@ cudaError_t norm_fwd_type(const NormArgs &a, cudaStream_t s) {
 template <typename T>
 cudaError_t norm_bwd_type(const NormBwdArgs &a, int *parts, cudaStream_t s) {
     const bool vec = row_vectors<T>(a.x, a.ldx, a.cols) && row_vectors<T>(a.dy, a.lddy, a.cols) &&
-                     (a.dx == nullptr || aligned_to(a.dx, 16));
+                     aligned_to(a.w, 16) && (a.dx == nullptr || aligned_to(a.dx, 16));
     return vec ? pick_bwd<T, true>(a, parts, s) : pick_bwd<T, false>(a, parts, s);
 }
 
@@ -512,7 +1007,8 @@ cudaError_t launch_layer_norm(const NormForward &n, cudaStream_t s) {
     }
     if (n.rows == 0 || n.cols == 0) return cudaSuccess;
     NormArgs a = {n.x, n.ldx, n.w, n.b, n.param_f32, n.rows, (int)n.cols, n.eps,
-                  n.y, n.yq, n.scale_inv, n.amax, n.mean, n.rstd};
+                  n.y, n.yq, n.scale_inv, n.amax, n.mean, n.rstd, 0,
+                  g_wait_limit_ns.load(std::memory_order_relaxed), device_status_word()};
     return n.x_f32 ? norm_fwd_type<float>(a, s) : norm_fwd_type<uint16_t>(a, s);
 }
 
@@ -522,13 +1018,14 @@ cudaError_t launch_layer_norm_backward(const NormBackward &n, cudaStream_t s) {
     int parts = 0;
     if (n.rows > 0) {
         NormBwdArgs a = {n.dy, n.x, n.lddy, n.ldx, n.w, n.param_f32, n.rows, (int)n.cols,
-                         n.mean, n.rstd, n.dx, sums ? n.workspace : nullptr};
+                         n.mean, n.rstd, n.dx, sums ? n.workspace : nullptr, 0,
+                         g_wait_limit_ns.load(std::memory_order_relaxed), device_status_word()};
         cudaError_t e = n.x_f32 ? norm_bwd_type<float>(a, &parts, s)
                                 : norm_bwd_type<uint16_t>(a, &parts, s);
         if (e != cudaSuccess) return e;
     }
     if (!sums) return cudaSuccess;
-    return launch_pdl(norm_reduce_kernel, dim3((unsigned)((n.cols + 31) / 32), 2), 256, 0, s,
+    return launch_pdl(norm_reduce_kernel, dim3((unsigned)((n.cols + 31) / 32), 2), 1024, 0, s,
                       (const float *)n.workspace, parts, (int)n.cols, n.dw, n.db, n.param_f32);
 }
 

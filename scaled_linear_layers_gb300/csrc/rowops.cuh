@@ -88,10 +88,66 @@ struct RowVec<T, false> {
     }
 };
 
+// Two fp32 values in one 64-bit register, and arithmetic on both in one
+// instruction (each lane rounds as the single one does).
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(a), "f"(b));
+    return p;
+}
+__device__ __forceinline__ float2 pair_split(uint64_t p) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
+    return f;
+}
+__device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t pair_mul(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// The larger of a and |b|; NaN if either is.
+__device__ __forceinline__ float max_abs_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(fabsf(b)));
+    return d;
+}
+
 // One element of a bf16 or fp32 parameter vector as fp32.
 __device__ __forceinline__ float load_param(const void *p, int f32, int64_t i) {
     return f32 ? reinterpret_cast<const float *>(p)[i]
                : elem_to_float(reinterpret_cast<const uint16_t *>(p)[i]);
+}
+
+// V neighbouring ones from a multiple of V on (V > 1: p is 16-byte aligned).
+template <int V>
+__device__ __forceinline__ void load_params(const void *p, int f32, int64_t i, float (&f)[V]) {
+    if constexpr (V == 1) {
+        f[0] = load_param(p, f32, i);
+    } else if (f32) {
+#pragma unroll
+        for (int k = 0; k < V; k += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + i + k);
+            f[k] = v.x, f[k + 1] = v.y, f[k + 2] = v.z, f[k + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; k += 4) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(p) + i + k);
+            f[k] = bf16_lo(v.x), f[k + 1] = bf16_hi(v.x);
+            f[k + 2] = bf16_lo(v.y), f[k + 3] = bf16_hi(v.y);
+        }
+    }
 }
 
 // Sum over a warp; every lane gets the same value.
@@ -125,6 +181,27 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float *red) {
             v[i] = __shfl_sync(0xFFFFFFFFu, t, 0);
         }
     }
+}
+
+// The sum of one value whose terms may cancel: each is split into its leading
+// 12 bits and the rest, which are added apart.  Sums of the leading parts of
+// values within 2^12 of each other are exact in fp32, and what the rests lose
+// is 2^-12 of what a plain sum would.
+template <int TPR>
+__device__ __forceinline__ float row_sum_split(float v, float rest, float *red) {
+    float s[2];
+    s[0] = __uint_as_float(__float_as_uint(v) & 0xFFFFF000u);
+    s[1] = fabsf(v) < INFINITY ? (v - s[0]) + rest : 0.f;  // an infinity or NaN is in s[0]
+    row_sum<TPR, 2>(s, red);
+    return s[0] + s[1];
+}
+
+// sum += v, with the addition's rounding error added to err.
+__device__ __forceinline__ void add_exact(float &sum, float &err, float v) {
+    const float t = __fadd_rn(sum, v);
+    const float z = __fsub_rn(t, sum);
+    err += __fadd_rn(__fsub_rn(sum, __fsub_rn(t, z)), __fsub_rn(v, z));
+    sum = t;
 }
 
 // |v|'s bit pattern (patterns of non-negative floats order like the values,
