@@ -189,7 +189,7 @@ cudaError_t launch_layer_norm_backward(const NormBackward &n, cudaStream_t s);
 
 // Tokens sorted by expert and back (moe.cu).
 constexpr int kMoeMaxExperts = 1024, kMoeMaxChunks = 128;
-constexpr int64_t kMoeMinChunk = 4096;  // assignments
+constexpr int64_t kMoeMinChunk = 1024;  // assignments
 // ids [n] int32 or int64; the outputs as fp8_moe_sort describes them.
 // workspace: kMoeMaxChunks * experts ints when n > kMoeMinChunk.
 cudaError_t launch_moe_sort(const void *ids, int ids_64, int64_t n, int experts, int64_t multiple,

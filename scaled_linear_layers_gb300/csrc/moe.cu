@@ -17,6 +17,8 @@
 // moves rows and is bound by HBM; all kernels go token by token, so x, dy and
 // y move once and the sorted rows once, and sums over j run in a fixed order
 // in fp32.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "occupancy.h"
@@ -27,6 +29,11 @@ namespace fp8 {
 namespace {
 
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
+// Assignments to a thread that are held in registers from the counting to the
+// placing; larger chunks (more than kMoeMaxChunks * 4096 assignments) are read
+// twice.
+constexpr int kSortFew = 2, kSortMany = 8;
+static_assert(kSortFew * kSortThreads == kMoeMinChunk, "the least chunk needs no workspace");
 
 struct SortArgs {
     const void *ids;
@@ -43,21 +50,6 @@ __device__ __forceinline__ int expert_at(const SortArgs &a, int64_t i, int64_t e
     return id >= 0 && id < a.experts ? (int)id : a.experts;
 }
 
-// Histogram of each warp's share of this block's chunk: hist[warp][expert].
-// A warp counts 32 assignments at a time; the lanes of one expert find each
-// other by a match, and the lowest of them adds their number, so no atomics.
-template <typename ID>
-__device__ __forceinline__ void warp_histogram(const SortArgs &a, int64_t lo, int64_t hi,
-                                               int32_t *mine) {
-    const int lane = threadIdx.x & 31;
-    for (int64_t i = lo; i < hi; i += 32) {
-        const int e = expert_at<ID>(a, i + lane, hi);
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-        if (e < a.experts && lane == __ffs(same) - 1) mine[e] += __popc(same);
-        __syncwarp();
-    }
-}
-
 __device__ __forceinline__ void warp_share(const SortArgs &a, int64_t &lo, int64_t &hi) {
     const int64_t begin = (int64_t)blockIdx.x * a.chunk, per = a.chunk / kSortWarps;
     const int64_t end = min(a.n, begin + a.chunk);
@@ -65,58 +57,97 @@ __device__ __forceinline__ void warp_share(const SortArgs &a, int64_t &lo, int64
     hi = min(end, lo + per);
 }
 
-// Assignments to each expert in each chunk.
-template <typename ID>
+// act(i, expert) for each 32 assignments of a warp's share, in order; with
+// KEPT > 0 the experts come from `kept`, loaded at once before.
+template <typename ID, int KEPT, typename F>
+__device__ __forceinline__ void each_32(const SortArgs &a, int64_t lo, int64_t hi,
+                                        const int (&kept)[KEPT > 0 ? KEPT : 1], F act) {
+    if constexpr (KEPT > 0) {
+#pragma unroll
+        for (int k = 0; k < KEPT; ++k)
+            if (lo + 32 * k < hi) act(lo + 32 * k, kept[k]);
+    } else {
+        for (int64_t i = lo; i < hi; i += 32)
+            act(i, expert_at<ID>(a, i + (threadIdx.x & 31), hi));
+    }
+}
+
+// Assignments to each expert in each chunk.  The lanes of one expert find each
+// other by a match, and the lowest of them adds their number.
+template <typename ID, int KEPT>
 __global__ void __launch_bounds__(kSortThreads) moe_count_kernel(const SortArgs a) {
-    extern __shared__ int32_t hist[];  // [kSortWarps][experts]
-    for (int i = threadIdx.x; i < kSortWarps * a.experts; i += kSortThreads) hist[i] = 0;
+    extern __shared__ int32_t hist[];  // [experts]
+    for (int i = threadIdx.x; i < a.experts; i += kSortThreads) hist[i] = 0;
     __syncthreads();
     pdl_wait_prior();
     pdl_allow_next();
+    const int lane = threadIdx.x & 31;
     int64_t lo, hi;
     warp_share(a, lo, hi);
-    warp_histogram<ID>(a, lo, hi, hist + (threadIdx.x >> 5) * a.experts);
+    int kept[KEPT > 0 ? KEPT : 1];
+#pragma unroll
+    for (int k = 0; k < KEPT; ++k) kept[k] = expert_at<ID>(a, lo + 32 * k + lane, hi);
+    each_32<ID, KEPT>(a, lo, hi, kept, [&](int64_t, int e) {
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+        if (e < a.experts && lane == __ffs(same) - 1) atomicAdd(&hist[e], __popc(same));
+    });
     __syncthreads();
-    for (int e = threadIdx.x; e < a.experts; e += kSortThreads) {
-        int32_t v = 0;
-        for (int w = 0; w < kSortWarps; ++w) v += hist[w * a.experts + e];
-        a.hist[(int64_t)blockIdx.x * a.experts + e] = v;
-    }
+    for (int e = threadIdx.x; e < a.experts; e += kSortThreads)
+        a.hist[(int64_t)blockIdx.x * a.experts + e] = hist[e];
 }
 
 // Places of one chunk's assignments.  Every block forms the segment offsets
 // itself from the chunks' counts (a few KB), so no block waits for another.
-template <typename ID>
+template <typename ID, int KEPT>
 __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(const SortArgs a) {
     extern __shared__ int32_t smem[];
-    int32_t *hist = smem;                          // [kSortWarps][experts]
+    int32_t *hist = smem;                            // [kSortWarps][experts]
     int32_t *total = hist + kSortWarps * a.experts;  // [experts]
-    int32_t *first = total + a.experts;            // [experts + 1] segment starts
+    int32_t *earlier = total + a.experts;            // [experts] in earlier chunks
+    int32_t *first = earlier + a.experts;            // [experts + 1] segment starts
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int i = threadIdx.x; i < kSortWarps * a.experts; i += kSortThreads) hist[i] = 0;
+    for (int i = threadIdx.x; i < (kSortWarps + 2) * a.experts; i += kSortThreads) hist[i] = 0;
     __syncthreads();
     pdl_wait_prior();
     pdl_allow_next();
     int64_t lo, hi;
     warp_share(a, lo, hi);
-    warp_histogram<ID>(a, lo, hi, hist + warp * a.experts);
+    int kept[KEPT > 0 ? KEPT : 1];
+#pragma unroll
+    for (int k = 0; k < KEPT; ++k) kept[k] = expert_at<ID>(a, lo + 32 * k + lane, hi);
+    if (a.chunks > 1) {
+        // the chunks' counts: warps side by side over the chunks, lanes over
+        // the experts (whole numbers: the order of additions does not matter)
+        for (int e = lane; e < a.experts; e += 32) {
+            int32_t all = 0, before = 0;
+#pragma unroll 8
+            for (int c = warp; c < a.chunks; c += kSortWarps) {
+                const int32_t v = a.hist[(int64_t)c * a.experts + e];
+                all += v;
+                before += c < (int)blockIdx.x ? v : 0;
+            }
+            atomicAdd(&total[e], all);
+            atomicAdd(&earlier[e], before);
+        }
+    }
+    int32_t *mine = hist + warp * a.experts;
+    each_32<ID, KEPT>(a, lo, hi, kept, [&](int64_t, int e) {
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+        if (e < a.experts && lane == __ffs(same) - 1) mine[e] += __popc(same);
+        __syncwarp();
+    });
     __syncthreads();
     // hist[w][e] = assignments to e in earlier warps of this chunk and, with
     // more than one chunk, in earlier chunks
     for (int e = threadIdx.x; e < a.experts; e += kSortThreads) {
-        int32_t before = 0, all = 0;
-        if (a.chunks > 1)
-            for (int c = 0; c < a.chunks; ++c) {
-                const int32_t v = a.hist[(int64_t)c * a.experts + e];
-                before += c < (int)blockIdx.x ? v : 0;
-                all += v;
-            }
+        int32_t before = earlier[e];
+#pragma unroll
         for (int w = 0; w < kSortWarps; ++w) {
             const int32_t v = hist[w * a.experts + e];
             hist[w * a.experts + e] = before;
             before += v;
         }
-        total[e] = a.chunks > 1 ? all : before;
+        if (a.chunks == 1) total[e] = before;
     }
     __syncthreads();
     // segment starts: a scan of the padded counts, 32 experts at a time
@@ -138,9 +169,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(const SortArgs 
         if (lane == 0) first[a.experts] = base;
     }
     __syncthreads();
-    int32_t *mine = hist + warp * a.experts;
-    for (int64_t i = lo; i < hi; i += 32) {
-        const int e = expert_at<ID>(a, i + lane, hi);
+    each_32<ID, KEPT>(a, lo, hi, kept, [&](int64_t i, int e) {
         const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
         const int rank = __popc(same & ((1u << lane) - 1u));
         const int32_t seen = e < a.experts ? mine[e] : 0;
@@ -155,7 +184,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(const SortArgs 
             a.row_of[i + lane] = row;
         }
         __syncwarp();
-    }
+    });
     if (blockIdx.x == 0) {
         for (int e = threadIdx.x; e <= a.experts; e += kSortThreads) {
             a.offsets[e] = first[e];
@@ -173,8 +202,6 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(const SortArgs 
 
 // ------------------------------------------------------------------ rows ---
 
-constexpr int kRowThreads = 256;
-
 struct RowArgs {
     MoeRows m;
     const void *x;     // [tokens, hidden]: x or dy
@@ -191,147 +218,522 @@ struct RowArgs {
     int rows_per_block; // rows that one padding block looks at
 };
 
-// Zeroes the padding rows (source = -1) among this block's share of them.
-template <typename O, int V>
+// A block is eight teams of a warp or one larger team; a team takes a token.
+constexpr int row_threads(int tpt) { return tpt == 32 ? 256 : tpt; }
+
+// Zeroes the padding rows (source = -1) among this block's share of them: the
+// block looks at as many rows as it has threads at once, and lists those.
+template <typename O>
 __device__ __forceinline__ void zero_padding(const RowArgs &a, O *out, int block) {
-    const int64_t lo = (int64_t)block * a.rows_per_block;
-    const int64_t hi = min(a.m.capacity, lo + a.rows_per_block);
-    struct alignas(sizeof(O) * V) Group {
-        O v[V];
-    };
-    const Group zero = {};
-    for (int64_t r = lo; r < hi; ++r) {
-        if (a.m.source[r] >= 0) continue;
-        O *to = out + r * a.m.hidden;
-        for (int64_t h = (int64_t)threadIdx.x * V; h < a.m.hidden; h += kRowThreads * V)
-            *reinterpret_cast<Group *>(to + h) = zero;
+    __shared__ int32_t list[256];
+    __shared__ int count;
+    const int64_t H = a.m.hidden;
+    const int64_t begin = (int64_t)block * a.rows_per_block;
+    const int64_t end = min(a.m.capacity, begin + a.rows_per_block);
+    for (int64_t lo = begin; lo < end; lo += blockDim.x) {
+        if (threadIdx.x == 0) count = 0;
+        __syncthreads();
+        const int64_t mine = lo + threadIdx.x;
+        if (mine < end && a.m.source[mine] < 0) list[atomicAdd(&count, 1)] = (int32_t)mine;
+        __syncthreads();
+        const int n = count;
+        for (int k = 0; k < n; ++k) {
+            // 16 bytes at a time from the first such boundary on
+            uint8_t *to = reinterpret_cast<uint8_t *>(out + list[k] * H);
+            const int64_t bytes = H * (int64_t)sizeof(O);
+            const int64_t head = min(bytes, (int64_t)(-reinterpret_cast<uintptr_t>(to) & 15u));
+            const int64_t body = head + ((bytes - head) & ~int64_t(15));
+            for (int64_t i = head + 16 * (int64_t)threadIdx.x; i < body; i += 16 * (int64_t)blockDim.x)
+                *reinterpret_cast<uint4 *>(to + i) = make_uint4(0, 0, 0, 0);
+            for (int64_t i = threadIdx.x; i < head; i += blockDim.x) to[i] = 0;
+            for (int64_t i = body + threadIdx.x; i < bytes; i += blockDim.x) to[i] = 0;
+        }
+        __syncthreads();
     }
 }
 
-// The place of assignment j of token t, or -1 (a place outside the sorted
-// rows counts as dropped, so a stale index cannot write out of bounds).
-__device__ __forceinline__ int64_t place_of(const MoeRows &m, int64_t t, int j) {
-    const int64_t r = m.row_of[t * m.topk + j];
-    return r < m.capacity ? r : -1;
+// The places of assignments j0 to j0 + KM - 1 of token t, -1 for none (a place
+// outside the sorted rows counts as dropped, so a stale index cannot reach out
+// of bounds), and their weights, 0 for none.
+template <int KM>
+__device__ __forceinline__ void places(const RowArgs &a, int64_t t, int j0, int32_t (&r)[KM],
+                                       float (&w)[KM]) {
+#pragma unroll
+    for (int i = 0; i < KM; ++i) {
+        const int64_t at = t * a.m.topk + j0 + i;
+        r[i] = t < a.m.tokens && j0 + i < a.m.topk ? a.m.row_of[at] : -1;
+        if (r[i] >= a.m.capacity) r[i] = -1;
+        w[i] = r[i] >= 0 ? (a.weights != nullptr ? a.weights[at] : 1.f) : 0.f;
+    }
 }
 
-// TPT threads to a token, which each carry one group of V columns at a time:
-// one load, topk stores.
-template <typename T, bool VECTOR, bool QUANT, int TPT>
-__global__ void __launch_bounds__(kRowThreads) moe_dispatch_kernel(const RowArgs a) {
-    using RV = RowVec<T, VECTOR>;
-    constexpr int V = RV::V, TPB = kRowThreads / TPT;
+// One load of each group of V columns, topk stores.  U groups at a time, and
+// the places of KM assignments, are loaded before anything waits for them.
+template <typename T, bool QUANT, int TPT, int KM>
+__global__ void __launch_bounds__(row_threads(TPT)) moe_dispatch_kernel(const RowArgs a) {
+    using RV = RowVec<T, true>;
+    constexpr int V = RV::V, TPB = row_threads(TPT) / TPT, U = 2;
     pdl_wait_prior();
     pdl_allow_next();
     if ((int)blockIdx.x >= a.token_blocks) {
         if constexpr (QUANT)
-            zero_padding<uint8_t, V>(a, a.outq, blockIdx.x - a.token_blocks);
+            zero_padding<uint8_t>(a, a.outq, blockIdx.x - a.token_blocks);
         else
-            zero_padding<T, V>(a, reinterpret_cast<T *>(a.out), blockIdx.x - a.token_blocks);
+            zero_padding<T>(a, reinterpret_cast<T *>(a.out), blockIdx.x - a.token_blocks);
         return;
     }
     const float si = QUANT ? *a.scale_inv : 0.f;
     const int64_t H = a.m.hidden;
-    uint32_t m = 0;
+    const int64_t h0 = (int64_t)(threadIdx.x % TPT) * V;
+    float m = 0.f;
     for (int64_t t = (int64_t)blockIdx.x * TPB + threadIdx.x / TPT; t < a.m.tokens;
          t += (int64_t)a.token_blocks * TPB) {
         const T *x = reinterpret_cast<const T *>(a.x) + t * a.ldx;
-        for (int64_t h = (int64_t)(threadIdx.x % TPT) * V; h < H; h += TPT * V) {
-            const typename RV::Raw v = RV::load(x + h);
-            float f[V];
-            if constexpr (QUANT) {
-                RV::unpack(v, f);
+        int32_t r[KM];
+        float w[KM];
+        places(a, t, 0, r, w);
+        for (int64_t h = h0; h < H; h += TPT * V * U) {
+            typename RV::Raw raw[U];
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    m = max(m, abs_bits(f[i]));
-                    f[i] = __fmul_rn(f[i], si);
+            for (int u = 0; u < U; ++u)
+                raw[u] = h + u * TPT * V < H ? RV::load(x + h + u * TPT * V) : RV::zero();
+            float f[U][V];
+            if constexpr (QUANT) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    RV::unpack(raw[u], f[u]);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        m = max_abs_nan(m, f[u][i]);
+                        f[u][i] = __fmul_rn(f[u][i], si);
+                    }
                 }
             }
-            for (int j = 0; j < a.m.topk; ++j) {
-                const int64_t r = place_of(a.m, t, j);
-                if (r < 0) continue;
-                if constexpr (QUANT)
-                    RV::store_e4m3(a.outq + r * H + h, f);
-                else
-                    RV::store_raw(reinterpret_cast<T *>(a.out) + r * H + h, v);
+            for (int j0 = 0; j0 < a.m.topk; j0 += KM) {
+                if (j0 > 0) places(a, t, j0, r, w);
+#pragma unroll
+                for (int i = 0; i < KM; ++i) {
+                    if (r[i] < 0) continue;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int64_t at = r[i] * H + h + u * TPT * V;
+                        if (h + u * TPT * V >= H) continue;
+                        if constexpr (QUANT)
+                            RV::store_e4m3(a.outq + at, f[u]);
+                        else
+                            RV::store_raw(reinterpret_cast<T *>(a.out) + at, raw[u]);
+                    }
+                }
+                if (a.m.topk > KM && j0 + KM >= a.m.topk) places(a, t, 0, r, w);
             }
         }
     }
     if constexpr (QUANT) {
         if (a.amax != nullptr) {
-            m = __reduce_max_sync(0xFFFFFFFFu, m);
-            if ((threadIdx.x & 31) == 0 && m != 0)
-                atomicMax(reinterpret_cast<unsigned int *>(a.amax), m);
+            const uint32_t bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m));
+            if ((threadIdx.x & 31) == 0 && bits != 0)
+                atomicMax(reinterpret_cast<unsigned int *>(a.amax), bits);
         }
     }
 }
 
-template <typename T, bool VECTOR, int TPT>
-__global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const RowArgs a) {
-    using RV = RowVec<T, VECTOR>;
-    constexpr int V = RV::V, TPB = kRowThreads / TPT;
+// All KM rows' groups are loaded before they are added, in the order of j.
+template <typename T, int TPT, int KM>
+__global__ void __launch_bounds__(row_threads(TPT)) moe_combine_kernel(const RowArgs a) {
+    using RV = RowVec<T, true>;
+    constexpr int V = RV::V, TPB = row_threads(TPT) / TPT, U = KM > 4 ? 1 : 2;
     pdl_wait_prior();
     pdl_allow_next();
     const int64_t H = a.m.hidden;
     const T *rows = reinterpret_cast<const T *>(a.rows);
+    const int64_t h0 = (int64_t)(threadIdx.x % TPT) * V;
     for (int64_t t = (int64_t)blockIdx.x * TPB + threadIdx.x / TPT; t < a.m.tokens;
          t += (int64_t)gridDim.x * TPB) {
-        for (int64_t h = (int64_t)(threadIdx.x % TPT) * V; h < H; h += TPT * V) {
-            float acc[V] = {};
-#pragma unroll 4
-            for (int j = 0; j < a.m.topk; ++j) {
-                const int64_t r = place_of(a.m, t, j);
-                if (r < 0) continue;
-                const float w = a.weights != nullptr ? a.weights[t * a.m.topk + j] : 1.f;
-                float f[V];
-                RV::unpack(RV::load(rows + r * a.ldr + h), f);
+        int32_t r[KM];
+        float w[KM];
+        places(a, t, 0, r, w);
+        for (int64_t h = h0; h < H; h += TPT * V * U) {
+            float acc[U][V] = {};
+            for (int j0 = 0; j0 < a.m.topk; j0 += KM) {
+                if (a.m.topk > KM) places(a, t, j0, r, w);
+                typename RV::Raw raw[U][KM];
 #pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] = fmaf(w, f[i], acc[i]);
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int i = 0; i < KM; ++i)
+                        raw[u][i] = r[i] >= 0 && h + u * TPT * V < H
+                                        ? RV::load(rows + r[i] * a.ldr + h + u * TPT * V)
+                                        : RV::zero();
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int i = 0; i < KM; ++i) {
+                        float f[V];
+                        RV::unpack(raw[u][i], f);
+#pragma unroll
+                        for (int v = 0; v < V; ++v) acc[u][v] = fmaf(w[i], f[v], acc[u][v]);
+                    }
             }
-            RV::store(reinterpret_cast<T *>(a.out) + t * H + h, acc);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (h + u * TPT * V < H)
+                    RV::store(reinterpret_cast<T *>(a.out) + t * H + h + u * TPT * V, acc[u]);
         }
     }
 }
 
-// One assignment at a time: the dot product's terms need every column of the
-// row before the next one starts.
-template <typename T, bool VECTOR, int TPT>
-__global__ void __launch_bounds__(kRowThreads) moe_combine_bwd_kernel(const RowArgs a) {
-    using RV = RowVec<T, VECTOR>;
-    constexpr int V = RV::V, TPB = kRowThreads / TPT;
-    __shared__ float red[2][TPT > 32 ? TPT / 32 : 1];
+// dy's groups are loaded once for KM assignments, whose dot products are
+// summed over the team together at the end of the row.
+template <typename T, int TPT, int KM>
+__global__ void __launch_bounds__(row_threads(TPT)) moe_combine_bwd_kernel(const RowArgs a) {
+    using RV = RowVec<T, true>;
+    constexpr int V = RV::V, TPB = row_threads(TPT) / TPT, U = KM > 4 ? 1 : 2;
+    __shared__ float red[2][KM * (TPT > 32 ? TPT / 32 : 1)];
     pdl_wait_prior();
     pdl_allow_next();
     if ((int)blockIdx.x >= a.token_blocks) {
-        zero_padding<T, V>(a, reinterpret_cast<T *>(a.out), blockIdx.x - a.token_blocks);
+        zero_padding<T>(a, reinterpret_cast<T *>(a.out), blockIdx.x - a.token_blocks);
         return;
     }
     const int64_t H = a.m.hidden;
     const T *rows = reinterpret_cast<const T *>(a.rows), *dy = reinterpret_cast<const T *>(a.x);
+    const int64_t h0 = (int64_t)(threadIdx.x % TPT) * V;
     int turn = 0;
     for (int64_t t0 = (int64_t)blockIdx.x * TPB; t0 < a.m.tokens;
          t0 += (int64_t)a.token_blocks * TPB) {
         const int64_t t = t0 + threadIdx.x / TPT;
-        for (int j = 0; j < a.m.topk; ++j, ++turn) {
-            const int64_t r = t < a.m.tokens ? place_of(a.m, t, j) : -1;
-            float s[1] = {0.f};
-            if (r >= 0) {
-                const float w = a.weights != nullptr ? a.weights[t * a.m.topk + j] : 1.f;
-                for (int64_t h = (int64_t)(threadIdx.x % TPT) * V; h < H; h += TPT * V) {
-                    float g[V], f[V];
-                    RV::unpack(RV::load(dy + t * a.ldx + h), g);
-                    RV::unpack(RV::load(rows + r * a.ldr + h), f);
+        for (int j0 = 0; j0 < a.m.topk; j0 += KM, ++turn) {
+            int32_t r[KM];
+            float w[KM], s[KM];
+            places(a, t, j0, r, w);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        s[0] = fmaf(g[i], f[i], s[0]);
-                        g[i] *= w;
+            for (int i = 0; i < KM; ++i) s[i] = 0.f;
+            for (int64_t h = t < a.m.tokens ? h0 : H; h < H; h += TPT * V * U) {
+                typename RV::Raw g[U], raw[U][KM];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const bool in = h + u * TPT * V < H;
+                    g[u] = in ? RV::load(dy + t * a.ldx + h + u * TPT * V) : RV::zero();
+#pragma unroll
+                    for (int i = 0; i < KM; ++i)
+                        raw[u][i] = in && r[i] >= 0 ? RV::load(rows + r[i] * a.ldr + h + u * TPT * V)
+                                                    : RV::zero();
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float fg[V];
+                    RV::unpack(g[u], fg);
+#pragma unroll
+                    for (int i = 0; i < KM; ++i) {
+                        if (r[i] < 0) continue;
+                        float f[V];
+                        RV::unpack(raw[u][i], f);
+#pragma unroll
+                        for (int v = 0; v < V; ++v) {
+                            s[i] = fmaf(fg[v], f[v], s[i]);
+                            f[v] = fg[v] * w[i];
+                        }
+                        if (h + u * TPT * V < H)
+                            RV::store(reinterpret_cast<T *>(a.out) + r[i] * H + h + u * TPT * V, f);
                     }
-                    RV::store(reinterpret_cast<T *>(a.out) + r * H + h, g);
                 }
             }
-            row_sum<TPT, 1>(s, red[turn & 1]);
-            if (a.dweights != nullptr && t < a.m.tokens && threadIdx.x % TPT == 0)
-                a.dweights[t * a.m.topk + j] = s[0];
+            if (a.dweights == nullptr) continue;
+            row_sum<TPT, KM>(s, red[turn & 1]);
+            if (t < a.m.tokens && threadIdx.x % TPT == 0) {
+#pragma unroll
+                for (int i = 0; i < KM; ++i)
+                    if (j0 + i < a.m.topk) a.dweights[t * a.m.topk + j0 + i] = s[i];
+            }
+        }
+    }
+}
+
+// Rows that 16-byte groups do not fit (an odd width, an unaligned address).  A
+// team goes along the row it writes by the 16-byte groups of *that* row's
+// addresses, so that stores stay whole (single elements only in the ragged
+// groups at its two ends); what it reads is shifted into place, without
+// branches, so that many loads are in flight.  The ragged groups' loads run up
+// to a group past the row, into the tensor's next or last one; where the tensor
+// has none, at its first and last rows, a token goes element by element.
+
+// The rows of a [rows, H] tensor of row stride ld that are far enough from its
+// ends: a group's loads reach less than 3 V elements past a row's.
+template <typename T>
+struct Inner {
+    const T *p;
+    int64_t ld, first, last;
+    __device__ __forceinline__ Inner(const void *base, int64_t rows, int64_t stride) {
+        constexpr int V = RowVec<T, true>::V;
+        p = reinterpret_cast<const T *>(base);
+        ld = stride;
+        const int64_t margin = ld > 0 ? (3 * V + ld - 1) / ld : rows;
+        first = margin;
+        last = rows - margin;
+    }
+    __device__ __forceinline__ const T *row(int64_t r) const { return p + r * ld; }
+    // (a dropped assignment loads row `first` instead, and drops what it got:
+    // loads under a condition of their own would wait for one another)
+    __device__ __forceinline__ bool holds(int64_t r) const { return r >= first && r < last; }
+};
+
+// Column of the first 16-byte group's start (V bytes' for E4M3) at or before
+// the row at p: 1 - V to 0.
+template <int V, typename O>
+__device__ __forceinline__ int first_group(const O *p) {
+    return -(int)((reinterpret_cast<uintptr_t>(p) / sizeof(O)) & (V - 1));
+}
+
+// Stores the elements of a group at column h that lie inside the row.
+template <int V, typename O, typename All, typename One>
+__device__ __forceinline__ void store_group(O *row, int64_t h, int64_t H, All all, One one) {
+    if (h >= 0 && h + V <= H) {
+        all(row + h);
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (h + v >= 0 && h + v < H) one(row + h + v, v);
+    }
+}
+
+template <typename T, bool QUANT, int TPT, int KM>
+__global__ void __launch_bounds__(row_threads(TPT)) moe_dispatch_any_kernel(const RowArgs a) {
+    using RV = RowVec<T, true>;
+    using O = typename std::conditional<QUANT, uint8_t, T>::type;
+    constexpr int V = RV::V, TPB = row_threads(TPT) / TPT;
+    pdl_wait_prior();
+    pdl_allow_next();
+    O *out = QUANT ? reinterpret_cast<O *>(a.outq) : reinterpret_cast<O *>(a.out);
+    if ((int)blockIdx.x >= a.token_blocks) {
+        zero_padding<O>(a, out, blockIdx.x - a.token_blocks);
+        return;
+    }
+    const float si = QUANT ? *a.scale_inv : 0.f;
+    const int64_t H = a.m.hidden, N = H / V + 2;
+    const int t0 = threadIdx.x % TPT;
+    const Inner<T> in(a.x, a.m.tokens, a.ldx);
+    float m = 0.f;
+    auto one = [&](O *to, float f) {
+        if constexpr (QUANT)
+            *to = (uint8_t)(cvt_e4m3x2(__fmul_rn(f, si), 0.f) & 0xFFu);
+        else
+            float_to_elem(to, f);
+    };
+    for (int64_t t = (int64_t)blockIdx.x * TPB + threadIdx.x / TPT; t < a.m.tokens;
+         t += (int64_t)a.token_blocks * TPB) {
+        const T *x = in.row(t);
+        const bool shifts = in.holds(t);
+        if (QUANT && a.amax != nullptr) {
+#pragma unroll 4
+            for (int64_t h = t0; h < H; h += TPT) m = max_abs_nan(m, elem_to_float(x[h]));
+        }
+        for (int j0 = 0; j0 < a.m.topk; j0 += KM) {
+            int32_t r[KM];
+            float w[KM];
+            places(a, t, j0, r, w);
+            if (!shifts) {
+                for (int i = 0; i < KM; ++i)
+                    if (r[i] >= 0)
+                        for (int64_t e = t0; e < H; e += TPT)
+                            one(out + r[i] * H + e, elem_to_float(x[e]));
+                continue;
+            }
+            int h0[KM];
+            ShiftedRow<T> src[KM];
+#pragma unroll
+            for (int i = 0; i < KM; ++i) {
+                h0[i] = r[i] >= 0 ? first_group<V>(out + r[i] * H) : 0;
+                src[i] = ShiftedRow<T>(x + h0[i]);
+            }
+            for (int64_t g = t0; g < N; g += TPT) {
+                typename RV::Raw raw[KM];
+#pragma unroll
+                for (int i = 0; i < KM; ++i)
+                    raw[i] = src[i].load(g);
+#pragma unroll
+                for (int i = 0; i < KM; ++i) {
+                    if (r[i] < 0) continue;
+                    float f[V];
+                    RV::unpack(raw[i], f);
+                    store_group<V>(
+                        out + r[i] * H, h0[i] + g * V, H,
+                        [&](O *to) {
+                            if constexpr (QUANT) {
+                                float q[V];
+#pragma unroll
+                                for (int v = 0; v < V; ++v) q[v] = __fmul_rn(f[v], si);
+                                RV::store_e4m3(to, q);
+                            } else {
+                                RV::store_raw(to, raw[i]);
+                            }
+                        },
+                        [&](O *to, int v) { one(to, f[v]); });
+                }
+            }
+        }
+    }
+    if constexpr (QUANT) {
+        if (a.amax != nullptr) {
+            const uint32_t bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m));
+            if ((threadIdx.x & 31) == 0 && bits != 0)
+                atomicMax(reinterpret_cast<unsigned int *>(a.amax), bits);
+        }
+    }
+}
+
+template <typename T, int TPT, int KM>
+__global__ void __launch_bounds__(row_threads(TPT)) moe_combine_any_kernel(const RowArgs a) {
+    using RV = RowVec<T, true>;
+    constexpr int V = RV::V, TPB = row_threads(TPT) / TPT;
+    pdl_wait_prior();
+    pdl_allow_next();
+    const int64_t H = a.m.hidden, N = H / V + 2;
+    const int t0 = threadIdx.x % TPT;
+    const Inner<T> in(a.rows, a.m.capacity, a.ldr);
+    for (int64_t t = (int64_t)blockIdx.x * TPB + threadIdx.x / TPT; t < a.m.tokens;
+         t += (int64_t)gridDim.x * TPB) {
+        T *to = reinterpret_cast<T *>(a.out) + t * H;
+        const int h0 = first_group<V>(to);
+        int32_t r[KM];
+        float w[KM];
+        ShiftedRow<T> src[KM];
+        bool shifts = in.first < in.last;
+        auto take = [&](int j0) {
+            places(a, t, j0, r, w);
+#pragma unroll
+            for (int i = 0; i < KM; ++i) {
+                shifts = shifts && (r[i] < 0 || in.holds(r[i]));
+                src[i] = ShiftedRow<T>(in.row(r[i] < 0 ? in.first : r[i]) + h0);
+            }
+        };
+        for (int j0 = 0; j0 < a.m.topk; j0 += KM) take(j0);
+        if (!shifts) {
+            for (int64_t e = t0; e < H; e += TPT) {
+                float acc = 0.f;
+                for (int j0 = 0; j0 < a.m.topk; j0 += KM) {
+                    places(a, t, j0, r, w);
+#pragma unroll
+                    for (int i = 0; i < KM; ++i)
+                        acc = fmaf(w[i], r[i] >= 0 ? elem_to_float(in.row(r[i])[e]) : 0.f, acc);
+                }
+                float_to_elem(to + e, acc);
+            }
+            continue;
+        }
+        for (int64_t g = t0; g < N && h0 + g * V < H; g += TPT) {
+            const int64_t h = h0 + g * V;
+            uint64_t sum[V / 2] = {};
+            for (int j0 = 0; j0 < a.m.topk; j0 += KM) {
+                if (a.m.topk > KM) take(j0);
+                typename RV::Raw raw[KM];
+#pragma unroll
+                for (int i = 0; i < KM; ++i) raw[i] = src[i].load(g);
+#pragma unroll
+                for (int i = 0; i < KM; ++i) {
+                    float f[V];
+                    RV::unpack(r[i] >= 0 ? raw[i] : RV::zero(), f);
+                    const uint64_t w2 = pair_of(w[i], w[i]);
+#pragma unroll
+                    for (int v = 0; v < V; v += 2)
+                        sum[v / 2] = pair_fma(w2, pair_of(f[v], f[v + 1]), sum[v / 2]);
+                }
+            }
+            float acc[V];
+#pragma unroll
+            for (int v = 0; v < V; v += 2) {
+                const float2 f = pair_split(sum[v / 2]);
+                acc[v] = f.x, acc[v + 1] = f.y;
+            }
+            store_group<V>(
+                to, h, H, [&](T *p) { RV::store(p, acc); },
+                [&](T *p, int v) { float_to_elem(p, acc[v]); });
+        }
+    }
+}
+
+template <typename T, int TPT, int KM>
+__global__ void __launch_bounds__(row_threads(TPT)) moe_combine_bwd_any_kernel(const RowArgs a) {
+    using RV = RowVec<T, true>;
+    constexpr int V = RV::V, TPB = row_threads(TPT) / TPT;
+    __shared__ float red[2][KM * (TPT > 32 ? TPT / 32 : 1)];
+    pdl_wait_prior();
+    pdl_allow_next();
+    if ((int)blockIdx.x >= a.token_blocks) {
+        zero_padding<T>(a, reinterpret_cast<T *>(a.out), blockIdx.x - a.token_blocks);
+        return;
+    }
+    const int64_t H = a.m.hidden, N = H / V + 2;
+    const int lane = threadIdx.x % TPT;
+    const Inner<T> in(a.rows, a.m.capacity, a.ldr), grad(a.x, a.m.tokens, a.ldx);
+    T *out = reinterpret_cast<T *>(a.out);
+    int turn = 0;
+    for (int64_t t0 = (int64_t)blockIdx.x * TPB; t0 < a.m.tokens;
+         t0 += (int64_t)a.token_blocks * TPB) {
+        const int64_t t = t0 + threadIdx.x / TPT;
+        const T *dy = grad.row(t);
+        for (int j0 = 0; j0 < a.m.topk; j0 += KM, ++turn) {
+            int32_t r[KM];
+            float w[KM], s[KM];
+            places(a, t, j0, r, w);
+            bool shifts = grad.holds(t) && in.first < in.last;
+            int h0[KM];
+            ShiftedRow<T> src[KM], gsrc[KM];
+#pragma unroll
+            for (int i = 0; i < KM; ++i) {
+                s[i] = 0.f;
+                shifts = shifts && (r[i] < 0 || in.holds(r[i]));
+                h0[i] = r[i] >= 0 ? first_group<V>(out + r[i] * H) : 0;
+                src[i] = ShiftedRow<T>(in.row(r[i] < 0 ? in.first : r[i]) + h0[i]);
+                gsrc[i] = ShiftedRow<T>(dy + h0[i]);
+            }
+            if (shifts) {
+                for (int64_t g = lane; g < N; g += TPT) {
+                    typename RV::Raw raw[KM], gr[KM];
+#pragma unroll
+                    for (int i = 0; i < KM; ++i) {
+                        gr[i] = gsrc[i].load(g);
+                        raw[i] = src[i].load(g);
+                    }
+#pragma unroll
+                    for (int i = 0; i < KM; ++i) {
+                        if (r[i] < 0) continue;
+                        const int64_t h = h0[i] + g * V;
+                        float f[V], fg[V];
+                        RV::unpack(raw[i], f);
+                        RV::unpack(gr[i], fg);
+                        store_group<V>(
+                            out + r[i] * H, h, H,
+                            [&](T *to) {
+#pragma unroll
+                                for (int v = 0; v < V; ++v) {
+                                    s[i] = fmaf(fg[v], f[v], s[i]);
+                                    f[v] = fg[v] * w[i];
+                                }
+                                RV::store(to, f);
+                            },
+                            [&](T *to, int v) {
+                                s[i] = fmaf(fg[v], f[v], s[i]);
+                                float_to_elem(to, fg[v] * w[i]);
+                            });
+                    }
+                }
+            } else if (t < a.m.tokens) {
+#pragma unroll
+                for (int i = 0; i < KM; ++i)
+                    if (r[i] >= 0)
+                        for (int64_t e = lane; e < H; e += TPT) {
+                            const float g = elem_to_float(dy[e]);
+                            s[i] = fmaf(g, elem_to_float(in.row(r[i])[e]), s[i]);
+                            float_to_elem(out + r[i] * H + e, g * w[i]);
+                        }
+            }
+            if (a.dweights == nullptr) continue;
+            row_sum<TPT, KM>(s, red[turn & 1]);
+            if (t < a.m.tokens && lane == 0) {
+#pragma unroll
+                for (int i = 0; i < KM; ++i)
+                    if (j0 + i < a.m.topk) a.dweights[t * a.m.topk + j0 + i] = s[i];
+            }
         }
     }
 }
@@ -340,20 +742,20 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_bwd_kernel(const RowA
 // write padding rows, the blocks after them.
 template <auto KERNEL, int TPT>
 cudaError_t launch_rows(RowArgs a, bool padding, cudaStream_t s) {
+    constexpr int THREADS = row_threads(TPT), TPB = THREADS / TPT;
     int per_sm = 0;
-    cudaError_t e = blocks_per_sm<KERNEL>(kRowThreads, &per_sm);
+    cudaError_t e = blocks_per_sm<KERNEL>(THREADS, &per_sm);
     if (e != cudaSuccess) return e;
-    const int64_t most = (int64_t)num_sms() * per_sm;
-    const int64_t units = (a.m.tokens + kRowThreads / TPT - 1) / (kRowThreads / TPT);
+    const int64_t most = (int64_t)num_sms() * per_sm, units = (a.m.tokens + TPB - 1) / TPB;
     a.token_blocks = (int)(units < most ? units : most);
     int64_t grid = a.token_blocks;
     if (padding && a.m.capacity > 0) {
-        int64_t rpb = (a.m.capacity + 4 * num_sms() - 1) / (4 * num_sms());
+        const int64_t rpb = (a.m.capacity + 4 * num_sms() - 1) / (4 * num_sms());
         a.rows_per_block = (int)rpb;
         grid += (a.m.capacity + rpb - 1) / rpb;
     }
     if (grid == 0) return cudaSuccess;
-    return launch_pdl(KERNEL, (int)grid, kRowThreads, 0, s, a);
+    return launch_pdl(KERNEL, (int)grid, THREADS, 0, s, a);
 }
 
 // Whether rows of `es`-byte elements at p, `ld` apart, can move 16 bytes at a time.
@@ -361,31 +763,53 @@ bool row_vectors(const void *p, int64_t ld, int64_t cols, int es) {
     return aligned_to(p, 16) && ld * es % 16 == 0 && cols * es % 16 == 0;
 }
 
-// A warp to a token of up to 32 16-byte groups, else a block.
-bool narrow(const MoeRows &m, bool vec) { return m.hidden <= 32 * (vec ? (m.f32 ? 4 : 8) : 1); }
-
-template <typename T, bool VECTOR>
-cudaError_t dispatch_rows(const RowArgs &a, cudaStream_t s) {
-    if (a.outq != nullptr)
-        return narrow(a.m, VECTOR)
-                   ? launch_rows<moe_dispatch_kernel<T, VECTOR, true, 32>, 32>(a, true, s)
-                   : launch_rows<moe_dispatch_kernel<T, VECTOR, true, 256>, 256>(a, true, s);
-    return narrow(a.m, VECTOR)
-               ? launch_rows<moe_dispatch_kernel<T, VECTOR, false, 32>, 32>(a, true, s)
-               : launch_rows<moe_dispatch_kernel<T, VECTOR, false, 256>, 256>(a, true, s);
+// f(threads to a token, assignments at a time): the fewest threads that have
+// at most `per_lane` groups each, at most 256; the fewest assignments at a
+// time that take them all, at most 8.
+template <typename F>
+cudaError_t with_team(const MoeRows &m, int per_lane, F f) {
+    const int64_t groups = m.hidden / (m.f32 ? 4 : 8);
+    auto km = [&](auto tpt) -> cudaError_t {
+        if (m.topk <= 1) return f(tpt, std::integral_constant<int, 1>{});
+        if (m.topk <= 2) return f(tpt, std::integral_constant<int, 2>{});
+        if (m.topk <= 4) return f(tpt, std::integral_constant<int, 4>{});
+        if (m.topk <= 6) return f(tpt, std::integral_constant<int, 6>{});
+        return f(tpt, std::integral_constant<int, 8>{});
+    };
+    if (groups <= 32 * per_lane) return km(std::integral_constant<int, 32>{});
+    if (groups <= 128 * per_lane) return km(std::integral_constant<int, 128>{});
+    return km(std::integral_constant<int, 256>{});
 }
 
-template <typename T, bool VECTOR>
-cudaError_t combine_rows(const RowArgs &a, cudaStream_t s) {
-    return narrow(a.m, VECTOR) ? launch_rows<moe_combine_kernel<T, VECTOR, 32>, 32>(a, false, s)
-                               : launch_rows<moe_combine_kernel<T, VECTOR, 256>, 256>(a, false, s);
+template <typename T>
+cudaError_t dispatch_rows(const RowArgs &a, bool vec, cudaStream_t s) {
+    return with_team(a.m, vec ? 4 : 1, [&](auto tpt, auto km) {
+        constexpr int TPT = decltype(tpt)::value, KM = decltype(km)::value;
+        if (vec)
+            return a.outq != nullptr
+                       ? launch_rows<moe_dispatch_kernel<T, true, TPT, KM>, TPT>(a, true, s)
+                       : launch_rows<moe_dispatch_kernel<T, false, TPT, KM>, TPT>(a, true, s);
+        return a.outq != nullptr ? launch_rows<moe_dispatch_any_kernel<T, true, TPT, (KM > 4 ? 4 : KM)>, TPT>(a, true, s)
+                                 : launch_rows<moe_dispatch_any_kernel<T, false, TPT, (KM > 4 ? 4 : KM)>, TPT>(a, true, s);
+    });
 }
 
-template <typename T, bool VECTOR>
-cudaError_t combine_bwd_rows(const RowArgs &a, cudaStream_t s) {
-    return narrow(a.m, VECTOR)
-               ? launch_rows<moe_combine_bwd_kernel<T, VECTOR, 32>, 32>(a, true, s)
-               : launch_rows<moe_combine_bwd_kernel<T, VECTOR, 256>, 256>(a, true, s);
+template <typename T>
+cudaError_t combine_rows(const RowArgs &a, bool vec, cudaStream_t s) {
+    return with_team(a.m, vec ? 2 : 1, [&](auto tpt, auto km) {
+        constexpr int TPT = decltype(tpt)::value, KM = decltype(km)::value;
+        return vec ? launch_rows<moe_combine_kernel<T, TPT, KM>, TPT>(a, false, s)
+                   : launch_rows<moe_combine_any_kernel<T, TPT, KM>, TPT>(a, false, s);
+    });
+}
+
+template <typename T>
+cudaError_t combine_bwd_rows(const RowArgs &a, bool vec, cudaStream_t s) {
+    return with_team(a.m, vec ? 4 : 1, [&](auto tpt, auto km) {
+        constexpr int TPT = decltype(tpt)::value, KM = decltype(km)::value;
+        return vec ? launch_rows<moe_combine_bwd_kernel<T, TPT, KM>, TPT>(a, true, s)
+                   : launch_rows<moe_combine_bwd_any_kernel<T, TPT, (KM > 2 ? 2 : KM)>, TPT>(a, true, s);
+    });
 }
 
 }  // namespace
@@ -393,30 +817,39 @@ cudaError_t combine_bwd_rows(const RowArgs &a, cudaStream_t s) {
 cudaError_t launch_moe_sort(const void *ids, int ids_64, int64_t n, int experts, int64_t multiple,
                             int64_t capacity, int32_t *row_of, int32_t *source, int32_t *offsets,
                             int32_t *counts, int32_t *workspace, cudaStream_t s) {
-    // chunks of a multiple of the block's threads, at most kMoeMaxChunks
-    int64_t chunk = kMoeMinChunk;
-    if ((n + chunk - 1) / chunk > kMoeMaxChunks)
+    // chunks of a multiple of the block's threads, at most kMoeMaxChunks, as
+    // small as that allows so that more SMs share the work
+    int64_t chunk = kSortFew * kSortThreads;
+    if (n > kMoeMaxChunks * chunk) chunk = kSortMany * kSortThreads;
+    if (n > kMoeMaxChunks * chunk)
         chunk = ((n + kMoeMaxChunks - 1) / kMoeMaxChunks + kSortThreads - 1) / kSortThreads *
                 kSortThreads;
     SortArgs a = {ids, n, chunk, capacity, multiple, experts, 0, row_of, source, offsets, counts,
                   workspace};
     a.chunks = n > 0 ? (int)((n + chunk - 1) / chunk) : 1;
     const size_t hist = (size_t)kSortWarps * experts * sizeof(int32_t);
-    const size_t all = hist + (size_t)(2 * experts + 1) * sizeof(int32_t);
-    void (*count)(SortArgs) = ids_64 ? moe_count_kernel<int64_t> : moe_count_kernel<int32_t>;
-    void (*place)(SortArgs) = ids_64 ? moe_place_kernel<int64_t> : moe_place_kernel<int32_t>;
-    cudaError_t e;
-    if (all > 48 * 1024) {
-        e = cudaFuncSetAttribute(count, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)hist);
-        if (e != cudaSuccess) return e;
-        e = cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)all);
-        if (e != cudaSuccess) return e;
-    }
-    if (a.chunks > 1) {
-        e = launch_pdl(count, a.chunks, kSortThreads, hist, s, a);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_pdl(place, a.chunks, kSortThreads, all, s, a);
+    const size_t all = hist + (size_t)(3 * experts + 1) * sizeof(int32_t);
+    auto run = [&](auto count, auto place) -> cudaError_t {
+        cudaError_t e;
+        if (all > 48 * 1024) {
+            e = cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)all);
+            if (e != cudaSuccess) return e;
+        }
+        if (a.chunks > 1) {
+            e = launch_pdl(count, a.chunks, kSortThreads, experts * sizeof(int32_t), s, a);
+            if (e != cudaSuccess) return e;
+        }
+        return launch_pdl(place, a.chunks, kSortThreads, all, s, a);
+    };
+    auto pick = [&](auto id) -> cudaError_t {
+        using ID = decltype(id);
+        if (chunk == kSortFew * kSortThreads)
+            return run(moe_count_kernel<ID, kSortFew>, moe_place_kernel<ID, kSortFew>);
+        if (chunk == kSortMany * kSortThreads)
+            return run(moe_count_kernel<ID, kSortMany>, moe_place_kernel<ID, kSortMany>);
+        return run(moe_count_kernel<ID, 0>, moe_place_kernel<ID, 0>);
+    };
+    return ids_64 ? pick(int64_t{}) : pick(int32_t{});
 }
 
 cudaError_t launch_moe_dispatch(const MoeRows &m, const void *x, int64_t ldx, void *out,
@@ -433,8 +866,7 @@ cudaError_t launch_moe_dispatch(const MoeRows &m, const void *x, int64_t ldx, vo
     a.out = out, a.outq = outq, a.scale_inv = scale_inv, a.amax = amax;
     const bool vec = row_vectors(x, ldx, m.hidden, m.f32 ? 4 : 2) &&
                      aligned_to(outq != nullptr ? outq : out, outq != nullptr ? (m.f32 ? 4 : 8) : 16);
-    if (m.f32) return vec ? dispatch_rows<float, true>(a, s) : dispatch_rows<float, false>(a, s);
-    return vec ? dispatch_rows<uint16_t, true>(a, s) : dispatch_rows<uint16_t, false>(a, s);
+    return m.f32 ? dispatch_rows<float>(a, vec, s) : dispatch_rows<uint16_t>(a, vec, s);
 }
 
 cudaError_t launch_moe_combine(const MoeRows &m, const void *rows, int64_t ldr,
@@ -444,8 +876,7 @@ cudaError_t launch_moe_combine(const MoeRows &m, const void *rows, int64_t ldr,
     a.m = m;
     a.rows = rows, a.ldr = ldr, a.weights = weights, a.out = y;
     const bool vec = row_vectors(rows, ldr, m.hidden, m.f32 ? 4 : 2) && aligned_to(y, 16);
-    if (m.f32) return vec ? combine_rows<float, true>(a, s) : combine_rows<float, false>(a, s);
-    return vec ? combine_rows<uint16_t, true>(a, s) : combine_rows<uint16_t, false>(a, s);
+    return m.f32 ? combine_rows<float>(a, vec, s) : combine_rows<uint16_t>(a, vec, s);
 }
 
 cudaError_t launch_moe_combine_backward(const MoeRows &m, const void *dy, int64_t lddy,
@@ -460,9 +891,7 @@ cudaError_t launch_moe_combine_backward(const MoeRows &m, const void *dy, int64_
     const int es = m.f32 ? 4 : 2;
     const bool vec = row_vectors(dy, lddy, m.hidden, es) && row_vectors(rows, ldr, m.hidden, es) &&
                      aligned_to(drows, 16);
-    if (m.f32)
-        return vec ? combine_bwd_rows<float, true>(a, s) : combine_bwd_rows<float, false>(a, s);
-    return vec ? combine_bwd_rows<uint16_t, true>(a, s) : combine_bwd_rows<uint16_t, false>(a, s);
+    return m.f32 ? combine_bwd_rows<float>(a, vec, s) : combine_bwd_rows<uint16_t>(a, vec, s);
 }
 
 }  // namespace fp8

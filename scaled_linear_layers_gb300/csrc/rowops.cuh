@@ -88,6 +88,43 @@ struct RowVec<T, false> {
     }
 };
 
+// 16-byte groups of a row from an address aligned only to its elements: two
+// aligned loads each, shifted together.  Group g reads the aligned 16 bytes
+// that hold its first and its last element and nothing else.
+template <typename T>
+struct ShiftedRow {
+    using Raw = typename RowVec<T, true>::Raw;
+    const uint8_t *at;
+    uint32_t shift, second;  // bytes into the aligned 16; to the second load
+
+    __device__ __forceinline__ ShiftedRow() {}
+    __device__ __forceinline__ explicit ShiftedRow(const T *p) {
+        shift = (uint32_t)reinterpret_cast<uintptr_t>(p) & 15u;
+        at = reinterpret_cast<const uint8_t *>(p) - shift;
+        second = shift ? 16 : 0;
+    }
+
+    __device__ __forceinline__ Raw load(int64_t g) const {
+        const uint8_t *a = at + 16 * g;
+        const uint4 q0 = *reinterpret_cast<const uint4 *>(a);
+        const uint4 q1 = *reinterpret_cast<const uint4 *>(a + second);
+        uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = shift & 8u ? w[i + 2] : w[i];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = shift & 4u ? w[i + 1] : w[i];
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (shift & 3u) * 8u);
+        }
+        Raw r;
+        uint32_t *rw = reinterpret_cast<uint32_t *>(&r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rw[i] = w[i];
+        return r;
+    }
+};
+
 // Two fp32 values in one 64-bit register, and arithmetic on both in one
 // instruction (each lane rounds as the single one does).
 __device__ __forceinline__ uint64_t pair_of(float a, float b) {
