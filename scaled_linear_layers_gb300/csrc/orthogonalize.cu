@@ -31,6 +31,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -63,9 +64,12 @@ struct PrepArgs {
     int parts;
     int tx;            // threads along a row (a power of two)
     __half *hi, *lo;   // [batch][rows][ldx]
+    uint32_t *flags;   // [batch][flags_per], cleared for the products' launch
+    int flags_per;
 };
 
 constexpr int kPrepThreads = 256;
+constexpr int kPrepRows = 4;  // rows whose loads a thread has in flight together
 
 template <typename T, bool VECTOR>
 __global__ void __launch_bounds__(kPrepThreads) ns_square_kernel(const PrepArgs a) {
@@ -74,20 +78,30 @@ __global__ void __launch_bounds__(kPrepThreads) ns_square_kernel(const PrepArgs 
     __shared__ float red[3 * kPrepThreads / 32];
     pdl_wait_prior();
     pdl_allow_next();
+    for (int i = blockIdx.x * kPrepThreads + threadIdx.x; i < a.flags_per; i += gridDim.x * kPrepThreads)
+        a.flags[(int64_t)blockIdx.y * a.flags_per + i] = 0;
     const T *g = reinterpret_cast<const T *>(a.g) + blockIdx.y * a.bsg;
     const int ty = kPrepThreads / a.tx;
     float s[3] = {0.f, 0.f, 0.f};
+    const int64_t step = (int64_t)a.parts * ty;
     for (int64_t r = (int64_t)blockIdx.x * ty + threadIdx.x / a.tx; r < a.rows;
-         r += (int64_t)a.parts * ty)
+         r += kPrepRows * step)
         for (int c = (threadIdx.x & (a.tx - 1)) * V; c < a.cols; c += a.tx * V) {
-            float f[V];
-            RV::unpack(RV::load(g + r * a.ldg + c), f);
+            typename RV::Raw raw[kPrepRows];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float b = f[i] * 0x1p-64f, l = f[i] * 0x1p64f;
-                s[0] = fmaf(f[i], f[i], s[0]);
-                s[1] = fmaf(b, b, s[1]);
-                s[2] = fmaf(l, l, s[2]);
+            for (int u = 0; u < kPrepRows; ++u)
+                raw[u] = r + u * step < a.rows ? RV::load(g + (r + u * step) * a.ldg + c) : RV::zero();
+#pragma unroll
+            for (int u = 0; u < kPrepRows; ++u) {
+                float f[V];
+                RV::unpack(raw[u], f);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float b = f[i] * 0x1p-64f, l = f[i] * 0x1p64f;
+                    s[0] = fmaf(f[i], f[i], s[0]);
+                    s[1] = fmaf(b, b, s[1]);
+                    s[2] = fmaf(l, l, s[2]);
+                }
             }
         }
     row_sum<kPrepThreads, 3>(s, red);
@@ -121,58 +135,96 @@ __global__ void __launch_bounds__(kPrepThreads) ns_scale_kernel(const PrepArgs a
     const T *g = reinterpret_cast<const T *>(a.g) + blockIdx.y * a.bsg;
     const int64_t at = (int64_t)blockIdx.y * a.rows;
     const int ty = kPrepThreads / a.tx;
+    const int64_t step = (int64_t)a.parts * ty;
     for (int64_t r = (int64_t)blockIdx.x * ty + threadIdx.x / a.tx; r < a.rows;
-         r += (int64_t)gridDim.x * ty)
+         r += kPrepRows * step)
         for (int c = (threadIdx.x & (a.tx - 1)) * V; c < a.cols; c += a.tx * V) {
-            float f[V];
-            RV::unpack(RV::load(g + r * a.ldg + c), f);
-            struct alignas(2 * V) Halves {
-                __half v[V];
-            } hi, lo;
+            typename RV::Raw raw[kPrepRows];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float x = (f[i] * pre) * mul;
-                hi.v[i] = __float2half_rn(x);
-                lo.v[i] = __float2half_rn((x - __half2float(hi.v[i])) * kLoScale);
+            for (int u = 0; u < kPrepRows; ++u)
+                raw[u] = r + u * step < a.rows ? RV::load(g + (r + u * step) * a.ldg + c) : RV::zero();
+#pragma unroll
+            for (int u = 0; u < kPrepRows; ++u) {
+                if (r + u * step >= a.rows) continue;
+                float f[V];
+                RV::unpack(raw[u], f);
+                struct alignas(2 * V) Halves {
+                    __half v[V];
+                } hi, lo;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float x = (f[i] * pre) * mul;
+                    hi.v[i] = __float2half_rn(x);
+                    lo.v[i] = __float2half_rn((x - __half2float(hi.v[i])) * kLoScale);
+                }
+                const int64_t o = (at + r + u * step) * a.ldx + c;
+                *reinterpret_cast<Halves *>(a.hi + o) = hi;
+                *reinterpret_cast<Halves *>(a.lo + o) = lo;
             }
-            const int64_t o = (at + r) * a.ldx + c;
-            *reinterpret_cast<Halves *>(a.hi + o) = hi;
-            *reinterpret_cast<Halves *>(a.lo + o) = lo;
         }
 }
 
 // ---------------------------------------------------------------- products ---
+//
+// All steps' products run in one launch whose CTAs (pairs of CTAs on large
+// matrices) stay resident and walk one list of output tiles: step by step the
+// tiles of A, of B and of the new X.  A tile may start before the ones that it
+// reads are all done: tiles announce themselves by counters in memory, and the
+// thread that loads a tile's operands waits, 128 or 256 columns of the
+// contraction at a time, for just the tiles those columns come from.  The list
+// is in the order in which the next product consumes its operand (A and B
+// column by column of the lower triangle, X along its longer side), so the
+// waits are short, no CTA idles while a product's last tiles finish (a launch
+// per product left 2 waves where 1.8 were full), and a product costs no launch.
+// Every tile only waits for tiles earlier in the list, all CTAs are resident
+// (a cooperative launch), and every wait is bounded.
+//
+// Reuse of a buffer needs no wait of its own: a tile of the next step's A is
+// written only after its operands, all of a row panel of the new X, are there,
+// which themselves needed every B tile, and so every read of A, of that panel;
+// likewise B, and X, which has two buffers.
 
-enum NsMode { kGram, kPoly, kUpdate };
+enum NsPhase { kGram, kPoly, kUpdate };
 
-struct NsArgs {
-    int M, N, K;
-    int m_tiles, n_tiles, tiles_per, tiles;  // per matrix, over the batch
-    float acc_mul;                           // output = acc_mul * acc + ...
-    float e_mul;                             //   e_mul * (E + lo 2^-11)
-    float diag;                              //   + diag on the diagonal
-    const __half *e, *e_lo;                  // [batch][M][lde]; e_lo nullable
-    int64_t lde, bse;
-    int last;                                // the output is bf16
-    uint16_t *direct;                        // bf16 output without a tensor map (nullable)
-    int write_lo;
+constexpr int kMaxSteps = 64;
+
+struct NsPlan {
+    // geometry (tiles of BT x BT)
+    int rows, cols, batch, steps, tall;
+    int T, U;                  // tiles along the shorter and the longer side
+    int tri, upd;              // tiles of a symmetric product and of X, per matrix
+    int per_step, tiles;       // over the batch; over all steps
+    // memory
+    uint16_t *direct;          // bf16 output without a tensor map (nullable)
+    uint32_t *flags;           // per matrix: A, B tiles, X tiles, three totals
+    int flags_per;
+    // arithmetic: step i has coefficients (a, b, c) at 3 i
+    float coefficients[3 * kMaxSteps];
+    float scale;
     uint64_t wait_limit_ns;
     unsigned int *status;
+};
+
+struct NsMaps {
+    // operands: boxes of 64 columns x 128 rows where the columns are
+    // contracted; where the rows are (xm), 64 rows x 2 groups of 64 columns
+    CUtensorMap x[2], xm[2], a, b;
+    CUtensorMap dx[2], dlo[2], da, db, dout;   // outputs: boxes of 32 x 32
 };
 
 constexpr int NS_EPI_WARPS = 8;                // two to each quarter of the lanes
 constexpr int NS_THREADS = 64 + 32 * NS_EPI_WARPS;
 constexpr int NS_BOX = 2048;                   // a 32 x 32 box of 2-byte outputs
-constexpr int NS_STAGING = NS_EPI_WARPS * 2 * NS_BOX;  // an output and a second one
+constexpr int NS_STAGING = NS_EPI_WARPS * 4 * NS_BOX;  // two that come in, two that go out
 constexpr int NS_OPERAND = 128 * 128;          // 128 rows of 64 fp16
 constexpr int NS_STAGE = 2 * NS_OPERAND;
-constexpr int NS_STAGES = 6;
+constexpr int NS_STAGES = 5;
 constexpr size_t NS_SMEM = 1024 + (size_t)NS_STAGES * NS_STAGE + 1024 + NS_STAGING;
 static_assert(NS_SMEM <= 227 * 1024, "shared memory");
 
 // Instruction descriptor, kind::f16: D fp32, A and B fp16; bits 15 / 16 set
 // for an operand whose M (N) dim is the contiguous one.
-constexpr uint32_t idesc_f16_f32(uint32_t m, uint32_t n, bool a_mn, bool b_mn) {
+__host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t m, uint32_t n, bool a_mn, bool b_mn) {
     return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) |
            ((m >> 4) << 24);
 }
@@ -205,20 +257,22 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a, uint64_t b,
             : "memory");
 }
 
+// A box at (x, y) of matrix z into shared memory at dst, completing on the
+// leader's barrier.
 template <int CG>
-__device__ __forceinline__ void ns_load(void *dst, const void *tmap, uint64_t *bar,
-                                        uint32_t leader_bar, int x, int y, int z) {
+__device__ __forceinline__ void ns_load(uint32_t dst, const void *tmap, uint32_t bar, int x, int y,
+                                        int z) {
     if constexpr (CG == 2)
         asm volatile(
             "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::"
-            "bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-            "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(leader_bar)
+            "bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
             : "memory");
     else
         asm volatile(
             "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-            "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
             : "memory");
 }
 
@@ -230,20 +284,86 @@ __device__ __forceinline__ void ns_store(const void *tmap, uint32_t src, int x, 
         : "memory");
 }
 
-// Tile index -> matrix, row tile, column tile.  Symmetric products walk the
-// tiles with tn <= tm, row by row.
-template <bool SYM>
-__device__ __forceinline__ void ns_locate(const NsArgs &p, int tile, int &z, int &tm, int &tn) {
-    z = tile / p.tiles_per;
-    const int t = tile - z * p.tiles_per;
-    if constexpr (SYM) {
-        tm = (int)((sqrtf(8.f * (float)t + 1.f) - 1.f) * 0.5f);
-        while ((tm + 1) * (tm + 2) / 2 <= t) ++tm;
-        while (tm * (tm + 1) / 2 > t) --tm;
-        tn = t - tm * (tm + 1) / 2;
-    } else {
-        grouped_tile(t, p.m_tiles, p.n_tiles, 8 / 2, tm, tn);
+// Orders this thread's accesses by the usual path with its bulk copies'.
+__device__ __forceinline__ void fence_proxy_async_all() {
+    asm volatile("fence.proxy.async;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t load_acquire(const uint32_t *p) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+// Waits until *p >= target; false (and the status word set) when the limit
+// runs out or another thread of the block gave up.
+__device__ __forceinline__ bool flag_wait_bounded(const uint32_t *p, uint32_t target,
+                                                  volatile int *abort, uint64_t limit_ns,
+                                                  unsigned int *status) {
+    if (load_acquire(p) >= target) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (load_acquire(p) >= target) return true;
+        if ((i & 63u) == 0) {
+            if (*abort) return false;
+            if (global_timer_ns() - t0 > limit_ns) {
+                *abort = 1;
+                atomicOr(status, kStatusTimeoutBarrier);
+                return false;
+            }
+        }
     }
+}
+
+// A tile of the list.  r, c: its place in A or B (r >= c), or in X with c
+// along the shorter and r along the longer side.
+struct NsTile {
+    int step, phase, z, r, c;
+    int tm, tn;  // row and column tile of the output
+};
+
+__device__ __forceinline__ NsTile ns_locate(const NsPlan &p, int i) {
+    NsTile t;
+    t.step = i / p.per_step;
+    int k = i - t.step * p.per_step;
+    const int tri_all = p.tri * p.batch;
+    t.phase = k < tri_all ? kGram : k < 2 * tri_all ? kPoly : kUpdate;
+    if (t.phase == kUpdate) {
+        k -= 2 * tri_all;
+        t.z = k / p.upd;
+        k -= t.z * p.upd;
+        t.r = k / p.T;
+        t.c = k - t.r * p.T;
+        t.tm = p.tall ? t.r : t.c;
+        t.tn = p.tall ? t.c : t.r;
+    } else {
+        k -= t.phase * tri_all;
+        t.z = k / p.tri;
+        // column by column: counted from the end, row by row of the mirrored
+        // triangle
+        const int u = p.tri - 1 - (k - t.z * p.tri);
+        int q = (int)((sqrtf(8.f * (float)u + 1.f) - 1.f) * 0.5f);
+        while ((q + 1) * (q + 2) / 2 <= u) ++q;
+        while (q * (q + 1) / 2 > u) --q;
+        t.c = p.T - 1 - q;
+        t.r = p.T - 1 - (u - q * (q + 1) / 2);
+        t.tm = t.r;
+        t.tn = t.c;
+    }
+    return t;
+}
+
+// The counters: of a tile of A or B at rows r and column c (in either order),
+// of a tile of X, and of all tiles of A, B or X of a matrix.
+__device__ __forceinline__ uint32_t *sym_flag(const NsPlan &p, int z, int phase, int r, int c) {
+    const int hi = max(r, c), lo = min(r, c);
+    return p.flags + (int64_t)z * p.flags_per + phase * p.tri + hi * (hi + 1) / 2 + lo;
+}
+__device__ __forceinline__ uint32_t *x_flag(const NsPlan &p, int z, int r, int c) {
+    return p.flags + (int64_t)z * p.flags_per + 2 * p.tri + r * p.T + c;
+}
+__device__ __forceinline__ uint32_t *total_flag(const NsPlan &p, int z, int phase) {
+    return p.flags + (int64_t)z * p.flags_per + 2 * p.tri + p.upd + phase;
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
@@ -255,35 +375,127 @@ __device__ __forceinline__ float2 half2_floats(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
-// D = A·Bᵀ tiles of 128*CG x BN by one CTA (CG = 1) or a pair on two SMs
-// (CG = 2): warp 0 loads, warp 1 issues the MMAs, the others write the output
-// from the other of two accumulators.  A_MN / B_MN: the operand's M (N) dim,
-// not K, is contiguous in memory.
-template <int CG, int BN, bool A_MN, bool B_MN, int MODE>
-__device__ __forceinline__ void ns_gemm_body(const CUtensorMap &tma_a, const CUtensorMap &tma_b,
-                                             const CUtensorMap &tma_d, const CUtensorMap &tma_lo,
-                                             const NsArgs &p) {
-    constexpr bool SYM = MODE != kUpdate;
-    constexpr int BM = 128 * CG, BNH = BN / CG;
-    static_assert(!SYM || BM == BN, "a symmetric product takes square tiles");
-    constexpr uint32_t TMEM_COLS = 256 * CG;  // two accumulators
-    constexpr uint32_t IDESC = idesc_f16_f32(BM, BN, A_MN, B_MN);
-    // an N-contiguous B is loaded 128 columns wide whatever BN is
-    constexpr uint32_t STAGE_TX = NS_OPERAND + (B_MN ? NS_OPERAND : BNH * 128);
+// A stage of an operand: 128 rows of M (N) x 64 of K from (row, k) on.
+template <int CG, bool MN>
+__device__ __forceinline__ void ns_load_operand(uint32_t dst, const CUtensorMap *map, uint32_t bar,
+                                                int row, int k, int z) {
+    if constexpr (!MN)
+        ns_load<CG>(dst, map, bar, k, row, z);
+    else if constexpr (CG == 2)
+        asm volatile(
+            "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::"
+            "bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(k), "r"(row / 64), "r"(z), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(k), "r"(row / 64), "r"(z), "r"(bar)
+            : "memory");
+}
+
+// The ring of operand stages as the thread that fills it or drains it sees it.
+struct NsRing {
+    uint64_t *full, *empty;
+    int stage;
+    uint32_t phase;
+    __device__ __forceinline__ void next() {
+        if (++stage == NS_STAGES) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+// Loads blocks kb to end - 1 of a tile's operands.  One loop for each kind of
+// operands: deciding inside it cost the loading thread so long (430 ns a block
+// instead of 290) that it, not the tensor cores, set the pace.
+template <int CG, bool A_MN, bool B_MN>
+__device__ __forceinline__ bool ns_fill(NsRing &ring, uint32_t a0, uint32_t b0,
+                                        const CUtensorMap *ma, const CUtensorMap *mb, int arow,
+                                        int brow, int z, int kb, int end, uint32_t rank,
+                                        volatile int *abort_flag, const NsPlan &p) {
+#pragma unroll 1
+    for (; kb < end; ++kb) {
+        if (!mbar_wait_bounded(&ring.empty[ring.stage], ring.phase ^ 1u, abort_flag,
+                               p.wait_limit_ns, kStatusTimeoutTma, p.status))
+            return false;
+        uint64_t *full = &ring.full[ring.stage];
+        if (rank == 0) mbar_arrive_expect_tx(full, CG * NS_STAGE);
+        const uint32_t bar = CG == 2 ? mapa_shared(smem_u32(full), 0) : smem_u32(full);
+        const uint32_t at = ring.stage * NS_OPERAND;
+        ns_load_operand<CG, A_MN>(a0 + at, ma, bar, arow, kb * 64, z);
+        ns_load_operand<CG, B_MN>(b0 + at, mb, bar, brow, kb * 64, z);
+        ring.next();
+    }
+    return true;
+}
+
+// Issues a tile's MMAs: blocks of 64 of K, two to a round, since this single
+// thread's path between two waits paces the tensor pipe.
+template <int CG, bool A_MN, bool B_MN>
+__device__ __forceinline__ bool ns_mma_tile(NsRing &ring, uint32_t a0, uint32_t b0, uint32_t d_tmem,
+                                            int nk, volatile int *abort_flag, const NsPlan &p) {
+    constexpr uint32_t IDESC = idesc_f16_f32(128 * CG, 128 * CG, A_MN, B_MN);
+    constexpr int A_STEP = (A_MN ? 2048 : 32) >> 4, B_STEP = (B_MN ? 2048 : 32) >> 4;
+    const uint64_t a_desc0 = A_MN ? smem_desc_mn128(a0) : smem_desc_sw128(a0);
+    const uint64_t b_desc0 = B_MN ? smem_desc_mn128(b0) : smem_desc_sw128(b0);
+    int kb = 0;
+    auto round = [&](auto count) -> bool {
+        constexpr int NB = decltype(count)::value;
+        NsRing look = ring;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            if (!mbar_wait_bounded(&look.full[look.stage], look.phase, abort_flag, p.wait_limit_ns,
+                                   kStatusTimeoutMma, p.status))
+                return false;
+            look.next();
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const uint64_t off = (uint64_t)((ring.stage * NS_OPERAND) >> 4);
+            const uint64_t ad = a_desc0 + off, bd = b_desc0 + off;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mma_f16<CG>(d_tmem, ad + (uint64_t)(k * A_STEP), bd + (uint64_t)(k * B_STEP), IDESC,
+                            ((kb + b) | k) != 0);
+            if constexpr (CG == 2) mma_commit_pair(&ring.empty[ring.stage], 0x3);
+            else mma_commit(&ring.empty[ring.stage]);
+            ring.next();
+        }
+        kb += NB;
+        return true;
+    };
+    while (kb + 2 <= nk)
+        if (!round(std::integral_constant<int, 2>{})) return false;
+    if (kb < nk) return round(std::integral_constant<int, 1>{});
+    return true;
+}
+
+// Warp 0 loads, warp 1 issues the MMAs, the others write the output from the
+// other of two accumulators.
+template <int CG>
+__device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
+    constexpr int BT = 128 * CG;
+    constexpr uint32_t TMEM_COLS = 2 * BT;
+    constexpr uint32_t ARRIVALS = NS_EPI_WARPS * CG;  // that complete a tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~uintptr_t(1023));
     uint8_t *sA = smem, *sB = smem + NS_STAGES * NS_OPERAND;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + NS_STAGES * NS_STAGE);
     uint64_t *full = bars, *empty = bars + NS_STAGES, *tfull = bars + 2 * NS_STAGES;
-    uint64_t *tempty = tfull + 2, *drain = tempty + 2;
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
+    uint64_t *tempty = tfull + 2, *drain = tempty + 2, *ebars = drain + 1;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(ebars + NS_EPI_WARPS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     uint8_t *staging = smem + NS_STAGES * NS_STAGE + 1024;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
     const int worker = blockIdx.x / CG, workers = gridDim.x / CG;
+    const int S = p.tall ? p.cols : p.rows, L = p.tall ? p.rows : p.cols;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS_STAGES; ++s) {
@@ -295,12 +507,13 @@ __device__ __forceinline__ void ns_gemm_body(const CUtensorMap &tma_a, const CUt
             mbar_init(&tempty[a], NS_EPI_WARPS * CG);
         }
         mbar_init(drain, 1);
+        for (int w = 0; w < NS_EPI_WARPS; ++w) mbar_init(&ebars[w], 1);
         *abort_flag = 0;
         fence_mbarrier_init();
-        tma_prefetch_desc(&tma_a);
-        tma_prefetch_desc(&tma_b);
-        tma_prefetch_desc(&tma_d);
-        tma_prefetch_desc(&tma_lo);
+        tma_prefetch_desc(&maps.x[0]);
+        tma_prefetch_desc(&maps.x[1]);
+        tma_prefetch_desc(&maps.a);
+        tma_prefetch_desc(&maps.b);
     }
     if (warp == 1) {
         if constexpr (CG == 2) {
@@ -316,95 +529,140 @@ __device__ __forceinline__ void ns_gemm_body(const CUtensorMap &tma_a, const CUt
     else __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
-    pdl_wait_prior();
-    pdl_allow_next();
 
-    const int nk = (p.K + 63) / 64;
+    // Contraction of a phase, in blocks of 64.  Which operands have M (N), not
+    // K, contiguous: A = X Xᵀ contracts X's columns: neither (tall: XᵀX, its
+    // rows: both); B X contracts the rows of X: the second (tall, X B: neither);
+    // A and B are their own transposes.
+    auto blocks = [&](int phase) { return ((phase == kGram ? L : S) + 63) / 64; };
+
     if (warp == 0) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int tile = worker; tile < p.tiles && ok; tile += workers) {
-                int z, tm, tn;
-                ns_locate<SYM>(p, tile, z, tm, tn);
-                const int arow = tm * BM + (int)rank * 128, brow = tn * BN + (int)rank * BNH;
-                for (int kb = 0; kb < nk; ++kb) {
-                    if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, p.wait_limit_ns,
-                                           kStatusTimeoutTma, p.status)) {
-                        ok = false;
-                        break;
-                    }
-                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * STAGE_TX);
-                    const uint32_t lead = CG == 2 ? mapa_shared(smem_u32(&full[stage]), 0) : 0u;
-                    uint8_t *da = sA + stage * NS_OPERAND, *db = sB + stage * NS_OPERAND;
-                    if constexpr (A_MN) {
-                        ns_load<CG>(da, &tma_a, &full[stage], lead, arow, kb * 64, z);
-                        ns_load<CG>(da + 8192, &tma_a, &full[stage], lead, arow + 64, kb * 64, z);
-                    } else {
-                        ns_load<CG>(da, &tma_a, &full[stage], lead, kb * 64, arow, z);
-                    }
-                    if constexpr (B_MN) {
-                        ns_load<CG>(db, &tma_b, &full[stage], lead, brow, kb * 64, z);
-                        ns_load<CG>(db + 8192, &tma_b, &full[stage], lead, brow + 64, kb * 64, z);
-                    } else {
-                        ns_load<CG>(db, &tma_b, &full[stage], lead, kb * 64, brow, z);
-                    }
-                    if (++stage == NS_STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
+        // ------------------------------------------------------- TMA producer
+        // The warp looks at the counters together, 32 panels of the
+        // contraction at a time; its first lane loads.
+        constexpr int PANEL = BT / 64;
+        NsRing ring = {full, empty, 0, 0};
+        bool ok = true;
+        for (int i = worker; i < p.tiles && ok; i += workers) {
+            const NsTile t = ns_locate(p, i);
+            const int cur = t.step & 1;
+            const CUtensorMap *ma, *mb;
+            if (t.phase == kGram) {
+                ma = mb = p.tall ? &maps.xm[cur] : &maps.x[cur];
+            } else if (t.phase == kPoly) {
+                ma = mb = &maps.a;
+            } else {
+                ma = p.tall ? &maps.x[cur] : &maps.b;
+                mb = p.tall ? &maps.b : &maps.xm[cur];
             }
-            if (!ok && rank == 0) {
-                // wait (bounded) for the copies in flight before teardown
-                for (int s = 0; s < NS_STAGES; ++s) {
-                    stage = stage == 0 ? NS_STAGES - 1 : stage - 1;
-                    if (stage == NS_STAGES - 1) phase ^= 1u;
-                    volatile int no_abort = 0;
-                    mbar_wait_bounded(&full[stage], phase, &no_abort, 10000000ull,
-                                      kStatusTimeoutTma, p.status);
+            const int arow = t.tm * BT + (int)rank * 128, brow = t.tn * BT + (int)rank * 128;
+            // what the operands come from: A from step's X, B from its A, the
+            // new X from its B; the first X is there already
+            const int source = t.phase == kGram ? kUpdate : t.phase - 1;
+            const uint32_t done = (uint32_t)(t.phase == kGram ? t.step : t.step + 1) * ARRIVALS;
+            const int nk = blocks(t.phase), panels = (nk + PANEL - 1) / PANEL;
+            int there = 0;  // panels known to be complete
+            if (done == 0) {
+                there = panels;
+            } else {
+                const uint32_t all = done * (uint32_t)(source == kUpdate ? p.upd : p.tri);
+                if (load_acquire(total_flag(p, t.z, source)) >= all) there = panels;
+                __syncwarp();
+                fence_proxy_async_all();
+            }
+            for (int kp = 0; kp < panels && ok; ++kp) {
+                if (kp >= there) {
+                    const int mine = kp + lane;
+                    const uint32_t *f0 = nullptr, *f1 = nullptr;
+                    if (mine < panels) {
+                        if (t.phase == kGram) {
+                            f0 = x_flag(p, t.z, mine, t.tm);
+                            f1 = x_flag(p, t.z, mine, t.tn);
+                        } else if (t.phase == kPoly) {
+                            f0 = sym_flag(p, t.z, kGram, t.tm, mine);
+                            f1 = sym_flag(p, t.z, kGram, t.tn, mine);
+                        } else {
+                            f0 = f1 = sym_flag(p, t.z, kPoly, t.c, mine);
+                        }
+                    }
+                    uint64_t t0 = 0;
+                    for (uint32_t turn = 0;; ++turn) {
+                        const bool have =
+                            f0 != nullptr && load_acquire(f0) >= done && load_acquire(f1) >= done;
+                        const uint32_t got = __ballot_sync(0xFFFFFFFFu, have);
+                        const int run = __ffs(~got) == 0 ? 32 : __ffs(~got) - 1;
+                        there = kp + run;
+                        if (run > 0) break;
+                        if ((turn & 63u) == 0) {
+                            const uint64_t now = global_timer_ns();
+                            if (turn == 0) t0 = now;
+                            const bool late = now - t0 > p.wait_limit_ns;
+                            if (__any_sync(0xFFFFFFFFu, late || *abort_flag != 0)) {
+                                if (lane == 0 && *abort_flag == 0) {
+                                    *abort_flag = 1;
+                                    atomicOr(p.status, kStatusTimeoutBarrier);
+                                }
+                                ok = false;
+                                break;
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    fence_proxy_async_all();
+                    if (!ok) break;
                 }
+                // up to the next panel that has to be looked at
+                const int next = kp + 1 > there ? kp + 1 : there;
+                if (lane == 0) {
+                    const int kb = kp * PANEL, end = min(nk, next * PANEL);
+                    const uint32_t a0 = smem_u32(sA), b0 = smem_u32(sB);
+                    if (t.phase == kGram && p.tall)
+                        ok = ns_fill<CG, true, true>(ring, a0, b0, ma, mb, arow, brow, t.z, kb, end,
+                                                     rank, abort_flag, p);
+                    else if (t.phase == kUpdate && !p.tall)
+                        ok = ns_fill<CG, false, true>(ring, a0, b0, ma, mb, arow, brow, t.z, kb, end,
+                                                      rank, abort_flag, p);
+                    else
+                        ok = ns_fill<CG, false, false>(ring, a0, b0, ma, mb, arow, brow, t.z, kb,
+                                                       end, rank, abort_flag, p);
+                }
+                kp = next - 1;
+                ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+            }
+        }
+        if (!ok && rank == 0 && lane == 0) {
+            // wait (bounded) for the copies in flight before teardown
+            for (int s = 0; s < NS_STAGES; ++s) {
+                ring.stage = ring.stage == 0 ? NS_STAGES - 1 : ring.stage - 1;
+                if (ring.stage == NS_STAGES - 1) ring.phase ^= 1u;
+                volatile int no_abort = 0;
+                mbar_wait_bounded(&full[ring.stage], ring.phase, &no_abort, 10000000ull,
+                                  kStatusTimeoutTma, p.status);
             }
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
-            int stage = 0, it = 0;
-            uint32_t phase = 0;
+            // ------------------------------------------- MMA issuer (leader)
+            NsRing ring = {full, empty, 0, 0};
+            int it = 0;
             bool ok = true;
-            const uint64_t a_desc0 = A_MN ? smem_desc_mn128(smem_u32(sA)) : smem_desc_sw128(smem_u32(sA));
-            const uint64_t b_desc0 = B_MN ? smem_desc_mn128(smem_u32(sB)) : smem_desc_sw128(smem_u32(sB));
-            constexpr int A_STEP = A_MN ? 2048 : 32, B_STEP = B_MN ? 2048 : 32;
-            for (int tile = worker; tile < p.tiles && ok; tile += workers, ++it) {
+            const uint32_t a0 = smem_u32(sA), b0 = smem_u32(sB);
+            for (int i = worker; i < p.tiles && ok; i += workers, ++it) {
+                const int what = ns_locate(p, i).phase;
                 const int acc = it & 1;
                 const uint32_t acc_phase = (it >> 1) & 1;
                 if (!mbar_wait_bounded(&tempty[acc], acc_phase ^ 1u, abort_flag, p.wait_limit_ns,
-                                       kStatusTimeoutMma, p.status)) {
-                    ok = false;
+                                       kStatusTimeoutMma, p.status))
                     break;
-                }
                 tc_fence_after();
-                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
-                for (int kb = 0; kb < nk; ++kb) {
-                    if (!mbar_wait_bounded(&full[stage], phase, abort_flag, p.wait_limit_ns,
-                                           kStatusTimeoutMma, p.status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t ad = a_desc0 + (uint64_t)((stage * NS_OPERAND) >> 4);
-                    const uint64_t bd = b_desc0 + (uint64_t)((stage * NS_OPERAND) >> 4);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_f16<CG>(d_tmem, ad + (uint64_t)((k * A_STEP) >> 4),
-                                    bd + (uint64_t)((k * B_STEP) >> 4), IDESC, (kb | k) != 0);
-                    if constexpr (CG == 2) mma_commit_pair(&empty[stage], 0x3);
-                    else mma_commit(&empty[stage]);
-                    if (++stage == NS_STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
+                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BT);
+                const int nk = blocks(what);
+                if (what == kGram && p.tall)
+                    ok = ns_mma_tile<CG, true, true>(ring, a0, b0, d_tmem, nk, abort_flag, p);
+                else if (what == kUpdate && !p.tall)
+                    ok = ns_mma_tile<CG, false, true>(ring, a0, b0, d_tmem, nk, abort_flag, p);
+                else
+                    ok = ns_mma_tile<CG, false, false>(ring, a0, b0, d_tmem, nk, abort_flag, p);
                 if (ok) {
                     if constexpr (CG == 2) mma_commit_pair(&tfull[acc], 0x3);
                     else mma_commit(&tfull[acc]);
@@ -416,83 +674,125 @@ __device__ __forceinline__ void ns_gemm_body(const CUtensorMap &tma_a, const CUt
             mbar_wait_bounded(drain, 0, &no_abort, p.wait_limit_ns, kStatusTimeoutMma, p.status);
         }
     } else {
+        // ------------------------------------------------ epilogue (both CTAs)
         // Two warps to each quarter of the accumulator's lanes (rows): chunks
         // of 32 columns go to them in turn.
         const int quarter = warp & 3, half = (warp - 2) >> 2;
-        uint8_t *box = staging + (warp - 2) * 2 * NS_BOX, *box2 = box + NS_BOX;
+        uint8_t *ebox = staging + (warp - 2) * 4 * NS_BOX, *box = ebox + 2 * NS_BOX;
+        uint8_t *box2 = box + NS_BOX;
+        uint64_t *ebar = &ebars[warp - 2];
+        uint32_t ephase = 0;
+        bool coming = false;  // (lane 0) a copy into ebox is on its way
         int it = 0;
-        for (int tile = worker; tile < p.tiles; tile += workers, ++it) {
+        for (int i = worker; i < p.tiles; i += workers, ++it) {
             const int acc = it & 1;
             const uint32_t acc_phase = (it >> 1) & 1;
-            int z, tm, tn;
-            ns_locate<SYM>(p, tile, z, tm, tn);
-            const int row0 = tm * BM + (int)rank * 128 + quarter * 32, row = row0 + lane;
-            const bool mirror = SYM && tm != tn;
-            const int width = row0 < p.M ? min(BN, p.N - tn * BN) : 0;
-            // The added matrix's values of a chunk, 8 columns at a time (rows
-            // are padded to a multiple of 8, so a group that starts inside
-            // the matrix is inside its row), loaded one chunk ahead of the
-            // accumulator: the first before the tile's products are done.
-            const int64_t at = z * p.bse + (int64_t)row * p.lde;
-            const bool add = MODE != kGram && p.e != nullptr && row < p.M;
-            uint4 eh[4], el[4];
+            const NsTile t = ns_locate(p, i);
+            const bool update = t.phase == kUpdate;
+            const bool fold = t.step >= p.steps - kFoldedSteps, last = t.step == p.steps - 1;
+            const int M = update ? p.rows : S, N = update ? p.cols : S;
+            const int row0 = t.tm * BT + (int)rank * 128 + quarter * 32, row = row0 + lane;
+            const bool mirror = !update && t.tm != t.tn;
+            const int width = row0 < M ? min(BT, N - t.tn * BT) : 0;
+            const float ca = p.coefficients[3 * t.step], cb = p.coefficients[3 * t.step + 1],
+                        cc = p.coefficients[3 * t.step + 2];
+            // output = acc_mul * acc + e_mul * (E + lo 2^-11) + diag on the diagonal
+            float acc_mul, e_mul = 0.f, diag = 0.f;
+            const CUtensorMap *e = nullptr, *e_lo = nullptr, *out, *out_lo = nullptr;
+            const uint32_t *e_flag = nullptr;
+            uint32_t e_done = 0;
+            if (t.phase == kGram) {
+                acc_mul = kAScale / (kXScale * kXScale);
+                out = &maps.da;
+            } else if (t.phase == kPoly) {
+                acc_mul = cc * (kBScale / (kAScale * kAScale));
+                e_mul = cb * (kBScale / kAScale);
+                diag = fold ? ca * kBScale : 0.f;
+                e = &maps.da;
+                e_flag = sym_flag(p, t.z, kGram, t.tm, t.tn);
+                e_done = (uint32_t)(t.step + 1) * ARRIVALS;
+                out = &maps.db;
+            } else {
+                acc_mul = last ? p.scale / (kBScale * kXScale) : 1.f / kBScale;
+                if (!fold) {
+                    e = &maps.dx[t.step & 1];
+                    e_lo = &maps.dlo[t.step & 1];
+                    e_mul = ca;
+                    e_flag = x_flag(p, t.z, t.r, t.c);
+                    e_done = (uint32_t)t.step * ARRIVALS;
+                }
+                out = last ? &maps.dout : &maps.dx[(t.step + 1) & 1];
+                if (t.step + 1 < p.steps - kFoldedSteps) out_lo = &maps.dlo[(t.step + 1) & 1];
+            }
+            // The added matrix's boxes of a chunk come in one chunk ahead of
+            // the accumulator, the first before the tile's products are done.
             auto fetch = [&](int c) {
-                if constexpr (MODE != kGram) {
-                    const int col = tn * BN + c * 32;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const bool in = add && c * 32 < BN && col + 8 * q < p.N;
-                        eh[q] = in ? *reinterpret_cast<const uint4 *>(p.e + at + col + 8 * q)
-                                   : make_uint4(0, 0, 0, 0);
-                        if constexpr (MODE == kUpdate)
-                            el[q] = in && p.e_lo != nullptr
-                                        ? *reinterpret_cast<const uint4 *>(p.e_lo + at + col + 8 * q)
-                                        : make_uint4(0, 0, 0, 0);
-                    }
+                if (lane == 0 && e != nullptr && c * 32 < width) {
+                    const int col = t.tn * BT + c * 32;
+                    mbar_arrive_expect_tx(ebar, e_lo != nullptr ? 2 * NS_BOX : NS_BOX);
+                    ns_load<1>(smem_u32(ebox), e, smem_u32(ebar), col, row0, t.z);
+                    if (e_lo != nullptr)
+                        ns_load<1>(smem_u32(ebox + NS_BOX), e_lo, smem_u32(ebar), col, row0, t.z);
+                    coming = true;
                 }
             };
+            bool ok = true;
+            if (lane == 0 && e_done > 0) {
+                ok = flag_wait_bounded(e_flag, e_done, abort_flag, p.wait_limit_ns, p.status);
+                fence_proxy_async_all();
+            }
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
             fetch(half);
-            const bool ok = mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, p.wait_limit_ns,
-                                              kStatusTimeoutEpilogue, p.status);
+            ok = mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, p.wait_limit_ns,
+                                   kStatusTimeoutEpilogue, p.status);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             tc_fence_after();
 #pragma unroll 1
             for (int c = half; c * 32 < width; c += 2) {
-                const int col = tn * BN + c * 32;
+                const int col = t.tn * BT + c * 32;
                 uint32_t r[32];
                 tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(quarter * 32) << 16) +
-                                       (uint32_t)(acc * BN + c * 32),
+                                       (uint32_t)(acc * BT + c * 32),
                                    r);
                 tmem_ld_wait();
                 float v[32];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * p.acc_mul;
-                if constexpr (MODE != kGram) {
+                for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * acc_mul;
+                if (e != nullptr) {
+                    ok = mbar_wait_bounded(ebar, ephase, abort_flag, p.wait_limit_ns,
+                                           kStatusTimeoutTma, p.status);
+                    if (!__all_sync(0xFFFFFFFFu, ok)) break;
+                    ephase ^= 1u;
+                    coming = false;
+                    uint4 eh[4], el[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint8_t *at = ebox + lane * 64 + 16 * (q ^ ((lane >> 1) & 3));
+                        eh[q] = *reinterpret_cast<const uint4 *>(at);
+                        el[q] = e_lo != nullptr ? *reinterpret_cast<const uint4 *>(at + NS_BOX)
+                                                : make_uint4(0, 0, 0, 0);
+                    }
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const uint32_t hw[4] = {eh[q].x, eh[q].y, eh[q].z, eh[q].w};
+                        const uint32_t lw[4] = {el[q].x, el[q].y, el[q].z, el[q].w};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int j = 8 * q + 2 * i;
-                            float2 e = half2_floats(hw[i]);
-                            if constexpr (MODE == kUpdate) {
-                                const uint32_t lw[4] = {el[q].x, el[q].y, el[q].z, el[q].w};
-                                const float2 l = half2_floats(lw[i]);
-                                e.x = fmaf(l.x, 1.f / kLoScale, e.x);
-                                e.y = fmaf(l.y, 1.f / kLoScale, e.y);
-                            }
-                            v[j] = fmaf(p.e_mul, e.x, v[j]);
-                            v[j + 1] = fmaf(p.e_mul, e.y, v[j + 1]);
+                        for (int k = 0; k < 4; ++k) {
+                            const int j = 8 * q + 2 * k;
+                            const float2 h = half2_floats(hw[k]), l = half2_floats(lw[k]);
+                            v[j] = fmaf(e_mul, fmaf(l.x, 1.f / kLoScale, h.x), v[j]);
+                            v[j + 1] = fmaf(e_mul, fmaf(l.y, 1.f / kLoScale, h.y), v[j + 1]);
                         }
                     }
+                    __syncwarp();  // every lane has read the boxes
                     fetch(c + 2);
                 }
-                if constexpr (MODE == kPoly) {
+                if (diag != 0.f) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] += row == col + j ? p.diag : 0.f;
+                    for (int j = 0; j < 32; ++j) v[j] += row == col + j ? diag : 0.f;
                 }
                 uint32_t packed[16];
-                if (MODE == kUpdate && p.last) {
+                if (update && last) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) packed[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
                 } else {
@@ -515,7 +815,7 @@ __device__ __forceinline__ void ns_gemm_body(const CUtensorMap &tma_a, const CUt
                                                       2 * (lane & 7)) =
                             (uint16_t)(packed[j >> 1] >> (16 * (j & 1)));
                 }
-                if (MODE == kUpdate && p.write_lo) {
+                if (out_lo != nullptr) {
                     uint32_t plo[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
@@ -528,15 +828,15 @@ __device__ __forceinline__ void ns_gemm_body(const CUtensorMap &tma_a, const CUt
                         *reinterpret_cast<uint4 *>(box2 + lane * 64 + 16 * (q ^ ((lane >> 1) & 3))) =
                             make_uint4(plo[4 * q], plo[4 * q + 1], plo[4 * q + 2], plo[4 * q + 3]);
                 }
-                if (MODE == kUpdate && p.direct != nullptr) {
+                if (update && last && p.direct != nullptr) {
                     // an output whose rows no tensor map can describe: row by
                     // row, 32 neighbouring values to a store
                     __syncwarp();
-                    for (int i = 0; i < 32; ++i)
-                        if (row0 + i < p.M && col + lane < p.N)
-                            p.direct[((int64_t)z * p.M + row0 + i) * p.N + col + lane] =
+                    for (int k = 0; k < 32; ++k)
+                        if (row0 + k < M && col + lane < N)
+                            p.direct[((int64_t)t.z * M + row0 + k) * N + col + lane] =
                                 *reinterpret_cast<const uint16_t *>(
-                                    box + i * 64 + 16 * ((lane >> 3) ^ ((i >> 1) & 3)) +
+                                    box + k * 64 + 16 * ((lane >> 3) ^ ((k >> 1) & 3)) +
                                     2 * (lane & 7));
                     __syncwarp();
                     continue;
@@ -544,20 +844,36 @@ __device__ __forceinline__ void ns_gemm_body(const CUtensorMap &tma_a, const CUt
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    ns_store(&tma_d, smem_u32(box), col, row0, z);
-                    if (mirror) ns_store(&tma_d, smem_u32(box2), row0, col, z);
-                    if (MODE == kUpdate && p.write_lo) ns_store(&tma_lo, smem_u32(box2), col, row0, z);
+                    ns_store(out, smem_u32(box), col, row0, t.z);
+                    if (mirror) ns_store(out, smem_u32(box2), row0, col, t.z);
+                    if (out_lo != nullptr) ns_store(out_lo, smem_u32(box2), col, row0, t.z);
                     bulk_commit_group();
                 }
             }
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
                 if constexpr (CG == 2) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
                 else mbar_arrive(&tempty[acc]);
+                if (!(update && last)) {
+                    // this warp's part is in memory: announce it
+                    bulk_wait_group_all();
+                    fence_proxy_async_all();
+                    __threadfence();
+                    atomicAdd(update ? x_flag(p, t.z, t.r, t.c)
+                                     : sym_flag(p, t.z, t.phase, t.tm, t.tn), 1u);
+                    atomicAdd(total_flag(p, t.z, t.phase), 1u);
+                }
             }
+            __syncwarp();
         }
-        if (lane == 0) bulk_wait_group_all();
+        if (lane == 0) {
+            bulk_wait_group_all();
+            volatile int no_abort = 0;
+            if (coming)  // after a wait that ran out: let the copy land
+                mbar_wait_bounded(ebar, ephase, &no_abort, 10000000ull, kStatusTimeoutTma, p.status);
+        }
     }
 
     __syncwarp();
@@ -572,137 +888,155 @@ __device__ __forceinline__ void ns_gemm_body(const CUtensorMap &tma_a, const CUt
     }
 }
 
-template <bool A_MN, bool B_MN, int MODE>
 __global__ void __launch_bounds__(NS_THREADS, 1)
-    ns_gemm_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_constant__ CUtensorMap tma_b,
-                   const __grid_constant__ CUtensorMap tma_d,
-                   const __grid_constant__ CUtensorMap tma_lo, const NsArgs p) {
-    ns_gemm_body<1, 128, A_MN, B_MN, MODE>(tma_a, tma_b, tma_d, tma_lo, p);
+    ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsPlan p) {
+    ns_body<1>(maps, p);
 }
 
-template <int BN, bool A_MN, bool B_MN, int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
-    ns_gemm_pair_kernel(const __grid_constant__ CUtensorMap tma_a,
-                        const __grid_constant__ CUtensorMap tma_b,
-                        const __grid_constant__ CUtensorMap tma_d,
-                        const __grid_constant__ CUtensorMap tma_lo, const NsArgs p) {
-    ns_gemm_body<2, BN, A_MN, B_MN, MODE>(tma_a, tma_b, tma_d, tma_lo, p);
+    ns_pair_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsPlan p) {
+    ns_body<2>(maps, p);
 }
+
+// ------------------------------------------------------------------- host ---
 
 // A batch of row-major 2-byte matrices [rows, cols] in memory, `ld` elements
 // from row to row and rows * ld from matrix to matrix.
-struct Mat {
-    const void *p;
-    int64_t rows, cols, ld;
-};
-
-bool ns_tmap(CUtensorMap *m, const Mat &a, int64_t batch, int box_cols, int box_rows,
-             CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promo) {
+bool ns_tmap(CUtensorMap *m, const void *base, int64_t batch, int64_t rows, int64_t cols,
+             int64_t ld, int box_cols, int box_rows, CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promo) {
     EncodeTiledFn fn = encode_fn();
     if (fn == nullptr) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)a.cols, (cuuint64_t)a.rows, (cuuint64_t)batch};
-    cuuint64_t strides[2] = {(cuuint64_t)(a.ld * 2), (cuuint64_t)(a.rows * a.ld * 2)};
-    cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
+    cuuint64_t strides[2] = {(cuuint64_t)(ld * 2), (cuuint64_t)(rows * ld * 2)};
+    cuuint32_t boxes[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
     cuuint32_t estr[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(a.p), dims, strides, box,
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(base), dims, strides, boxes,
               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promo,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool ns_operand(CUtensorMap *m, const Mat &a, int64_t batch, bool mn, int box_rows) {
-    return ns_tmap(m, a, batch, 64, mn ? 64 : box_rows, CU_TENSOR_MAP_SWIZZLE_128B,
+// The matrices as [batch][groups of 64 columns][rows][64]: one copy brings 64
+// rows of two groups, an operand stage whose contraction runs over the rows.
+// In a last group that is not full the columns past the end are the next
+// row's first (in the workspace, which goes on behind X); they only reach
+// output rows or columns past the end, which are not stored.
+bool ns_operand_mn(CUtensorMap *m, const void *base, int64_t batch, int64_t rows, int64_t cols,
+                   int64_t ld) {
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[4] = {64, (cuuint64_t)rows, (cuuint64_t)((cols + 63) / 64), (cuuint64_t)batch};
+    cuuint64_t strides[3] = {(cuuint64_t)(ld * 2), 128, (cuuint64_t)(rows * ld * 2)};
+    cuuint32_t boxes[4] = {64, 64, 2, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void *>(base), dims, strides, boxes,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool ns_operand(CUtensorMap *m, const void *base, int64_t batch, int64_t rows, int64_t cols,
+                int64_t ld) {
+    return ns_tmap(m, base, batch, rows, cols, ld, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
-bool ns_output(CUtensorMap *m, const Mat &a, int64_t batch) {
-    return ns_tmap(m, a, batch, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+bool ns_output(CUtensorMap *m, const void *base, int64_t batch, int64_t rows, int64_t cols,
+               int64_t ld) {
+    return ns_tmap(m, base, batch, rows, cols, ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
-int64_t ns_tiles(const NsArgs &p, int bm, int bn, bool sym) {
-    const int64_t mt = (p.M + bm - 1) / bm, nt = (p.N + bn - 1) / bn;
-    return sym ? mt * (mt + 1) / 2 : mt * nt;
-}
-
-template <auto KERNEL>
-cudaError_t ns_launch_kernel(int grid, cudaStream_t s, const CUtensorMap &a, const CUtensorMap &b,
-                             const CUtensorMap &d, const CUtensorMap &lo, const NsArgs &p) {
-    static std::atomic<bool> done[64];
+// CTAs (CG = 1) or pairs that are resident at once, asked once per device.
+template <int CG>
+cudaError_t ns_resident(int *workers) {
+    static std::atomic<int> known[64];
     int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64 || !done[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)NS_SMEM);
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool cached = dev >= 0 && dev < 64;
+    int n = cached ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+        if constexpr (CG == 2) {
+            e = cudaFuncSetAttribute(ns_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)NS_SMEM);
+            if (e != cudaSuccess) return e;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = 2 * (num_sms() / 2);
+            cfg.blockDim = NS_THREADS;
+            cfg.dynamicSmemBytes = NS_SMEM;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 2;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&n, ns_pair_kernel, &cfg);
+        } else {
+            e = cudaFuncSetAttribute(ns_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)NS_SMEM);
+            if (e != cudaSuccess) return e;
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, ns_kernel, NS_THREADS, NS_SMEM);
+            n *= num_sms();
+        }
         if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) done[dev] = true;
+        if (n < 1) return cudaErrorInvalidConfiguration;
+        if (cached) known[dev].store(n, std::memory_order_relaxed);
     }
-    return launch_pdl(KERNEL, grid, NS_THREADS, NS_SMEM, s, a, b, d, lo, p);
+    *workers = n;
+    return cudaSuccess;
 }
 
-// One product of the whole batch: d [M, N] from a and b (see ns_gemm_body).
-template <bool A_MN, bool B_MN, int MODE>
-cudaError_t ns_gemm(NsArgs p, int64_t batch, const Mat &a, const Mat &b, const Mat &d, const Mat &lo,
-                    cudaStream_t s, const char **why) {
-    constexpr bool SYM = MODE != kUpdate;
-    // Tiles of 256 x bn by a CTA pair or of 128 x 128 by one CTA (bn = 0):
-    // the least waves times a tile's time, which goes by the rows that each
-    // CTA loads for 64 of K, 128 + bn/2 of a pair's tile (375 ns measured at
-    // 256) and, with less to do between two loads, 205 to 256 of the single
-    // CTA's (297 ns).
-    const int64_t sms = num_sms(), pairs = sms / 2 > 0 ? sms / 2 : 1;
-    int bn = 0;
-    int64_t best = ((ns_tiles(p, 128, 128, SYM) * batch + sms - 1) / sms) * 205;
-    for (int c : {256, 224, 192}) {
-        if (SYM && c != 256) break;
-        const int64_t cost = ((ns_tiles(p, 256, c, SYM) * batch + pairs - 1) / pairs) * (128 + c / 2);
-        if (cost < best) best = cost, bn = c;
+// Cooperative: the CTAs wait for one another's tiles.
+cudaError_t ns_launch(void (*kernel)(NsMaps, NsPlan), int grid, cudaStream_t s, const NsMaps &maps,
+                      const NsPlan &p) {
+    if (tl_fail_launches > 0) {
+        --tl_fail_launches;
+        return cudaErrorLaunchFailure;
     }
-    const int bm = bn ? 256 : 128, bw = bn ? bn : 128;
-    p.m_tiles = (p.M + bm - 1) / bm;
-    p.n_tiles = (p.N + bw - 1) / bw;
-    p.tiles_per = (int)ns_tiles(p, bm, bw, SYM);
-    p.tiles = (int)(p.tiles_per * batch);
-    p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
-    p.status = device_status_word();
-    CUtensorMap ta, tb, td, tl;
-    if (!ns_operand(&ta, a, batch, A_MN, 128) || !ns_operand(&tb, b, batch, B_MN, bn ? bn / 2 : 128) ||
-        !ns_output(&td, d, batch) || !ns_output(&tl, lo, batch)) {
-        *why = "cuTensorMapEncodeTiled failed";
-        return cudaErrorInvalidValue;
-    }
-    const int grid = (int)(bn ? 2 * std::min<int64_t>(p.tiles, pairs) : std::min<int64_t>(p.tiles, sms));
-    if (bn == 0) return ns_launch_kernel<ns_gemm_kernel<A_MN, B_MN, MODE>>(grid, s, ta, tb, td, tl, p);
-    if constexpr (!SYM) {
-        if (bn == 224)
-            return ns_launch_kernel<ns_gemm_pair_kernel<224, A_MN, B_MN, MODE>>(grid, s, ta, tb, td, tl, p);
-        if (bn == 192)
-            return ns_launch_kernel<ns_gemm_pair_kernel<192, A_MN, B_MN, MODE>>(grid, s, ta, tb, td, tl, p);
-    }
-    return ns_launch_kernel<ns_gemm_pair_kernel<256, A_MN, B_MN, MODE>>(grid, s, ta, tb, td, tl, p);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = NS_THREADS;
+    cfg.dynamicSmemBytes = NS_SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, maps, p);
 }
 
 int64_t pad8(int64_t v) { return (v + 7) / 8 * 8; }
 int64_t pad256(int64_t v) { return (v + 255) / 256 * 256; }
 
-constexpr int kPrepParts = 1024;  // blocks a matrix's sum of squares is split over, at most
+constexpr int kPrepParts = 2048;  // blocks that share a matrix in the scaling, at most
 
 struct NsLayout {
-    int64_t ldx, lds, hi0, hi1, lo0, lo1, a, b, sums, bytes;
+    int64_t ldx, lds, x[2], lo[2], a, b, sums, flags, bytes;
 };
+
+int64_t ns_flags_per(int64_t T, int64_t U) { return T * (T + 1) + U * T + 3; }
 
 NsLayout ns_layout(int64_t batch, int64_t rows, int64_t cols) {
     NsLayout w;
-    const int64_t s = std::min(rows, cols);
+    const int64_t s = std::min(rows, cols), l = std::max(rows, cols);
     w.ldx = pad8(cols);
     w.lds = pad8(s);
     const int64_t x = pad256(batch * rows * w.ldx * 2), q = pad256(batch * s * w.lds * 2);
-    w.hi0 = 0;
-    w.hi1 = w.hi0 + x;
-    w.lo0 = w.hi1 + x;
-    w.lo1 = w.lo0 + x;
-    w.a = w.lo1 + x;
-    w.b = w.a + q;
-    w.sums = w.b + q;
-    w.bytes = w.sums + pad256(batch * kPrepParts * (int64_t)sizeof(SquareSums));
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += bytes;
+        return here;
+    };
+    w.x[0] = take(x);
+    w.x[1] = take(x);
+    w.lo[0] = take(x);
+    w.lo[1] = take(x);
+    w.a = take(q);
+    w.b = take(q);
+    w.sums = take(pad256(batch * kPrepParts * (int64_t)sizeof(SquareSums)));
+    w.flags = take(pad256(batch * ns_flags_per((s + 127) / 128, (l + 127) / 128) * 4));
+    w.bytes = at;
     return w;
 }
 
@@ -716,11 +1050,10 @@ cudaError_t ns_prepare(const PrepArgs &a, int64_t batch, cudaStream_t s) {
         p.sums += z * a.parts;
         p.hi += z * (int64_t)a.rows * a.ldx;
         p.lo += z * (int64_t)a.rows * a.ldx;
+        p.flags += z * a.flags_per;
         cudaError_t e = launch_pdl(ns_square_kernel<T, VECTOR>, dim3(a.parts, n), kPrepThreads, 0, s, p);
         if (e != cudaSuccess) return e;
-        const int ty = kPrepThreads / a.tx;
-        const int64_t blocks = std::min<int64_t>((a.rows + ty - 1) / ty, 16 * (int64_t)num_sms());
-        e = launch_pdl(ns_scale_kernel<T, VECTOR>, dim3((unsigned)blocks, n), kPrepThreads, 0, s, p);
+        e = launch_pdl(ns_scale_kernel<T, VECTOR>, dim3(a.parts, n), kPrepThreads, 0, s, p);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -734,80 +1067,96 @@ int64_t orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols)
 
 cudaError_t launch_orthogonalize(const Orthogonalize &o, cudaStream_t s, const char **why) {
     if (o.batch == 0 || o.rows == 0 || o.cols == 0) return cudaSuccess;
-    const bool tall = o.rows > o.cols;
     const int64_t S = std::min(o.rows, o.cols), L = std::max(o.rows, o.cols);
     const NsLayout w = ns_layout(o.batch, o.rows, o.cols);
     uint8_t *base = reinterpret_cast<uint8_t *>(o.workspace);
     auto half = [&](int64_t off) { return reinterpret_cast<__half *>(base + off); };
 
-    PrepArgs p = {};
-    p.g = o.g, p.ldg = o.ldg, p.bsg = o.bsg;
-    p.rows = (int)o.rows, p.cols = (int)o.cols, p.ldx = (int)w.ldx;
-    p.eps = o.eps;
-    p.sums = reinterpret_cast<SquareSums *>(base + w.sums);
-    p.hi = half(w.hi0), p.lo = half(w.lo0);
+    // Tiles of 256 by CTA pairs or of 128 by single CTAs, whichever is done
+    // sooner: a step's tiles over the workers, but no fewer than one tile of
+    // each product after another, times the blocks of 64 of the contraction
+    // and the time of one (375 ns a pair's, 297 ns a CTA's: those are bound by
+    // their loads).
+    int pairs = 0, singles = 0;
+    cudaError_t e = ns_resident<2>(&pairs);
+    if (e != cudaSuccess) return e;
+    e = ns_resident<1>(&singles);
+    if (e != cudaSuccess) return e;
+    auto cost = [&](int bt, int workers, double block) {
+        const int64_t T = (S + bt - 1) / bt, U = (L + bt - 1) / bt;
+        const double tri = (double)(o.batch * T * (T + 1) / 2) / workers,
+                     upd = (double)(o.batch * T * U) / workers;
+        return block * ((tri > 1 ? tri : 1) * (double)(L + S) + (upd > 1 ? upd : 1) * (double)S);
+    };
+    const bool pair = cost(256, pairs, 375) <= cost(128, singles, 297);
+    const int bt = pair ? 256 : 128;
+
+    NsPlan p = {};
+    p.rows = (int)o.rows, p.cols = (int)o.cols, p.batch = (int)o.batch, p.steps = o.steps;
+    p.tall = o.rows > o.cols;
+    p.T = (int)((S + bt - 1) / bt);
+    p.U = (int)((L + bt - 1) / bt);
+    p.tri = p.T * (p.T + 1) / 2;
+    p.upd = p.T * p.U;
+    const int64_t per_step = o.batch * (2 * (int64_t)p.tri + p.upd);
+    if (per_step * o.steps > 0x7FFFFFFF) {
+        *why = "too many tiles";
+        return cudaErrorInvalidValue;
+    }
+    p.per_step = (int)per_step;
+    p.tiles = (int)(per_step * o.steps);
+    p.flags = reinterpret_cast<uint32_t *>(base + w.flags);
+    p.flags_per = (int)ns_flags_per(p.T, p.U);
+    for (int i = 0; i < 3 * o.steps; ++i) p.coefficients[i] = o.coefficients[i];
+    p.scale = o.scale;
+    p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+    p.status = device_status_word();
+
+    NsMaps maps;
+    const bool out_map = o.cols % 8 == 0 && aligned_to(o.out, 16);
+    if (!out_map) p.direct = o.out;
+    bool ok = true;
+    for (int i = 0; i < 2; ++i)
+        ok = ok && ns_operand(&maps.x[i], half(w.x[i]), o.batch, o.rows, o.cols, w.ldx) &&
+             ns_operand_mn(&maps.xm[i], half(w.x[i]), o.batch, o.rows, o.cols, w.ldx) &&
+             ns_output(&maps.dx[i], half(w.x[i]), o.batch, o.rows, o.cols, w.ldx) &&
+             ns_output(&maps.dlo[i], half(w.lo[i]), o.batch, o.rows, o.cols, w.ldx);
+    ok = ok && ns_operand(&maps.a, half(w.a), o.batch, S, S, w.lds) &&
+         ns_operand(&maps.b, half(w.b), o.batch, S, S, w.lds) &&
+         ns_output(&maps.da, half(w.a), o.batch, S, S, w.lds) &&
+         ns_output(&maps.db, half(w.b), o.batch, S, S, w.lds) &&
+         (out_map ? ns_output(&maps.dout, o.out, o.batch, o.rows, o.cols, o.cols)
+                  : ns_output(&maps.dout, half(w.x[0]), o.batch, o.rows, o.cols, w.ldx));
+    if (!ok) {
+        *why = "cuTensorMapEncodeTiled failed";
+        return cudaErrorInvalidValue;
+    }
+
+    PrepArgs a = {};
+    a.g = o.g, a.ldg = o.ldg, a.bsg = o.bsg;
+    a.rows = (int)o.rows, a.cols = (int)o.cols, a.ldx = (int)w.ldx;
+    a.eps = o.eps;
+    a.sums = reinterpret_cast<SquareSums *>(base + w.sums);
+    a.hi = half(w.x[0]), a.lo = half(w.lo[0]);
+    a.flags = p.flags;
+    a.flags_per = p.flags_per;
     const int es = o.g_f32 ? 4 : 2;
     const bool vec = aligned_to(o.g, 16) && o.ldg * es % 16 == 0 && o.bsg * es % 16 == 0 &&
                      o.cols * es % 16 == 0;
     const int64_t groups = vec ? o.cols * es / 16 : o.cols;
-    p.tx = 8;
-    while (p.tx < kPrepThreads && p.tx < groups) p.tx *= 2;
-    const int64_t row_blocks = (o.rows + kPrepThreads / p.tx - 1) / (kPrepThreads / p.tx);
-    p.parts = (int)std::min<int64_t>(row_blocks, kPrepParts);
-    cudaError_t e = o.g_f32 ? (vec ? ns_prepare<float, true>(p, o.batch, s)
-                                   : ns_prepare<float, false>(p, o.batch, s))
-                            : (vec ? ns_prepare<uint16_t, true>(p, o.batch, s)
-                                   : ns_prepare<uint16_t, false>(p, o.batch, s));
+    a.tx = 8;
+    while (a.tx < kPrepThreads && a.tx < groups) a.tx *= 2;
+    const int64_t row_blocks = (o.rows + kPrepThreads / a.tx - 1) / (kPrepThreads / a.tx);
+    // eight blocks to an SM over the batch; more would add up more partial sums
+    const int64_t share = 8 * (int64_t)num_sms() / o.batch;
+    a.parts = (int)std::min<int64_t>(row_blocks, std::min<int64_t>(kPrepParts, share > 16 ? share : 16));
+    e = o.g_f32 ? (vec ? ns_prepare<float, true>(a, o.batch, s) : ns_prepare<float, false>(a, o.batch, s))
+                : (vec ? ns_prepare<uint16_t, true>(a, o.batch, s)
+                       : ns_prepare<uint16_t, false>(a, o.batch, s));
     if (e != cudaSuccess) return e;
-
-    const Mat A = {half(w.a), S, S, w.lds}, B = {half(w.b), S, S, w.lds};
-    int cur = 0;
-    for (int i = 0; i < o.steps; ++i) {
-        const float a = o.coefficients[3 * i], b = o.coefficients[3 * i + 1],
-                    c = o.coefficients[3 * i + 2];
-        const bool fold = i >= o.steps - kFoldedSteps, last = i == o.steps - 1;
-        const Mat X = {half(cur ? w.hi1 : w.hi0), o.rows, o.cols, w.ldx};
-        const Mat Y = {half(cur ? w.hi0 : w.hi1), o.rows, o.cols, w.ldx};
-        const Mat Ylo = {half(cur ? w.lo0 : w.lo1), o.rows, o.cols, w.ldx};
-
-        NsArgs q = {};  // A = X Xᵀ (tall: Xᵀ X)
-        q.M = q.N = (int)S;
-        q.K = (int)L;
-        q.acc_mul = kAScale / (kXScale * kXScale);
-        e = tall ? ns_gemm<true, true, kGram>(q, o.batch, X, X, A, A, s, why)
-                 : ns_gemm<false, false, kGram>(q, o.batch, X, X, A, A, s, why);
-        if (e != cudaSuccess) return e;
-
-        q.K = (int)S;  // B = b A + c A A (+ a I); A is its own transpose
-        q.acc_mul = c * (kBScale / (kAScale * kAScale));
-        q.e = half(w.a), q.lde = w.lds, q.bse = S * w.lds;
-        q.e_mul = b * (kBScale / kAScale);
-        q.diag = fold ? a * kBScale : 0.f;
-        e = ns_gemm<false, false, kPoly>(q, o.batch, A, A, B, B, s, why);
-        if (e != cudaSuccess) return e;
-
-        q = {};  // X <- a X + B X (tall: a X + X B)
-        q.M = (int)o.rows, q.N = (int)o.cols, q.K = (int)S;
-        q.acc_mul = last ? o.scale / (kBScale * kXScale) : 1.f / kBScale;
-        if (!fold) {
-            q.e = reinterpret_cast<const __half *>(X.p);
-            q.e_lo = half(cur ? w.lo1 : w.lo0);
-            q.lde = w.ldx, q.bse = o.rows * w.ldx;
-            q.e_mul = a;
-            q.write_lo = i + 1 < o.steps - kFoldedSteps;
-        }
-        Mat D = Y;
-        if (last) {
-            q.last = 1;
-            if (o.cols % 8 == 0 && aligned_to(o.out, 16)) D = Mat{o.out, o.rows, o.cols, o.cols};
-            else q.direct = o.out;
-        }
-        e = tall ? ns_gemm<false, false, kUpdate>(q, o.batch, X, B, D, Ylo, s, why)
-                 : ns_gemm<false, true, kUpdate>(q, o.batch, B, X, D, Ylo, s, why);
-        if (e != cudaSuccess) return e;
-        cur ^= 1;
-    }
-    return cudaSuccess;
+    const int workers = std::min(pair ? pairs : singles, p.per_step);
+    return pair ? ns_launch(ns_pair_kernel, 2 * workers, s, maps, p)
+                : ns_launch(ns_kernel, workers, s, maps, p);
 }
 
 }  // namespace fp8
