@@ -196,7 +196,7 @@ struct NsPlan {
     int per_step, tiles;       // over the batch; over all steps
     // memory
     uint16_t *direct;          // bf16 output without a tensor map (nullable)
-    uint32_t *flags;           // per matrix: A, B tiles, X tiles, three totals
+    uint32_t *flags;           // per matrix: of its A, B and X tiles
     int flags_per;
     // arithmetic: step i has coefficients (a, b, c) at 3 i
     float coefficients[3 * kMaxSteps];
@@ -213,7 +213,7 @@ struct NsMaps {
 };
 
 constexpr int NS_EPI_WARPS = 8;                // two to each quarter of the lanes
-constexpr int NS_THREADS = 64 + 32 * NS_EPI_WARPS;
+constexpr int NS_THREADS = 64 + 32 * NS_EPI_WARPS + 32;  // loads, MMAs, output, scout
 constexpr int NS_BOX = 2048;                   // a 32 x 32 box of 2-byte outputs
 constexpr int NS_STAGING = NS_EPI_WARPS * 4 * NS_BOX;  // two that come in, two that go out
 constexpr int NS_OPERAND = 128 * 128;          // 128 rows of 64 fp16
@@ -315,6 +315,35 @@ __device__ __forceinline__ bool flag_wait_bounded(const uint32_t *p, uint32_t ta
     }
 }
 
+// The scout's word to the producer, in shared memory.
+__device__ __forceinline__ void store_release_cta(uint32_t *p, uint32_t v) {
+    asm volatile("st.release.cta.shared.u32 [%0], %1;" ::"r"(smem_u32(p)), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t load_acquire_cta(const uint32_t *p) {
+    uint32_t v;
+    asm volatile("ld.acquire.cta.shared.u32 %0, [%1];" : "=r"(v) : "r"(smem_u32(p)) : "memory");
+    return v;
+}
+
+// Waits until the scout has found more than `have` panels; *seen: how many.
+__device__ __forceinline__ bool scout_wait_bounded(const uint32_t *p, uint32_t have, uint32_t *seen,
+                                                   volatile int *abort, uint64_t limit_ns,
+                                                   unsigned int *status) {
+    if ((*seen = load_acquire_cta(p)) != have) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t i = 1;; ++i) {
+        if ((*seen = load_acquire_cta(p)) != have) return true;
+        if ((i & 63u) == 0) {
+            if (*abort) return false;
+            if (global_timer_ns() - t0 > limit_ns) {
+                *abort = 1;
+                atomicOr(status, kStatusTimeoutBarrier);
+                return false;
+            }
+        }
+    }
+}
+
 // A tile of the list.  r, c: its place in A or B (r >= c), or in X with c
 // along the shorter and r along the longer side.
 struct NsTile {
@@ -353,8 +382,8 @@ __device__ __forceinline__ NsTile ns_locate(const NsPlan &p, int i) {
     return t;
 }
 
-// The counters: of a tile of A or B at rows r and column c (in either order),
-// of a tile of X, and of all tiles of A, B or X of a matrix.
+// The counters: of a tile of A or B at row r and column c (in either order),
+// and of a tile of X.
 __device__ __forceinline__ uint32_t *sym_flag(const NsPlan &p, int z, int phase, int r, int c) {
     const int hi = max(r, c), lo = min(r, c);
     return p.flags + (int64_t)z * p.flags_per + phase * p.tri + hi * (hi + 1) / 2 + lo;
@@ -362,10 +391,6 @@ __device__ __forceinline__ uint32_t *sym_flag(const NsPlan &p, int z, int phase,
 __device__ __forceinline__ uint32_t *x_flag(const NsPlan &p, int z, int r, int c) {
     return p.flags + (int64_t)z * p.flags_per + 2 * p.tri + r * p.T + c;
 }
-__device__ __forceinline__ uint32_t *total_flag(const NsPlan &p, int z, int phase) {
-    return p.flags + (int64_t)z * p.flags_per + 2 * p.tri + p.upd + phase;
-}
-
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
@@ -481,6 +506,7 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
     constexpr int BT = 128 * CG;
     constexpr uint32_t TMEM_COLS = 2 * BT;
     constexpr uint32_t ARRIVALS = NS_EPI_WARPS * CG;  // that complete a tile
+    constexpr int PANEL = BT / 64;                    // blocks of 64 that a tile spans
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~uintptr_t(1023));
@@ -490,6 +516,7 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
     uint64_t *tempty = tfull + 2, *drain = tempty + 2, *ebars = drain + 1;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(ebars + NS_EPI_WARPS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+    uint32_t *scouted = tmem_holder + 2;
     uint8_t *staging = smem + NS_STAGES * NS_STAGE + 1024;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -509,6 +536,7 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
         mbar_init(drain, 1);
         for (int w = 0; w < NS_EPI_WARPS; ++w) mbar_init(&ebars[w], 1);
         *abort_flag = 0;
+        *scouted = 0;
         fence_mbarrier_init();
         tma_prefetch_desc(&maps.x[0]);
         tma_prefetch_desc(&maps.x[1]);
@@ -538,84 +566,34 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
 
     if (warp == 0) {
         // ------------------------------------------------------- TMA producer
-        // The warp looks at the counters together, 32 panels of the
-        // contraction at a time; its first lane loads.
-        constexpr int PANEL = BT / 64;
         NsRing ring = {full, empty, 0, 0};
         bool ok = true;
-        for (int i = worker; i < p.tiles && ok; i += workers) {
-            const NsTile t = ns_locate(p, i);
-            const int cur = t.step & 1;
-            const CUtensorMap *ma, *mb;
-            if (t.phase == kGram) {
-                ma = mb = p.tall ? &maps.xm[cur] : &maps.x[cur];
-            } else if (t.phase == kPoly) {
-                ma = mb = &maps.a;
-            } else {
-                ma = p.tall ? &maps.x[cur] : &maps.b;
-                mb = p.tall ? &maps.b : &maps.xm[cur];
-            }
-            const int arow = t.tm * BT + (int)rank * 128, brow = t.tn * BT + (int)rank * 128;
-            // what the operands come from: A from step's X, B from its A, the
-            // new X from its B; the first X is there already
-            const int source = t.phase == kGram ? kUpdate : t.phase - 1;
-            const uint32_t done = (uint32_t)(t.phase == kGram ? t.step : t.step + 1) * ARRIVALS;
-            const int nk = blocks(t.phase), panels = (nk + PANEL - 1) / PANEL;
-            int there = 0;  // panels known to be complete
-            if (done == 0) {
-                there = panels;
-            } else {
-                const uint32_t all = done * (uint32_t)(source == kUpdate ? p.upd : p.tri);
-                if (load_acquire(total_flag(p, t.z, source)) >= all) there = panels;
-                __syncwarp();
-                fence_proxy_async_all();
-            }
-            for (int kp = 0; kp < panels && ok; ++kp) {
-                if (kp >= there) {
-                    const int mine = kp + lane;
-                    const uint32_t *f0 = nullptr, *f1 = nullptr;
-                    if (mine < panels) {
-                        if (t.phase == kGram) {
-                            f0 = x_flag(p, t.z, mine, t.tm);
-                            f1 = x_flag(p, t.z, mine, t.tn);
-                        } else if (t.phase == kPoly) {
-                            f0 = sym_flag(p, t.z, kGram, t.tm, mine);
-                            f1 = sym_flag(p, t.z, kGram, t.tn, mine);
-                        } else {
-                            f0 = f1 = sym_flag(p, t.z, kPoly, t.c, mine);
-                        }
-                    }
-                    uint64_t t0 = 0;
-                    for (uint32_t turn = 0;; ++turn) {
-                        const bool have =
-                            f0 != nullptr && load_acquire(f0) >= done && load_acquire(f1) >= done;
-                        const uint32_t got = __ballot_sync(0xFFFFFFFFu, have);
-                        const int run = __ffs(~got) == 0 ? 32 : __ffs(~got) - 1;
-                        there = kp + run;
-                        if (run > 0) break;
-                        if ((turn & 63u) == 0) {
-                            const uint64_t now = global_timer_ns();
-                            if (turn == 0) t0 = now;
-                            const bool late = now - t0 > p.wait_limit_ns;
-                            if (__any_sync(0xFFFFFFFFu, late || *abort_flag != 0)) {
-                                if (lane == 0 && *abort_flag == 0) {
-                                    *abort_flag = 1;
-                                    atomicOr(p.status, kStatusTimeoutBarrier);
-                                }
-                                ok = false;
-                                break;
-                            }
-                        }
-                    }
-                    __syncwarp();
-                    fence_proxy_async_all();
-                    if (!ok) break;
+        if (lane == 0) {
+            uint32_t want = 0, seen = 0;  // panels of the contraction, over all tiles
+            const uint32_t a0 = smem_u32(sA), b0 = smem_u32(sB);
+            for (int i = worker; i < p.tiles && ok; i += workers) {
+                const NsTile t = ns_locate(p, i);
+                const int cur = t.step & 1;
+                const CUtensorMap *ma, *mb;
+                if (t.phase == kGram) {
+                    ma = mb = p.tall ? &maps.xm[cur] : &maps.x[cur];
+                } else if (t.phase == kPoly) {
+                    ma = mb = &maps.a;
+                } else {
+                    ma = p.tall ? &maps.x[cur] : &maps.b;
+                    mb = p.tall ? &maps.b : &maps.xm[cur];
                 }
-                // up to the next panel that has to be looked at
-                const int next = kp + 1 > there ? kp + 1 : there;
-                if (lane == 0) {
+                const int arow = t.tm * BT + (int)rank * 128, brow = t.tn * BT + (int)rank * 128;
+                const int nk = blocks(t.phase), panels = (nk + PANEL - 1) / PANEL;
+                for (int kp = 0; kp < panels && ok;) {
+                    if (seen == want) {
+                        ok = scout_wait_bounded(scouted, want, &seen, abort_flag, p.wait_limit_ns,
+                                                p.status);
+                        fence_proxy_async_all();
+                        if (!ok) break;
+                    }
+                    const int next = min(panels, kp + (int)(seen - want));
                     const int kb = kp * PANEL, end = min(nk, next * PANEL);
-                    const uint32_t a0 = smem_u32(sA), b0 = smem_u32(sB);
                     if (t.phase == kGram && p.tall)
                         ok = ns_fill<CG, true, true>(ring, a0, b0, ma, mb, arow, brow, t.z, kb, end,
                                                      rank, abort_flag, p);
@@ -625,9 +603,9 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
                     else
                         ok = ns_fill<CG, false, false>(ring, a0, b0, ma, mb, arow, brow, t.z, kb,
                                                        end, rank, abort_flag, p);
+                    want += next - kp;
+                    kp = next;
                 }
-                kp = next - 1;
-                ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
             }
         }
         if (!ok && rank == 0 && lane == 0) {
@@ -672,6 +650,67 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
             else mma_commit(drain);
             volatile int no_abort = 0;
             mbar_wait_bounded(drain, 0, &no_abort, p.wait_limit_ns, kStatusTimeoutMma, p.status);
+        }
+    } else if (warp == NS_THREADS / 32 - 1) {
+        // ---------------------------------------------------------- scout
+        // Looks at the counters ahead of the producer, 32 panels of the
+        // contraction at a time, and tells it how many are there: the looking
+        // takes longer than the producer has between two tiles.
+        uint32_t found = 0;
+        bool ok = true;
+        for (int i = worker; i < p.tiles && ok; i += workers) {
+            const NsTile t = ns_locate(p, i);
+            // what the operands come from: A from the step's X, B from its A,
+            // the new X from its B; the first X is there already
+            const uint32_t done = (uint32_t)(t.phase == kGram ? t.step : t.step + 1) * ARRIVALS;
+            const int panels = (blocks(t.phase) + PANEL - 1) / PANEL;
+            for (int kp = 0; kp < panels && ok;) {
+                const int mine = kp + lane;
+                int run = 32;
+                if (done > 0) {
+                    const uint32_t *f0 = nullptr, *f1 = nullptr;
+                    if (mine < panels) {
+                        if (t.phase == kGram) {
+                            f0 = x_flag(p, t.z, mine, t.tm);
+                            f1 = x_flag(p, t.z, mine, t.tn);
+                        } else if (t.phase == kPoly) {
+                            f0 = sym_flag(p, t.z, kGram, t.tm, mine);
+                            f1 = sym_flag(p, t.z, kGram, t.tn, mine);
+                        } else {
+                            f0 = f1 = sym_flag(p, t.z, kPoly, t.c, mine);
+                        }
+                    }
+                    uint64_t t0 = 0;
+                    for (uint32_t turn = 0;; ++turn) {
+                        bool have = true;
+                        if (f0 != nullptr) {
+                            const uint32_t v0 = load_acquire(f0), v1 = load_acquire(f1);
+                            have = v0 >= done && v1 >= done;
+                        }
+                        const uint32_t got = __ballot_sync(0xFFFFFFFFu, have);
+                        run = ~got == 0 ? 32 : __ffs(~got) - 1;
+                        if (run > 0) break;
+                        if ((turn & 63u) == 0) {
+                            const uint64_t now = global_timer_ns();
+                            if (turn == 0) t0 = now;
+                            const bool late = now - t0 > p.wait_limit_ns;
+                            if (__any_sync(0xFFFFFFFFu, late || *abort_flag != 0)) {
+                                if (lane == 0 && *abort_flag == 0) {
+                                    *abort_flag = 1;
+                                    atomicOr(p.status, kStatusTimeoutBarrier);
+                                }
+                                ok = false;
+                                break;
+                            }
+                        }
+                    }
+                }
+                run = min(run, panels - kp);
+                kp += run;
+                found += run;
+                __syncwarp();
+                if (lane == 0 && ok) store_release_cta(scouted, found);
+            }
         }
     } else {
         // ------------------------------------------------ epilogue (both CTAs)
@@ -863,7 +902,6 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
                     __threadfence();
                     atomicAdd(update ? x_flag(p, t.z, t.r, t.c)
                                      : sym_flag(p, t.z, t.phase, t.tm, t.tn), 1u);
-                    atomicAdd(total_flag(p, t.z, t.phase), 1u);
                 }
             }
             __syncwarp();
@@ -917,9 +955,9 @@ bool ns_tmap(CUtensorMap *m, const void *base, int64_t batch, int64_t rows, int6
 
 // The matrices as [batch][groups of 64 columns][rows][64]: one copy brings 64
 // rows of two groups, an operand stage whose contraction runs over the rows.
-// In a last group that is not full the columns past the end are the next
-// row's first (in the workspace, which goes on behind X); they only reach
-// output rows or columns past the end, which are not stored.
+// The columns past the end of a last group that is not full are the rows'
+// padding: unwritten memory that only reaches output rows or columns past the
+// end, which are not stored.
 bool ns_operand_mn(CUtensorMap *m, const void *base, int64_t batch, int64_t rows, int64_t cols,
                    int64_t ld) {
     EncodeTiledFn fn = encode_fn();
@@ -1005,7 +1043,8 @@ cudaError_t ns_launch(void (*kernel)(NsMaps, NsPlan), int grid, cudaStream_t s, 
     return cudaLaunchKernelEx(&cfg, kernel, maps, p);
 }
 
-int64_t pad8(int64_t v) { return (v + 7) / 8 * 8; }
+// Rows of 128-byte lines: a copy's 128-byte row then is one line, not two.
+int64_t pad64(int64_t v) { return (v + 63) / 64 * 64; }
 int64_t pad256(int64_t v) { return (v + 255) / 256 * 256; }
 
 constexpr int kPrepParts = 2048;  // blocks that share a matrix in the scaling, at most
@@ -1014,13 +1053,13 @@ struct NsLayout {
     int64_t ldx, lds, x[2], lo[2], a, b, sums, flags, bytes;
 };
 
-int64_t ns_flags_per(int64_t T, int64_t U) { return T * (T + 1) + U * T + 3; }
+int64_t ns_flags_per(int64_t T, int64_t U) { return T * (T + 1) + U * T; }
 
 NsLayout ns_layout(int64_t batch, int64_t rows, int64_t cols) {
     NsLayout w;
     const int64_t s = std::min(rows, cols), l = std::max(rows, cols);
-    w.ldx = pad8(cols);
-    w.lds = pad8(s);
+    w.ldx = pad64(cols);
+    w.lds = pad64(s);
     const int64_t x = pad256(batch * rows * w.ldx * 2), q = pad256(batch * s * w.lds * 2);
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
