@@ -98,20 +98,34 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 
 // A team's ring: `stages` slots of `slot` bytes with a barrier each.  The
 // dynamic shared memory holds all teams' slots, then their barriers, then the
-// block's give-up flag (a wait that runs out is recorded, and the block
-// carries on with what it has: its outputs are invalid).
+// block's give-up flag.  After a wait that ran out the status word says so and
+// the block walks on, without further copies, over what the slots hold: its
+// outputs are invalid, but its barriers stay paired; the copies on their way
+// are waited for at the end.
 struct Ring {
     uint8_t *data;
     uint64_t *bars;
     volatile int *abort;
     int stages;
     uint32_t slot;
+    int64_t asked;  // (leader) rows requested: the k-th uses slot k % stages
+
+    __device__ __forceinline__ bool open() { return *abort == 0 && ++asked > 0; }
+
+    __device__ __forceinline__ void settle(unsigned int *status) {
+        if (*abort == 0) return;
+        volatile int no_abort = 0;
+        for (int64_t k = asked > stages ? asked - stages : 0; k < asked; ++k)
+            mbar_wait_bounded(&bars[k % stages], (uint32_t)(k / stages) & 1u, &no_abort, 10000000ull,
+                              kStatusTimeoutTma, status);
+    }
 
     template <int TEAMS>
     __device__ __forceinline__ void init(uint8_t *smem, int n, uint32_t slot_bytes, int team,
                                          bool leader) {
         stages = n;
         slot = slot_bytes;
+        asked = 0;
         data = smem + (size_t)team * n * slot_bytes;
         uint64_t *all = reinterpret_cast<uint64_t *>(smem + (size_t)TEAMS * n * slot_bytes);
         bars = all + team * n;
@@ -334,7 +348,7 @@ __global__ void __launch_bounds__(block_threads(TPR), fwd_blocks(TPR, EPT))
     const int64_t step = (int64_t)gridDim.x * teams(TPR);
     int64_t row = (int64_t)blockIdx.x * teams(TPR) + team;
     auto request = [&](int64_t r, int slot) {
-        if (r < a.rows) {
+        if (r < a.rows && ring.open()) {
             mbar_arrive_expect_tx(&ring.bars[slot], bytes);
             bulk_load(ring.data + slot * bytes, x + r * a.ldx, bytes, &ring.bars[slot]);
         }
@@ -369,6 +383,7 @@ __global__ void __launch_bounds__(block_threads(TPR), fwd_blocks(TPR, EPT))
             phase ^= 1u;
         }
     }
+    if (t == 0) ring.settle(a.status);
     if (a.amax != nullptr) amax_commit(n.amax, a.amax);
 }
 
@@ -662,7 +677,7 @@ __global__ void __launch_bounds__(block_threads(TPR), bwd_blocks(TPR))
     const int64_t step = (int64_t)gridDim.x * teams(TPR);
     int64_t row = (int64_t)blockIdx.x * teams(TPR) + team;
     auto request = [&](int64_t r, int slot) {
-        if (r < a.rows) {
+        if (r < a.rows && ring.open()) {
             uint8_t *to = ring.data + slot * ring.slot;
             mbar_arrive_expect_tx(&ring.bars[slot], 2 * bytes);
             bulk_load(to, x + r * a.ldx, bytes, &ring.bars[slot]);
@@ -703,6 +718,7 @@ __global__ void __launch_bounds__(block_threads(TPR), bwd_blocks(TPR))
             phase ^= 1u;
         }
     }
+    if (t == 0) ring.settle(a.status);
     // every copy has arrived and been read: the teams' sums meet in the ring
     if (a.partial != nullptr) n.commit(a, reinterpret_cast<float *>(smem));
 }
@@ -864,7 +880,7 @@ cudaError_t run_fwd_ring(NormArgs a, cudaStream_t s, bool *done) {
 }
 
 // Many rows: 32 elements to a thread where the row fills them, so that the
-// sums over the team cost less an element (16384 x 4096 to E4M3: TODO).
+// sums over the team cost less an element (16384 x 4096 to E4M3: 39 us; with 16 elements 53).
 template <typename T>
 cudaError_t pick_fwd_ring(const NormArgs &a, cudaStream_t s, bool *done) {
     if (a.cols <= 512) return run_fwd_ring<T, 32, 16>(a, s, done);
@@ -963,6 +979,8 @@ cudaError_t pick_bwd(const NormBwdArgs &a, int *parts, cudaStream_t s) {
     case 256: return run_bwd<T, VECTOR, 256, EPT>(a, parts, s);
     case 512: return run_bwd<T, VECTOR, 512, EPT>(a, parts, s);
     }
+    if constexpr (!VECTOR)
+        if (threads_for(a.cols, 2 * EPT, 512)) return run_bwd<T, VECTOR, 512, 2 * EPT>(a, parts, s);
     int grid = 0;
     cudaError_t e = cudaSuccess;
     if (a.dx != nullptr) {

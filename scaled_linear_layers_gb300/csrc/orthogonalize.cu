@@ -648,8 +648,8 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
             }
             if constexpr (CG == 2) mma_commit_pair(drain, 0x1);
             else mma_commit(drain);
-            volatile int no_abort = 0;
-            mbar_wait_bounded(drain, 0, &no_abort, p.wait_limit_ns, kStatusTimeoutMma, p.status);
+            volatile int no_abort = 0;  // a short limit must not cut this wait short
+            mbar_wait_bounded(drain, 0, &no_abort, kDefaultWaitLimitNs, kStatusTimeoutMma, p.status);
         }
     } else if (warp == NS_THREADS / 32 - 1) {
         // ---------------------------------------------------------- scout

@@ -273,3 +273,28 @@ def test_python_refusals():
                 dict(yq=torch.empty(4, 8, dtype=torch.uint8, device="cuda"))):
         with pytest.raises(fp8.Fp8Error):
             ok(**bad)
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
+    """A limit of 1 ns makes the waits for rows on their way give up; the call
+    ends, the status says so, and nothing is left behind."""
+    x, dy = rnd(6000, 1024, seed=60, dtype=BF), rnd(6000, 1024, seed=61, dtype=BF)
+    y, mean, rstd = torch.empty_like(x), f32(6000), f32(6000)
+    dw = f32(1024)
+    ws = torch.empty(fp8.fp8_layer_norm_workspace_bytes(6000, 1024), dtype=torch.uint8,
+                     device="cuda")
+    fp8.fp8_check_device_status()
+    old = fp8.fp8_set_wait_limit_ns(1)
+    try:
+        fp8.fp8_layer_norm(x, None, None, EPS, y, mean, rstd)
+        fp8.fp8_layer_norm_backward(dy, x, None, mean, rstd, y, dw, None, ws)
+        try:
+            fp8.fp8_check_device_status()
+        except fp8.Fp8Error as e:
+            assert e.status == 6  # FP8_ERR_TIMEOUT
+    finally:
+        fp8.fp8_set_wait_limit_ns(old)
+    fp8.fp8_layer_norm(x, None, None, EPS, y, mean, rstd)
+    check_forward(x, None, None, y, mean, rstd)
+    run_backward(x, dy, None, F)
+    fp8.fp8_check_device_status()

@@ -197,3 +197,41 @@ def test_python_refusals():
                 lambda: fp8.fp8_orthogonalize(g[None, None], out, ws)):
         with pytest.raises(fp8.Fp8Error):
             bad()
+
+
+@pytest.mark.parametrize("rows, cols", [(600, 700), (4096, 1024)])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(rows, cols):
+    """A limit of 1 ns makes every wait give up: for copies, for products, for
+    other tiles.  The call ends, the status says so, the next call is right."""
+    g = rnd(rows, cols, seed=19, dtype=BF)
+    out = torch.empty_like(g)
+    ws = torch.empty(fp8.fp8_orthogonalize_workspace_bytes(1, rows, cols), dtype=torch.uint8,
+                     device="cuda")
+    fp8.fp8_check_device_status()
+    old = fp8.fp8_set_wait_limit_ns(1)
+    try:
+        fp8.fp8_orthogonalize(g, out, ws)
+        with pytest.raises(fp8.Fp8Error) as e:
+            fp8.fp8_check_device_status()
+        assert e.value.status == 6  # FP8_ERR_TIMEOUT
+    finally:
+        fp8.fp8_set_wait_limit_ns(old)
+    check(run(g), by_products(g, [ABC] * 5))
+
+
+def test_two_streams_at_once():
+    """Two calls that may overlap, each with its own workspace: their resident
+    CTAs wait for one another within a call only."""
+    gs = [rnd(1500, 1500, seed=20 + i, dtype=BF) for i in range(2)]
+    outs = [torch.empty_like(g) for g in gs]
+    n = fp8.fp8_orthogonalize_workspace_bytes(1, 1500, 1500)
+    wss = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in gs]
+    streams = [torch.cuda.Stream() for _ in gs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, out, ws, s in zip(gs, outs, wss, streams):
+            fp8.fp8_orthogonalize(g, out, ws, stream=s)
+    torch.cuda.synchronize()
+    fp8.fp8_check_device_status()
+    for g, out in zip(gs, outs):
+        check(out, by_products(g, [ABC] * 5))
