@@ -11,7 +11,7 @@ orthogonalised gradients.  ``MoeLayer.serve`` is a forward of a few tokens
 whose rows are dispatched as E4M3 bytes under a scale kept from training, so
 the linears take them as they are.
 
-Run it:  python examples/moe_layer.py
+Run it:  python examples/moe_layer.py [tokens hidden experts topk steps]
 """
 from __future__ import annotations
 
@@ -169,4 +169,4 @@ def main(tokens=2048, hidden=1024, experts=8, topk=2, steps=5):
 
 
 if __name__ == "__main__":
-    main()
+    main(*map(int, sys.argv[1:]))

@@ -1255,7 +1255,7 @@ bool orthogonalize_fits(int64_t batch, int64_t rows, int64_t cols) {
     if (batch < 0 || rows < 0 || cols < 0 || rows > kOrthoMaxDim || cols > kOrthoMaxDim)
         return false;
     const int64_t tiles = ((rows + 127) / 128) * ((cols + 127) / 128);
-    return batch == 0 || tiles <= 0x7FFFFFFF / (3 * 64) / batch;
+    return batch == 0 || tiles <= 0x7FFFFFFF / (4 * 64) / batch;
 }
 
 }  // namespace

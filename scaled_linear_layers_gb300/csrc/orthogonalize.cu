@@ -193,10 +193,13 @@ struct NsPlan {
     int rows, cols, batch, steps, tall;
     int T, U;                  // tiles along the shorter and the longer side
     int tri, upd;              // tiles of a symmetric product and of X, per matrix
+    int splits;                // parts of A's contraction (128-tiles only)
     int per_step, tiles;       // over the batch; over all steps
     // memory
     uint16_t *direct;          // bf16 output without a tensor map (nullable)
-    uint32_t *flags;           // per matrix: of its A, B and X tiles
+    float *parts;              // [batch][tri][splits][BT][BT] of A, with splits
+    uint32_t *flags;           // per matrix: of its A, B and X tiles, and 8 of
+                               // each A tile's parts
     int flags_per;
     // arithmetic: step i has coefficients (a, b, c) at 3 i
     float coefficients[3 * kMaxSteps];
@@ -348,17 +351,19 @@ __device__ __forceinline__ bool scout_wait_bounded(const uint32_t *p, uint32_t h
 // along the shorter and r along the longer side.
 struct NsTile {
     int step, phase, z, r, c;
-    int tm, tn;  // row and column tile of the output
+    int tm, tn;   // row and column tile of the output
+    int split;    // which part of A's contraction
 };
 
 __device__ __forceinline__ NsTile ns_locate(const NsPlan &p, int i) {
     NsTile t;
     t.step = i / p.per_step;
     int k = i - t.step * p.per_step;
-    const int tri_all = p.tri * p.batch;
-    t.phase = k < tri_all ? kGram : k < 2 * tri_all ? kPoly : kUpdate;
+    const int gram = p.tri * p.splits, gram_all = gram * p.batch, poly_all = p.tri * p.batch;
+    t.phase = k < gram_all ? kGram : k < gram_all + poly_all ? kPoly : kUpdate;
+    t.split = 0;
     if (t.phase == kUpdate) {
-        k -= 2 * tri_all;
+        k -= gram_all + poly_all;
         t.z = k / p.upd;
         k -= t.z * p.upd;
         t.r = k / p.T;
@@ -366,11 +371,14 @@ __device__ __forceinline__ NsTile ns_locate(const NsPlan &p, int i) {
         t.tm = p.tall ? t.r : t.c;
         t.tn = p.tall ? t.c : t.r;
     } else {
-        k -= t.phase * tri_all;
-        t.z = k / p.tri;
+        const int per = t.phase == kGram ? gram : p.tri;
+        k -= t.phase == kGram ? 0 : gram_all;
+        t.z = k / per;
+        k -= t.z * per;
+        t.split = k / p.tri;
         // column by column: counted from the end, row by row of the mirrored
         // triangle
-        const int u = p.tri - 1 - (k - t.z * p.tri);
+        const int u = p.tri - 1 - (k - t.split * p.tri);
         int q = (int)((sqrtf(8.f * (float)u + 1.f) - 1.f) * 0.5f);
         while ((q + 1) * (q + 2) / 2 <= u) ++q;
         while (q * (q + 1) / 2 > u) --q;
@@ -391,6 +399,12 @@ __device__ __forceinline__ uint32_t *sym_flag(const NsPlan &p, int z, int phase,
 __device__ __forceinline__ uint32_t *x_flag(const NsPlan &p, int z, int r, int c) {
     return p.flags + (int64_t)z * p.flags_per + 2 * p.tri + r * p.T + c;
 }
+// The part of a tile's A that each epilogue warp keeps count of.
+__device__ __forceinline__ uint32_t *part_flag(const NsPlan &p, int z, int r, int c, int warp) {
+    return p.flags + (int64_t)z * p.flags_per + 2 * p.tri + p.upd +
+           NS_EPI_WARPS * (r * (r + 1) / 2 + c) + warp;
+}
+
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
@@ -563,6 +577,18 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
     // rows: both); B X contracts the rows of X: the second (tall, X B: neither);
     // A and B are their own transposes.
     auto blocks = [&](int phase) { return ((phase == kGram ? L : S) + 63) / 64; };
+    // the panels (of PANEL blocks) that a tile contracts
+    auto panels_of = [&](const NsTile &t, int &first, int &end) {
+        const int all = (blocks(t.phase) + PANEL - 1) / PANEL;
+        if (t.phase == kGram) {
+            const int per = (all + p.splits - 1) / p.splits;
+            first = min(all, t.split * per);
+            end = min(all, first + per);
+        } else {
+            first = 0;
+            end = all;
+        }
+    };
 
     if (warp == 0) {
         // ------------------------------------------------------- TMA producer
@@ -584,8 +610,10 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
                     mb = p.tall ? &maps.b : &maps.xm[cur];
                 }
                 const int arow = t.tm * BT + (int)rank * 128, brow = t.tn * BT + (int)rank * 128;
-                const int nk = blocks(t.phase), panels = (nk + PANEL - 1) / PANEL;
-                for (int kp = 0; kp < panels && ok;) {
+                const int nk = blocks(t.phase);
+                int first, panels;
+                panels_of(t, first, panels);
+                for (int kp = first; kp < panels && ok;) {
                     if (seen == want) {
                         ok = scout_wait_bounded(scouted, want, &seen, abort_flag, p.wait_limit_ns,
                                                 p.status);
@@ -626,7 +654,8 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
             bool ok = true;
             const uint32_t a0 = smem_u32(sA), b0 = smem_u32(sB);
             for (int i = worker; i < p.tiles && ok; i += workers, ++it) {
-                const int what = ns_locate(p, i).phase;
+                const NsTile t = ns_locate(p, i);
+                const int what = t.phase;
                 const int acc = it & 1;
                 const uint32_t acc_phase = (it >> 1) & 1;
                 if (!mbar_wait_bounded(&tempty[acc], acc_phase ^ 1u, abort_flag, p.wait_limit_ns,
@@ -634,7 +663,9 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
                     break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BT);
-                const int nk = blocks(what);
+                int first, panels;
+                panels_of(t, first, panels);
+                const int nk = min(blocks(what), panels * PANEL) - first * PANEL;
                 if (what == kGram && p.tall)
                     ok = ns_mma_tile<CG, true, true>(ring, a0, b0, d_tmem, nk, abort_flag, p);
                 else if (what == kUpdate && !p.tall)
@@ -663,8 +694,9 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
             // what the operands come from: A from the step's X, B from its A,
             // the new X from its B; the first X is there already
             const uint32_t done = (uint32_t)(t.phase == kGram ? t.step : t.step + 1) * ARRIVALS;
-            const int panels = (blocks(t.phase) + PANEL - 1) / PANEL;
-            for (int kp = 0; kp < panels && ok;) {
+            int first, panels;
+            panels_of(t, first, panels);
+            for (int kp = first; kp < panels && ok;) {
                 const int mine = kp + lane;
                 int run = 32;
                 if (done > 0) {
@@ -786,17 +818,75 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
                                    kStatusTimeoutEpilogue, p.status);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             tc_fence_after();
+            // A tile whose contraction is split: each part leaves its sums in
+            // fp32, and the warp that comes last to its 32 rows adds the parts,
+            // in their order, and goes on as if it had contracted alone.
+            const bool split = CG == 1 && t.phase == kGram && p.splits > 1;
+            const float *parts = nullptr;
+            if (split) {
+                const int64_t tile = (int64_t)t.z * p.tri + t.r * (t.r + 1) / 2 + t.c;
+                // a chunk's 32 x 32 sums as [8][32 lanes][4]: whole lines
+                float *all = p.parts + tile * p.splits * (BT * BT) + quarter * 32 * BT + lane * 4;
+                float *mine = all + (int64_t)t.split * (BT * BT);
 #pragma unroll 1
-            for (int c = half; c * 32 < width; c += 2) {
-                const int col = t.tn * BT + c * 32;
-                uint32_t r[32];
-                tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(quarter * 32) << 16) +
-                                       (uint32_t)(acc * BT + c * 32),
-                                   r);
-                tmem_ld_wait();
-                float v[32];
+                for (int c = half; c * 32 < width; c += 2) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(quarter * 32) << 16) +
+                                           (uint32_t)(acc * BT + c * 32),
+                                       r);
+                    tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * acc_mul;
+                    for (int j = 0; j < 32; j += 4)
+                        *reinterpret_cast<uint4 *>(mine + c * 1024 + j * 32) =
+                            make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
+                }
+                __threadfence();
+                __syncwarp();
+                uint32_t before = 0;
+                if (lane == 0)
+                    before = atomicAdd(part_flag(p, t.z, t.r, t.c, warp - 2), 1u);
+                before = __shfl_sync(0xFFFFFFFFu, before, 0);
+                __threadfence();
+                if (before + 1 == (uint32_t)(t.step + 1) * p.splits) parts = all;
+            }
+#pragma unroll 1
+            for (int c = half; c * 32 < width && (!split || parts != nullptr); c += 2) {
+                const int col = t.tn * BT + c * 32;
+                float v[32];
+                if (split) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0.f;
+                    const float *from = parts + c * 1024;
+#pragma unroll 1
+                    for (int k = 0; k < p.splits; k += 2) {
+                        const bool two = k + 1 < p.splits;
+                        float4 f[2][8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float *at = from + (int64_t)k * (BT * BT) + j * 128;
+                            f[0][j] = __ldcg(reinterpret_cast<const float4 *>(at));
+                            f[1][j] = two ? __ldcg(reinterpret_cast<const float4 *>(at + BT * BT))
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+                        }
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                v[4 * j] += f[u][j].x, v[4 * j + 1] += f[u][j].y;
+                                v[4 * j + 2] += f[u][j].z, v[4 * j + 3] += f[u][j].w;
+                            }
+                    }
+                } else {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(quarter * 32) << 16) +
+                                           (uint32_t)(acc * BT + c * 32),
+                                       r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] *= acc_mul;
                 if (e != nullptr) {
                     ok = mbar_wait_bounded(ebar, ephase, abort_flag, p.wait_limit_ns,
                                            kStatusTimeoutTma, p.status);
@@ -895,7 +985,7 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
             if (lane == 0) {
                 if constexpr (CG == 2) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
                 else mbar_arrive(&tempty[acc]);
-                if (!(update && last)) {
+                if (!(update && last) && (!split || parts != nullptr)) {
                     // this warp's part is in memory: announce it
                     bulk_wait_group_all();
                     fence_proxy_async_all();
@@ -1049,11 +1139,20 @@ int64_t pad256(int64_t v) { return (v + 255) / 256 * 256; }
 
 constexpr int kPrepParts = 2048;  // blocks that share a matrix in the scaling, at most
 
+// A's contraction is split where its 128-tiles would leave CTAs idle: up to 16
+// tiles to a side, 8 parts of at least 8 blocks of 64, from a contraction of
+// 2048 on (us without / with: 128 x 8192 240 / 131, 512 x 4096 196 / 158, 512 x
+// 2048 150 / 143; 256 x 1024, not split, 114 / 118; 16 parts of 128 x 8192: 135).
+constexpr int64_t kSplitMaxSide = 2048, kSplitMinLength = 2048, kSplitMinBlocks = 8,
+                  kSplitMost = 8;
+
 struct NsLayout {
-    int64_t ldx, lds, x[2], lo[2], a, b, sums, flags, bytes;
+    int64_t ldx, lds, x[2], lo[2], a, b, sums, flags, parts, parts_bytes, bytes;
 };
 
-int64_t ns_flags_per(int64_t T, int64_t U) { return T * (T + 1) + U * T; }
+int64_t ns_flags_per(int64_t T, int64_t U) {
+    return T * (T + 1) + U * T + NS_EPI_WARPS * T * (T + 1) / 2;
+}
 
 NsLayout ns_layout(int64_t batch, int64_t rows, int64_t cols) {
     NsLayout w;
@@ -1075,6 +1174,9 @@ NsLayout ns_layout(int64_t batch, int64_t rows, int64_t cols) {
     w.b = take(q);
     w.sums = take(pad256(batch * kPrepParts * (int64_t)sizeof(SquareSums)));
     w.flags = take(pad256(batch * ns_flags_per((s + 127) / 128, (l + 127) / 128) * 4));
+    // parts of A where its tiles are few and its contraction is long
+    w.parts_bytes = s <= kSplitMaxSide && l >= kSplitMinLength ? x : 0;
+    w.parts = take(w.parts_bytes);
     w.bytes = at;
     return w;
 }
@@ -1121,13 +1223,25 @@ cudaError_t launch_orthogonalize(const Orthogonalize &o, cudaStream_t s, const c
     if (e != cudaSuccess) return e;
     e = ns_resident<1>(&singles);
     if (e != cudaSuccess) return e;
-    auto cost = [&](int bt, int workers, double block) {
+    // Parts of A's contraction for the single CTAs: as many as give idle ones
+    // work, leave each enough to do and fit the memory for their sums.
+    int64_t splits = 1;
+    {
+        const int64_t T = (S + 127) / 128, tiles = o.batch * (T * (T + 1) / 2);
+        splits = std::min<int64_t>(singles / tiles, (L + 63) / 64 / kSplitMinBlocks);
+        splits = std::min<int64_t>(splits, kSplitMost);
+        splits = std::min<int64_t>(splits, w.parts_bytes / (tiles * 128 * 128 * 4));
+        if (splits < 2) splits = 1;
+        const int64_t panels = (L + 127) / 128, per = (panels + splits - 1) / splits;
+        splits = (panels + per - 1) / per;  // none without a panel
+    }
+    auto cost = [&](int bt, int workers, double block, int64_t parts) {
         const int64_t T = (S + bt - 1) / bt, U = (L + bt - 1) / bt;
         const double tri = (double)(o.batch * T * (T + 1) / 2) / workers,
                      upd = (double)(o.batch * T * U) / workers;
-        return block * ((tri > 1 ? tri : 1) * (double)(L + S) + (upd > 1 ? upd : 1) * (double)S);
+        return block * (std::max(tri, 1. / parts) * L + std::max(tri, 1.) * S + std::max(upd, 1.) * S);
     };
-    const bool pair = cost(256, pairs, 375) <= cost(128, singles, 297);
+    const bool pair = cost(256, pairs, 375, 1) <= cost(128, singles, 297, splits);
     const int bt = pair ? 256 : 128;
 
     NsPlan p = {};
@@ -1137,7 +1251,9 @@ cudaError_t launch_orthogonalize(const Orthogonalize &o, cudaStream_t s, const c
     p.U = (int)((L + bt - 1) / bt);
     p.tri = p.T * (p.T + 1) / 2;
     p.upd = p.T * p.U;
-    const int64_t per_step = o.batch * (2 * (int64_t)p.tri + p.upd);
+    p.splits = pair ? 1 : (int)splits;
+    p.parts = reinterpret_cast<float *>(base + w.parts);
+    const int64_t per_step = o.batch * ((int64_t)p.tri * (p.splits + 1) + p.upd);
     if (per_step * o.steps > 0x7FFFFFFF) {
         *why = "too many tiles";
         return cudaErrorInvalidValue;

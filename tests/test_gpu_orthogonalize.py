@@ -100,6 +100,17 @@ def test_many_tiles_of_both_kinds():
     check(run(g), by_products(g, [ABC] * 5))
 
 
+@pytest.mark.parametrize("batch, rows, cols", [
+    (1, 64, 1024), (1, 100, 8000), (1, 8191, 130), (1, 128, 1100), (1, 200, 5001), (3, 257, 2049),
+    (2, 3000, 300), (1, 640, 4097), (20, 50, 1500)])
+def test_few_tiles_and_a_long_contraction(batch, rows, cols):
+    """A's contraction is split over CTAs and its parts are added in order."""
+    g = rnd(batch, rows, cols, seed=21, dtype=BF)
+    out = run(g)
+    check(out, by_products(g, [ABC] * 5))
+    assert torch.equal(out, run(g))
+
+
 @pytest.mark.parametrize("kind", ["low rank", "decay", "outlier"])
 def test_spectra(kind):
     """Small singular values beside large ones, which the first steps raise."""
