@@ -76,7 +76,7 @@ constexpr int teams(int tpr) { return block_threads(tpr) / tpr; }
 // Blocks an SM should hold, by the registers that a thread needs; the
 // backward's also by the partial sums that each block leaves.
 constexpr int fwd_blocks(int tpr, int ept) {
-    return tpr > 512 ? 1 : (ept > 16 ? 512 : 768) / block_threads(tpr);
+    return tpr > 512 ? 1 : (ept > 16 ? 512 : ept > 8 ? 768 : 1024) / block_threads(tpr);
 }
 constexpr int bwd_blocks(int tpr) { return tpr > 256 ? 1 : tpr == 128 ? 3 : 2; }
 
@@ -108,16 +108,32 @@ struct Ring {
     volatile int *abort;
     int stages;
     uint32_t slot;
-    int64_t asked;  // (leader) rows requested: the k-th uses slot k % stages
+    int failed_slot;  // of this thread's first wait that ran out; -1: none did
+    uint32_t failed_phase;
 
-    __device__ __forceinline__ bool open() { return *abort == 0 && ++asked > 0; }
+    __device__ __forceinline__ void wait(int at, uint32_t phase, uint64_t limit_ns,
+                                         unsigned int *status) {
+        if (!mbar_wait_bounded(&bars[at], phase, abort, limit_ns, kStatusTimeoutTma, status) &&
+            failed_slot < 0) {
+            failed_slot = at;
+            failed_phase = phase;
+        }
+    }
 
+    // (leader, which requests nothing after a wait of its own that ran out)
+    __device__ __forceinline__ bool open() const { return failed_slot < 0; }
+
+    // The leader waited for all it requested, or, after a failure, for all but
+    // what went into the slots from that one on: bounded waits for those.
     __device__ __forceinline__ void settle(unsigned int *status) {
-        if (*abort == 0) return;
+        if (failed_slot < 0) return;
         volatile int no_abort = 0;
-        for (int64_t k = asked > stages ? asked - stages : 0; k < asked; ++k)
-            mbar_wait_bounded(&bars[k % stages], (uint32_t)(k / stages) & 1u, &no_abort, 10000000ull,
-                              kStatusTimeoutTma, status);
+        for (int i = 0; i < stages; ++i) {
+            const int at = failed_slot + i;
+            const bool wrapped = at >= stages;
+            mbar_wait_bounded(&bars[wrapped ? at - stages : at], failed_phase ^ (wrapped ? 1u : 0u),
+                              &no_abort, 10000000ull, kStatusTimeoutTma, status);
+        }
     }
 
     template <int TEAMS>
@@ -125,7 +141,7 @@ struct Ring {
                                          bool leader) {
         stages = n;
         slot = slot_bytes;
-        asked = 0;
+        failed_slot = -1;
         data = smem + (size_t)team * n * slot_bytes;
         uint64_t *all = reinterpret_cast<uint64_t *>(smem + (size_t)TEAMS * n * slot_bytes);
         bars = all + team * n;
@@ -363,8 +379,7 @@ __global__ void __launch_bounds__(block_threads(TPR), fwd_blocks(TPR, EPT))
          first += step, row += step) {
         const bool in = row < a.rows;
         if (in)
-            mbar_wait_bounded(&ring.bars[slot], phase, ring.abort, a.wait_limit_ns,
-                              kStatusTimeoutTma, a.status);
+            ring.wait(slot, phase, a.wait_limit_ns, a.status);
         const T *src = reinterpret_cast<const T *>(ring.data + slot * bytes);
         uint64_t f[Row::P];
         Row::unpack(
@@ -697,8 +712,7 @@ __global__ void __launch_bounds__(block_threads(TPR), bwd_blocks(TPR))
         const float mean = nmean, rstd = nrstd;
         if (row + step < a.rows) nmean = a.mean[row + step], nrstd = a.rstd[row + step];
         if (in)
-            mbar_wait_bounded(&ring.bars[slot], phase, ring.abort, a.wait_limit_ns,
-                              kStatusTimeoutTma, a.status);
+            ring.wait(slot, phase, a.wait_limit_ns, a.status);
         const T *sx = reinterpret_cast<const T *>(ring.data + slot * ring.slot);
         const T *sg = reinterpret_cast<const T *>(ring.data + slot * ring.slot + bytes);
         auto load = [&](const T *p, int j) {
