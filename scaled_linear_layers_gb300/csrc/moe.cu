@@ -15,8 +15,18 @@
 // An id outside 0..experts-1 drops its assignment (row_of = -1): it has no
 // row, adds nothing and has a zero weight gradient.  Everything but the sort
 // moves rows and is bound by HBM; all kernels go token by token, so x, dy and
-// y move once and the sorted rows once, and sums over j run in a fixed order
-// in fp32.
+// y move once and the sorted rows once (expert by expert the tokens' rows
+// would be read topk times: copies of one token lie far apart), and sums over j
+// run in a fixed order in fp32.  All of a token's loads are issued before the
+// first is used.
+//
+// Measured (device time; share of the copy bandwidth): combine of 16384 x 2048,
+// top 6 of 64, bf16 69 us (1.00); its backward 150 us (0.86), of 16384 x 4096
+// top 4 of 32 191 us (0.94); dispatch of 16384 x 4096 to 2 of 8 as E4M3 with the
+// sort 54 us (0.74: the sort 5 us, clearing the amax 2); rows of odd width,
+// 5003 x 1001 top 6, combine 27 us (0.39), backward 54 us (0.36): their instructions
+// for shifting rows into place, and waves of few tokens, keep them from it.  The
+// sort: 64 assignments 2.7 us, 32768 4.8 us, 131072 8.3 us.
 #include <type_traits>
 
 #include "common.cuh"
