@@ -325,7 +325,8 @@ __device__ __forceinline__ bool flag_wait_bounded(const uint32_t *p, uint32_t ta
     }
 }
 
-// The scout's word to the producer, in shared memory.
+// The words of the scout to the producer (panels found) and back (its tile),
+// in shared memory.
 __device__ __forceinline__ void store_release_cta(uint32_t *p, uint32_t v) {
     asm volatile("st.release.cta.shared.u32 [%0], %1;" ::"r"(smem_u32(p)), "r"(v) : "memory");
 }
@@ -335,14 +336,14 @@ __device__ __forceinline__ uint32_t load_acquire_cta(const uint32_t *p) {
     return v;
 }
 
-// Waits until the scout has found more than `have` panels; *seen: how many.
-__device__ __forceinline__ bool scout_wait_bounded(const uint32_t *p, uint32_t have, uint32_t *seen,
-                                                   volatile int *abort, uint64_t limit_ns,
-                                                   unsigned int *status) {
-    if ((*seen = load_acquire_cta(p)) != have) return true;
+// Waits until a word of shared memory is at least `least`; *seen: what it is.
+__device__ __forceinline__ bool word_wait_bounded(const uint32_t *p, uint32_t least, uint32_t *seen,
+                                                  volatile int *abort, uint64_t limit_ns,
+                                                  unsigned int *status) {
+    if ((*seen = load_acquire_cta(p)) >= least) return true;
     const uint64_t t0 = global_timer_ns();
     for (uint32_t i = 1;; ++i) {
-        if ((*seen = load_acquire_cta(p)) != have) return true;
+        if ((*seen = load_acquire_cta(p)) >= least) return true;
         if ((i & 63u) == 0) {
             if (*abort) return false;
             if (global_timer_ns() - t0 > limit_ns) {
@@ -537,7 +538,7 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
     uint64_t *tempty = tfull + 2, *drain = tempty + 2, *ebars = drain + 1;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(ebars + NS_EPI_WARPS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
-    uint32_t *scouted = tmem_holder + 2;
+    uint32_t *scouted = tmem_holder + 2, *filling = tmem_holder + 3;
     uint8_t *staging = smem + NS_STAGES * NS_STAGE + 1024;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -557,7 +558,7 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
         mbar_init(drain, 1);
         for (int w = 0; w < NS_EPI_WARPS; ++w) mbar_init(&ebars[w], 1);
         *abort_flag = 0;
-        *scouted = 0;
+        *scouted = *filling = 0;
         fence_mbarrier_init();
         tma_prefetch_desc(&maps.x[0]);
         tma_prefetch_desc(&maps.x[1]);
@@ -604,7 +605,9 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
         if (lane == 0) {
             uint32_t want = 0, seen = 0;  // panels of the contraction, over all tiles
             const uint32_t a0 = smem_u32(sA), b0 = smem_u32(sB);
-            for (int i = worker; i < p.tiles && ok; i += workers) {
+            uint32_t n = 0;
+            for (int i = worker; i < p.tiles && ok; i += workers, ++n) {
+                store_release_cta(filling, n);
                 const NsTile t = ns_locate(p, i);
                 const int cur = t.step & 1;
                 const CUtensorMap *ma, *mb;
@@ -622,8 +625,8 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
                 panels_of(t, first, panels);
                 for (int kp = first; kp < panels && ok;) {
                     if (seen == want) {
-                        ok = scout_wait_bounded(scouted, want, &seen, abort_flag, p.wait_limit_ns,
-                                                p.status);
+                        ok = word_wait_bounded(scouted, want + 1, &seen, abort_flag,
+                                               p.wait_limit_ns, p.status);
                         fence_proxy_async_all();
                         if (!ok) break;
                     }
@@ -693,10 +696,15 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
         // ---------------------------------------------------------- scout
         // Looks at the counters ahead of the producer, 32 panels of the
         // contraction at a time, and tells it how many are there: the looking
-        // takes longer than the producer has between two tiles.
-        uint32_t found = 0;
+        // takes longer than the producer has between two tiles.  It stays one
+        // tile ahead (further, its waits would last as long as a product).
+        uint32_t found = 0, n = 0, at;
         bool ok = true;
-        for (int i = worker; i < p.tiles && ok; i += workers) {
+        for (int i = worker; i < p.tiles && ok; i += workers, ++n) {
+            ok = word_wait_bounded(filling, n > 0 ? n - 1 : 0, &at, abort_flag, p.wait_limit_ns,
+                                   p.status);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
             const NsTile t = ns_locate(p, i);
             // what the operands come from: A from the step's X, B from its A,
             // the new X from its B; the first X is there already
