@@ -16,9 +16,8 @@
 // squares about the mean (a second sum over registers: no cancellation) and
 // the output need one read of the row.  Many rows (norm_*_ring_kernel) come
 // through a ring of bulk copies in shared memory, several rows ahead of the
-// sums, so the loads in flight do not depend on registers; few rows, and rows
-// that 16-byte copies cannot take, are loaded straight into registers one row
-// ahead.  All sums are fp32; the mean's, whose terms cancel, adds leading bits
+// sums, so the loads in flight do not depend on registers; few rows are loaded
+// straight into registers one row ahead.  All sums are fp32; the mean's, whose terms cancel, adds leading bits
 // and rests apart.
 //
 // Measured at 16384 x 4096 (device time; share of the copy bandwidth): bf16
@@ -28,8 +27,8 @@
 // within 0.05 of that.  What keeps the E4M3 form from its 30 us is the work on a
 // row between two barriers (issue slots 60 % busy, DRAM 62 %), which is why
 // elements are worked on in pairs and a thread holds as many as fit.  Rows of odd
-// width move single elements: bf16 3001 x 4095 forward 19 us (0.38), fp32 22 us
-// (0.66).  One row of 4096: 3.5 us, a launch's latency.
+// width move single elements: bf16 8192 x 8191 forward 74 us (0.53), fp32 89 us
+// (0.89).  One row of 4096: 3.5 us, a launch's latency.
 #include <algorithm>
 #include <atomic>
 
@@ -168,6 +167,59 @@ struct Ring {
 
 size_t ring_bytes(int team_count, int stages, size_t slot) {
     return (size_t)team_count * stages * (slot + sizeof(uint64_t)) + 16;
+}
+
+// A row's place in a slot.  Rows that 16-byte copies fit are copied as they
+// are; of others the whole aligned 16-byte groups that hold them, so the row
+// starts up to 15 bytes into the slot.  A row whose groups reach past its
+// tensor (its first or last) is not copied: it is read where it is.
+template <typename T, bool VECTOR>
+struct RowSource {
+    const T *p;
+    int64_t ld;
+    uint32_t bytes;     // of a row
+    uintptr_t lo, hi;   // of the tensor
+
+    __device__ __forceinline__ RowSource(const void *base, int64_t rows, int64_t stride, int cols) {
+        p = reinterpret_cast<const T *>(base);
+        ld = stride;
+        bytes = (uint32_t)cols * sizeof(T);
+        lo = reinterpret_cast<uintptr_t>(p);
+        hi = reinterpret_cast<uintptr_t>(p + (rows - 1) * ld + cols);
+    }
+    static __host__ __device__ __forceinline__ uint32_t slot(uint32_t row_bytes) {
+        return VECTOR ? row_bytes : ((row_bytes + 15u) & ~15u) + 16u;
+    }
+    __device__ __forceinline__ bool copied(int64_t r, uintptr_t &first, uintptr_t &end) const {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p + r * ld);
+        first = VECTOR ? at : at & ~uintptr_t(15);
+        end = VECTOR ? at + bytes : (at + bytes + 15) & ~uintptr_t(15);
+        return VECTOR || (first >= lo && end <= hi);
+    }
+    // (leader) bytes that request() will bring
+    __device__ __forceinline__ uint32_t size(int64_t r) const {
+        uintptr_t first, end;
+        return copied(r, first, end) ? (uint32_t)(end - first) : 0u;
+    }
+    __device__ __forceinline__ void request(int64_t r, uint8_t *to, uint64_t *bar) const {
+        uintptr_t first, end;
+        if (copied(r, first, end))
+            bulk_load(to, reinterpret_cast<const void *>(first), (uint32_t)(end - first), bar);
+    }
+    __device__ __forceinline__ const T *row(int64_t r, const uint8_t *from) const {
+        uintptr_t first, end;
+        if (VECTOR) return reinterpret_cast<const T *>(from);
+        const T *global = p + r * ld;
+        return copied(r, first, end)
+                   ? reinterpret_cast<const T *>(from + (reinterpret_cast<uintptr_t>(global) & 15u))
+                   : global;
+    }
+};
+
+// Arms a slot's barrier for `bytes` (a phase without a copy completes at once).
+__device__ __forceinline__ void slot_expect(uint64_t *bar, uint32_t bytes) {
+    if (bytes > 0) mbar_arrive_expect_tx(bar, bytes);
+    else mbar_arrive(bar);
 }
 
 // ---------------------------------------------------------------- forward ---
@@ -357,26 +409,26 @@ __global__ void __launch_bounds__(block_threads(TPR), fwd_blocks(TPR, EPT))
     if (a.amax != nullptr) amax_commit(n.amax, a.amax);
 }
 
-template <typename T, int TPR, int EPT, bool FULL>
+template <typename T, bool VECTOR, int TPR, int EPT, bool FULL>
 __global__ void __launch_bounds__(block_threads(TPR), fwd_blocks(TPR, EPT))
     norm_fwd_ring_kernel(const NormArgs a) {
-    using RV = RowVec<T, true>;
-    using Row = NormRow<T, true, TPR, EPT, FULL>;
+    using RV = RowVec<T, VECTOR>;
+    using Row = NormRow<T, VECTOR, TPR, EPT, FULL>;
+    using Source = RowSource<T, VECTOR>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float red[2][2 * (TPR > 32 ? TPR / 32 : 1)];
     const int t = threadIdx.x % TPR, team = threadIdx.x / TPR;
-    const uint32_t bytes = (uint32_t)a.cols * sizeof(T);
+    const Source x(a.x, a.rows, a.ldx, a.cols);
     Ring ring = {};
-    ring.init<teams(TPR)>(smem, a.stages, bytes, team, t == 0);
+    ring.init<teams(TPR)>(smem, a.stages, Source::slot(x.bytes), team, t == 0);
     pdl_wait_prior();
     pdl_allow_next();
-    const T *x = reinterpret_cast<const T *>(a.x);
     const int64_t step = (int64_t)gridDim.x * teams(TPR);
     int64_t row = (int64_t)blockIdx.x * teams(TPR) + team;
     auto request = [&](int64_t r, int slot) {
         if (r < a.rows && ring.open()) {
-            mbar_arrive_expect_tx(&ring.bars[slot], bytes);
-            bulk_load(ring.data + slot * bytes, x + r * a.ldx, bytes, &ring.bars[slot]);
+            slot_expect(&ring.bars[slot], x.size(r));
+            x.request(r, ring.data + slot * ring.slot, &ring.bars[slot]);
         }
     };
     if (t == 0)
@@ -390,7 +442,7 @@ __global__ void __launch_bounds__(block_threads(TPR), fwd_blocks(TPR, EPT))
         const bool in = row < a.rows;
         if (in)
             ring.wait(slot, phase, a.wait_limit_ns, a.status);
-        const T *src = reinterpret_cast<const T *>(ring.data + slot * bytes);
+        const T *src = x.row(row, ring.data + slot * ring.slot);
         uint64_t f[Row::P];
         Row::unpack(
             [&](int j) {
@@ -685,28 +737,29 @@ __global__ void __launch_bounds__(block_threads(TPR), bwd_blocks(TPR))
 // A slot holds the row's x, then its dy; it is read twice, for the sums and
 // for dx, and asked to be filled again one turn later, when the next row's
 // sums show that every member is past it.
-template <typename T, int TPR, int EPT, bool FULL>
+template <typename T, bool VECTOR, int TPR, int EPT, bool FULL>
 __global__ void __launch_bounds__(block_threads(TPR), bwd_blocks(TPR))
     norm_bwd_ring_kernel(const NormBwdArgs a) {
-    using Row = NormBwdRow<T, true, TPR, EPT, FULL>;
+    using Row = NormBwdRow<T, VECTOR, TPR, EPT, FULL>;
     using RV = typename Row::RV;
+    using Source = RowSource<T, VECTOR>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float red[2][2 * (TPR > 32 ? TPR / 32 : 1)];
     const int t = threadIdx.x % TPR, team = threadIdx.x / TPR;
-    const uint32_t bytes = (uint32_t)a.cols * sizeof(T);
+    const Source x(a.x, a.rows, a.ldx, a.cols), dy(a.dy, a.rows, a.lddy, a.cols);
+    const uint32_t half = Source::slot(x.bytes);
     Ring ring = {};
-    ring.init<teams(TPR)>(smem, a.stages, 2 * bytes, team, t == 0);
+    ring.init<teams(TPR)>(smem, a.stages, 2 * half, team, t == 0);
     pdl_wait_prior();
     pdl_allow_next();
-    const T *x = reinterpret_cast<const T *>(a.x), *dy = reinterpret_cast<const T *>(a.dy);
     const int64_t step = (int64_t)gridDim.x * teams(TPR);
     int64_t row = (int64_t)blockIdx.x * teams(TPR) + team;
     auto request = [&](int64_t r, int slot) {
         if (r < a.rows && ring.open()) {
             uint8_t *to = ring.data + slot * ring.slot;
-            mbar_arrive_expect_tx(&ring.bars[slot], 2 * bytes);
-            bulk_load(to, x + r * a.ldx, bytes, &ring.bars[slot]);
-            bulk_load(to + bytes, dy + r * a.lddy, bytes, &ring.bars[slot]);
+            slot_expect(&ring.bars[slot], x.size(r) + dy.size(r));
+            x.request(r, to, &ring.bars[slot]);
+            dy.request(r, to + half, &ring.bars[slot]);
         }
     };
     if (t == 0)
@@ -723,8 +776,8 @@ __global__ void __launch_bounds__(block_threads(TPR), bwd_blocks(TPR))
         if (row + step < a.rows) nmean = a.mean[row + step], nrstd = a.rstd[row + step];
         if (in)
             ring.wait(slot, phase, a.wait_limit_ns, a.status);
-        const T *sx = reinterpret_cast<const T *>(ring.data + slot * ring.slot);
-        const T *sg = reinterpret_cast<const T *>(ring.data + slot * ring.slot + bytes);
+        const T *sx = x.row(row, ring.data + slot * ring.slot);
+        const T *sg = dy.row(row, ring.data + slot * ring.slot + half);
         auto load = [&](const T *p, int j) {
             return in && Row::inside(a.cols, j * Row::V) ? RV::load(p + Row::column(j * Row::V))
                                                          : RV::zero();
@@ -889,14 +942,14 @@ cudaError_t plan_ring(int threads, int team_count, int64_t rows, size_t slot, Ri
     return cudaSuccess;
 }
 
-template <typename T, int TPR, int EPT, bool FULL = false>
+template <typename T, bool VECTOR, int TPR, int EPT, bool FULL = false>
 cudaError_t run_fwd_ring(NormArgs a, cudaStream_t s, bool *done) {
-    if constexpr (!FULL && TPR * EPT % 1024 == 0)
-        if (a.cols == TPR * EPT) return run_fwd_ring<T, TPR, EPT, true>(a, s, done);
-    constexpr auto ring = norm_fwd_ring_kernel<T, TPR, EPT, FULL>;
+    if constexpr (VECTOR && !FULL && TPR * EPT % 1024 == 0)
+        if (a.cols == TPR * EPT) return run_fwd_ring<T, true, TPR, EPT, true>(a, s, done);
+    constexpr auto ring = norm_fwd_ring_kernel<T, VECTOR, TPR, EPT, FULL>;
     RingPlan r;
-    cudaError_t e =
-        plan_ring<ring>(block_threads(TPR), teams(TPR), a.rows, a.cols * sizeof(T), &r);
+    cudaError_t e = plan_ring<ring>(block_threads(TPR), teams(TPR), a.rows,
+                                    RowSource<T, VECTOR>::slot(a.cols * sizeof(T)), &r);
     if (e != cudaSuccess || r.stages == 0) return e;
     a.stages = r.stages;
     *done = true;
@@ -905,14 +958,20 @@ cudaError_t run_fwd_ring(NormArgs a, cudaStream_t s, bool *done) {
 
 // Many rows: 32 elements to a thread where the row fills them, so that the
 // sums over the team cost less an element (16384 x 4096 to E4M3: 39 us; with 16 elements 53).
-template <typename T>
+// Rows that 16-byte copies do not fit gain by the ring (bf16 16384 x 333: 13 us,
+// straight into registers 21; 8192 x 8191: 74 and 97) except where a warp would
+// work on 32 single elements a thread (16384 x 1001: 30 and 23).
+template <typename T, bool VECTOR>
 cudaError_t pick_fwd_ring(const NormArgs &a, cudaStream_t s, bool *done) {
-    if (a.cols <= 512) return run_fwd_ring<T, 32, 16>(a, s, done);
-    if (a.cols <= 1024) return run_fwd_ring<T, 32, 32>(a, s, done);
-    if (a.cols <= 2048) return run_fwd_ring<T, 128, 16>(a, s, done);
-    if (a.cols <= 4096) return run_fwd_ring<T, 128, 32>(a, s, done);
-    if (a.cols <= 8192) return run_fwd_ring<T, 256, 32>(a, s, done);
-    if (a.cols <= 16384) return run_fwd_ring<T, 512, 32>(a, s, done);
+    if (a.cols <= 512) return run_fwd_ring<T, VECTOR, 32, 16>(a, s, done);
+    if (a.cols <= 1024) {
+        if constexpr (VECTOR) return run_fwd_ring<T, VECTOR, 32, 32>(a, s, done);
+        else return cudaSuccess;
+    }
+    if (a.cols <= 2048) return run_fwd_ring<T, VECTOR, 128, 16>(a, s, done);
+    if (a.cols <= 4096) return run_fwd_ring<T, VECTOR, 128, 32>(a, s, done);
+    if (a.cols <= 8192) return run_fwd_ring<T, VECTOR, 256, 32>(a, s, done);
+    if (a.cols <= 16384) return run_fwd_ring<T, VECTOR, 512, 32>(a, s, done);
     return cudaSuccess;
 }
 
@@ -929,11 +988,9 @@ cudaError_t run_fwd(const NormArgs &a, cudaStream_t s) {
 template <typename T, bool VECTOR>
 cudaError_t pick_fwd(const NormArgs &a, cudaStream_t s) {
     constexpr int EPT = VECTOR ? 16 : 8;
-    if constexpr (VECTOR) {
-        bool done = false;
-        cudaError_t e = pick_fwd_ring<T>(a, s, &done);
-        if (e != cudaSuccess || done) return e;
-    }
+    bool done = false;
+    cudaError_t re = pick_fwd_ring<T, VECTOR>(a, s, &done);
+    if (re != cudaSuccess || done) return re;
     switch (threads_for(a.cols, EPT, 1024)) {
     case 32: return run_fwd<T, VECTOR, 32, EPT>(a, s);
     case 128: return run_fwd<T, VECTOR, 128, EPT>(a, s);
@@ -947,14 +1004,15 @@ cudaError_t pick_fwd(const NormArgs &a, cudaStream_t s) {
     return launch_pdl(norm_fwd_wide_kernel<T>, grid, kWideThreads, 0, s, a);
 }
 
-template <typename T, int TPR, int EPT, bool FULL = false>
+template <typename T, bool VECTOR, int TPR, int EPT, bool FULL = false>
 cudaError_t run_bwd_ring(NormBwdArgs a, int *parts, cudaStream_t s, bool *done) {
-    if constexpr (!FULL && TPR * EPT % 1024 == 0)
-        if (a.cols == TPR * EPT) return run_bwd_ring<T, TPR, EPT, true>(a, parts, s, done);
-    constexpr auto ring = norm_bwd_ring_kernel<T, TPR, EPT, FULL>;
+    if constexpr (VECTOR && !FULL && TPR * EPT % 1024 == 0)
+        if (a.cols == TPR * EPT) return run_bwd_ring<T, true, TPR, EPT, true>(a, parts, s, done);
+    constexpr auto ring = norm_bwd_ring_kernel<T, VECTOR, TPR, EPT, FULL>;
     RingPlan r;
     cudaError_t e =
-        plan_ring<ring>(block_threads(TPR), teams(TPR), a.rows, 2 * a.cols * sizeof(T), &r,
+        plan_ring<ring>(block_threads(TPR), teams(TPR), a.rows,
+                        2 * (size_t)RowSource<T, VECTOR>::slot(a.cols * sizeof(T)), &r,
                         teams(TPR) > 1 ? teams(TPR) * TPR * EPT * sizeof(float) : 0);
     if (e != cudaSuccess || r.stages == 0) return e;
     a.stages = r.stages;
@@ -963,17 +1021,26 @@ cudaError_t run_bwd_ring(NormBwdArgs a, int *parts, cudaStream_t s, bool *done) 
     return launch_pdl(ring, r.grid, block_threads(TPR), r.bytes, s, a);
 }
 
-template <typename T>
+// Rows that 16-byte copies do not fit: narrow ones gain by the ring (bf16 16384
+// x 333: 18 us, straight into registers 28), wide ones only in fp32 (16384 x
+// 1999: 66 and 77; bf16 66 and 56, whose single elements are taken apart twice
+// from a slot but once from registers; at 1001 columns neither gains).
+template <typename T, bool VECTOR>
 cudaError_t pick_bwd_ring(const NormBwdArgs &a, int *parts, cudaStream_t s, bool *done) {
-    if (a.cols <= 512) return run_bwd_ring<T, 32, 16>(a, parts, s, done);
-    if (a.cols <= 1024) {
-        if constexpr (sizeof(T) == 2) return run_bwd_ring<T, 32, 32>(a, parts, s, done);
-        else return run_bwd_ring<T, 128, 8>(a, parts, s, done);
+    if (a.cols <= 512) return run_bwd_ring<T, VECTOR, 32, 16>(a, parts, s, done);
+    if constexpr (VECTOR) {
+        if (a.cols <= 1024) {
+            if constexpr (sizeof(T) == 2) return run_bwd_ring<T, VECTOR, 32, 32>(a, parts, s, done);
+            else return run_bwd_ring<T, VECTOR, 128, 8>(a, parts, s, done);
+        }
     }
-    if (a.cols <= 2048) return run_bwd_ring<T, 128, 16>(a, parts, s, done);
-    if (a.cols <= 4096) return run_bwd_ring<T, 256, 16>(a, parts, s, done);
-    if (a.cols <= 8192) return run_bwd_ring<T, 512, 16>(a, parts, s, done);
-    if (a.cols <= 16384) return run_bwd_ring<T, 512, 32>(a, parts, s, done);
+    if constexpr (VECTOR || sizeof(T) == 4) {
+        if (a.cols <= 1024) return cudaSuccess;
+        if (a.cols <= 2048) return run_bwd_ring<T, VECTOR, 128, 16>(a, parts, s, done);
+        if (a.cols <= 4096) return run_bwd_ring<T, VECTOR, 256, 16>(a, parts, s, done);
+        if (a.cols <= 8192) return run_bwd_ring<T, VECTOR, 512, 16>(a, parts, s, done);
+        if (a.cols <= 16384) return run_bwd_ring<T, VECTOR, 512, 32>(a, parts, s, done);
+    }
     return cudaSuccess;
 }
 
@@ -991,11 +1058,9 @@ cudaError_t run_bwd(const NormBwdArgs &a, int *parts, cudaStream_t s) {
 template <typename T, bool VECTOR>
 cudaError_t pick_bwd(const NormBwdArgs &a, int *parts, cudaStream_t s) {
     constexpr int EPT = VECTOR ? 16 : 8;
-    if constexpr (VECTOR) {
-        bool done = false;
-        cudaError_t e = pick_bwd_ring<T>(a, parts, s, &done);
-        if (e != cudaSuccess || done) return e;
-    }
+    bool done = false;
+    cudaError_t re = pick_bwd_ring<T, VECTOR>(a, parts, s, &done);
+    if (re != cudaSuccess || done) return re;
     // 1024 threads leave 64 registers each, too few for the column sums
     switch (threads_for(a.cols, EPT, 512)) {
     case 32: return run_bwd<T, VECTOR, 32, EPT>(a, parts, s);
