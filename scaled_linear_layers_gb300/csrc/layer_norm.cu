@@ -17,14 +17,16 @@
 // the output need one read of the row.  Many rows (norm_*_ring_kernel) come
 // through a ring of bulk copies in shared memory, several rows ahead of the
 // sums, so the loads in flight do not depend on registers; few rows are loaded
-// straight into registers one row ahead.  All sums are fp32; the mean's, whose terms cancel, adds leading bits
+// straight into registers one row ahead.  The backward of wide rows, whose sums
+// by column alone would fill the registers, shares a row between the blocks of a
+// cluster.  All sums are fp32; the mean's, whose terms cancel, adds leading bits
 // and rests apart.
 //
 // Measured at 16384 x 4096 (device time; share of the copy bandwidth): bf16
 // forward 48 us (0.83), to E4M3 40 us (0.75, its amax cleared in a launch of
 // its own), backward 68 us (0.88, 5 us of it the reduction over the blocks'
 // column sums); fp32 forward 94 us (0.84), backward 132 us (0.90); 8192 columns
-// within 0.05 of that.  What keeps the E4M3 form from its 30 us is the work on a
+// within 0.05 of that; 4096 x 16384 backward bf16 82 us (0.72), fp32 128 us (0.92).  What keeps the E4M3 form from its 30 us is the work on a
 // row between two barriers (issue slots 60 % busy, DRAM 62 %), which is why
 // elements are worked on in pairs and a thread holds as many as fit.  Rows of odd
 // width move single elements: bf16 8192 x 8191 forward 74 us (0.53), fp32 89 us
@@ -71,10 +73,10 @@ struct NormBwdArgs {
     const void *w;  // nullable
     int param_f32;
     int64_t rows;
-    int cols;
+    int cols, width;  // worked on by the block; of the rows
     const float *mean, *rstd;
-    void *dx;        // nullable
-    float *partial;  // [2][blocks][cols]: dw then db of each block's rows; nullable
+    void *dx;        // [rows, width]; nullable
+    float *partial;  // [2][parts][width]: dw then db of each part of the rows; nullable
     int stages;
     uint64_t wait_limit_ns;
     unsigned int *status;
@@ -215,6 +217,30 @@ struct RowSource {
                    : global;
     }
 };
+
+// Columns of a row that each block of a cluster works on, the last of them the
+// rest: whole 16-byte groups, and groups of 8 parameters.
+__host__ __device__ constexpr int cluster_share(int width, int ctas) {
+    return ((width + ctas - 1) / ctas + 15) / 16 * 16;
+}
+
+// 8 bytes to the shared memory of a block of the cluster, counted there.
+__device__ __forceinline__ void st_async64(uint32_t to, uint64_t v, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(
+                     to),
+                 "l"(v), "r"(bar)
+                 : "memory");
+}
+
+// After a wait for the phase: what other blocks wrote before it is seen.
+__device__ __forceinline__ void mbar_acquire_cluster(uint64_t *bar, uint32_t parity) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(
+            smem_u32(bar)),
+        "r"(parity)
+        : "memory");
+}
 
 // Arms a slot's barrier for `bytes` (a phase without a copy completes at once).
 __device__ __forceinline__ void slot_expect(uint64_t *bar, uint32_t bytes) {
@@ -558,7 +584,7 @@ struct NormBwdRow {
     }
 
     __device__ __forceinline__ void init(const NormBwdArgs &a) {
-        inv_c = 1.f / (float)a.cols;
+        inv_c = 1.f / (float)a.width;
 #pragma unroll
         for (int i = 0; i < P; ++i) dw[i] = db[i] = 0;
         if constexpr (W_IN_REGISTERS) {
@@ -630,7 +656,7 @@ struct NormBwdRow {
 #pragma unroll
             for (int k = 0; k < STEP; ++k) {
                 if (inside(a.cols, (j + k) * V))
-                    RV::store(reinterpret_cast<T *>(a.dx) + row * a.cols + column((j + k) * V),
+                    RV::store(reinterpret_cast<T *>(a.dx) + row * a.width + column((j + k) * V),
                               reinterpret_cast<float(&)[V]>(o[k * V]));
             }
         }
@@ -652,11 +678,12 @@ struct NormBwdRow {
         }
     }
 
-    // the block's column sums; with several teams in a block theirs meet in
-    // `meet` [teams][TPR * EPT] first
-    __device__ __forceinline__ void commit(const NormBwdArgs &a, float *meet) const {
-        float *pw = a.partial + (int64_t)blockIdx.x * a.cols;
-        float *pb = pw + (int64_t)gridDim.x * a.cols;
+    // the column sums of part `part` of the rows; with several teams in a block
+    // theirs meet in `meet` [teams][TPR * EPT] first
+    __device__ __forceinline__ void commit(const NormBwdArgs &a, int part, int parts,
+                                           float *meet) const {
+        float *pw = a.partial + (int64_t)part * a.width;
+        float *pb = pw + (int64_t)parts * a.width;
         if constexpr (teams(TPR) == 1) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
@@ -731,7 +758,7 @@ __global__ void __launch_bounds__(block_threads(TPR), bwd_blocks(TPR))
         row_sum<TPR, 2>(s, red[turn & 1]);
         if (a.dx != nullptr && row < a.rows) n.store(a, row, lx, lg, mean, rstd, s);
     }
-    if (a.partial != nullptr) n.commit(a, meet);
+    if (a.partial != nullptr) n.commit(a, blockIdx.x, gridDim.x, meet);
 }
 
 // A slot holds the row's x, then its dy; it is read twice, for the sums and
@@ -797,7 +824,119 @@ __global__ void __launch_bounds__(block_threads(TPR), bwd_blocks(TPR))
     }
     if (t == 0) ring.settle(a.status);
     // every copy has arrived and been read: the teams' sums meet in the ring
-    if (a.partial != nullptr) n.commit(a, reinterpret_cast<float *>(smem));
+    if (a.partial != nullptr) n.commit(a, blockIdx.x, gridDim.x, reinterpret_cast<float *>(smem));
+}
+
+// Rows too wide for one block's registers and ring: each is shared by a
+// cluster of CTAS blocks, a block's columns always the same, which tell each
+// other their parts of the row's two sums.  A row's sums are told before the
+// row before it is finished, so their way between the blocks is not waited for.
+// Sums of up to four turns are on their way: a block tells those of turn i + 2
+// when it has turn i's from all, who then are past turn i - 2.
+template <typename T, bool VECTOR, int CTAS, int TPR, int EPT, bool FULL>
+__global__ void __launch_bounds__(TPR, 1) __cluster_dims__(CTAS, 1, 1)
+    norm_bwd_cluster_kernel(NormBwdArgs a) {
+    using Row = NormBwdRow<T, VECTOR, TPR, EPT, FULL>;
+    using RV = typename Row::RV;
+    using Source = RowSource<T, VECTOR>;
+    static_assert(teams(TPR) == 1, "one row at a time");
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float red[2][2 * (TPR / 32)];
+    __shared__ __align__(16) uint64_t theirs[4][CTAS];
+    __shared__ uint64_t told[4];
+    const int t = threadIdx.x, rank = (int)cluster_ctarank();
+    const int first = rank * cluster_share(a.width, CTAS);
+    a.cols = min(cluster_share(a.width, CTAS), a.width - first);
+    a.x = reinterpret_cast<const T *>(a.x) + first;
+    a.dy = reinterpret_cast<const T *>(a.dy) + first;
+    if (a.w != nullptr)
+        a.w = reinterpret_cast<const uint8_t *>(a.w) + (size_t)first * (a.param_f32 ? 4 : 2);
+    if (a.dx != nullptr) a.dx = reinterpret_cast<T *>(a.dx) + first;
+    if (a.partial != nullptr) a.partial += first;
+    const Source x(a.x, a.rows, a.ldx, a.cols), dy(a.dy, a.rows, a.lddy, a.cols);
+    const uint32_t half = Source::slot(x.bytes);
+    if (t == 0)
+        for (int i = 0; i < 4; ++i) mbar_init(&told[i], 1);
+    Ring ring = {};
+    ring.init<1>(smem, a.stages, 2 * half, 0, t == 0);
+    cluster_sync_all();
+    pdl_wait_prior();
+    pdl_allow_next();
+    const int64_t step = gridDim.x / CTAS;
+    int64_t row = blockIdx.x / CTAS;
+    auto request = [&](int64_t r, int slot) {
+        if (r < a.rows && ring.open()) {
+            uint8_t *to = ring.data + slot * ring.slot;
+            slot_expect(&ring.bars[slot], x.size(r) + dy.size(r));
+            x.request(r, to, &ring.bars[slot]);
+            dy.request(r, to + half, &ring.bars[slot]);
+        }
+    };
+    if (t == 0)
+        for (int i = 0; i < a.stages; ++i) request(row + i * step, i);
+    Row n;
+    n.init(a);
+    auto load = [&](const T *p, int j) {
+        return Row::inside(a.cols, j * Row::V) ? RV::load(p + Row::column(j * Row::V)) : RV::zero();
+    };
+    auto in_x = [&](int64_t r, int slot) { return x.row(r, ring.data + slot * ring.slot); };
+    auto in_dy = [&](int64_t r, int slot) { return dy.row(r, ring.data + slot * ring.slot + half); };
+    int ahead = 0;  // slot of the next row to tell the sums of
+    uint32_t phase = 0;
+    auto tell = [&](int64_t r, float mean, float rstd, int turn) {
+        ring.wait(ahead, phase, a.wait_limit_ns, a.status);
+        const T *sx = in_x(r, ahead), *sg = in_dy(r, ahead);
+        float s[2];
+        n.sums(a, [&](int j) { return load(sx, j); }, [&](int j) { return load(sg, j); }, mean, rstd,
+               s);
+        row_sum<TPR, 2>(s, red[turn & 1]);
+        // (after a wait that ran out the barrier may not have turned)
+        if (t == 0 && !*ring.abort)
+            mbar_arrive_expect_tx(&told[turn & 3], CTAS * sizeof(uint64_t));
+        if (t < CTAS)
+            st_async64(mapa_shared(smem_u32(&theirs[turn & 3][rank]), t), pair_of(s[0], s[1]),
+                       mapa_shared(smem_u32(&told[turn & 3]), t));
+        if (++ahead == a.stages) {
+            ahead = 0;
+            phase ^= 1u;
+        }
+    };
+    float mean = row < a.rows ? a.mean[row] : 0.f, rstd = row < a.rows ? a.rstd[row] : 0.f;
+    float nmean = 0.f, nrstd = 0.f;
+    if (row + step < a.rows) nmean = a.mean[row + step], nrstd = a.rstd[row + step];
+    if (row < a.rows) tell(row, mean, rstd, 0);
+    int slot = 0, before = 0;
+    for (int turn = 0; row < a.rows; row += step, ++turn) {
+        const float hmean = nmean, hrstd = nrstd;
+        if (row + 2 * step < a.rows) nmean = a.mean[row + 2 * step], nrstd = a.rstd[row + 2 * step];
+        if (row + step < a.rows) {
+            tell(row + step, hmean, hrstd, turn + 1);
+            // every member is past the row before
+            if (t == 0 && turn > 0) request(row + (a.stages - 1) * step, before);
+        }
+        const uint32_t parity = (uint32_t)(turn >> 2) & 1u;
+        if (mbar_wait_bounded(&told[turn & 3], parity, ring.abort, a.wait_limit_ns,
+                              kStatusTimeoutTma, a.status))
+            mbar_acquire_cluster(&told[turn & 3], parity);
+        float s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < CTAS; ++i) {
+            const float2 v = pair_split(*(volatile uint64_t *)&theirs[turn & 3][i]);
+            s[0] += v.x;
+            s[1] += v.y;
+        }
+        if (a.dx != nullptr) {
+            const T *sx = in_x(row, slot), *sg = in_dy(row, slot);
+            n.store(a, row, [&](int j) { return load(sx, j); }, [&](int j) { return load(sg, j); },
+                    mean, rstd, s);
+        }
+        mean = hmean, rstd = hrstd;
+        before = slot;
+        if (++slot == a.stages) slot = 0;
+    }
+    if (t == 0) ring.settle(a.status);
+    if (a.partial != nullptr) n.commit(a, blockIdx.x / CTAS, gridDim.x / CTAS, nullptr);
+    cluster_sync_all();  // no block leaves while another may still write to it
 }
 
 // Rows too wide for a team: dx with one block to a row (two passes), the
@@ -1039,9 +1178,47 @@ cudaError_t pick_bwd_ring(const NormBwdArgs &a, int *parts, cudaStream_t s, bool
         if (a.cols <= 2048) return run_bwd_ring<T, VECTOR, 128, 16>(a, parts, s, done);
         if (a.cols <= 4096) return run_bwd_ring<T, VECTOR, 256, 16>(a, parts, s, done);
         if (a.cols <= 8192) return run_bwd_ring<T, VECTOR, 512, 16>(a, parts, s, done);
-        if (a.cols <= 16384) return run_bwd_ring<T, VECTOR, 512, 32>(a, parts, s, done);
     }
     return cudaSuccess;
+}
+
+// Slots of the ring of a cluster's block.
+template <typename T, bool VECTOR>
+int cluster_slots(int width, int ctas, size_t *slot) {
+    *slot = 2 * (size_t)RowSource<T, VECTOR>::slot(cluster_share(width, ctas) * sizeof(T));
+    return (int)std::min<size_t>((kRingBytes - 1024) / (*slot + sizeof(uint64_t)), kMaxStages);
+}
+
+// A cluster of CTAS blocks to a row.  Its ring has three slots or more: the row
+// told about, the row finished, one on its way.
+template <typename T, bool VECTOR, int CTAS, int TPR, int EPT, bool FULL = false>
+cudaError_t run_bwd_cluster(NormBwdArgs a, int *parts, cudaStream_t s) {
+    if constexpr (VECTOR && !FULL)
+        if (a.width == CTAS * TPR * EPT)
+            return run_bwd_cluster<T, true, CTAS, TPR, EPT, true>(a, parts, s);
+    constexpr auto kernel = norm_bwd_cluster_kernel<T, VECTOR, CTAS, TPR, EPT, FULL>;
+    static_assert(3 * (2 * (TPR * EPT * sizeof(T) + 16) + 8) + 1024 <= kRingBytes, "three slots");
+    size_t slot = 0;
+    a.stages = cluster_slots<T, VECTOR>(a.width, CTAS, &slot);
+    int clusters = 0;
+    cudaError_t e = clusters_resident<kernel>(CTAS, TPR, kRingBytes, &clusters);
+    if (e != cudaSuccess) return e;
+    *parts = (int)std::min<int64_t>(std::min(clusters, kNormMaxPartials), a.rows);
+    return launch_pdl(kernel, *parts * CTAS, TPR, ring_bytes(1, a.stages, slot), s, a);
+}
+
+// Two blocks as far as their registers go; four also where two leave only three
+// slots (fp32 4096 x 16384: 128 us, by two 151; x 12000: by two 100, by four
+// 127), unless single elements bound the row (x 16383: 187 and 184).
+template <typename T, bool VECTOR>
+cudaError_t pick_bwd_cluster(const NormBwdArgs &a, int *parts, cudaStream_t s) {
+    if (a.width > 16384) return run_bwd_cluster<T, VECTOR, 4, 512, 16>(a, parts, s);
+    if constexpr (VECTOR && sizeof(T) == 4) {
+        size_t slot = 0;
+        if (cluster_slots<T, VECTOR>(a.width, 2, &slot) < 4)
+            return run_bwd_cluster<T, VECTOR, 4, 512, 8>(a, parts, s);
+    }
+    return run_bwd_cluster<T, VECTOR, 2, 512, 16>(a, parts, s);
 }
 
 template <typename T, bool VECTOR, int TPR, int EPT>
@@ -1061,6 +1238,7 @@ cudaError_t pick_bwd(const NormBwdArgs &a, int *parts, cudaStream_t s) {
     bool done = false;
     cudaError_t re = pick_bwd_ring<T, VECTOR>(a, parts, s, &done);
     if (re != cudaSuccess || done) return re;
+    if (a.cols > 8192 && a.cols <= 32768) return pick_bwd_cluster<T, VECTOR>(a, parts, s);
     // 1024 threads leave 64 registers each, too few for the column sums
     switch (threads_for(a.cols, EPT, 512)) {
     case 32: return run_bwd<T, VECTOR, 32, EPT>(a, parts, s);
@@ -1069,7 +1247,7 @@ cudaError_t pick_bwd(const NormBwdArgs &a, int *parts, cudaStream_t s) {
     case 512: return run_bwd<T, VECTOR, 512, EPT>(a, parts, s);
     }
     if constexpr (!VECTOR)
-        if (threads_for(a.cols, 2 * EPT, 512)) return run_bwd<T, VECTOR, 512, 2 * EPT>(a, parts, s);
+        if (a.cols <= 8192) return run_bwd<T, VECTOR, 512, 2 * EPT>(a, parts, s);
     int grid = 0;
     cudaError_t e = cudaSuccess;
     if (a.dx != nullptr) {
@@ -1125,7 +1303,7 @@ cudaError_t launch_layer_norm_backward(const NormBackward &n, cudaStream_t s) {
     int parts = 0;
     if (n.rows > 0) {
         NormBwdArgs a = {n.dy, n.x, n.lddy, n.ldx, n.w, n.param_f32, n.rows, (int)n.cols,
-                         n.mean, n.rstd, n.dx, sums ? n.workspace : nullptr, 0,
+                         (int)n.cols, n.mean, n.rstd, n.dx, sums ? n.workspace : nullptr, 0,
                          g_wait_limit_ns.load(std::memory_order_relaxed), device_status_word()};
         cudaError_t e = n.x_f32 ? norm_bwd_type<float>(a, &parts, s)
                                 : norm_bwd_type<uint16_t>(a, &parts, s);

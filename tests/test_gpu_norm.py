@@ -205,6 +205,48 @@ def test_backward_strided_and_broadcast_inputs():
     run_backward(base[:, :256], gb[:1, :256].expand(50, 256), None, F)
 
 
+# rows shared by two blocks or four (and wider): widths at both ends of each, one
+# row to more than each has slots for
+@pytest.mark.parametrize("rows, cols", [(1, 8200), (3, 9001), (400, 8208), (700, 12288), (900, 13256),
+                                        (420, 16384), (350, 16383), (2, 16392), (5, 20001),
+                                        (250, 32768), (260, 32767), (70, 32776), (2, 40001)])
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_backward_of_shared_rows(rows, cols, dtype):
+    x = rnd(rows, cols, seed=50, dtype=dtype, scale=2.0, shift=0.5)
+    dy = rnd(rows, cols, seed=51, dtype=dtype, scale=1e-2)
+    run_backward(x, dy, rnd(cols, seed=52, dtype=F, shift=1.0), F)
+
+
+def test_backward_of_shared_rows_strided_and_some_outputs():
+    base, gb = rnd(300, 9100, seed=53), rnd(300, 9031, seed=54)
+    x, dy = base[:, 3:3 + 9001], gb[:, 5:5 + 9001]
+    run_backward(x, dy, rnd(9001, seed=55, dtype=BF), BF)
+    run_backward(x, gb[:1, :9001].expand(300, 9001), None, F, (True, False, False))
+    run_backward(x, dy, None, F, (False, True, True))
+    a, b = run_backward(x, dy, None, F), run_backward(x, dy, None, F)
+    for s, t in zip(a, b):
+        assert torch.equal(s, t)
+
+
+# enough rows for the ring, which 16-byte copies do not fit: odd widths, odd
+# strides, starts between two elements' 16-byte groups
+@pytest.mark.parametrize("rows, cols, stride, offset", [(9000, 1, 1, 0), (9000, 7, 11, 3),
+                                                        (9001, 333, 333, 1), (3500, 1999, 2001, 5),
+                                                        (1700, 3001, 3001, 7), (900, 8191, 8192, 1),
+                                                        (500, 9001, 9001, 0)])
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_many_rows_of_odd_width(rows, cols, stride, offset, dtype):
+    room = offset + rows * stride
+    x = rnd(1, room, seed=56, dtype=dtype, shift=0.5)[0, offset:].view(rows, stride)[:, :cols]
+    dy = rnd(1, room, seed=57, dtype=dtype)[0, offset:].view(rows, stride)[:, :cols]
+    w, b = rnd(cols, seed=58, dtype=F, shift=1.0), rnd(cols, seed=59, dtype=F)
+    y, mean, rstd = torch.empty(rows, cols, dtype=dtype, device="cuda"), f32(rows), f32(rows)
+    fp8.fp8_layer_norm(x, w, b, EPS, y, mean, rstd)
+    check_forward(x, w, b, y, mean, rstd)
+    if cols > 1:
+        run_backward(x, dy, w, F)
+
+
 def test_backward_of_no_rows_is_zero():
     x = torch.empty(0, 96, dtype=BF, device="cuda")
     e = torch.empty(0, device="cuda")
