@@ -24,9 +24,11 @@
 // top 6 of 64, bf16 69 us (1.00); its backward 150 us (0.86), of 16384 x 4096
 // top 4 of 32 191 us (0.94); dispatch of 16384 x 4096 to 2 of 8 as E4M3 with the
 // sort 54 us (0.74: the sort 5 us, clearing the amax 2); rows of odd width,
-// 5003 x 1001 top 6, combine 27 us (0.39), backward 54 us (0.36): their instructions
-// for shifting rows into place, and waves of few tokens, keep them from it.  The
-// sort: 64 assignments 2.7 us, 32768 4.8 us, 131072 8.3 us.
+// 5003 x 1001 top 6, combine bf16 27 us (0.39), fp32 26 us (0.78), backward 53 us
+// (0.37) and 50 us (0.78): of 4-byte words twice as many are in flight for as many
+// bytes where bf16 elements must be shifted together, and a token's setup weighs
+// as much as its words.  The sort: 64 assignments 2.7 us, 32768 4.8 us, 131072
+// 8.3 us.
 #include <type_traits>
 
 #include "common.cuh"
@@ -460,24 +462,22 @@ __global__ void __launch_bounds__(row_threads(TPT)) moe_combine_bwd_kernel(const
 }
 
 // Rows that 16-byte groups do not fit (an odd width, an unaligned address).  A
-// team goes along the row it writes by the 16-byte groups of *that* row's
-// addresses, so that stores stay whole (single elements only in the ragged
-// groups at its two ends); what it reads is shifted into place, without
-// branches, so that many loads are in flight.  The ragged groups' loads run up
-// to a group past the row, into the tensor's next or last one; where the tensor
-// has none, at its first and last rows, a token goes element by element.
+// team goes along the row it writes by *that* row's aligned words of WordRow's
+// V elements, so that stores stay whole; elements of half a word, at the row's
+// ends, go singly.  What it reads is shifted into place, without branches, so
+// that many loads are in flight.  A word's loads may take in the element before
+// the row or the two after it; where the tensor has none, at its first and last rows, a
+// token goes element by element.
 
-// The rows of a [rows, H] tensor of row stride ld that are far enough from its
-// ends: a group's loads reach less than 3 V elements past a row's.
+// The rows of a [rows, H] tensor of row stride ld that have neighbours for that.
 template <typename T>
 struct Inner {
     const T *p;
     int64_t ld, first, last;
     __device__ __forceinline__ Inner(const void *base, int64_t rows, int64_t stride) {
-        constexpr int V = RowVec<T, true>::V;
         p = reinterpret_cast<const T *>(base);
         ld = stride;
-        const int64_t margin = ld > 0 ? (3 * V + ld - 1) / ld : rows;
+        const int64_t margin = WordRow<T>::V == 1 ? 0 : ld > 1 ? 1 : ld > 0 ? 2 : rows;
         first = margin;
         last = rows - margin;
     }
@@ -487,30 +487,24 @@ struct Inner {
     __device__ __forceinline__ bool holds(int64_t r) const { return r >= first && r < last; }
 };
 
-// Column of the first 16-byte group's start (V bytes' for E4M3) at or before
-// the row at p: 1 - V to 0.
+// Elements of the row at p before its first whole word of V (0 or 1).
 template <int V, typename O>
-__device__ __forceinline__ int first_group(const O *p) {
-    return -(int)((reinterpret_cast<uintptr_t>(p) / sizeof(O)) & (V - 1));
+__device__ __forceinline__ int before_words(const O *p) {
+    return (int)((reinterpret_cast<uintptr_t>(p) / sizeof(O)) & (V - 1));
 }
 
-// Stores the elements of a group at column h that lie inside the row.
-template <int V, typename O, typename All, typename One>
-__device__ __forceinline__ void store_group(O *row, int64_t h, int64_t H, All all, One one) {
-    if (h >= 0 && h + V <= H) {
-        all(row + h);
-    } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (h + v >= 0 && h + v < H) one(row + h + v, v);
-    }
+// Whether a row of H elements, `head` before its first word, leaves an element
+// out of its words for this lane: lane 0 the first, lane 1 the last.
+template <int V>
+__device__ __forceinline__ bool at_end(int lane, int head, int64_t H) {
+    return V > 1 && ((lane == 0 && head > 0) || (lane == 1 && ((H - head) & (V - 1)) != 0));
 }
 
 template <typename T, bool QUANT, int TPT, int KM>
 __global__ void __launch_bounds__(row_threads(TPT)) moe_dispatch_any_kernel(const RowArgs a) {
-    using RV = RowVec<T, true>;
+    using W = WordRow<T>;
     using O = typename std::conditional<QUANT, uint8_t, T>::type;
-    constexpr int V = RV::V, TPB = row_threads(TPT) / TPT;
+    constexpr int V = W::V, TPB = row_threads(TPT) / TPT, U = 4;
     pdl_wait_prior();
     pdl_allow_next();
     O *out = QUANT ? reinterpret_cast<O *>(a.outq) : reinterpret_cast<O *>(a.out);
@@ -519,8 +513,8 @@ __global__ void __launch_bounds__(row_threads(TPT)) moe_dispatch_any_kernel(cons
         return;
     }
     const float si = QUANT ? *a.scale_inv : 0.f;
-    const int64_t H = a.m.hidden, N = H / V + 2;
-    const int t0 = threadIdx.x % TPT;
+    const int64_t H = a.m.hidden;
+    const int lane = threadIdx.x % TPT;
     const Inner<T> in(a.x, a.m.tokens, a.ldx);
     float m = 0.f;
     auto one = [&](O *to, float f) {
@@ -532,52 +526,79 @@ __global__ void __launch_bounds__(row_threads(TPT)) moe_dispatch_any_kernel(cons
     for (int64_t t = (int64_t)blockIdx.x * TPB + threadIdx.x / TPT; t < a.m.tokens;
          t += (int64_t)a.token_blocks * TPB) {
         const T *x = in.row(t);
-        const bool shifts = in.holds(t);
-        if (QUANT && a.amax != nullptr) {
-#pragma unroll 4
-            for (int64_t h = t0; h < H; h += TPT) m = max_abs_nan(m, elem_to_float(x[h]));
-        }
+        const bool whole = in.holds(t);
         for (int j0 = 0; j0 < a.m.topk; j0 += KM) {
             int32_t r[KM];
             float w[KM];
             places(a, t, j0, r, w);
-            if (!shifts) {
-                for (int i = 0; i < KM; ++i)
-                    if (r[i] >= 0)
-                        for (int64_t e = t0; e < H; e += TPT)
-                            one(out + r[i] * H + e, elem_to_float(x[e]));
+            if (!whole) {
+                for (int64_t e = lane; e < H; e += TPT) {
+                    const float f = elem_to_float(x[e]);
+                    m = max_abs_nan(m, f);
+                    for (int i = 0; i < KM; ++i)
+                        if (r[i] >= 0) one(out + r[i] * H + e, f);
+                }
                 continue;
             }
-            int h0[KM];
-            ShiftedRow<T> src[KM];
+            int head[KM];
 #pragma unroll
             for (int i = 0; i < KM; ++i) {
-                h0[i] = r[i] >= 0 ? first_group<V>(out + r[i] * H) : 0;
-                src[i] = ShiftedRow<T>(x + h0[i]);
+                head[i] = r[i] >= 0 ? before_words<V>(out + r[i] * H) : 0;
+                if (r[i] < 0) continue;
+                if (at_end<V>(lane, head[i], H)) {
+                    const int64_t e = lane > 0 ? H - 1 : 0;
+                    one(out + r[i] * H + e, elem_to_float(x[e]));
+                }
             }
-            for (int64_t g = t0; g < N; g += TPT) {
-                typename RV::Raw raw[KM];
+            // x in words from its first element on and from its second on:
+            // each row takes those that its own words hold
+            const W even(x), odd(x + (V - 1));
+            for (int64_t w0 = lane; w0 * V < H; w0 += U * TPT) {
+                typename W::Raw from[V][U];
+                uint32_t raw[V][U];
 #pragma unroll
-                for (int i = 0; i < KM; ++i)
-                    raw[i] = src[i].load(g);
+                for (int u = 0; u < U; ++u) {
+                    const int64_t at = w0 + u * TPT;
+                    from[0][u] = even.load(at, at * V < H);
+                    if constexpr (V == 2) from[1][u] = odd.load(at, at * V + 1 < H);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    raw[0][u] = even.word(from[0][u]);
+                    if constexpr (V == 2) raw[1][u] = odd.word(from[1][u]);
+                }
+                if constexpr (QUANT) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            float f[V], q[2] = {0.f, 0.f};
+                            W::unpack(raw[v][u], f);
+                            const int64_t e = (w0 + u * TPT) * V + v;
+#pragma unroll
+                            for (int k = 0; k < V; ++k) {
+                                if (v == 0 && e + k < H) m = max_abs_nan(m, f[k]);
+                                q[k] = __fmul_rn(f[k], si);
+                            }
+                            raw[v][u] = cvt_e4m3x2(q[0], q[1]);
+                        }
+                }
 #pragma unroll
                 for (int i = 0; i < KM; ++i) {
                     if (r[i] < 0) continue;
-                    float f[V];
-                    RV::unpack(raw[i], f);
-                    store_group<V>(
-                        out + r[i] * H, h0[i] + g * V, H,
-                        [&](O *to) {
-                            if constexpr (QUANT) {
-                                float q[V];
+                    O *to = out + r[i] * H + head[i];
 #pragma unroll
-                                for (int v = 0; v < V; ++v) q[v] = __fmul_rn(f[v], si);
-                                RV::store_e4m3(to, q);
-                            } else {
-                                RV::store_raw(to, raw[i]);
-                            }
-                        },
-                        [&](O *to, int v) { one(to, f[v]); });
+                    for (int u = 0; u < U; ++u) {
+                        const int64_t at = w0 + u * TPT;
+                        if (head[i] + at * V + V > H) continue;
+                        const uint32_t v = V == 2 && head[i] > 0 ? raw[V - 1][u] : raw[0][u];
+                        if constexpr (!QUANT)
+                            *reinterpret_cast<uint32_t *>(to + at * V) = v;
+                        else if constexpr (V == 2)
+                            *reinterpret_cast<uint16_t *>(to + at * V) = (uint16_t)v;
+                        else
+                            to[at] = (uint8_t)v;
+                    }
                 }
             }
         }
@@ -593,78 +614,80 @@ __global__ void __launch_bounds__(row_threads(TPT)) moe_dispatch_any_kernel(cons
 
 template <typename T, int TPT, int KM>
 __global__ void __launch_bounds__(row_threads(TPT)) moe_combine_any_kernel(const RowArgs a) {
-    using RV = RowVec<T, true>;
-    constexpr int V = RV::V, TPB = row_threads(TPT) / TPT;
+    using W = WordRow<T>;
+    constexpr int V = W::V, TPB = row_threads(TPT) / TPT, U = KM <= 2 ? 4 : 2;
     pdl_wait_prior();
     pdl_allow_next();
-    const int64_t H = a.m.hidden, N = H / V + 2;
-    const int t0 = threadIdx.x % TPT;
+    const int64_t H = a.m.hidden;
+    const int lane = threadIdx.x % TPT;
     const Inner<T> in(a.rows, a.m.capacity, a.ldr);
     for (int64_t t = (int64_t)blockIdx.x * TPB + threadIdx.x / TPT; t < a.m.tokens;
          t += (int64_t)gridDim.x * TPB) {
         T *to = reinterpret_cast<T *>(a.out) + t * H;
-        const int h0 = first_group<V>(to);
+        const int head = before_words<V>(to);
+        const int64_t words = (H - head) / V;
         int32_t r[KM];
         float w[KM];
-        ShiftedRow<T> src[KM];
-        bool shifts = in.first < in.last;
+        W src[KM];
+        bool whole = in.first < in.last;
         auto take = [&](int j0) {
             places(a, t, j0, r, w);
 #pragma unroll
             for (int i = 0; i < KM; ++i) {
-                shifts = shifts && (r[i] < 0 || in.holds(r[i]));
-                src[i] = ShiftedRow<T>(in.row(r[i] < 0 ? in.first : r[i]) + h0);
+                whole = whole && (r[i] < 0 || in.holds(r[i]));
+                src[i] = W(in.row(r[i] < 0 ? in.first : r[i]) + head);
             }
         };
-        for (int j0 = 0; j0 < a.m.topk; j0 += KM) take(j0);
-        if (!shifts) {
-            for (int64_t e = t0; e < H; e += TPT) {
-                float acc = 0.f;
-                for (int j0 = 0; j0 < a.m.topk; j0 += KM) {
-                    places(a, t, j0, r, w);
+        auto single = [&](int64_t e) {
+            float acc = 0.f;
+            for (int j0 = 0; j0 < a.m.topk; j0 += KM) {
+                places(a, t, j0, r, w);
 #pragma unroll
-                    for (int i = 0; i < KM; ++i)
-                        acc = fmaf(w[i], r[i] >= 0 ? elem_to_float(in.row(r[i])[e]) : 0.f, acc);
-                }
-                float_to_elem(to + e, acc);
+                for (int i = 0; i < KM; ++i)
+                    acc = fmaf(w[i], r[i] >= 0 ? elem_to_float(in.row(r[i])[e]) : 0.f, acc);
             }
+            float_to_elem(to + e, acc);
+        };
+        for (int j0 = 0; j0 < a.m.topk; j0 += KM) take(j0);
+        if (!whole) {
+            for (int64_t e = lane; e < H; e += TPT) single(e);
             continue;
         }
-        for (int64_t g = t0; g < N && h0 + g * V < H; g += TPT) {
-            const int64_t h = h0 + g * V;
-            uint64_t sum[V / 2] = {};
+        for (int64_t w0 = lane; w0 < words; w0 += U * TPT) {
+            float acc[U][V] = {};
             for (int j0 = 0; j0 < a.m.topk; j0 += KM) {
                 if (a.m.topk > KM) take(j0);
-                typename RV::Raw raw[KM];
+                typename W::Raw raw[KM][U];
 #pragma unroll
-                for (int i = 0; i < KM; ++i) raw[i] = src[i].load(g);
+                for (int i = 0; i < KM; ++i)
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        raw[i][u] = src[i].load(w0 + u * TPT, w0 + u * TPT < words);
 #pragma unroll
                 for (int i = 0; i < KM; ++i) {
-                    float f[V];
-                    RV::unpack(r[i] >= 0 ? raw[i] : RV::zero(), f);
-                    const uint64_t w2 = pair_of(w[i], w[i]);
+                    if (r[i] < 0) continue;
 #pragma unroll
-                    for (int v = 0; v < V; v += 2)
-                        sum[v / 2] = pair_fma(w2, pair_of(f[v], f[v + 1]), sum[v / 2]);
+                    for (int u = 0; u < U; ++u) {
+                        float f[V];
+                        W::unpack(src[i].word(raw[i][u]), f);
+#pragma unroll
+                        for (int v = 0; v < V; ++v) acc[u][v] = fmaf(w[i], f[v], acc[u][v]);
+                    }
                 }
             }
-            float acc[V];
 #pragma unroll
-            for (int v = 0; v < V; v += 2) {
-                const float2 f = pair_split(sum[v / 2]);
-                acc[v] = f.x, acc[v + 1] = f.y;
-            }
-            store_group<V>(
-                to, h, H, [&](T *p) { RV::store(p, acc); },
-                [&](T *p, int v) { float_to_elem(p, acc[v]); });
+            for (int u = 0; u < U; ++u)
+                if (w0 + u * TPT < words)
+                    *reinterpret_cast<uint32_t *>(to + head + (w0 + u * TPT) * V) = W::pack(acc[u]);
         }
+        if (at_end<V>(lane, head, H)) single(lane > 0 ? H - 1 : 0);
     }
 }
 
 template <typename T, int TPT, int KM>
 __global__ void __launch_bounds__(row_threads(TPT)) moe_combine_bwd_any_kernel(const RowArgs a) {
-    using RV = RowVec<T, true>;
-    constexpr int V = RV::V, TPB = row_threads(TPT) / TPT;
+    using W = WordRow<T>;
+    constexpr int V = W::V, TPB = row_threads(TPT) / TPT, U = 4;
     __shared__ float red[2][KM * (TPT > 32 ? TPT / 32 : 1)];
     pdl_wait_prior();
     pdl_allow_next();
@@ -672,7 +695,7 @@ __global__ void __launch_bounds__(row_threads(TPT)) moe_combine_bwd_any_kernel(c
         zero_padding<T>(a, reinterpret_cast<T *>(a.out), blockIdx.x - a.token_blocks);
         return;
     }
-    const int64_t H = a.m.hidden, N = H / V + 2;
+    const int64_t H = a.m.hidden;
     const int lane = threadIdx.x % TPT;
     const Inner<T> in(a.rows, a.m.capacity, a.ldr), grad(a.x, a.m.tokens, a.ldx);
     T *out = reinterpret_cast<T *>(a.out);
@@ -683,59 +706,74 @@ __global__ void __launch_bounds__(row_threads(TPT)) moe_combine_bwd_any_kernel(c
         const T *dy = grad.row(t);
         for (int j0 = 0; j0 < a.m.topk; j0 += KM, ++turn) {
             int32_t r[KM];
-            float w[KM], s[KM];
+            float w[KM], s[KM] = {};
             places(a, t, j0, r, w);
-            bool shifts = grad.holds(t) && in.first < in.last;
-            int h0[KM];
-            ShiftedRow<T> src[KM], gsrc[KM];
+            bool whole = grad.holds(t) && in.first < in.last;
+            auto single = [&](int i, int64_t e) {
+                const float g = elem_to_float(dy[e]);
+                s[i] = fmaf(g, elem_to_float(in.row(r[i])[e]), s[i]);
+                float_to_elem(out + r[i] * H + e, g * w[i]);
+            };
+            int head[KM];
+            W src[KM];
 #pragma unroll
             for (int i = 0; i < KM; ++i) {
-                s[i] = 0.f;
-                shifts = shifts && (r[i] < 0 || in.holds(r[i]));
-                h0[i] = r[i] >= 0 ? first_group<V>(out + r[i] * H) : 0;
-                src[i] = ShiftedRow<T>(in.row(r[i] < 0 ? in.first : r[i]) + h0[i]);
-                gsrc[i] = ShiftedRow<T>(dy + h0[i]);
+                whole = whole && (r[i] < 0 || in.holds(r[i]));
+                head[i] = r[i] >= 0 ? before_words<V>(out + r[i] * H) : 0;
+                src[i] = W(in.row(r[i] < 0 ? in.first : r[i]) + head[i]);
             }
-            if (shifts) {
-                for (int64_t g = lane; g < N; g += TPT) {
-                    typename RV::Raw raw[KM], gr[KM];
+            if (whole) {
+                const W even(dy), odd(dy + (V - 1));  // as the dispatch's
+                for (int64_t w0 = lane; w0 * V < H; w0 += U * TPT) {
+                    typename W::Raw raw[KM][U], from[V][U];
+                    uint32_t g[V][U];
 #pragma unroll
-                    for (int i = 0; i < KM; ++i) {
-                        gr[i] = gsrc[i].load(g);
-                        raw[i] = src[i].load(g);
+                    for (int u = 0; u < U; ++u) {
+                        const int64_t at = w0 + u * TPT;
+                        from[0][u] = even.load(at, at * V < H);
+                        if constexpr (V == 2) from[1][u] = odd.load(at, at * V + 1 < H);
+                    }
+#pragma unroll
+                    for (int i = 0; i < KM; ++i)
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            const int64_t at = w0 + u * TPT;
+                            raw[i][u] = src[i].load(at, head[i] + at * V + V <= H);
+                        }
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        g[0][u] = even.word(from[0][u]);
+                        if constexpr (V == 2) g[1][u] = odd.word(from[1][u]);
                     }
 #pragma unroll
                     for (int i = 0; i < KM; ++i) {
                         if (r[i] < 0) continue;
-                        const int64_t h = h0[i] + g * V;
-                        float f[V], fg[V];
-                        RV::unpack(raw[i], f);
-                        RV::unpack(gr[i], fg);
-                        store_group<V>(
-                            out + r[i] * H, h, H,
-                            [&](T *to) {
+                        T *to = out + r[i] * H + head[i];
 #pragma unroll
-                                for (int v = 0; v < V; ++v) {
-                                    s[i] = fmaf(fg[v], f[v], s[i]);
-                                    f[v] = fg[v] * w[i];
-                                }
-                                RV::store(to, f);
-                            },
-                            [&](T *to, int v) {
+                        for (int u = 0; u < U; ++u) {
+                            const int64_t at = w0 + u * TPT;
+                            if (head[i] + at * V + V > H) continue;
+                            float f[V], fg[V];
+                            W::unpack(src[i].word(raw[i][u]), f);
+                            W::unpack(V == 2 && head[i] > 0 ? g[V - 1][u] : g[0][u], fg);
+#pragma unroll
+                            for (int v = 0; v < V; ++v) {
                                 s[i] = fmaf(fg[v], f[v], s[i]);
-                                float_to_elem(to, fg[v] * w[i]);
-                            });
+                                f[v] = fg[v] * w[i];
+                            }
+                            *reinterpret_cast<uint32_t *>(to + at * V) = W::pack(f);
+                        }
                     }
+                }
+#pragma unroll
+                for (int i = 0; i < KM; ++i) {
+                    if (r[i] >= 0 && at_end<V>(lane, head[i], H)) single(i, lane > 0 ? H - 1 : 0);
                 }
             } else if (t < a.m.tokens) {
 #pragma unroll
                 for (int i = 0; i < KM; ++i)
                     if (r[i] >= 0)
-                        for (int64_t e = lane; e < H; e += TPT) {
-                            const float g = elem_to_float(dy[e]);
-                            s[i] = fmaf(g, elem_to_float(in.row(r[i])[e]), s[i]);
-                            float_to_elem(out + r[i] * H + e, g * w[i]);
-                        }
+                        for (int64_t e = lane; e < H; e += TPT) single(i, e);
             }
             if (a.dweights == nullptr) continue;
             row_sum<TPT, KM>(s, red[turn & 1]);
@@ -774,11 +812,10 @@ bool row_vectors(const void *p, int64_t ld, int64_t cols, int es) {
 }
 
 // f(threads to a token, assignments at a time): the fewest threads that have
-// at most `per_lane` groups each, at most 256; the fewest assignments at a
+// at most `per_lane` of `units` each, at most 256; the fewest assignments at a
 // time that take them all, at most 8.
 template <typename F>
-cudaError_t with_team(const MoeRows &m, int per_lane, F f) {
-    const int64_t groups = m.hidden / (m.f32 ? 4 : 8);
+cudaError_t with_team(const MoeRows &m, int64_t units, int per_lane, F f) {
     auto km = [&](auto tpt) -> cudaError_t {
         if (m.topk <= 1) return f(tpt, std::integral_constant<int, 1>{});
         if (m.topk <= 2) return f(tpt, std::integral_constant<int, 2>{});
@@ -786,39 +823,66 @@ cudaError_t with_team(const MoeRows &m, int per_lane, F f) {
         if (m.topk <= 6) return f(tpt, std::integral_constant<int, 6>{});
         return f(tpt, std::integral_constant<int, 8>{});
     };
-    if (groups <= 32 * per_lane) return km(std::integral_constant<int, 32>{});
-    if (groups <= 128 * per_lane) return km(std::integral_constant<int, 128>{});
+    if (units <= 32 * per_lane) return km(std::integral_constant<int, 32>{});
+    if (units <= 128 * per_lane) return km(std::integral_constant<int, 128>{});
     return km(std::integral_constant<int, 256>{});
+}
+
+// Rows of 16-byte groups, `per_lane` of them to a thread.
+template <typename F>
+cudaError_t with_groups(const MoeRows &m, int per_lane, F f) {
+    return with_team(m, m.hidden / (m.f32 ? 4 : 8), per_lane, f);
+}
+
+// Rows of 4-byte words: as few threads as share a row (5003 x 1001 fp32 by 128
+// threads: combine 26 us, by 256 29), unless there are too few tokens to fill
+// the GPU with (100 x 2047 bf16: 5.5 and 7.6 the other way).  The gradient takes
+// two assignments at a time (1000 x 4095 top 8 bf16: 73 us, by four 81).
+template <typename F>
+cudaError_t with_words(const MoeRows &m, F f) {
+    return with_team(m, m.hidden / (m.f32 ? 1 : 2), m.tokens >= 8 * (int64_t)num_sms() ? 8 : 4, f);
 }
 
 template <typename T>
 cudaError_t dispatch_rows(const RowArgs &a, bool vec, cudaStream_t s) {
-    return with_team(a.m, vec ? 4 : 1, [&](auto tpt, auto km) {
-        constexpr int TPT = decltype(tpt)::value, KM = decltype(km)::value;
-        if (vec)
+    if (vec)
+        return with_groups(a.m, 4, [&](auto tpt, auto km) {
+            constexpr int TPT = decltype(tpt)::value, KM = decltype(km)::value;
             return a.outq != nullptr
                        ? launch_rows<moe_dispatch_kernel<T, true, TPT, KM>, TPT>(a, true, s)
                        : launch_rows<moe_dispatch_kernel<T, false, TPT, KM>, TPT>(a, true, s);
-        return a.outq != nullptr ? launch_rows<moe_dispatch_any_kernel<T, true, TPT, (KM > 4 ? 4 : KM)>, TPT>(a, true, s)
-                                 : launch_rows<moe_dispatch_any_kernel<T, false, TPT, (KM > 4 ? 4 : KM)>, TPT>(a, true, s);
+        });
+    return with_words(a.m, [&](auto tpt, auto km) {
+        constexpr int TPT = decltype(tpt)::value, KM = decltype(km)::value;
+        return a.outq != nullptr
+                   ? launch_rows<moe_dispatch_any_kernel<T, true, TPT, KM>, TPT>(a, true, s)
+                   : launch_rows<moe_dispatch_any_kernel<T, false, TPT, KM>, TPT>(a, true, s);
     });
 }
 
 template <typename T>
 cudaError_t combine_rows(const RowArgs &a, bool vec, cudaStream_t s) {
-    return with_team(a.m, vec ? 2 : 1, [&](auto tpt, auto km) {
+    if (vec)
+        return with_groups(a.m, 2, [&](auto tpt, auto km) {
+            constexpr int TPT = decltype(tpt)::value, KM = decltype(km)::value;
+            return launch_rows<moe_combine_kernel<T, TPT, KM>, TPT>(a, false, s);
+        });
+    return with_words(a.m, [&](auto tpt, auto km) {
         constexpr int TPT = decltype(tpt)::value, KM = decltype(km)::value;
-        return vec ? launch_rows<moe_combine_kernel<T, TPT, KM>, TPT>(a, false, s)
-                   : launch_rows<moe_combine_any_kernel<T, TPT, KM>, TPT>(a, false, s);
+        return launch_rows<moe_combine_any_kernel<T, TPT, KM>, TPT>(a, false, s);
     });
 }
 
 template <typename T>
 cudaError_t combine_bwd_rows(const RowArgs &a, bool vec, cudaStream_t s) {
-    return with_team(a.m, vec ? 4 : 1, [&](auto tpt, auto km) {
-        constexpr int TPT = decltype(tpt)::value, KM = decltype(km)::value;
-        return vec ? launch_rows<moe_combine_bwd_kernel<T, TPT, KM>, TPT>(a, true, s)
-                   : launch_rows<moe_combine_bwd_any_kernel<T, TPT, (KM > 2 ? 2 : KM)>, TPT>(a, true, s);
+    if (vec)
+        return with_groups(a.m, 4, [&](auto tpt, auto km) {
+            constexpr int TPT = decltype(tpt)::value, KM = decltype(km)::value;
+            return launch_rows<moe_combine_bwd_kernel<T, TPT, KM>, TPT>(a, true, s);
+        });
+    return with_words(a.m, [&](auto tpt, auto km) {
+        constexpr int TPT = decltype(tpt)::value, KM = decltype(km)::value > 2 ? 2 : decltype(km)::value;
+        return launch_rows<moe_combine_bwd_any_kernel<T, TPT, KM>, TPT>(a, true, s);
     });
 }
 

@@ -88,40 +88,50 @@ struct RowVec<T, false> {
     }
 };
 
-// 16-byte groups of a row from an address aligned only to its elements: two
-// aligned loads each, shifted together.  Group g reads the aligned 16 bytes
-// that hold its first and its last element and nothing else.
+// 4-byte words of a row from an address aligned only to its elements: an fp32
+// element, or two bf16 ones, shifted together from the two aligned words that
+// hold them when they lie across two.  Word i then also reads the element
+// before its first and the one after its second.
 template <typename T>
-struct ShiftedRow {
-    using Raw = typename RowVec<T, true>::Raw;
-    const uint8_t *at;
-    uint32_t shift, second;  // bytes into the aligned 16; to the second load
+struct WordRow {
+    static constexpr int V = 4 / sizeof(T);
+    const uint32_t *at, *next;
+    uint32_t shift;  // bits
 
-    __device__ __forceinline__ ShiftedRow() {}
-    __device__ __forceinline__ explicit ShiftedRow(const T *p) {
-        shift = (uint32_t)reinterpret_cast<uintptr_t>(p) & 15u;
-        at = reinterpret_cast<const uint8_t *>(p) - shift;
-        second = shift ? 16 : 0;
+    __device__ __forceinline__ WordRow() {}
+    __device__ __forceinline__ explicit WordRow(const T *p) {
+        const uint32_t u = (uint32_t)reinterpret_cast<uintptr_t>(p) & 3u;
+        at = reinterpret_cast<const uint32_t *>(reinterpret_cast<const uint8_t *>(p) - u);
+        next = at + (u != 0);
+        shift = u * 8u;
     }
 
-    __device__ __forceinline__ Raw load(int64_t g) const {
-        const uint8_t *a = at + 16 * g;
-        const uint4 q0 = *reinterpret_cast<const uint4 *>(a);
-        const uint4 q1 = *reinterpret_cast<const uint4 *>(a + second);
-        uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-#pragma unroll
-        for (int i = 0; i < 6; ++i) w[i] = shift & 8u ? w[i + 2] : w[i];
-#pragma unroll
-        for (int i = 0; i < 5; ++i) w[i] = shift & 4u ? w[i + 1] : w[i];
-        if constexpr (sizeof(T) == 2) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (shift & 3u) * 8u);
-        }
+    // what word i lies in; zeros unless `on`.  Shifted together apart from the
+    // loads, so that none of them is waited for before the next is issued.
+    struct Raw {
+        uint32_t lo, hi;
+    };
+    __device__ __forceinline__ Raw load(int64_t i, bool on) const {
         Raw r;
-        uint32_t *rw = reinterpret_cast<uint32_t *>(&r);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) rw[i] = w[i];
+        r.lo = on ? at[i] : 0u;
+        r.hi = V == 2 && on ? next[i] : 0u;
         return r;
+    }
+    __device__ __forceinline__ uint32_t word(const Raw &r) const {
+        return V == 1 ? r.lo : __funnelshift_r(r.lo, r.hi, shift);
+    }
+
+    static __device__ __forceinline__ void unpack(uint32_t w, float (&f)[V]) {
+        if constexpr (V == 1) {
+            f[0] = __uint_as_float(w);
+        } else {
+            f[0] = __uint_as_float(w << 16);
+            f[1] = __uint_as_float(w & 0xFFFF0000u);
+        }
+    }
+    static __device__ __forceinline__ uint32_t pack(const float (&f)[V]) {
+        if constexpr (V == 1) return __float_as_uint(f[0]);
+        else return pack_bf16x2(f[0], f[1]);
     }
 };
 

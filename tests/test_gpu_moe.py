@@ -290,3 +290,14 @@ def test_python_refusals():
     for call in bad:
         with pytest.raises(fp8.Fp8Error):
             call()
+
+
+# widths that 16-byte groups do not fit, with enough tokens that few threads
+# share a row, and with few; one and two elements; every share of threads
+@pytest.mark.parametrize("tokens, topk, experts, hidden, multiple", [
+    (3000, 3, 5, 1, 1), (900, 2, 4, 2, 1), (2500, 2, 8, 65, 1), (2000, 6, 16, 333, 16),
+    (1500, 8, 64, 2047, 1), (1300, 2, 4, 7001, 16), (40, 3, 4, 4097, 1), (1400, 9, 16, 515, 16)])
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_rows_of_odd_width(tokens, topk, experts, hidden, multiple, dtype):
+    test_dispatch(tokens, topk, experts, hidden, multiple, dtype)
+    test_combine_and_gradients(tokens, topk, experts, hidden, multiple, dtype)
