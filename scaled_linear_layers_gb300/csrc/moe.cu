@@ -248,17 +248,17 @@ __device__ __forceinline__ void zero_padding(const RowArgs &a, O *out, int block
         const int64_t mine = lo + threadIdx.x;
         if (mine < end && a.m.source[mine] < 0) list[atomicAdd(&count, 1)] = (int32_t)mine;
         __syncthreads();
-        const int n = count;
-        for (int k = 0; k < n; ++k) {
-            // 16 bytes at a time from the first such boundary on
+        // a warp to a row, 16 bytes at a time from the first such boundary on
+        const int n = count, lane = threadIdx.x & 31;
+        for (int k = threadIdx.x >> 5; k < n; k += blockDim.x >> 5) {
             uint8_t *to = reinterpret_cast<uint8_t *>(out + list[k] * H);
             const int64_t bytes = H * (int64_t)sizeof(O);
             const int64_t head = min(bytes, (int64_t)(-reinterpret_cast<uintptr_t>(to) & 15u));
             const int64_t body = head + ((bytes - head) & ~int64_t(15));
-            for (int64_t i = head + 16 * (int64_t)threadIdx.x; i < body; i += 16 * (int64_t)blockDim.x)
+            for (int64_t i = head + 16 * lane; i < body; i += 16 * 32)
                 *reinterpret_cast<uint4 *>(to + i) = make_uint4(0, 0, 0, 0);
-            for (int64_t i = threadIdx.x; i < head; i += blockDim.x) to[i] = 0;
-            for (int64_t i = body + threadIdx.x; i < bytes; i += blockDim.x) to[i] = 0;
+            if (lane < head) to[lane] = 0;
+            if (body + lane < bytes) to[body + lane] = 0;
         }
         __syncthreads();
     }
