@@ -234,19 +234,22 @@ struct RowArgs {
 constexpr int row_threads(int tpt) { return tpt == 32 ? 256 : tpt; }
 
 // Zeroes the padding rows (source = -1) among this block's share of them: the
-// block looks at as many rows as it has threads at once, and lists those.
+// block looks at as many rows as it has threads at once, and lists those.  (One
+// stretch of rows to a block left what follows the last segment to few blocks:
+// the gradient of 16384 x 1024 top 8 of 128, padded to 128 rows, 109 us, now 98.)
 template <typename O>
 __device__ __forceinline__ void zero_padding(const RowArgs &a, O *out, int block) {
     __shared__ int32_t list[256];
     __shared__ int count;
     const int64_t H = a.m.hidden;
-    const int64_t begin = (int64_t)block * a.rows_per_block;
-    const int64_t end = min(a.m.capacity, begin + a.rows_per_block);
-    for (int64_t lo = begin; lo < end; lo += blockDim.x) {
+    // every blocks-th row: the padding past the last segment is spread over all
+    const int64_t blocks = gridDim.x - a.token_blocks;
+    for (int64_t lo = 0; lo < a.rows_per_block; lo += blockDim.x) {
         if (threadIdx.x == 0) count = 0;
         __syncthreads();
-        const int64_t mine = lo + threadIdx.x;
-        if (mine < end && a.m.source[mine] < 0) list[atomicAdd(&count, 1)] = (int32_t)mine;
+        const int64_t mine = (lo + threadIdx.x) * blocks + block;
+        if (mine < a.m.capacity && a.m.source[mine] < 0)
+            list[atomicAdd(&count, 1)] = (int32_t)mine;
         __syncthreads();
         // a warp to a row, 16 bytes at a time from the first such boundary on
         const int n = count, lane = threadIdx.x & 31;
