@@ -9,6 +9,7 @@ streams.  Importing this package requires the built library (no fallback).
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -423,14 +424,17 @@ def _rows(t, who, name, dtype=None, shape=None):
     returns (pointer, row stride)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         _refuse(_lib.FP8_ERR_NULL, f"{who}: {name} is not a CUDA tensor")
-    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
-        _refuse(_lib.FP8_ERR_UNSUPPORTED, f"{who}: {name} has type {t.dtype}")
-    if t.dim() != 2 or (shape is not None and t.shape != shape):
-        _refuse(_lib.FP8_ERR_SHAPE, f"{who}: {name} has shape {tuple(t.shape)}")
-    n, width = t.shape
-    if width > 1 and t.stride(1) != 1:
+    own = t.dtype
+    if own not in _DTYPES or (dtype is not None and own != dtype):
+        _refuse(_lib.FP8_ERR_UNSUPPORTED, f"{who}: {name} has type {own}")
+    size = t.shape
+    if len(size) != 2 or (shape is not None and size != shape):
+        _refuse(_lib.FP8_ERR_SHAPE, f"{who}: {name} has shape {tuple(size)}")
+    n, width = size
+    ld, step = t.stride()
+    if width > 1 and step != 1:
         _refuse(_lib.FP8_ERR_SHAPE, f"{who}: {name}'s rows are not contiguous")
-    return t.data_ptr(), t.stride(0) if n > 1 else width
+    return t.data_ptr(), ld if n > 1 else width
 
 
 def _dense(t, who, name, dtypes, shape):
@@ -462,6 +466,7 @@ def _workspace(t, who, nbytes):
 
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
+_INTS = (torch.int32, torch.int64)
 _E4M3 = (torch.uint8, torch.float8_e4m3fn)
 _BF16 = (torch.bfloat16,)
 
@@ -489,17 +494,20 @@ def fp8_layer_norm(x, weight, bias, eps, y=None, mean=None, rstd=None, yq=None, 
     into y (x's type) and/or yq (E4M3 bytes of y * scale_inv)."""
     who = "fp8_layer_norm"
     xp, ldx = _rows(x, who, "x")
-    rows, cols = x.shape
+    shape, dtype = x.shape, x.dtype
+    rows, cols = shape
     pt = _param_type(who, weight, bias)
+    width, column = (cols,), (rows,)
     _check(_LIB.fp8_layer_norm(
-        xp, ldx, _DTYPES[x.dtype], _dense(weight, who, "weight", pt, (cols,)),
-        _dense(bias, who, "bias", pt, (cols,)), _DTYPES[pt[0]], rows, cols, eps,
-        _dense(y, who, "y", (x.dtype,), x.shape), _dense(yq, who, "yq", _E4M3, x.shape),
+        xp, ldx, _DTYPES[dtype], _dense(weight, who, "weight", pt, width),
+        _dense(bias, who, "bias", pt, width), _DTYPES[pt[0]], rows, cols, eps,
+        _dense(y, who, "y", (dtype,), shape), _dense(yq, who, "yq", _E4M3, shape),
         _dense(scale_inv, who, "scale_inv", _F32, (1,)),
-        _dense(amax_out, who, "amax_out", _F32, (1,)), _dense(mean, who, "mean", _F32, (rows,)),
-        _dense(rstd, who, "rstd", _F32, (rows,)), _stream(stream)))
+        _dense(amax_out, who, "amax_out", _F32, (1,)), _dense(mean, who, "mean", _F32, column),
+        _dense(rstd, who, "rstd", _F32, column), _stream(stream)))
 
 
+@functools.lru_cache(maxsize=256)
 def fp8_layer_norm_workspace_bytes(rows: int, cols: int) -> int:
     return int(_LIB.fp8_layer_norm_workspace_bytes(rows, cols))
 
@@ -509,16 +517,17 @@ def fp8_layer_norm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, db
     """Gradients of fp8_layer_norm's y; mean and rstd are the forward's."""
     who = "fp8_layer_norm_backward"
     xp, ldx = _rows(x, who, "x")
-    rows, cols = x.shape
-    gp, lddy = _rows(dy, who, "dy", x.dtype, x.shape)
+    shape, dtype = x.shape, x.dtype
+    rows, cols = shape
+    gp, lddy = _rows(dy, who, "dy", dtype, shape)
     pt = _param_type(who, weight, dweight, dbias)
     sums = dweight is not None or dbias is not None
     ws = _workspace(workspace, who, fp8_layer_norm_workspace_bytes(rows, cols) if sums else 0)
     _check(_LIB.fp8_layer_norm_backward(
-        gp, lddy, xp, ldx, _DTYPES[x.dtype], _dense(weight, who, "weight", pt, (cols,)),
+        gp, lddy, xp, ldx, _DTYPES[dtype], _dense(weight, who, "weight", pt, (cols,)),
         _DTYPES[pt[0]], _dense(mean, who, "mean", _F32, (rows,)),
         _dense(rstd, who, "rstd", _F32, (rows,)), rows, cols,
-        _dense(dx, who, "dx", (x.dtype,), x.shape), _dense(dweight, who, "dweight", pt, (cols,)),
+        _dense(dx, who, "dx", (dtype,), shape), _dense(dweight, who, "dweight", pt, (cols,)),
         _dense(dbias, who, "dbias", pt, (cols,)), ws, _stream(stream)))
 
 
@@ -526,6 +535,7 @@ def fp8_moe_capacity(assignments: int, experts: int, multiple: int) -> int:
     return int(_LIB.fp8_moe_capacity(assignments, experts, multiple))
 
 
+@functools.lru_cache(maxsize=256)
 def fp8_moe_sort_workspace_bytes(assignments: int, experts: int) -> int:
     return int(_LIB.fp8_moe_sort_workspace_bytes(assignments, experts))
 
@@ -537,13 +547,14 @@ def fp8_moe_sort(ids, experts, multiple, row_of, source, offsets, counts, worksp
     who = "fp8_moe_sort"
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
         _refuse(_lib.FP8_ERR_SHAPE, f"{who}: ids must be [tokens, topk]")
-    ip = _dense(ids, who, "ids", (torch.int32, torch.int64), ids.shape)
+    shape = ids.shape
+    ip = _dense(ids, who, "ids", _INTS, shape)
     n = ids.numel()
     sp, cap = _source(who, source)
     ws = _workspace(workspace, who, fp8_moe_sort_workspace_bytes(n, experts))
     _check(_LIB.fp8_moe_sort(
         ip, ids.dtype == torch.int64, n, experts, multiple, cap,
-        _dense(row_of, who, "row_of", _I32, ids.shape), sp,
+        _dense(row_of, who, "row_of", _I32, shape), sp,
         _dense(offsets, who, "offsets", _I32, (experts + 1,)),
         _dense(counts, who, "counts", _I32, (experts,)), ws, _stream(stream)))
 
@@ -618,6 +629,7 @@ def fp8_moe_combine_backward(dy, rows, row_of, source, weights, drows, dweights=
         _dense(dweights, who, "dweights", _F32, (tokens, topk)), _stream(stream)))
 
 
+@functools.lru_cache(maxsize=256)
 def fp8_orthogonalize_workspace_bytes(batch: int, rows: int, cols: int) -> int:
     return int(_LIB.fp8_orthogonalize_workspace_bytes(batch, rows, cols))
 
