@@ -608,8 +608,10 @@ fp8_status fp8_moe_combine_backward(const void *dy, int64_t lddy, const void *ro
  * rows and cols <= 65536, batch * ceil(rows/128) * ceil(cols/128) < 2^31
  * (FP8_ERR_SHAPE); eps >= 0.  workspace:
  * fp8_orthogonalize_workspace_bytes(batch, rows, cols) bytes (8 a matrix
- * element and 4 an element of A; 0 for bad arguments), 16-byte aligned,
- * overwritten; calls that may overlap need their own. */
+ * element, rows padded to 64, and 4 an element of A; 10 where the shorter side
+ * is at most 2048 and the longer at least 2048, for A's parts; 0 for bad
+ * arguments), 16-byte aligned, overwritten; calls that may overlap need their
+ * own. */
 size_t fp8_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
 fp8_status fp8_orthogonalize(const void *g, int64_t ldg, int64_t bsg, fp8_dtype gt, int64_t batch,
                              int64_t rows, int64_t cols, int32_t steps, const float *coefficients,

@@ -26,11 +26,12 @@
 // forward 48 us (0.83), to E4M3 40 us (0.75, its amax cleared in a launch of
 // its own), backward 68 us (0.88, 5 us of it the reduction over the blocks'
 // column sums); fp32 forward 94 us (0.84), backward 132 us (0.90); 8192 columns
-// within 0.05 of that; 4096 x 16384 backward bf16 82 us (0.72), fp32 128 us (0.92).  What keeps the E4M3 form from its 30 us is the work on a
-// row between two barriers (issue slots 60 % busy, DRAM 62 %), which is why
-// elements are worked on in pairs and a thread holds as many as fit.  Rows of odd
-// width move single elements: bf16 8192 x 8191 forward 74 us (0.53), fp32 89 us
-// (0.89).  One row of 4096: 3.5 us, a launch's latency.
+// within 0.05 of that; 4096 x 16384 backward bf16 82 us (0.72), fp32 128 us
+// (0.92).  What keeps the E4M3 form from its 30 us is the work on a row between
+// two barriers (issue slots 60 % busy, DRAM 62 %), which is why elements are
+// worked on in pairs and a thread holds as many as fit.  Rows of odd width move
+// single elements: bf16 8192 x 8191 forward 74 us (0.53), fp32 89 us (0.89).  One
+// row of 4096: 3.5 us, a launch's latency.
 #include <algorithm>
 #include <atomic>
 

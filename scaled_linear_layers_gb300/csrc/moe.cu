@@ -21,14 +21,13 @@
 // first is used.
 //
 // Measured (device time; share of the copy bandwidth): combine of 16384 x 2048,
-// top 6 of 64, bf16 69 us (1.00); its backward 150 us (0.86), of 16384 x 4096
-// top 4 of 32 191 us (0.94); dispatch of 16384 x 4096 to 2 of 8 as E4M3 with the
-// sort 54 us (0.74: the sort 5 us, clearing the amax 2); rows of odd width,
-// 5003 x 1001 top 6, combine bf16 27 us (0.39), fp32 26 us (0.78), backward 53 us
-// (0.37) and 50 us (0.78): of 4-byte words twice as many are in flight for as many
-// bytes where bf16 elements must be shifted together, and a token's setup weighs
-// as much as its words.  The sort: 64 assignments 2.7 us, 32768 4.8 us, 131072
-// 8.3 us.
+// top 6 of 64, bf16 69 us (1.00); its backward 130 us (0.99), of 16384 x 4096
+// top 4 of 32 190 us (0.94); dispatch of 16384 x 4096 to 2 of 8 as E4M3 with the
+// sort 50 us (0.81: the sort 5 us, clearing the amax 2); rows of odd width,
+// 5003 x 1001 top 6, combine bf16 27 us (0.39), fp32 26 us (0.78), backward 52 us
+// (0.37) and 49 us (0.80): a token's setup weighs as much as its words, and a
+// bf16 word that lies across two costs two loads.  The sort: 64 assignments 2.7
+// us, 32768 4.8 us, 131072 8.3 us.
 #include <type_traits>
 
 #include "common.cuh"
