@@ -1001,9 +1001,8 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
                 if constexpr (CG == 2) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
                 else mbar_arrive(&tempty[acc]);
                 if (!(update && last) && (!split || parts != nullptr)) {
-                    // this warp's part is in memory: announce it
-                    bulk_wait_group_all();
-                    fence_proxy_async_all();
+                    // announce this warp's part once it is in memory
+                    bulk_wait_group_all();  // its writes are this thread's from here on
                     __threadfence();
                     atomicAdd(update ? x_flag(p, t.z, t.r, t.c)
                                      : sym_flag(p, t.z, t.phase, t.tm, t.tn), 1u);
