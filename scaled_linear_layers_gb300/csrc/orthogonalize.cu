@@ -28,11 +28,11 @@
 // either of its dims as the contraction, straight from its row-major tiles.
 //
 // Large matrices are bound by the tensor cores at the clock that the power
-// limit leaves: 4096 x 4096 in 0.88 to 0.96 ms (1430 to 1560 TFLOP/s of the
+// limit leaves: 4096 x 4096 in 0.88 to 0.94 ms (1460 to 1570 TFLOP/s of the
 // operations above; the launch of the products 0.83 ms), 4096 x 14336 in 2.64 to
 // 2.79 ms, eight of 4096 x 4096 in 7.4 ms.  Small ones are bound by the 15
-// dependent products, about 6 us each from tile to tile: 256 x 256 90 us, 1024 x
-// 1024 158 us.  Eight of 1531 x 1000: 280 us, between the two.
+// dependent products, about 6 us each from tile to tile: 256 x 256 90 to 94 us,
+// 1024 x 1024 150 us.  Eight of 1531 x 1000: 268 to 276 us, between the two.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
