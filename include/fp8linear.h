@@ -602,9 +602,9 @@ fp8_status fp8_moe_combine_backward(const void *dy, int64_t lddy, const void *ro
  * from X = g / (|g|_F + eps), each matrix of the batch by itself; step i takes
  * (a, b, c) = coefficients[3 i .. 3 i + 2] (host).  g has type gt, row stride
  * ldg >= 0 and batch stride bsg >= 0 elements.  The products run on the tensor
- * cores with fp16 operands and fp32 accumulation; singular values must stay
- * below 4 throughout (the usual coefficients keep them below 1.3), beyond
- * which fp16 overflows and the result is not finite.  1 <= steps <= 64,
+ * cores with fp16 operands and fp32 accumulation; the singular values that a
+ * step starts from must be below 4 (the usual coefficients keep them below 1.3),
+ * beyond which fp16 overflows and the result is not finite.  1 <= steps <= 64,
  * rows and cols <= 65536, batch * ceil(rows/128) * ceil(cols/128) < 2^31
  * (FP8_ERR_SHAPE); eps >= 0.  workspace:
  * fp8_orthogonalize_workspace_bytes(batch, rows, cols) bytes (8 a matrix

@@ -11,9 +11,11 @@
 //
 // Every product is a tcgen05 GEMM on fp16 operands with fp32 accumulation.
 // fp16 holds 11 significant bits where bf16 holds 8; its short exponent is
-// enough because the values are bounded: X, A and B are stored times 2^12,
-// 2^12 and 2^10, which leaves room for singular values up to 4 and keeps
-// entries down to 2^-26 (2^-24) normal.  Rounding X itself to fp16 would cost
+// enough because the values are bounded: X and A are stored times 2^12, which
+// leaves room for singular values up to 4 and keeps entries down to 2^-26
+// normal, and B times a power of two of the step's own, the largest up to 2^10
+// that leaves room for what (a, b, c) make of such singular values (2^7 with the
+// usual coefficients).  Rounding X itself to fp16 would cost
 // more than the products' roundings do: its error lies in all directions
 // alike, and the first steps multiply small singular values by `a` each.  So X
 // is held as the sum of two fp16 numbers (22 bits) until the last two steps,
@@ -38,6 +40,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "common.cuh"
@@ -51,7 +54,8 @@ extern std::atomic<uint64_t> g_wait_limit_ns;
 
 namespace {
 
-constexpr float kXScale = 4096.f, kAScale = 4096.f, kBScale = 1024.f, kLoScale = 2048.f;
+constexpr float kXScale = 4096.f, kAScale = 4096.f, kLoScale = 2048.f;
+constexpr int kBScaleMost = 10;  // log2
 constexpr int kFoldedSteps = 2;
 
 // ---------------------------------------------------------------- scaling ---
@@ -210,6 +214,7 @@ struct NsPlan {
     int flags_per;
     // arithmetic: step i has coefficients (a, b, c) at 3 i
     float coefficients[3 * kMaxSteps];
+    float b_scale[kMaxSteps];  // of B as it is stored
     float scale;
     uint64_t wait_limit_ns;
     unsigned int *status;
@@ -781,7 +786,7 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
             const bool mirror = !update && t.tm != t.tn;
             const int width = row0 < M ? min(BT, N - t.tn * BT) : 0;
             const float ca = p.coefficients[3 * t.step], cb = p.coefficients[3 * t.step + 1],
-                        cc = p.coefficients[3 * t.step + 2];
+                        cc = p.coefficients[3 * t.step + 2], b_scale = p.b_scale[t.step];
             // output = acc_mul * acc + e_mul * (E + lo 2^-11) + diag on the diagonal
             float acc_mul, e_mul = 0.f, diag = 0.f;
             const CUtensorMap *e = nullptr, *e_lo = nullptr, *out, *out_lo = nullptr;
@@ -791,15 +796,15 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
                 acc_mul = kAScale / (kXScale * kXScale);
                 out = &maps.da;
             } else if (t.phase == kPoly) {
-                acc_mul = cc * (kBScale / (kAScale * kAScale));
-                e_mul = cb * (kBScale / kAScale);
-                diag = fold ? ca * kBScale : 0.f;
+                acc_mul = cc * (b_scale / (kAScale * kAScale));
+                e_mul = cb * (b_scale / kAScale);
+                diag = fold ? ca * b_scale : 0.f;
                 e = &maps.da;
                 e_flag = sym_flag(p, t.z, kGram, t.tm, t.tn);
                 e_done = (uint32_t)(t.step + 1) * ARRIVALS;
                 out = &maps.db;
             } else {
-                acc_mul = last ? p.scale / (kBScale * kXScale) : 1.f / kBScale;
+                acc_mul = last ? p.scale / (b_scale * kXScale) : 1.f / b_scale;
                 if (!fold) {
                     e = &maps.dx[t.step & 1];
                     e_lo = &maps.dlo[t.step & 1];
@@ -1151,6 +1156,20 @@ cudaError_t ns_launch(void (*kernel)(NsMaps, NsPlan), int grid, cudaStream_t s, 
 int64_t pad64(int64_t v) { return (v + 63) / 64 * 64; }
 int64_t pad256(int64_t v) { return (v + 255) / 256 * 256; }
 
+// The power of two that B = b A + c A A (+ a I) is stored times.  No entry of a
+// symmetric matrix is larger than its largest |eigenvalue|, here |a + b t + c t^2|
+// for t = s^2 of a singular value s below 4.
+float poly_scale(float a, float b, float c) {
+    auto value = [&](double t) { return std::fabs((double)a + (double)b * t + (double)c * t * t); };
+    double most = std::max(value(0.), value(16.));
+    const double turn = c != 0.f ? -(double)b / (2. * (double)c) : 0.;
+    if (turn > 0. && turn < 16.) most = std::max(most, value(turn));
+    // (65504 is fp16's largest; the rest is for A's rounding)
+    const double room = 60000. / most;
+    if (!(room < std::exp2(kBScaleMost))) return std::exp2f(kBScaleMost);  // also NaN, and 0 / 0
+    return std::exp2f((float)std::max(-100, std::ilogb(room)));
+}
+
 constexpr int kPrepParts = 2048;  // blocks that share a matrix in the scaling, at most
 
 // A's contraction is split where its 128-tiles would leave CTAs idle: up to 16
@@ -1277,6 +1296,10 @@ cudaError_t launch_orthogonalize(const Orthogonalize &o, cudaStream_t s, const c
     p.flags = reinterpret_cast<uint32_t *>(base + w.flags);
     p.flags_per = (int)ns_flags_per(p.T, p.U);
     for (int i = 0; i < 3 * o.steps; ++i) p.coefficients[i] = o.coefficients[i];
+    for (int i = 0; i < o.steps; ++i) {
+        const float *abc = o.coefficients + 3 * i;
+        p.b_scale[i] = poly_scale(i >= o.steps - kFoldedSteps ? abc[0] : 0.f, abc[1], abc[2]);
+    }
     p.scale = o.scale;
     p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
     p.status = device_status_word();

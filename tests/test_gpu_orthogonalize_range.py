@@ -1,0 +1,25 @@
+"""Orthogonalisation at the ends of its range: coefficients and singular values
+whose polynomial is large, few steps, entries near the ends of fp32."""
+import pytest
+import torch
+
+from test_gpu_orthogonalize import ABC, by_products, check, rnd, run
+
+pytestmark = pytest.mark.gpu
+
+
+# |b s^2 + c s^4|, plus a where the step multiplies by (a I + B), is the largest
+# entry of the matrix that a step multiplies X by.  Singular values equal to one
+# another leave no cancellation: the largest error is the rounding of the operands,
+# 2e-4 (2-norm) each, through the slope of the polynomial, 2.2 relative at s = 3.5
+# (t (b + 2 c t) / (a + b t + c t^2) at t = 12.25); the bound of 5e-3 stays.
+@pytest.mark.parametrize("n, coefficients", [
+    (64, [(28.0, 0.0, 0.0), ABC]),                     # s = 3.5: 250 in the last step
+    (64, [(20.0, 0.0, 0.0), ABC]),                     # s = 2.5: 53
+    (1024, [(100.0, 0.0, 0.0), (0.5, 0.0, 0.0)]),      # 100 on the diagonal
+    (1024, [(-28.0, 131072.0, 0.0)] + [(0.5, 0.0, 0.0)] * 3),  # 128 in an early step
+])
+def test_polynomials_of_large_values(n, coefficients):
+    q = torch.linalg.qr(rnd(n, n, seed=31).double().cpu())[0].float().contiguous().cuda()
+    out = run(q, steps=len(coefficients), coefficients=coefficients)
+    check(out, by_products(q, coefficients))
