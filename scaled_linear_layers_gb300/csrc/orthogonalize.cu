@@ -60,11 +60,15 @@ constexpr int kFoldedSteps = 2;
 
 // ---------------------------------------------------------------- scaling ---
 
-// The input's sum of squares by parts: of x, of x 2^-64 and of x 2^64, so
-// that one of them neither overflows nor loses its small terms.
+// The input's sum of squares three times: of x, of x 2^-96 and of x 2^90.  The
+// first is used from 2^-60 to 2^100 (|G| from 2^-30 to 2^50); above that the
+// second, whose terms are below 2^64 each, and below it the third, whose sum is
+// below 2^120 and whose terms are 2^-118 or more.  So the one that is used
+// neither overflows nor loses terms that count.
 struct SquareSums {
     float mid, big, small;
 };
+constexpr float kSquareBig = 0x1p-96f, kSquareSmall = 0x1p90f;
 
 struct PrepArgs {
     const void *g;
@@ -108,7 +112,7 @@ __global__ void __launch_bounds__(kPrepThreads) ns_square_kernel(const PrepArgs 
                 RV::unpack(raw[u], f);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const float b = f[i] * 0x1p-64f, l = f[i] * 0x1p64f;
+                    const float b = f[i] * kSquareBig, l = f[i] * kSquareSmall;
                     s[0] = fmaf(f[i], f[i], s[0]);
                     s[1] = fmaf(b, b, s[1]);
                     s[2] = fmaf(l, l, s[2]);
@@ -139,8 +143,8 @@ __global__ void __launch_bounds__(kPrepThreads) ns_scale_kernel(const PrepArgs a
     row_sum<kPrepThreads, 3>(s, red);
     // |G| 2^k = sqrt(sum), X = (g 2^k) / (|G| 2^k + eps 2^k)
     float pre = 1.f, sum = s[0];
-    if (!(s[0] < 0x1p100f)) pre = 0x1p-64f, sum = s[1];
-    else if (s[0] < 0x1p-60f) pre = 0x1p64f, sum = s[2];
+    if (!(s[0] < 0x1p100f)) pre = kSquareBig, sum = s[1];
+    else if (s[0] < 0x1p-60f) pre = kSquareSmall, sum = s[2];
     const float den = sqrtf(sum) + a.eps * pre;
     const float mul = kXScale / den;
     const T *g = reinterpret_cast<const T *>(a.g) + blockIdx.y * a.bsg;

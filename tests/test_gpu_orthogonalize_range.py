@@ -3,7 +3,7 @@ whose polynomial is large, few steps, entries near the ends of fp32."""
 import pytest
 import torch
 
-from test_gpu_orthogonalize import ABC, by_products, check, rnd, run
+from test_gpu_orthogonalize import ABC, by_products, by_singular_values, check, rnd, run
 
 pytestmark = pytest.mark.gpu
 
@@ -23,3 +23,11 @@ def test_polynomials_of_large_values(n, coefficients):
     q = torch.linalg.qr(rnd(n, n, seed=31).double().cpu())[0].float().contiguous().cuda()
     out = run(q, steps=len(coefficients), coefficients=coefficients)
     check(out, by_products(q, coefficients))
+
+
+@pytest.mark.parametrize("scale", [6e37, 1e-42])
+@pytest.mark.parametrize("cols", [80, 81])
+def test_entries_at_the_ends_of_fp32(scale, cols):
+    g = rnd(64, cols, seed=32, scale=scale)
+    assert g.isfinite().all() and g.count_nonzero() > 0.9 * g.numel()
+    check(run(g, eps=0.0), by_singular_values(g, [ABC] * 5, eps=0.0))
