@@ -18,11 +18,11 @@
 // usual coefficients).  Rounding X itself to fp16 would cost
 // more than the products' roundings do: its error lies in all directions
 // alike, and the first steps multiply small singular values by `a` each.  So X
-// is held as the sum of two fp16 numbers (22 bits) until the last two steps,
-// and a X is added from that sum in the epilogue; only the products see the
-// rounded X.  In the last two steps the singular values are all of order 1
-// and a X goes through the product instead, as (a I + B) X, which rounds less
-// and reads nothing in the epilogue.  Measured in 64 bits against the formula,
+// is held as the sum of two fp16 numbers (22 bits) in the first three steps and
+// until the last two, and a X is added from that sum in the epilogue; only the
+// products see the rounded X.  In the other steps the singular values are of
+// order 1 and a X goes through the product instead, as (a I + B) X, which rounds
+// less and reads nothing in the epilogue.  Measured in 64 bits against the formula,
 // the result is 0.4e-3 to 1.3e-3 off (2-norm, matrices of 128 and more), below
 // the 1.7e-3 of the bf16 output's own rounding; bf16 operands: 1e-2 and more.
 //
@@ -56,7 +56,11 @@ namespace {
 
 constexpr float kXScale = 4096.f, kAScale = 4096.f, kLoScale = 2048.f;
 constexpr int kBScaleMost = 10;  // log2
-constexpr int kFoldedSteps = 2;
+// The steps whose a X goes through the product: the last two, but none of the
+// first three, before which small singular values have not been raised.
+__host__ __device__ constexpr bool folded(int step, int steps) {
+    return step >= 3 && step >= steps - 2;
+}
 
 // ---------------------------------------------------------------- scaling ---
 
@@ -784,7 +788,7 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
             const uint32_t acc_phase = (it >> 1) & 1;
             const NsTile t = ns_locate(p, i);
             const bool update = t.phase == kUpdate;
-            const bool fold = t.step >= p.steps - kFoldedSteps, last = t.step == p.steps - 1;
+            const bool fold = folded(t.step, p.steps), last = t.step == p.steps - 1;
             const int M = update ? p.rows : S, N = update ? p.cols : S;
             const int row0 = t.tm * BT + (int)rank * 128 + quarter * 32, row = row0 + lane;
             const bool mirror = !update && t.tm != t.tn;
@@ -812,12 +816,12 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
                 if (!fold) {
                     e = &maps.dx[t.step & 1];
                     e_lo = &maps.dlo[t.step & 1];
-                    e_mul = ca;
+                    e_mul = last ? ca * (p.scale / kXScale) : ca;
                     e_flag = x_flag(p, t.z, t.r, t.c);
                     e_done = (uint32_t)t.step * ARRIVALS;
                 }
                 out = last ? &maps.dout : &maps.dx[(t.step + 1) & 1];
-                if (t.step + 1 < p.steps - kFoldedSteps) out_lo = &maps.dlo[(t.step + 1) & 1];
+                if (!last && !folded(t.step + 1, p.steps)) out_lo = &maps.dlo[(t.step + 1) & 1];
             }
             // The added matrix's boxes of a chunk come in one chunk ahead of
             // the accumulator, the first before the tile's products are done.
@@ -1302,7 +1306,7 @@ cudaError_t launch_orthogonalize(const Orthogonalize &o, cudaStream_t s, const c
     for (int i = 0; i < 3 * o.steps; ++i) p.coefficients[i] = o.coefficients[i];
     for (int i = 0; i < o.steps; ++i) {
         const float *abc = o.coefficients + 3 * i;
-        p.b_scale[i] = poly_scale(i >= o.steps - kFoldedSteps ? abc[0] : 0.f, abc[1], abc[2]);
+        p.b_scale[i] = poly_scale(folded(i, o.steps) ? abc[0] : 0.f, abc[1], abc[2]);
     }
     p.scale = o.scale;
     p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);

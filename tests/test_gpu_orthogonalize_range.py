@@ -18,6 +18,7 @@ pytestmark = pytest.mark.gpu
     (64, [(20.0, 0.0, 0.0), ABC]),                     # s = 2.5: 53
     (1024, [(100.0, 0.0, 0.0), (0.5, 0.0, 0.0)]),      # 100 on the diagonal
     (1024, [(-28.0, 131072.0, 0.0)] + [(0.5, 0.0, 0.0)] * 3),  # 128 in an early step
+    (1024, [(1.0, 0.0, 0.0)] * 3 + [(100.0, 0.0, 0.0), (0.5, 0.0, 0.0)]),  # 100 in a late one
 ])
 def test_polynomials_of_large_values(n, coefficients):
     q = torch.linalg.qr(rnd(n, n, seed=31).double().cpu())[0].float().contiguous().cuda()
@@ -31,3 +32,16 @@ def test_entries_at_the_ends_of_fp32(scale, cols):
     g = rnd(64, cols, seed=32, scale=scale)
     assert g.isfinite().all() and g.count_nonzero() > 0.9 * g.numel()
     check(run(g, eps=0.0), by_singular_values(g, [ABC] * 5, eps=0.0))
+
+
+@pytest.mark.parametrize("steps", [1, 2, 3])
+@pytest.mark.parametrize("scale", [1.0, 0.3])
+def test_few_steps_keep_the_input_to_its_own_rounding(steps, scale):
+    """With (1, 0, 0) the result is X itself.  Held to 22 bits and rounded once
+    to bf16's 8, it differs from the 64-bit X's rounding where X lies within 2^-22
+    of the middle of two values 2^-8 apart, one entry in 2^13; 11 bits differ in
+    one of 30."""
+    g = rnd(96, 160, seed=33)
+    out = run(g, steps=steps, coefficients=[(1.0, 0.0, 0.0)] * steps, scale=scale)
+    want = (scale * by_products(g, [(1.0, 0.0, 0.0)] * steps)).to(torch.bfloat16)
+    assert (out != want).double().mean().item() <= 0.005
