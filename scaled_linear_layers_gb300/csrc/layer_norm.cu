@@ -492,23 +492,24 @@ __global__ void __launch_bounds__(block_threads(TPR), fwd_blocks(TPR, EPT))
 }
 
 // Rows too wide for a team: one block to a row, three passes over it (the
-// second and third find it in L2).
+// second and third find it in L2).  Columns are unsigned here and below: up to
+// 2^31 - 1 of them, the step past the last passes 2^31.
 template <typename T>
 __global__ void __launch_bounds__(kWideThreads) norm_fwd_wide_kernel(const NormArgs a) {
     __shared__ float red[2][2 * kWideThreads / 32];
     pdl_wait_prior();
     pdl_allow_next();
-    const int C = a.cols;
+    const unsigned C = a.cols;
     const float inv_c = 1.f / (float)C;
     const float si = a.yq != nullptr ? *a.scale_inv : 0.f;
     float m = 0.f;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const T *x = reinterpret_cast<const T *>(a.x) + row * a.ldx;
         float s = 0.f, e = 0.f;
-        for (int c = threadIdx.x; c < C; c += kWideThreads) add_exact(s, e, elem_to_float(x[c]));
+        for (unsigned c = threadIdx.x; c < C; c += kWideThreads) add_exact(s, e, elem_to_float(x[c]));
         const float mean = row_sum_split<kWideThreads>(s, e, red[0]) * inv_c;
         float q[1] = {0.f};
-        for (int c = threadIdx.x; c < C; c += kWideThreads) {
+        for (unsigned c = threadIdx.x; c < C; c += kWideThreads) {
             const float d = elem_to_float(x[c]) - mean;
             q[0] = fmaf(d, d, q[0]);
         }
@@ -518,7 +519,7 @@ __global__ void __launch_bounds__(kWideThreads) norm_fwd_wide_kernel(const NormA
             if (a.mean != nullptr) a.mean[row] = mean;
             if (a.rstd != nullptr) a.rstd[row] = rstd;
         }
-        for (int c = threadIdx.x; c < C; c += kWideThreads) {
+        for (unsigned c = threadIdx.x; c < C; c += kWideThreads) {
             const float w = a.w != nullptr ? load_param(a.w, a.param_f32, c) : 1.f;
             const float b = a.b != nullptr ? load_param(a.b, a.param_f32, c) : 0.f;
             float o[1] = {fmaf((elem_to_float(x[c]) - mean) * rstd, w, b)};
@@ -947,7 +948,7 @@ __global__ void __launch_bounds__(kWideThreads) norm_bwd_wide_kernel(const NormB
     __shared__ float red[2][2 * kWideThreads / 32];
     pdl_wait_prior();
     pdl_allow_next();
-    const int C = a.cols;
+    const unsigned C = a.cols;
     const float inv_c = 1.f / (float)C;
     int turn = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ++turn) {
@@ -955,7 +956,7 @@ __global__ void __launch_bounds__(kWideThreads) norm_bwd_wide_kernel(const NormB
         const T *dy = reinterpret_cast<const T *>(a.dy) + row * a.lddy;
         const float mean = a.mean[row], rstd = a.rstd[row];
         float s[2] = {0.f, 0.f};
-        for (int c = threadIdx.x; c < C; c += kWideThreads) {
+        for (unsigned c = threadIdx.x; c < C; c += kWideThreads) {
             const float w = a.w != nullptr ? load_param(a.w, a.param_f32, c) : 1.f;
             const float wg = w * elem_to_float(dy[c]);
             s[0] += wg;
@@ -963,7 +964,7 @@ __global__ void __launch_bounds__(kWideThreads) norm_bwd_wide_kernel(const NormB
         }
         row_sum<kWideThreads, 2>(s, red[turn & 1]);
         const float m1 = s[0] * inv_c, m2 = s[1] * inv_c;
-        for (int c = threadIdx.x; c < C; c += kWideThreads) {
+        for (unsigned c = threadIdx.x; c < C; c += kWideThreads) {
             const float w = a.w != nullptr ? load_param(a.w, a.param_f32, c) : 1.f;
             const float h = (elem_to_float(x[c]) - mean) * rstd;
             float_to_elem(reinterpret_cast<T *>(a.dx) + row * C + c,
@@ -976,8 +977,8 @@ template <typename T>
 __global__ void __launch_bounds__(256) norm_colsum_wide_kernel(const NormBwdArgs a) {
     pdl_wait_prior();
     pdl_allow_next();
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= a.cols) return;
+    const unsigned c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= (unsigned)a.cols) return;
     const T *x = reinterpret_cast<const T *>(a.x), *dy = reinterpret_cast<const T *>(a.dy);
     float dw = 0.f, db = 0.f;
     for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
@@ -1000,12 +1001,12 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *partial,
     pdl_wait_prior();
     pdl_allow_next();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = blockIdx.x * 32 + lane;
+    const unsigned c = blockIdx.x * 32 + lane;
     void *out = blockIdx.y ? db : dw;
     if (out == nullptr) return;
     const float *p = partial + (int64_t)blockIdx.y * parts * cols;
     float v = 0.f;
-    if (c < cols) {
+    if (c < (unsigned)cols) {
 #pragma unroll 8
         for (int i = warp; i < parts; i += 32) v += p[(int64_t)i * cols + c];
     }
@@ -1013,8 +1014,8 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *partial,
     __syncthreads();
     // transposed: warp w sums column w
     v = warp_sum(acc[lane][warp]);
-    const int col = blockIdx.x * 32 + warp;
-    if (lane == 0 && col < cols) {
+    const unsigned col = blockIdx.x * 32 + warp;
+    if (lane == 0 && col < (unsigned)cols) {
         if (param_f32)
             reinterpret_cast<float *>(out)[col] = v;
         else
@@ -1259,7 +1260,7 @@ cudaError_t pick_bwd(const NormBwdArgs &a, int *parts, cudaStream_t s) {
     }
     if (a.partial == nullptr) return cudaSuccess;
     *parts = a.rows < 64 ? (int)a.rows : 64;
-    return launch_pdl(norm_colsum_wide_kernel<T>, dim3((a.cols + 255) / 256, *parts), 256, 0, s, a);
+    return launch_pdl(norm_colsum_wide_kernel<T>, dim3((a.cols + 255u) / 256, *parts), 256, 0, s, a);
 }
 
 // Whether rows of T at p, `ld` apart, can be read 16 bytes at a time.

@@ -1,0 +1,43 @@
+"""Layer norm at the ends of its arguments' ranges."""
+import pytest
+import torch
+
+import scaled_linear_layers_gb300 as fp8
+from test_gpu_norm import BF, EPS, f32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.slow
+@pytest.mark.parametrize("cols", [2 ** 31 - 1, 2 ** 31 - 1024])
+def test_the_widest_row(cols):
+    """The last step of a thread's columns passes 2^31.  A thread adds 2^21 terms
+    in fp32, whose roundings of random terms grow as their square root: 1448 * 2^-24
+    = 1e-4 of a sum; 5e-4 is allowed, besides the output's 2^-8."""
+    g = torch.Generator(device="cuda").manual_seed(80)
+    x, dy = (torch.randn(1, cols, generator=g, device="cuda", dtype=BF) for _ in range(2))
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    mean, rstd, db = f32(1), f32(1), torch.empty(cols, device="cuda", dtype=BF)
+    chunks = [slice(lo, min(cols, lo + 2 ** 26)) for lo in range(0, cols, 2 ** 26)]
+
+    def total(f):
+        return sum(f(c).sum() for c in chunks)
+
+    fp8.fp8_layer_norm(x, None, None, EPS, y, mean, rstd)
+    m = total(lambda c: x[0, c].double()) / cols
+    r = (total(lambda c: (x[0, c].double() - m).square()) / cols + EPS).rsqrt()
+    assert abs(mean.item() - m.item()) <= 32 * 2.0 ** -24
+    assert abs(rstd.item() - r.item()) <= 5e-4 * r.item()
+    for c in chunks:
+        ref = (x[0, c].double() - m) * r
+        assert ((y[0, c].double() - ref).abs() <= (2.0 ** -8 + 5e-4) * ref.abs() + 1e-5).all()
+    ws = torch.empty(fp8.fp8_layer_norm_workspace_bytes(1, cols), dtype=torch.uint8, device="cuda")
+    fp8.fp8_layer_norm_backward(dy, x, None, mean, rstd, dx, None, db, ws)
+    assert torch.equal(db, dy[0])
+    m1 = total(lambda c: dy[0, c].double()) / cols
+    m2 = total(lambda c: dy[0, c].double() * (x[0, c].double() - m) * r) / cols
+    for c in chunks:
+        xhat = (x[0, c].double() - m) * r
+        ref = r * (dy[0, c].double() - m1 - xhat * m2)
+        assert ((dx[0, c].double() - ref).abs() <= (2.0 ** -8 + 5e-4) * ref.abs()
+                + 1e-4 * (1 + xhat.abs())).all()
