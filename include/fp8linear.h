@@ -513,7 +513,8 @@ typedef enum { FP8_DT_BF16 = 0, FP8_DT_F32 = 1 } fp8_dtype;
  * rounded to nearest even and saturating (scale_inv [1] is read: delayed
  * scaling, as in fp8_quantize); amax_out [1] = max |y| of that fp32 y (NaN if
  * any is), overwritten; mean, rstd [rows], which the backward call takes.
- * rows >= 0, 0 <= cols < 2^31 (FP8_ERR_SHAPE); eps >= 0. */
+ * rows >= 0, 0 <= cols < 2^31 (FP8_ERR_SHAPE; rows without columns have a mean
+ * and rstd of 0/0, NaN); eps >= 0. */
 fp8_status fp8_layer_norm(const void *x, int64_t ldx, fp8_dtype xt, const void *weight,
                           const void *bias, fp8_dtype wt, int64_t rows, int64_t cols, float eps,
                           void *y, uint8_t *yq, const float *scale_inv, float *amax_out,

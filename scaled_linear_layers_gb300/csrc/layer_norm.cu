@@ -534,6 +534,19 @@ __global__ void __launch_bounds__(kWideThreads) norm_fwd_wide_kernel(const NormA
     if (a.amax != nullptr) amax_commit(m, a.amax);
 }
 
+// The statistics of rows without columns: 0 / 0.
+__global__ void __launch_bounds__(256) norm_no_columns_kernel(float *mean, float *rstd,
+                                                              int64_t rows) {
+    pdl_wait_prior();
+    pdl_allow_next();
+    const float nan = __int_as_float(0x7FFFFFFF);
+    for (int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x; r < rows;
+         r += (int64_t)gridDim.x * 256) {
+        if (mean != nullptr) mean[r] = nan;
+        if (rstd != nullptr) rstd[r] = nan;
+    }
+}
+
 // --------------------------------------------------------------- backward ---
 
 // A team member's part of the gradient: its columns' sums so far.
@@ -1292,7 +1305,12 @@ cudaError_t launch_layer_norm(const NormForward &n, cudaStream_t s) {
         cudaError_t e = launch_zero_f32(n.amax, 1, s);
         if (e != cudaSuccess) return e;
     }
-    if (n.rows == 0 || n.cols == 0) return cudaSuccess;
+    if (n.rows == 0) return cudaSuccess;
+    if (n.cols == 0) {
+        if (n.mean == nullptr && n.rstd == nullptr) return cudaSuccess;
+        const int64_t grid = std::min<int64_t>((n.rows + 255) / 256, 8 * (int64_t)num_sms());
+        return launch_pdl(norm_no_columns_kernel, (int)grid, 256, 0, s, n.mean, n.rstd, n.rows);
+    }
     NormArgs a = {n.x, n.ldx, n.w, n.b, n.param_f32, n.rows, (int)n.cols, n.eps,
                   n.y, n.yq, n.scale_inv, n.amax, n.mean, n.rstd, 0,
                   g_wait_limit_ns.load(std::memory_order_relaxed), device_status_word()};

@@ -41,3 +41,15 @@ def test_the_widest_row(cols):
         ref = r * (dy[0, c].double() - m1 - xhat * m2)
         assert ((dx[0, c].double() - ref).abs() <= (2.0 ** -8 + 5e-4) * ref.abs()
                 + 1e-4 * (1 + xhat.abs())).all()
+
+
+@pytest.mark.parametrize("rows", [1, 1000, 300000])
+def test_rows_without_columns_have_no_mean(rows):
+    x = torch.empty(rows, 0, dtype=BF, device="cuda")
+    mean, rstd, amax = f32(rows).fill_(3.0), f32(rows).fill_(3.0), f32(1).fill_(3.0)
+    fp8.fp8_layer_norm(x, None, None, EPS, torch.empty_like(x), mean, rstd, amax_out=amax)
+    assert mean.isnan().all() and rstd.isnan().all()  # 0 / 0, as the formula gives
+    assert amax.item() == 0.0
+    rstd.fill_(3.0)
+    fp8.fp8_layer_norm(x, None, None, EPS, torch.empty_like(x), rstd=rstd)
+    assert rstd.isnan().all()
