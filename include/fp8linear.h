@@ -524,8 +524,9 @@ fp8_status fp8_layer_norm(const void *x, int64_t ldx, fp8_dtype xt, const void *
  *   dx = rstd * (weight*dy - mean_c(weight*dy) - xhat * mean_c(weight*dy*xhat)),
  *   dweight = sum over rows of dy*xhat, dbias = sum over rows of dy.
  * dy, x, dx have type xt; weight, dweight, dbias type wt.  dx, dweight, dbias
- * are nullable (not all).  The column sums are formed per block of the launch,
- * then over the blocks in order: the same call gives the same bits.
+ * are nullable (not all); dx may be dy or x itself, written over.  The column
+ * sums are formed per block of the launch, then over the blocks in order: the
+ * same call gives the same bits.
  * workspace: fp8_layer_norm_workspace_bytes(rows, cols) bytes, 16-byte
  * aligned, overwritten; needed with dweight or dbias.  rows = 0 gives
  * dweight = dbias = 0. */

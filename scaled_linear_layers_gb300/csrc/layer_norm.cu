@@ -1263,17 +1263,18 @@ cudaError_t pick_bwd(const NormBwdArgs &a, int *parts, cudaStream_t s) {
     }
     if constexpr (!VECTOR)
         if (a.cols <= 8192) return run_bwd<T, VECTOR, 512, 2 * EPT>(a, parts, s);
-    int grid = 0;
+    // the column sums first: dx may be written over dy or x
     cudaError_t e = cudaSuccess;
-    if (a.dx != nullptr) {
-        e = walk_grid<norm_bwd_wide_kernel<T>>(kWideThreads, a.rows, &grid);
-        if (e != cudaSuccess) return e;
-        e = launch_pdl(norm_bwd_wide_kernel<T>, grid, kWideThreads, 0, s, a);
+    if (a.partial != nullptr) {
+        *parts = a.rows < 64 ? (int)a.rows : 64;
+        e = launch_pdl(norm_colsum_wide_kernel<T>, dim3((a.cols + 255u) / 256, *parts), 256, 0, s, a);
         if (e != cudaSuccess) return e;
     }
-    if (a.partial == nullptr) return cudaSuccess;
-    *parts = a.rows < 64 ? (int)a.rows : 64;
-    return launch_pdl(norm_colsum_wide_kernel<T>, dim3((a.cols + 255u) / 256, *parts), 256, 0, s, a);
+    if (a.dx == nullptr) return cudaSuccess;
+    int grid = 0;
+    e = walk_grid<norm_bwd_wide_kernel<T>>(kWideThreads, a.rows, &grid);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(norm_bwd_wide_kernel<T>, grid, kWideThreads, 0, s, a);
 }
 
 // Whether rows of T at p, `ld` apart, can be read 16 bytes at a time.

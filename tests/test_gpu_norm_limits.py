@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import scaled_linear_layers_gb300 as fp8
-from test_gpu_norm import BF, EPS, f32
+from test_gpu_norm import BF, EPS, f32, rnd
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +53,22 @@ def test_rows_without_columns_have_no_mean(rows):
     rstd.fill_(3.0)
     fp8.fp8_layer_norm(x, None, None, EPS, torch.empty_like(x), rstd=rstd)
     assert rstd.isnan().all()
+
+
+@pytest.mark.parametrize("rows, cols", [(7, 96), (3000, 1024), (3000, 333), (400, 8208),
+                                        (400, 9001), (3, 40001)])
+@pytest.mark.parametrize("into", ["dy", "x"])
+def test_gradient_written_over_its_input(rows, cols, into):
+    x, dy = rnd(rows, cols, seed=70), rnd(rows, cols, seed=71)
+    w, m = rnd(cols, seed=72), x.double().mean(1)
+    r = ((x.double() - m[:, None]).square().mean(1) + EPS).rsqrt()
+    ws = torch.empty(fp8.fp8_layer_norm_workspace_bytes(rows, cols), dtype=torch.uint8,
+                     device="cuda")
+    outs = []
+    for over in (False, True):
+        xi, gi, dw, db = x.clone(), dy.clone(), f32(cols), f32(cols)
+        dx = (gi if into == "dy" else xi) if over else torch.empty_like(x)
+        fp8.fp8_layer_norm_backward(gi, xi, w, m.float(), r.float(), dx, dw, db, ws)
+        outs.append((dx, dw, db))
+    for apart, over in zip(*outs):
+        assert torch.equal(apart, over)
