@@ -1170,7 +1170,8 @@ fp8_status fp8_moe_dispatch(const void *x, int64_t ldx, fp8_dtype xt, int64_t to
         FP8_NEED(source, who);
         if (rows == nullptr && hidden > 0) FP8_NEED(rows_q, who);
     }
-    if (rows_q != nullptr) FP8_NEED(scale_inv, who);
+    if (rows_q != nullptr || (amax_out != nullptr && tokens > 0 && hidden > 0))
+        FP8_NEED(scale_inv, who);
     FP8_ELEM(x, xt, who);
     FP8_ELEM(rows, xt, who);
     FP8_ELEM(row_of, FP8_DT_F32, who);
@@ -1179,7 +1180,9 @@ fp8_status fp8_moe_dispatch(const void *x, int64_t ldx, fp8_dtype xt, int64_t to
     FP8_ELEM(amax_out, FP8_DT_F32, who);
     FP8_TRY(check_device(who));
     const MoeRows m = {row_of, source, tokens, capacity, hidden, (int)topk, xt == FP8_DT_F32};
-    return cuda_status(launch_moe_dispatch(m, x, ldx, rows, rows_q, scale_inv, amax_out, s), who);
+    return cuda_status(launch_moe_dispatch(m, x, ldx, rows, rows_q, rows ? nullptr : scale_inv,
+                                           amax_out, s),
+                       who);
 }
 
 namespace {

@@ -850,13 +850,13 @@ cudaError_t dispatch_rows(const RowArgs &a, bool vec, cudaStream_t s) {
     if (vec)
         return with_groups(a.m, 4, [&](auto tpt, auto km) {
             constexpr int TPT = decltype(tpt)::value, KM = decltype(km)::value;
-            return a.outq != nullptr
+            return a.scale_inv != nullptr
                        ? launch_rows<moe_dispatch_kernel<T, true, TPT, KM>, TPT>(a, true, s)
                        : launch_rows<moe_dispatch_kernel<T, false, TPT, KM>, TPT>(a, true, s);
         });
     return with_words(a.m, [&](auto tpt, auto km) {
         constexpr int TPT = decltype(tpt)::value, KM = decltype(km)::value;
-        return a.outq != nullptr
+        return a.scale_inv != nullptr
                    ? launch_rows<moe_dispatch_any_kernel<T, true, TPT, KM>, TPT>(a, true, s)
                    : launch_rows<moe_dispatch_any_kernel<T, false, TPT, KM>, TPT>(a, true, s);
     });
@@ -940,8 +940,10 @@ cudaError_t launch_moe_dispatch(const MoeRows &m, const void *x, int64_t ldx, vo
     a.m = m;
     a.x = x, a.ldx = ldx;
     a.out = out, a.outq = outq, a.scale_inv = scale_inv, a.amax = amax;
+    // (a cast without rows to write still finds the amax)
+    const bool quant = scale_inv != nullptr;
     const bool vec = row_vectors(x, ldx, m.hidden, m.f32 ? 4 : 2) &&
-                     aligned_to(outq != nullptr ? outq : out, outq != nullptr ? (m.f32 ? 4 : 8) : 16);
+                     aligned_to(quant ? outq : out, quant ? (m.f32 ? 4 : 8) : 16);
     return m.f32 ? dispatch_rows<float>(a, vec, s) : dispatch_rows<uint16_t>(a, vec, s);
 }
 
