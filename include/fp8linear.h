@@ -636,6 +636,13 @@ fp8_status fp8_check_device_status(cudaStream_t s);
  * kernels may have enqueued the earlier ones before the failing launch. */
 fp8_status fp8_inject_launch_failures(int32_t n);
 
+/* Test hook: in the calling thread's next n layer-norm calls (forward or
+ * backward) the rows that come by bulk copies are waited for but not copied, so
+ * these waits run out (fp8_set_wait_limit_ns; a copy that is under way arrives
+ * long before a wait looks at the clock).  The kernels end by themselves with
+ * the status word set and invalid outputs; n = 0 clears it. */
+fp8_status fp8_inject_lost_copies(int32_t n);
+
 /* Limit of every bounded wait in the library's kernels (mbarrier waits of the
  * GEMMs, the grid barrier of the single-launch dynamic quantiser), in
  * nanoseconds of the GPU's global timer; default 2 s, and 0 restores the

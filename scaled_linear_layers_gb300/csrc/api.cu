@@ -40,6 +40,7 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 }  // namespace
 
 thread_local int tl_fail_launches = 0;
+thread_local int tl_lose_copies = 0;
 
 namespace {
 
@@ -994,6 +995,12 @@ fp8_status fp8_pad_tokens(const uint16_t *x, int64_t rows, int64_t cols, int64_t
 fp8_status fp8_inject_launch_failures(int32_t n) {
     if (n < 0) return fail(FP8_ERR_SHAPE, "fp8_inject_launch_failures: n=%d", n);
     tl_fail_launches = n;
+    return FP8_OK;
+}
+
+fp8_status fp8_inject_lost_copies(int32_t n) {
+    if (n < 0) return fail(FP8_ERR_SHAPE, "fp8_inject_lost_copies: n=%d", n);
+    tl_lose_copies = n;
     return FP8_OK;
 }
 

@@ -13,6 +13,9 @@ int num_sms();  // SM count of the current device (cached per device)
 // calling thread's next n launches through launch_pdl return
 // cudaErrorLaunchFailure without launching anything.
 extern thread_local int tl_fail_launches;
+// (fp8_inject_lost_copies) the thread's next n layer-norm calls wait for rows
+// that no copy brings.
+extern thread_local int tl_lose_copies;
 
 // Launches `kernel` on `s` with programmatic stream serialisation allowed: it
 // may begin while the previous kernel on the stream drains, and must wait

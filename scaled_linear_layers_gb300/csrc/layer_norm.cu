@@ -64,6 +64,7 @@ struct NormArgs {
     float *amax;             // nullable, zero on entry
     float *mean, *rstd;      // nullable
     int stages;              // of the ring
+    int lose;                // (tests) rows are waited for but not copied
     uint64_t wait_limit_ns;
     unsigned int *status;
 };
@@ -79,6 +80,7 @@ struct NormBwdArgs {
     void *dx;        // [rows, width]; nullable
     float *partial;  // [2][parts][width]: dw then db of each part of the rows; nullable
     int stages;
+    int lose;        // (tests) rows are waited for but not copied
     uint64_t wait_limit_ns;
     unsigned int *status;
 };
@@ -455,7 +457,7 @@ __global__ void __launch_bounds__(block_threads(TPR), fwd_blocks(TPR, EPT))
     auto request = [&](int64_t r, int slot) {
         if (r < a.rows && ring.open()) {
             slot_expect(&ring.bars[slot], x.size(r));
-            x.request(r, ring.data + slot * ring.slot, &ring.bars[slot]);
+            if (!a.lose) x.request(r, ring.data + slot * ring.slot, &ring.bars[slot]);
         }
     };
     if (t == 0)
@@ -800,6 +802,7 @@ __global__ void __launch_bounds__(block_threads(TPR), bwd_blocks(TPR))
         if (r < a.rows && ring.open()) {
             uint8_t *to = ring.data + slot * ring.slot;
             slot_expect(&ring.bars[slot], x.size(r) + dy.size(r));
+            if (a.lose) return;
             x.request(r, to, &ring.bars[slot]);
             dy.request(r, to + half, &ring.bars[slot]);
         }
@@ -883,6 +886,7 @@ __global__ void __launch_bounds__(TPR, 1) __cluster_dims__(CTAS, 1, 1)
         if (r < a.rows && ring.open()) {
             uint8_t *to = ring.data + slot * ring.slot;
             slot_expect(&ring.bars[slot], x.size(r) + dy.size(r));
+            if (a.lose) return;
             x.request(r, to, &ring.bars[slot]);
             dy.request(r, to + half, &ring.bars[slot]);
         }
@@ -1299,6 +1303,12 @@ cudaError_t norm_bwd_type(const NormBwdArgs &a, int *parts, cudaStream_t s) {
     return vec ? pick_bwd<T, true>(a, parts, s) : pick_bwd<T, false>(a, parts, s);
 }
 
+int take_lost_copies() {
+    if (tl_lose_copies == 0) return 0;
+    --tl_lose_copies;
+    return 1;
+}
+
 }  // namespace
 
 cudaError_t launch_layer_norm(const NormForward &n, cudaStream_t s) {
@@ -1313,7 +1323,7 @@ cudaError_t launch_layer_norm(const NormForward &n, cudaStream_t s) {
         return launch_pdl(norm_no_columns_kernel, (int)grid, 256, 0, s, n.mean, n.rstd, n.rows);
     }
     NormArgs a = {n.x, n.ldx, n.w, n.b, n.param_f32, n.rows, (int)n.cols, n.eps,
-                  n.y, n.yq, n.scale_inv, n.amax, n.mean, n.rstd, 0,
+                  n.y, n.yq, n.scale_inv, n.amax, n.mean, n.rstd, 0, take_lost_copies(),
                   g_wait_limit_ns.load(std::memory_order_relaxed), device_status_word()};
     return n.x_f32 ? norm_fwd_type<float>(a, s) : norm_fwd_type<uint16_t>(a, s);
 }
@@ -1325,6 +1335,7 @@ cudaError_t launch_layer_norm_backward(const NormBackward &n, cudaStream_t s) {
     if (n.rows > 0) {
         NormBwdArgs a = {n.dy, n.x, n.lddy, n.ldx, n.w, n.param_f32, n.rows, (int)n.cols,
                          (int)n.cols, n.mean, n.rstd, n.dx, sums ? n.workspace : nullptr, 0,
+                         take_lost_copies(),
                          g_wait_limit_ns.load(std::memory_order_relaxed), device_status_word()};
         cudaError_t e = n.x_f32 ? norm_bwd_type<float>(a, &parts, s)
                                 : norm_bwd_type<uint16_t>(a, &parts, s);

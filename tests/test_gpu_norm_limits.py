@@ -3,7 +3,8 @@ import pytest
 import torch
 
 import scaled_linear_layers_gb300 as fp8
-from test_gpu_norm import BF, EPS, f32, rnd
+from scaled_linear_layers_gb300 import _lib
+from test_gpu_norm import BF, EPS, F, check_forward, f32, rnd, run_backward
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +73,46 @@ def test_gradient_written_over_its_input(rows, cols, into):
         outs.append((dx, dw, db))
     for apart, over in zip(*outs):
         assert torch.equal(apart, over)
+
+
+LIMIT_NS = 1_000_000
+
+
+def lose_a_call(call):
+    """`call` with its rows' copies left out: it ends, and the status says that
+    its waits ran out."""
+    lib = _lib.load()
+    fp8.fp8_check_device_status()
+    old = fp8.fp8_set_wait_limit_ns(LIMIT_NS)
+    try:
+        assert lib.fp8_inject_lost_copies(1) == 0
+        call()
+        with pytest.raises(fp8.Fp8Error) as e:
+            fp8.fp8_check_device_status()
+        assert e.value.status == 6  # FP8_ERR_TIMEOUT
+    finally:
+        lib.fp8_inject_lost_copies(0)
+        fp8.fp8_set_wait_limit_ns(old)
+
+
+# rows enough for the rings: teams of a warp and larger ones, rows that 16-byte
+# copies fit and rows that they do not
+@pytest.mark.parametrize("rows, cols, dtype", [(12000, 512, BF), (4000, 4096, BF), (12000, 333, BF),
+                                               (3500, 1999, F)])
+def test_rows_that_never_arrive_are_reported(rows, cols, dtype):
+    x, dy = rnd(rows, cols, seed=73, dtype=dtype), rnd(rows, cols, seed=74, dtype=dtype)
+    y, mean, rstd = torch.empty_like(x), f32(rows), f32(rows)
+    lose_a_call(lambda: fp8.fp8_layer_norm(x, None, None, EPS, y, mean, rstd))
+    fp8.fp8_layer_norm(x, None, None, EPS, y, mean, rstd)
+    fp8.fp8_check_device_status()
+    check_forward(x, None, None, y, mean, rstd)
+    ws = torch.empty(fp8.fp8_layer_norm_workspace_bytes(rows, cols), dtype=torch.uint8,
+                     device="cuda")
+    dw = f32(cols)
+    lose_a_call(lambda: fp8.fp8_layer_norm_backward(dy, x, None, mean, rstd, y, dw, None, ws))
+    run_backward(x, dy, None, F)
+    fp8.fp8_check_device_status()
+
+
+def test_lost_copies_refusal():
+    assert _lib.load().fp8_inject_lost_copies(-1) == 2
