@@ -886,7 +886,7 @@ __global__ void __launch_bounds__(TPR, 1) __cluster_dims__(CTAS, 1, 1)
         if (r < a.rows && ring.open()) {
             uint8_t *to = ring.data + slot * ring.slot;
             slot_expect(&ring.bars[slot], x.size(r) + dy.size(r));
-            if (a.lose) return;
+            if (a.lose && rank == 0) return;  // the others then wait for this block's sums
             x.request(r, to, &ring.bars[slot]);
             dy.request(r, to + half, &ring.bars[slot]);
         }
@@ -908,11 +908,14 @@ __global__ void __launch_bounds__(TPR, 1) __cluster_dims__(CTAS, 1, 1)
         float s[2];
         n.sums(a, [&](int j) { return load(sx, j); }, [&](int j) { return load(sg, j); }, mean, rstd,
                s);
+        // (after a wait that ran out, up to the turn before, the barrier may not
+        // have turned, and nothing paces this block: it tells no more, and the
+        // others' waits run out in turn)
+        const bool tells = t < CTAS && !*ring.abort;
         row_sum<TPR, 2>(s, red[turn & 1]);
-        // (after a wait that ran out the barrier may not have turned)
-        if (t == 0 && !*ring.abort)
+        if (t == 0 && tells)
             mbar_arrive_expect_tx(&told[turn & 3], CTAS * sizeof(uint64_t));
-        if (t < CTAS)
+        if (tells)
             st_async64(mapa_shared(smem_u32(&theirs[turn & 3][rank]), t), pair_of(s[0], s[1]),
                        mapa_shared(smem_u32(&told[turn & 3]), t));
         if (++ahead == a.stages) {
@@ -956,6 +959,13 @@ __global__ void __launch_bounds__(TPR, 1) __cluster_dims__(CTAS, 1, 1)
     if (t == 0) ring.settle(a.status);
     if (a.partial != nullptr) n.commit(a, blockIdx.x / CTAS, gridDim.x / CTAS, nullptr);
     cluster_sync_all();  // no block leaves while another may still write to it
+    // A block that has had every row's sums has nothing on its way to it.  One
+    // that gave up may have: what the others told before they came here lands
+    // within a few us.
+    if (t == 0 && *ring.abort) {
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 1000000) __nanosleep(1000);
+    }
 }
 
 // Rows too wide for a team: dx with one block to a row (two passes), the

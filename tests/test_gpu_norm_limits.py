@@ -114,5 +114,20 @@ def test_rows_that_never_arrive_are_reported(rows, cols, dtype):
     fp8.fp8_check_device_status()
 
 
+# rows shared by two blocks and by four: the first block's part never arrives, and
+# the others wait for its sums
+@pytest.mark.parametrize("rows, cols, dtype", [(400, 12288, BF), (300, 16384, F), (400, 9001, BF),
+                                               (200, 32768, BF)])
+def test_shared_rows_that_never_arrive_are_reported(rows, cols, dtype):
+    x, dy = rnd(rows, cols, seed=75, dtype=dtype), rnd(rows, cols, seed=76, dtype=dtype)
+    mean, rstd = x.float().mean(1), f32(rows).fill_(1.0)
+    ws = torch.empty(fp8.fp8_layer_norm_workspace_bytes(rows, cols), dtype=torch.uint8,
+                     device="cuda")
+    dx, dw = torch.empty_like(x), f32(cols)
+    lose_a_call(lambda: fp8.fp8_layer_norm_backward(dy, x, None, mean, rstd, dx, dw, None, ws))
+    run_backward(x, dy, None, F)
+    fp8.fp8_check_device_status()
+
+
 def test_lost_copies_refusal():
     assert _lib.load().fp8_inject_lost_copies(-1) == 2
