@@ -607,13 +607,16 @@ fp8_status fp8_moe_combine_backward(const void *dy, int64_t lddy, const void *ro
  * cores with fp16 operands and fp32 accumulation; the singular values that a
  * step starts from must be below 4 (the usual coefficients keep them below 1.3),
  * beyond which fp16 overflows and the result is not finite.  1 <= steps <= 64,
- * rows and cols <= 65536, batch * ceil(rows/128) * ceil(cols/128) < 2^31
+ * rows and cols <= 65536, batch * ceil(rows/128) * ceil(cols/128) < 2^23
  * (FP8_ERR_SHAPE); eps >= 0.  workspace:
- * fp8_orthogonalize_workspace_bytes(batch, rows, cols) bytes (8 a matrix
- * element, rows padded to 64, and 4 an element of A; 10 where the shorter side
- * is at most 2048 and the longer at least 2048, for A's parts; 0 for bad
- * arguments), 16-byte aligned, overwritten; calls that may overlap need their
- * own. */
+ * fp8_orthogonalize_workspace_bytes(batch, rows, cols) bytes, 16-byte aligned,
+ * overwritten; calls that may overlap need their own.  It is 8 bytes an element
+ * of the matrices, their rows padded to 64, and 4 an element of A, its rows
+ * padded likewise; 2 more an element of the matrices for A's parts where the
+ * shorter side is at most 2048 and the longer at least 2048; 12 for each of up to
+ * min(rows, max(16, 2048 / batch)) parts of a matrix's norm; and a matrix's
+ * counters, 4 bytes each, 5 T (T + 1) + T U of them for T x U tiles of 128 with
+ * T along the shorter side.  0 for bad arguments. */
 size_t fp8_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
 fp8_status fp8_orthogonalize(const void *g, int64_t ldg, int64_t bsg, fp8_dtype gt, int64_t batch,
                              int64_t rows, int64_t cols, int32_t steps, const float *coefficients,

@@ -1178,7 +1178,11 @@ float poly_scale(float a, float b, float c) {
     return std::exp2f((float)std::max(-100, std::ilogb(room)));
 }
 
-constexpr int kPrepParts = 2048;  // blocks that share a matrix in the scaling, at most
+// Blocks that share a matrix in the scaling, at most: a large batch fills the
+// GPU with few to a matrix, and a block takes a row or more.
+int64_t prep_parts(int64_t batch, int64_t rows) {
+    return std::min<int64_t>(rows, std::max<int64_t>(16, 2048 / batch));
+}
 
 // A's contraction is split where its 128-tiles would leave CTAs idle: up to 16
 // tiles to a side, 8 parts of at least 8 blocks of 64, from a contraction of
@@ -1213,7 +1217,7 @@ NsLayout ns_layout(int64_t batch, int64_t rows, int64_t cols) {
     w.lo[1] = take(x);
     w.a = take(q);
     w.b = take(q);
-    w.sums = take(pad256(batch * kPrepParts * (int64_t)sizeof(SquareSums)));
+    w.sums = take(pad256(batch * prep_parts(batch, rows) * (int64_t)sizeof(SquareSums)));
     w.flags = take(pad256(batch * ns_flags_per((s + 127) / 128, (l + 127) / 128) * 4));
     // parts of A where its tiles are few and its contraction is long
     w.parts_bytes = s <= kSplitMaxSide && l >= kSplitMinLength ? x : 0;
@@ -1349,7 +1353,8 @@ cudaError_t launch_orthogonalize(const Orthogonalize &o, cudaStream_t s, const c
     const int64_t row_blocks = (o.rows + kPrepThreads / a.tx - 1) / (kPrepThreads / a.tx);
     // eight blocks to an SM over the batch; more would add up more partial sums
     const int64_t share = 8 * (int64_t)num_sms() / o.batch;
-    a.parts = (int)std::min<int64_t>(row_blocks, std::min<int64_t>(kPrepParts, share > 16 ? share : 16));
+    a.parts = (int)std::min<int64_t>(std::min<int64_t>(row_blocks, prep_parts(o.batch, o.rows)),
+                                     share > 16 ? share : 16);
     e = o.g_f32 ? (vec ? ns_prepare<float, true>(a, o.batch, s) : ns_prepare<float, false>(a, o.batch, s))
                 : (vec ? ns_prepare<uint16_t, true>(a, o.batch, s)
                        : ns_prepare<uint16_t, false>(a, o.batch, s));

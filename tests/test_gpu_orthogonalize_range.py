@@ -45,3 +45,12 @@ def test_few_steps_keep_the_input_to_its_own_rounding(steps, scale):
     out = run(g, steps=steps, coefficients=[(1.0, 0.0, 0.0)] * steps, scale=scale)
     want = (scale * by_products(g, [(1.0, 0.0, 0.0)] * steps)).to(torch.bfloat16)
     assert (out != want).double().mean().item() <= 0.005
+
+
+def test_a_batch_of_many_small_matrices():
+    """More matrices than one launch of the scaling takes, with few parts each."""
+    g = rnd(70000, 5, 3, seed=34)
+    out = run(g)
+    ref = by_products(g, [ABC] * 5)
+    check(out, ref)
+    check(out[-1], ref[-1])
