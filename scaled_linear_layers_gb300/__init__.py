@@ -54,10 +54,16 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
+# current_stream() without the Stream object around the handle, in the torch
+# builds that have it (it is not part of torch's public interface)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
-        # current_stream() without the Stream object around the handle
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        if _current_raw_stream is not None:
+            return _current_raw_stream(torch.cuda.current_device())
+        stream = torch.cuda.current_stream()
     return stream.cuda_stream
 
 

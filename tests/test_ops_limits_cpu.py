@@ -39,3 +39,16 @@ def test_sort_needs_a_workspace_from_1025_assignments(lib):
     assert lib.fp8_moe_sort_workspace_bytes(1025, 8) > 0
     a = 0x10000  # never dereferenced: the refusal comes first
     assert lib.fp8_moe_sort(a, 0, 1025, 8, 16, 1 << 20, a, a, a, a, None, None) == 1  # FP8_ERR_NULL
+
+
+def test_current_stream_without_the_private_call(lib, monkeypatch):
+    import scaled_linear_layers_gb300 as fp8
+    import torch
+
+    class Stream:
+        cuda_stream = 0x1234
+
+    monkeypatch.setattr(fp8, "_current_raw_stream", None)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream)
+    assert fp8._stream(None) == 0x1234
+    assert fp8._stream(Stream) == 0x1234
