@@ -636,15 +636,20 @@ def fp8_moe_combine_backward(dy, rows, row_of, source, weights, drows, dweights=
 
 
 @functools.lru_cache(maxsize=256)
-def fp8_orthogonalize_workspace_bytes(batch: int, rows: int, cols: int) -> int:
-    return int(_LIB.fp8_orthogonalize_workspace_bytes(batch, rows, cols))
+def fp8_orthogonalize_workspace_bytes(batch: int, rows: int, cols: int,
+                                      precise: bool = False) -> int:
+    size = _LIB.fp8_orthogonalize_precise_workspace_bytes if precise else \
+        _LIB.fp8_orthogonalize_workspace_bytes
+    return int(size(batch, rows, cols))
 
 
 def fp8_orthogonalize(g, out, workspace, steps=5, coefficients=(3.4445, -4.7750, 2.0315),
-                      eps=1e-7, scale=1.0, stream=None):
+                      eps=1e-7, scale=1.0, stream=None, precise=False):
     """out (bf16) = scale * the Newton-Schulz orthogonalisation of g [rows,
     cols] or of each matrix of g [batch, rows, cols] (bf16 or fp32).
-    ``coefficients`` is (a, b, c) for every step or one such triple a step."""
+    ``coefficients`` is (a, b, c) for every step or one such triple a step.
+    ``precise``: operands of 22 bits in the products instead of fp16's 11, in
+    about three times the time; its workspace is asked for with it."""
     who = "fp8_orthogonalize"
     if not isinstance(g, torch.Tensor) or not g.is_cuda:
         _refuse(_lib.FP8_ERR_NULL, f"{who}: g is not a CUDA tensor")
@@ -663,12 +668,14 @@ def fp8_orthogonalize(g, out, workspace, steps=5, coefficients=(3.4445, -4.7750,
     flat = [float(v) for t in triples for v in t]
     if out is None:
         _refuse(_lib.FP8_ERR_NULL, f"{who}: out is None")
-    _check(_LIB.fp8_orthogonalize(
+    call = _LIB.fp8_orthogonalize_precise if precise else _LIB.fp8_orthogonalize
+    _check(call(
         g.data_ptr(), g.stride(-2) if rows > 1 else cols,
         g.stride(0) if batch > 1 and g.dim() == 3 else rows * cols, _DTYPES[g.dtype], batch, rows,
         cols, steps, (ctypes.c_float * max(1, len(flat)))(*flat), eps, scale,
         _dense(out, who, "out", _BF16, g.shape),
-        _workspace(workspace, who, fp8_orthogonalize_workspace_bytes(batch, rows, cols)),
+        _workspace(workspace, who,
+                   fp8_orthogonalize_workspace_bytes(batch, rows, cols, bool(precise))),
         _stream(stream)))
 
 

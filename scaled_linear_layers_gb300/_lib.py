@@ -102,6 +102,9 @@ SIGNATURES = {
     "fp8_orthogonalize_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64]),
     "fp8_orthogonalize": (S, [P, I64, I64, S, I64, I64, I64, I32, ctypes.POINTER(F32), F32, F32,
                               P, P, P]),
+    "fp8_orthogonalize_precise_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64]),
+    "fp8_orthogonalize_precise": (S, [P, I64, I64, S, I64, I64, I64, I32, ctypes.POINTER(F32), F32,
+                                      F32, P, P, P]),
     "fp8_check_device_status": (S, [P]),
     "fp8_inject_launch_failures": (S, [I32]),
     "fp8_inject_lost_copies": (S, [I32]),

@@ -1268,18 +1268,15 @@ bool orthogonalize_fits(int64_t batch, int64_t rows, int64_t cols) {
     return batch == 0 || tiles <= 0x7FFFFFFF / (4 * 64) / batch;
 }
 
-}  // namespace
-
-size_t fp8_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
+size_t orthogonalize_bytes(int64_t batch, int64_t rows, int64_t cols, bool precise) {
     if (!orthogonalize_fits(batch, rows, cols) || batch == 0 || rows == 0 || cols == 0) return 0;
-    return (size_t)orthogonalize_workspace_bytes(batch, rows, cols);
+    return (size_t)orthogonalize_workspace_bytes(batch, rows, cols, precise);
 }
 
-fp8_status fp8_orthogonalize(const void *g, int64_t ldg, int64_t bsg, fp8_dtype gt, int64_t batch,
-                             int64_t rows, int64_t cols, int32_t steps, const float *coefficients,
-                             float eps, float scale, uint16_t *out, void *workspace,
-                             cudaStream_t s) {
-    const char *who = "fp8_orthogonalize";
+fp8_status orthogonalize(const char *who, bool precise, const void *g, int64_t ldg, int64_t bsg,
+                         fp8_dtype gt, int64_t batch, int64_t rows, int64_t cols, int32_t steps,
+                         const float *coefficients, float eps, float scale, uint16_t *out,
+                         void *workspace, cudaStream_t s) {
     FP8_TRY(check_dtype(who, gt));
     if (!orthogonalize_fits(batch, rows, cols) || ldg < 0 || bsg < 0)
         return fail(FP8_ERR_SHAPE, "%s: shape [%lld, %lld, %lld], strides %lld, %lld", who,
@@ -1299,10 +1296,36 @@ fp8_status fp8_orthogonalize(const void *g, int64_t ldg, int64_t bsg, fp8_dtype 
     FP8_ALIGN(workspace, who);
     FP8_TRY(check_device(who));
     const Orthogonalize o = {g, ldg, bsg, gt == FP8_DT_F32, batch, rows, cols, steps, coefficients,
-                             eps, scale, out, workspace};
+                             eps, scale, out, workspace, precise};
     const char *why = nullptr;
     const cudaError_t e = launch_orthogonalize(o, s, &why);
     return cuda_status(e, who, why);
+}
+
+}  // namespace
+
+size_t fp8_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
+    return orthogonalize_bytes(batch, rows, cols, false);
+}
+
+size_t fp8_orthogonalize_precise_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
+    return orthogonalize_bytes(batch, rows, cols, true);
+}
+
+fp8_status fp8_orthogonalize(const void *g, int64_t ldg, int64_t bsg, fp8_dtype gt, int64_t batch,
+                             int64_t rows, int64_t cols, int32_t steps, const float *coefficients,
+                             float eps, float scale, uint16_t *out, void *workspace,
+                             cudaStream_t s) {
+    return orthogonalize("fp8_orthogonalize", false, g, ldg, bsg, gt, batch, rows, cols, steps,
+                         coefficients, eps, scale, out, workspace, s);
+}
+
+fp8_status fp8_orthogonalize_precise(const void *g, int64_t ldg, int64_t bsg, fp8_dtype gt,
+                                     int64_t batch, int64_t rows, int64_t cols, int32_t steps,
+                                     const float *coefficients, float eps, float scale,
+                                     uint16_t *out, void *workspace, cudaStream_t s) {
+    return orthogonalize("fp8_orthogonalize_precise", true, g, ldg, bsg, gt, batch, rows, cols,
+                         steps, coefficients, eps, scale, out, workspace, s);
 }
 
 fp8_status fp8_check_device_status(cudaStream_t s) {

@@ -226,8 +226,9 @@ struct Orthogonalize {
     float eps, scale;
     uint16_t *out;
     void *workspace;
+    bool precise;  // operands as sums of two fp16 numbers
 };
-int64_t orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
+int64_t orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols, bool precise);
 cudaError_t launch_orthogonalize(const Orthogonalize &o, cudaStream_t s, const char **why);
 
 cudaError_t launch_meta_init(float *dev, int interval, cudaStream_t s);

@@ -15,26 +15,36 @@
 // leaves room for singular values up to 4 and keeps entries down to 2^-26
 // normal, and B times a power of two of the step's own, the largest up to 2^10
 // that leaves room for what (a, b, c) make of such singular values (2^7 with the
-// usual coefficients).  Rounding X itself to fp16 would cost
-// more than the products' roundings do: its error lies in all directions
-// alike, and the first steps multiply small singular values by `a` each.  So X
-// is held as the sum of two fp16 numbers (22 bits) in the first three steps and
-// until the last two, and a X is added from that sum in the epilogue; only the
-// products see the rounded X.  In the other steps the singular values are of
+// usual coefficients).  Rounding X itself to fp16 would cost more than the
+// products' roundings do: its error lies in all directions alike, and the first
+// steps multiply small singular values by `a` each.  So X is held as the sum of
+// two fp16 numbers (22 bits) in the first three steps and until the last two, and
+// a X is added from that sum in the epilogue; only the products see the rounded X.  In the other steps the singular values are of
 // order 1 and a X goes through the product instead, as (a I + B) X, which rounds
-// less and reads nothing in the epilogue.  Measured in 64 bits against the formula,
-// the result is 0.4e-3 to 1.3e-3 off (2-norm, matrices of 128 and more), below
-// the 1.7e-3 of the bf16 output's own rounding; bf16 operands: 1e-2 and more.
+// less and reads nothing in the epilogue.
+//
+// Accuracy, besides the bf16 output's own rounding (1.66e-3 in the 2-norm):
+// 0.5e-3 to 2e-3 for Gaussian matrices and noise of 1 % and more on a low rank,
+// 2.9e-3 for noise of 1e-3 and less and after eight steps.  Roundings grow by the
+// slopes of the steps' polynomials: coefficients whose intervals end at the largest
+// singular value, where their slope is largest, leave a nearly rank-one matrix
+// (noise 1e-4) 2.5e-2 off; divided by a safety factor of 1.01 (a / f, b / f^3,
+// c / f^5) 2.9e-3.  The PRECISE form holds both operands of every product as sums
+// of two fp16 numbers, three products for one: as near the formula as fp32
+// products are (0 to 6e-4 from its rounded value, fp32 0 to 8e-4; in that worst
+// case 2.9e-3 and 1.3e-3).  bf16 operands: 1e-2 and more.
 //
 // Neither operand is ever transposed in memory: the tensor core reads X with
 // either of its dims as the contraction, straight from its row-major tiles.
 //
 // Large matrices are bound by the tensor cores at the clock that the power
-// limit leaves: 4096 x 4096 in 0.88 to 0.94 ms (1460 to 1570 TFLOP/s of the
-// operations above; the launch of the products 0.83 ms), 4096 x 14336 in 2.64 to
-// 2.79 ms, eight of 4096 x 4096 in 7.4 ms.  Small ones are bound by the 15
-// dependent products, about 6 us each from tile to tile: 256 x 256 90 to 94 us,
-// 1024 x 1024 150 us.  Eight of 1531 x 1000: 268 to 276 us, between the two.
+// limit leaves: 4096 x 4096 in 0.88 to 0.94 ms replayed from a graph (1460 to 1570
+// TFLOP/s of the operations above; the launch of the products 0.83 ms), 1.0 ms a
+// call on inputs that are not in L2; 4096 x 14336 in 2.64 to 2.83 ms, eight of
+// 4096 x 4096 in 7.4 ms.  Small ones are bound by the 15 dependent products, about
+// 6 us each from tile to tile: 256 x 256 89 to 96 us, 1024 x 1024 150 us.  Eight of
+// 1531 x 1000: 267 to 280 us, between the two.  PRECISE: 2.8 ms, 8.1 ms, 138 us,
+// 288 us and 553 us.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -54,7 +64,10 @@ extern std::atomic<uint64_t> g_wait_limit_ns;
 
 namespace {
 
-constexpr float kXScale = 4096.f, kAScale = 4096.f, kLoScale = 2048.f;
+constexpr float kXScale = 4096.f, kAScale = 4096.f;
+// Of the low parts: where they are only added, in the epilogue, they keep 11 bits
+// however small; as operands they have the high parts' scale.
+__host__ __device__ constexpr float lo_scale(bool precise) { return precise ? 1.f : 2048.f; }
 constexpr int kBScaleMost = 10;  // log2
 // The steps whose a X goes through the product: the last two, but none of the
 // first three, before which small singular values have not been raised.
@@ -78,7 +91,7 @@ struct PrepArgs {
     const void *g;
     int64_t ldg, bsg;  // row and batch strides in elements
     int rows, cols, ldx;
-    float eps;
+    float eps, lo_scale;
     SquareSums *sums;  // [batch][parts]
     int parts;
     int tx;            // threads along a row (a power of two)
@@ -128,7 +141,7 @@ __global__ void __launch_bounds__(kPrepThreads) ns_square_kernel(const PrepArgs 
         a.sums[(int64_t)blockIdx.y * a.parts + blockIdx.x] = SquareSums{s[0], s[1], s[2]};
 }
 
-// X 2^12 = hi + lo 2^-11; every block adds the partial sums itself, in the
+// X 2^12 = hi + lo / lo_scale; every block adds the partial sums itself, in the
 // same order.
 template <typename T, bool VECTOR>
 __global__ void __launch_bounds__(kPrepThreads) ns_scale_kernel(const PrepArgs a) {
@@ -174,7 +187,7 @@ __global__ void __launch_bounds__(kPrepThreads) ns_scale_kernel(const PrepArgs a
                 for (int i = 0; i < V; ++i) {
                     const float x = (f[i] * pre) * mul;
                     hi.v[i] = __float2half_rn(x);
-                    lo.v[i] = __float2half_rn((x - __half2float(hi.v[i])) * kLoScale);
+                    lo.v[i] = __float2half_rn((x - __half2float(hi.v[i])) * a.lo_scale);
                 }
                 const int64_t o = (at + r + u * step) * a.ldx + c;
                 *reinterpret_cast<Halves *>(a.hi + o) = hi;
@@ -232,7 +245,9 @@ struct NsMaps {
     // operands: boxes of 64 columns x 128 rows where the columns are
     // contracted; where the rows are (xm), 64 rows x 2 groups of 64 columns
     CUtensorMap x[2], xm[2], a, b;
+    CUtensorMap xl[2], xml[2], al, bl;         // PRECISE: of their low parts
     CUtensorMap dx[2], dlo[2], da, db, dout;   // outputs: boxes of 32 x 32
+    CUtensorMap dal, dbl;
 };
 
 constexpr int NS_EPI_WARPS = 8;                // two to each quarter of the lanes
@@ -535,12 +550,16 @@ __device__ __forceinline__ bool ns_mma_tile(NsRing &ring, uint32_t a0, uint32_t 
 }
 
 // Warp 0 loads, warp 1 issues the MMAs, the others write the output from the
-// other of two accumulators.
-template <int CG>
+// other of two accumulators.  PRECISE: every operand is the sum of two fp16
+// numbers and a product three of theirs (the low parts' own is below what the
+// others round away), one after the other into the same accumulator.
+template <int CG, bool PRECISE>
 __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
     constexpr int BT = 128 * CG;
     constexpr uint32_t TMEM_COLS = 2 * BT;
     constexpr uint32_t ARRIVALS = NS_EPI_WARPS * CG;  // that complete a tile
+    constexpr int PRODUCTS = PRECISE ? 3 : 1;
+    constexpr float LO_SCALE = lo_scale(PRECISE);
     constexpr int PANEL = BT / 64;                    // blocks of 64 that a tile spans
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -623,19 +642,35 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
                 store_release_cta(filling, n);
                 const NsTile t = ns_locate(p, i);
                 const int cur = t.step & 1;
-                const CUtensorMap *ma, *mb;
+                const CUtensorMap *ma, *mb, *la = nullptr, *lb = nullptr;
                 if (t.phase == kGram) {
                     ma = mb = p.tall ? &maps.xm[cur] : &maps.x[cur];
+                    if constexpr (PRECISE) la = lb = p.tall ? &maps.xml[cur] : &maps.xl[cur];
                 } else if (t.phase == kPoly) {
                     ma = mb = &maps.a;
+                    if constexpr (PRECISE) la = lb = &maps.al;
                 } else {
                     ma = p.tall ? &maps.x[cur] : &maps.b;
                     mb = p.tall ? &maps.b : &maps.xm[cur];
+                    if constexpr (PRECISE) {
+                        la = p.tall ? &maps.xl[cur] : &maps.bl;
+                        lb = p.tall ? &maps.bl : &maps.xml[cur];
+                    }
                 }
                 const int arow = t.tm * BT + (int)rank * 128, brow = t.tn * BT + (int)rank * 128;
                 const int nk = blocks(t.phase);
                 int first, panels;
                 panels_of(t, first, panels);
+                auto fill = [&](const CUtensorMap *a, const CUtensorMap *b, int kb, int end) {
+                    if (t.phase == kGram && p.tall)
+                        return ns_fill<CG, true, true>(ring, a0, b0, a, b, arow, brow, t.z, kb, end,
+                                                       rank, abort_flag, p);
+                    if (t.phase == kUpdate && !p.tall)
+                        return ns_fill<CG, false, true>(ring, a0, b0, a, b, arow, brow, t.z, kb, end,
+                                                        rank, abort_flag, p);
+                    return ns_fill<CG, false, false>(ring, a0, b0, a, b, arow, brow, t.z, kb, end,
+                                                     rank, abort_flag, p);
+                };
                 for (int kp = first; kp < panels && ok;) {
                     if (seen == want) {
                         ok = word_wait_bounded(scouted, want + 1, &seen, abort_flag,
@@ -644,18 +679,14 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
                         if (!ok) break;
                     }
                     const int next = min(panels, kp + (int)(seen - want));
-                    const int kb = kp * PANEL, end = min(nk, next * PANEL);
-                    if (t.phase == kGram && p.tall)
-                        ok = ns_fill<CG, true, true>(ring, a0, b0, ma, mb, arow, brow, t.z, kb, end,
-                                                     rank, abort_flag, p);
-                    else if (t.phase == kUpdate && !p.tall)
-                        ok = ns_fill<CG, false, true>(ring, a0, b0, ma, mb, arow, brow, t.z, kb, end,
-                                                      rank, abort_flag, p);
-                    else
-                        ok = ns_fill<CG, false, false>(ring, a0, b0, ma, mb, arow, brow, t.z, kb,
-                                                       end, rank, abort_flag, p);
+                    // (PRECISE: the small products first; then all panels are there)
+                    ok = fill(PRECISE ? la : ma, mb, kp * PANEL, min(nk, next * PANEL));
                     want += next - kp;
                     kp = next;
+                }
+                if constexpr (PRECISE) {
+                    const int kb = first * PANEL, end = min(nk, panels * PANEL);
+                    ok = ok && fill(ma, lb, kb, end) && fill(ma, mb, kb, end);
                 }
             }
         }
@@ -688,7 +719,7 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
                 const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BT);
                 int first, panels;
                 panels_of(t, first, panels);
-                const int nk = min(blocks(what), panels * PANEL) - first * PANEL;
+                const int nk = PRODUCTS * (min(blocks(what), panels * PANEL) - first * PANEL);
                 if (what == kGram && p.tall)
                     ok = ns_mma_tile<CG, true, true>(ring, a0, b0, d_tmem, nk, abort_flag, p);
                 else if (what == kUpdate && !p.tall)
@@ -788,14 +819,14 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
             const uint32_t acc_phase = (it >> 1) & 1;
             const NsTile t = ns_locate(p, i);
             const bool update = t.phase == kUpdate;
-            const bool fold = folded(t.step, p.steps), last = t.step == p.steps - 1;
+            const bool fold = !PRECISE && folded(t.step, p.steps), last = t.step == p.steps - 1;
             const int M = update ? p.rows : S, N = update ? p.cols : S;
             const int row0 = t.tm * BT + (int)rank * 128 + quarter * 32, row = row0 + lane;
             const bool mirror = !update && t.tm != t.tn;
             const int width = row0 < M ? min(BT, N - t.tn * BT) : 0;
             const float ca = p.coefficients[3 * t.step], cb = p.coefficients[3 * t.step + 1],
                         cc = p.coefficients[3 * t.step + 2], b_scale = p.b_scale[t.step];
-            // output = acc_mul * acc + e_mul * (E + lo 2^-11) + diag on the diagonal
+            // output = acc_mul * acc + e_mul * (E + lo / LO_SCALE) + diag on the diagonal
             float acc_mul, e_mul = 0.f, diag = 0.f;
             const CUtensorMap *e = nullptr, *e_lo = nullptr, *out, *out_lo = nullptr;
             const uint32_t *e_flag = nullptr;
@@ -803,11 +834,13 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
             if (t.phase == kGram) {
                 acc_mul = kAScale / (kXScale * kXScale);
                 out = &maps.da;
+                if constexpr (PRECISE) out_lo = &maps.dal;
             } else if (t.phase == kPoly) {
                 acc_mul = cc * (b_scale / (kAScale * kAScale));
                 e_mul = cb * (b_scale / kAScale);
                 diag = fold ? ca * b_scale : 0.f;
                 e = &maps.da;
+                if constexpr (PRECISE) e_lo = &maps.dal, out_lo = &maps.dbl;
                 e_flag = sym_flag(p, t.z, kGram, t.tm, t.tn);
                 e_done = (uint32_t)(t.step + 1) * ARRIVALS;
                 out = &maps.db;
@@ -821,7 +854,7 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
                     e_done = (uint32_t)t.step * ARRIVALS;
                 }
                 out = last ? &maps.dout : &maps.dx[(t.step + 1) & 1];
-                if (!last && !folded(t.step + 1, p.steps)) out_lo = &maps.dlo[(t.step + 1) & 1];
+                if (!last && (PRECISE || !folded(t.step + 1, p.steps))) out_lo = &maps.dlo[(t.step + 1) & 1];
             }
             // The added matrix's boxes of a chunk come in one chunk ahead of
             // the accumulator, the first before the tile's products are done.
@@ -937,8 +970,8 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
                         for (int k = 0; k < 4; ++k) {
                             const int j = 8 * q + 2 * k;
                             const float2 h = half2_floats(hw[k]), l = half2_floats(lw[k]);
-                            v[j] = fmaf(e_mul, fmaf(l.x, 1.f / kLoScale, h.x), v[j]);
-                            v[j + 1] = fmaf(e_mul, fmaf(l.y, 1.f / kLoScale, h.y), v[j + 1]);
+                            v[j] = fmaf(e_mul, fmaf(l.x, 1.f / LO_SCALE, h.x), v[j]);
+                            v[j + 1] = fmaf(e_mul, fmaf(l.y, 1.f / LO_SCALE, h.y), v[j + 1]);
                         }
                     }
                     __syncwarp();  // every lane has read the boxes
@@ -956,34 +989,52 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) packed[j] = pack_half2(v[2 * j], v[2 * j + 1]);
                 }
-                if (lane == 0) bulk_wait_group_read<0>();  // the last copies have read the boxes
-                __syncwarp();
+                // box <- a lane's 32 values to a row; mirrored: box row j holds
+                // column j, lane's value at place `lane`
+                auto put = [&](uint8_t *to, const uint32_t (&w)[16]) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    *reinterpret_cast<uint4 *>(box + lane * 64 + 16 * (q ^ ((lane >> 1) & 3))) =
-                        make_uint4(packed[4 * q], packed[4 * q + 1], packed[4 * q + 2],
-                                   packed[4 * q + 3]);
-                if (mirror) {
-                    // box row j holds column j: lane's value at place `lane`
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<uint4 *>(to + lane * 64 + 16 * (q ^ ((lane >> 1) & 3))) =
+                            make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+                };
+                auto put_mirrored = [&](uint8_t *to, const uint32_t (&w)[16]) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        *reinterpret_cast<uint16_t *>(box2 + j * 64 +
+                        *reinterpret_cast<uint16_t *>(to + j * 64 +
                                                       16 * ((lane >> 3) ^ ((j >> 1) & 3)) +
                                                       2 * (lane & 7)) =
-                            (uint16_t)(packed[j >> 1] >> (16 * (j & 1)));
-                }
-                if (out_lo != nullptr) {
-                    uint32_t plo[16];
+                            (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+                };
+                auto low_parts = [&](uint32_t (&w)[16]) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         const float2 h = half2_floats(packed[j]);
-                        plo[j] = pack_half2((v[2 * j] - h.x) * kLoScale,
-                                            (v[2 * j + 1] - h.y) * kLoScale);
+                        w[j] = pack_half2((v[2 * j] - h.x) * LO_SCALE, (v[2 * j + 1] - h.y) * LO_SCALE);
                     }
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        *reinterpret_cast<uint4 *>(box2 + lane * 64 + 16 * (q ^ ((lane >> 1) & 3))) =
-                            make_uint4(plo[4 * q], plo[4 * q + 1], plo[4 * q + 2], plo[4 * q + 3]);
+                };
+                if (lane == 0) bulk_wait_group_read<0>();  // the last copies have read the boxes
+                __syncwarp();
+                if (PRECISE && out_lo != nullptr) {
+                    uint32_t plo[16];
+                    low_parts(plo);
+                    put(box, plo);
+                    if (mirror) put_mirrored(box2, plo);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        ns_store(out_lo, smem_u32(box), col, row0, t.z);
+                        if (mirror) ns_store(out_lo, smem_u32(box2), row0, col, t.z);
+                        bulk_commit_group();
+                        bulk_wait_group_read<0>();
+                    }
+                    __syncwarp();
+                }
+                put(box, packed);
+                if (mirror) put_mirrored(box2, packed);
+                if (!PRECISE && out_lo != nullptr) {
+                    uint32_t plo[16];
+                    low_parts(plo);
+                    put(box2, plo);
                 }
                 if (update && last && p.direct != nullptr) {
                     // an output whose rows no tensor map can describe: row by
@@ -1003,7 +1054,8 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
                 if (lane == 0) {
                     ns_store(out, smem_u32(box), col, row0, t.z);
                     if (mirror) ns_store(out, smem_u32(box2), row0, col, t.z);
-                    if (out_lo != nullptr) ns_store(out_lo, smem_u32(box2), col, row0, t.z);
+                    if (!PRECISE && out_lo != nullptr)
+                        ns_store(out_lo, smem_u32(box2), col, row0, t.z);
                     bulk_commit_group();
                 }
             }
@@ -1043,14 +1095,16 @@ __device__ __forceinline__ void ns_body(const NsMaps &maps, const NsPlan &p) {
     }
 }
 
+template <bool PRECISE>
 __global__ void __launch_bounds__(NS_THREADS, 1)
     ns_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsPlan p) {
-    ns_body<1>(maps, p);
+    ns_body<1, PRECISE>(maps, p);
 }
 
+template <bool PRECISE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
     ns_pair_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsPlan p) {
-    ns_body<2>(maps, p);
+    ns_body<2, PRECISE>(maps, p);
 }
 
 // ------------------------------------------------------------------- host ---
@@ -1101,7 +1155,7 @@ bool ns_output(CUtensorMap *m, const void *base, int64_t batch, int64_t rows, in
 }
 
 // CTAs (CG = 1) or pairs that are resident at once, asked once per device.
-template <int CG>
+template <int CG, bool PRECISE>
 cudaError_t ns_resident(int *workers) {
     static std::atomic<int> known[64];
     int dev = 0;
@@ -1111,7 +1165,7 @@ cudaError_t ns_resident(int *workers) {
     int n = cached ? known[dev].load(std::memory_order_relaxed) : 0;
     if (n == 0) {
         if constexpr (CG == 2) {
-            e = cudaFuncSetAttribute(ns_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            e = cudaFuncSetAttribute(ns_pair_kernel<PRECISE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)NS_SMEM);
             if (e != cudaSuccess) return e;
             cudaLaunchConfig_t cfg = {};
@@ -1124,12 +1178,12 @@ cudaError_t ns_resident(int *workers) {
             attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
             cfg.attrs = attr;
             cfg.numAttrs = 1;
-            e = cudaOccupancyMaxActiveClusters(&n, ns_pair_kernel, &cfg);
+            e = cudaOccupancyMaxActiveClusters(&n, ns_pair_kernel<PRECISE>, &cfg);
         } else {
-            e = cudaFuncSetAttribute(ns_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            e = cudaFuncSetAttribute(ns_kernel<PRECISE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)NS_SMEM);
             if (e != cudaSuccess) return e;
-            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, ns_kernel, NS_THREADS, NS_SMEM);
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, ns_kernel<PRECISE>, NS_THREADS, NS_SMEM);
             n *= num_sms();
         }
         if (e != cudaSuccess) return e;
@@ -1192,14 +1246,14 @@ constexpr int64_t kSplitMaxSide = 2048, kSplitMinLength = 2048, kSplitMinBlocks 
                   kSplitMost = 8;
 
 struct NsLayout {
-    int64_t ldx, lds, x[2], lo[2], a, b, sums, flags, parts, parts_bytes, bytes;
+    int64_t ldx, lds, x[2], lo[2], a, b, alo, blo, sums, flags, parts, parts_bytes, bytes;
 };
 
 int64_t ns_flags_per(int64_t T, int64_t U) {
     return T * (T + 1) + U * T + NS_EPI_WARPS * T * (T + 1) / 2;
 }
 
-NsLayout ns_layout(int64_t batch, int64_t rows, int64_t cols) {
+NsLayout ns_layout(int64_t batch, int64_t rows, int64_t cols, bool precise) {
     NsLayout w;
     const int64_t s = std::min(rows, cols), l = std::max(rows, cols);
     w.ldx = pad64(cols);
@@ -1217,6 +1271,8 @@ NsLayout ns_layout(int64_t batch, int64_t rows, int64_t cols) {
     w.lo[1] = take(x);
     w.a = take(q);
     w.b = take(q);
+    w.alo = take(precise ? q : 0);
+    w.blo = take(precise ? q : 0);
     w.sums = take(pad256(batch * prep_parts(batch, rows) * (int64_t)sizeof(SquareSums)));
     w.flags = take(pad256(batch * ns_flags_per((s + 127) / 128, (l + 127) / 128) * 4));
     // parts of A where its tiles are few and its contraction is long
@@ -1247,14 +1303,14 @@ cudaError_t ns_prepare(const PrepArgs &a, int64_t batch, cudaStream_t s) {
 
 }  // namespace
 
-int64_t orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
-    return ns_layout(batch, rows, cols).bytes;
+int64_t orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols, bool precise) {
+    return ns_layout(batch, rows, cols, precise).bytes;
 }
 
 cudaError_t launch_orthogonalize(const Orthogonalize &o, cudaStream_t s, const char **why) {
     if (o.batch == 0 || o.rows == 0 || o.cols == 0) return cudaSuccess;
     const int64_t S = std::min(o.rows, o.cols), L = std::max(o.rows, o.cols);
-    const NsLayout w = ns_layout(o.batch, o.rows, o.cols);
+    const NsLayout w = ns_layout(o.batch, o.rows, o.cols, o.precise);
     uint8_t *base = reinterpret_cast<uint8_t *>(o.workspace);
     auto half = [&](int64_t off) { return reinterpret_cast<__half *>(base + off); };
 
@@ -1264,9 +1320,9 @@ cudaError_t launch_orthogonalize(const Orthogonalize &o, cudaStream_t s, const c
     // and the time of one (375 ns a pair's, 297 ns a CTA's: those are bound by
     // their loads).
     int pairs = 0, singles = 0;
-    cudaError_t e = ns_resident<2>(&pairs);
+    cudaError_t e = o.precise ? ns_resident<2, true>(&pairs) : ns_resident<2, false>(&pairs);
     if (e != cudaSuccess) return e;
-    e = ns_resident<1>(&singles);
+    e = o.precise ? ns_resident<1, true>(&singles) : ns_resident<1, false>(&singles);
     if (e != cudaSuccess) return e;
     // Parts of A's contraction for the single CTAs: as many as give idle ones
     // work, leave each enough to do and fit the memory for their sums.
@@ -1310,13 +1366,13 @@ cudaError_t launch_orthogonalize(const Orthogonalize &o, cudaStream_t s, const c
     for (int i = 0; i < 3 * o.steps; ++i) p.coefficients[i] = o.coefficients[i];
     for (int i = 0; i < o.steps; ++i) {
         const float *abc = o.coefficients + 3 * i;
-        p.b_scale[i] = poly_scale(folded(i, o.steps) ? abc[0] : 0.f, abc[1], abc[2]);
+        p.b_scale[i] = poly_scale(!o.precise && folded(i, o.steps) ? abc[0] : 0.f, abc[1], abc[2]);
     }
     p.scale = o.scale;
     p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
     p.status = device_status_word();
 
-    NsMaps maps;
+    NsMaps maps = {};
     const bool out_map = o.cols % 8 == 0 && aligned_to(o.out, 16);
     if (!out_map) p.direct = o.out;
     bool ok = true;
@@ -1325,6 +1381,15 @@ cudaError_t launch_orthogonalize(const Orthogonalize &o, cudaStream_t s, const c
              ns_operand_mn(&maps.xm[i], half(w.x[i]), o.batch, o.rows, o.cols, w.ldx) &&
              ns_output(&maps.dx[i], half(w.x[i]), o.batch, o.rows, o.cols, w.ldx) &&
              ns_output(&maps.dlo[i], half(w.lo[i]), o.batch, o.rows, o.cols, w.ldx);
+    if (o.precise) {
+        for (int i = 0; i < 2; ++i)
+            ok = ok && ns_operand(&maps.xl[i], half(w.lo[i]), o.batch, o.rows, o.cols, w.ldx) &&
+                 ns_operand_mn(&maps.xml[i], half(w.lo[i]), o.batch, o.rows, o.cols, w.ldx);
+        ok = ok && ns_operand(&maps.al, half(w.alo), o.batch, S, S, w.lds) &&
+             ns_operand(&maps.bl, half(w.blo), o.batch, S, S, w.lds) &&
+             ns_output(&maps.dal, half(w.alo), o.batch, S, S, w.lds) &&
+             ns_output(&maps.dbl, half(w.blo), o.batch, S, S, w.lds);
+    }
     ok = ok && ns_operand(&maps.a, half(w.a), o.batch, S, S, w.lds) &&
          ns_operand(&maps.b, half(w.b), o.batch, S, S, w.lds) &&
          ns_output(&maps.da, half(w.a), o.batch, S, S, w.lds) &&
@@ -1340,6 +1405,7 @@ cudaError_t launch_orthogonalize(const Orthogonalize &o, cudaStream_t s, const c
     a.g = o.g, a.ldg = o.ldg, a.bsg = o.bsg;
     a.rows = (int)o.rows, a.cols = (int)o.cols, a.ldx = (int)w.ldx;
     a.eps = o.eps;
+    a.lo_scale = lo_scale(o.precise);
     a.sums = reinterpret_cast<SquareSums *>(base + w.sums);
     a.hi = half(w.x[0]), a.lo = half(w.lo[0]);
     a.flags = p.flags;
@@ -1360,8 +1426,10 @@ cudaError_t launch_orthogonalize(const Orthogonalize &o, cudaStream_t s, const c
                        : ns_prepare<uint16_t, false>(a, o.batch, s));
     if (e != cudaSuccess) return e;
     const int workers = std::min(pair ? pairs : singles, p.per_step);
-    return pair ? ns_launch(ns_pair_kernel, 2 * workers, s, maps, p)
-                : ns_launch(ns_kernel, workers, s, maps, p);
+    if (pair)
+        return ns_launch(o.precise ? ns_pair_kernel<true> : ns_pair_kernel<false>, 2 * workers, s,
+                         maps, p);
+    return ns_launch(o.precise ? ns_kernel<true> : ns_kernel<false>, workers, s, maps, p);
 }
 
 }  // namespace fp8

@@ -1,4 +1,6 @@
 """Sizes of workspaces and their borders: host arithmetic only."""
+import ctypes
+
 import pytest
 
 import __graft_entry__
@@ -26,12 +28,24 @@ def test_orthogonalize_workspace_is_what_the_header_says(lib, batch, rows, cols)
         + 12 * batch * min(rows, max(16, 2048 // batch)) + 4 * batch * (5 * t * (t + 1) + t * u)
     got = lib.fp8_orthogonalize_workspace_bytes(batch, rows, cols)
     assert want <= got <= want + 10 * 256  # ten regions, each from a multiple of 256
+    precise = lib.fp8_orthogonalize_precise_workspace_bytes(batch, rows, cols)
+    assert want + 4 * batch * s * pad(s, 64) <= precise <= got + 4 * batch * s * pad(s, 64) + 512
 
 
 def test_orthogonalize_tiles(lib):
     f = lib.fp8_orthogonalize_workspace_bytes
     assert f(2 ** 23 - 1, 1, 1) > 0 and f(2 ** 23, 1, 1) == 0
     assert f(2 ** 23 // 4, 129, 129) == 0 and f(2 ** 23 // 4 - 1, 129, 129) > 0
+    assert lib.fp8_orthogonalize_precise_workspace_bytes(2 ** 23, 1, 1) == 0
+
+
+def test_precise_refusals_name_their_entry_point(lib):
+    a, abc = 0x10000, (ctypes.c_float * 3)(1, 0, 0)
+    call = lib.fp8_orthogonalize_precise
+    assert call(a, 64, 4096, 0, 1, 64, 64, 0, abc, 0.0, 1.0, a, a, None) == 2   # steps
+    assert "fp8_orthogonalize_precise" in lib.fp8_last_error().decode()
+    assert call(a, 64, 4096, 0, 1, 64, 64, 1, None, 0.0, 1.0, a, a, None) == 1  # coefficients
+    assert call(a, 64, 4096, 0, 1, 64, 64, 1, abc, 0.0, 1.0, a, a + 8, None) == 3  # workspace
 
 
 def test_sort_needs_a_workspace_from_1025_assignments(lib):
