@@ -606,7 +606,12 @@ fp8_status fp8_moe_combine_backward(const void *dy, int64_t lddy, const void *ro
  * ldg >= 0 and batch stride bsg >= 0 elements.  The products run on the tensor
  * cores with fp16 operands and fp32 accumulation; the singular values that a
  * step starts from must be below 4 (the usual coefficients keep them below 1.3),
- * beyond which fp16 overflows and the result is not finite.  1 <= steps <= 64,
+ * beyond which fp16 overflows and the result is not finite.  Besides the bf16
+ * rounding of out (1.7e-3 in the 2-norm) the result is up to 3e-3 off with the
+ * usual coefficients, or with others whose intervals leave 1 % above the largest
+ * singular value (a / 1.01, b / 1.01^3, c / 1.01^5); without that margin roundings
+ * grow by the polynomials' slopes, to 2.5e-2 and more for nearly rank-one
+ * matrices.  fp8_orthogonalize_precise is for those.  1 <= steps <= 64,
  * rows and cols <= 65536, batch * ceil(rows/128) * ceil(cols/128) < 2^23
  * (FP8_ERR_SHAPE); eps >= 0.  workspace:
  * fp8_orthogonalize_workspace_bytes(batch, rows, cols) bytes, 16-byte aligned,
@@ -624,8 +629,9 @@ fp8_status fp8_orthogonalize(const void *g, int64_t ldg, int64_t bsg, fp8_dtype 
                              cudaStream_t s);
 
 /* The same with every operand of the products held as the sum of two fp16
- * numbers (22 bits), for about three times the time and a workspace larger by
- * 4 bytes an element of A. */
+ * numbers (22 bits): as near the formula as fp32 products are, for 1.3 (small
+ * matrices) to 3 times the time and a workspace larger by 4 bytes an element of
+ * A. */
 size_t fp8_orthogonalize_precise_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
 fp8_status fp8_orthogonalize_precise(const void *g, int64_t ldg, int64_t bsg, fp8_dtype gt,
                                      int64_t batch, int64_t rows, int64_t cols, int32_t steps,

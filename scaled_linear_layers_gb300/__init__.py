@@ -649,7 +649,7 @@ def fp8_orthogonalize(g, out, workspace, steps=5, coefficients=(3.4445, -4.7750,
     cols] or of each matrix of g [batch, rows, cols] (bf16 or fp32).
     ``coefficients`` is (a, b, c) for every step or one such triple a step.
     ``precise``: operands of 22 bits in the products instead of fp16's 11, in
-    about three times the time; its workspace is asked for with it."""
+    1.3 to 3 times the time; its workspace is asked for with it."""
     who = "fp8_orthogonalize"
     if not isinstance(g, torch.Tensor) or not g.is_cuda:
         _refuse(_lib.FP8_ERR_NULL, f"{who}: g is not a CUDA tensor")

@@ -54,3 +54,29 @@ def test_a_batch_of_many_small_matrices():
     ref = by_products(g, [ABC] * 5)
     check(out, ref)
     check(out[-1], ref[-1])
+
+
+# The first steps' errors grow with the slopes of the later ones: 2.4e-3 to 2.9e-3
+# (2-norm) in these cases besides the output's 1.7e-3, together 3.4e-3; 5e-3 as for
+# the others.
+@pytest.mark.parametrize("rank", [1, 2, 8])
+@pytest.mark.parametrize("noise", [1e-3, 1e-4])
+@pytest.mark.parametrize("coefficients", ["usual", "own interval a step"])
+def test_nearly_low_rank(rank, noise, coefficients):
+    g = rnd(256, rank, seed=35) @ rnd(rank, 384, seed=36) / rank ** 0.5
+    g += noise * rnd(256, 384, seed=37)
+    triples = [ABC] * 5
+    if coefficients != "usual":
+        # the odd quintics nearest to 1 on [1e-3, 1] and the ranges after it, with
+        # 1 % between the largest singular value and the end
+        triples = [(a / 1.01, b / 1.01 ** 3, c / 1.01 ** 5) for a, b, c in (
+            (8.470329, -25.108078, 18.629279), (4.182834, -3.108701, 0.580607),
+            (3.961856, -2.954063, 0.562976), (3.286584, -2.464719, 0.507358),
+            (2.273748, -1.644659, 0.416191), (1.888716, -1.265157, 0.376519))]
+    check(run(g, steps=len(triples), coefficients=triples), by_products(g, triples))
+
+
+@pytest.mark.parametrize("steps", [8, 10])
+def test_many_steps(steps):
+    g = rnd(256, 384, seed=38)
+    check(run(g, steps=steps), by_products(g, [ABC] * steps))
