@@ -205,7 +205,8 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(const SortArgs 
     // padding: each expert's last rows (a warp to an expert), and what lies
     // past the last segment
     for (int e = blockIdx.x * kSortWarps + warp; e < a.experts; e += gridDim.x * kSortWarps)
-        for (int32_t r = first[e] + total[e] + lane; r < first[e + 1]; r += 32) a.source[r] = -1;
+        for (int64_t r = (int64_t)first[e] + total[e] + lane; r < first[e + 1]; r += 32)
+            a.source[r] = -1;
     for (int64_t r = first[a.experts] + (int64_t)blockIdx.x * kSortThreads + threadIdx.x;
          r < a.capacity; r += (int64_t)gridDim.x * kSortThreads)
         a.source[r] = -1;

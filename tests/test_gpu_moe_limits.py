@@ -21,3 +21,17 @@ def test_amax_of_tokens_without_rows(hidden):
                              amax_out=amax)
         assert amax.item() == x.float().abs().max().item()
         assert (rows == 0).all()
+
+
+@pytest.mark.slow
+def test_a_segment_that_ends_at_the_last_row():
+    """Padding up to row 2^31 - 2, the last that a place of 32 bits reaches."""
+    capacity = 2 ** 31 - 1
+    i32 = lambda *s: torch.full(s, 7, dtype=torch.int32, device="cuda")  # noqa: E731
+    row_of, source, offsets, counts = i32(3, 1), i32(capacity), i32(2), i32(1)
+    ids = torch.tensor([[0], [-1], [0]], dtype=torch.int32, device="cuda")
+    fp8.fp8_moe_sort(ids, 1, capacity - 2, row_of, source, offsets, counts)
+    torch.cuda.synchronize()
+    assert row_of.flatten().tolist() == [0, -1, 1] and source[:2].tolist() == [0, 2]
+    assert offsets.tolist() == [0, capacity - 2] and counts.tolist() == [2]
+    assert all((part == -1).all() for part in source[2:].split(2 ** 28))
