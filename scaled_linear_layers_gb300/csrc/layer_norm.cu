@@ -26,8 +26,8 @@
 // forward 48 us (0.83), to E4M3 40 us (0.75, its amax cleared in a launch of
 // its own), backward 68 us (0.88, 5 us of it the reduction over the blocks'
 // column sums); fp32 forward 94 us (0.84), backward 132 us (0.90); 8192 columns
-// within 0.05 of that; 4096 x 16384 backward bf16 82 us (0.72), fp32 128 us
-// (0.92).  What keeps the E4M3 form from its 30 us is the work on a row between
+// within 0.05 of that; 4096 x 16384 backward bf16 80 us (0.74), fp32 125 us
+// (0.95).  What keeps the E4M3 form from its 30 us is the work on a row between
 // two barriers (issue slots 60 % busy, DRAM 62 %), which is why elements are
 // worked on in pairs and a thread holds as many as fit.  Rows of odd width move
 // single elements: bf16 8192 x 8191 forward 74 us (0.53), fp32 89 us (0.89).  One
@@ -1237,7 +1237,7 @@ cudaError_t run_bwd_cluster(NormBwdArgs a, int *parts, cudaStream_t s) {
 }
 
 // Two blocks as far as their registers go; four also where two leave only three
-// slots (fp32 4096 x 16384: 128 us, by two 151; x 12000: by two 100, by four
+// slots (fp32 4096 x 16384: 125 us, by two 151; x 12000: by two 98, by four
 // 127), unless single elements bound the row (x 16383: 187 and 184).
 template <typename T, bool VECTOR>
 cudaError_t pick_bwd_cluster(const NormBwdArgs &a, int *parts, cudaStream_t s) {

@@ -38,10 +38,10 @@
 // either of its dims as the contraction, straight from its row-major tiles.
 //
 // Large matrices are bound by the tensor cores at the clock that the power
-// limit leaves: 4096 x 4096 in 0.88 to 0.94 ms replayed from a graph (1460 to 1570
-// TFLOP/s of the operations above; the launch of the products 0.83 ms), 1.0 ms a
-// call on inputs that are not in L2; 4096 x 14336 in 2.64 to 2.83 ms, eight of
-// 4096 x 4096 in 7.4 ms.  Small ones are bound by the 15 dependent products, about
+// limit leaves: 4096 x 4096 in 0.88 to 0.94 ms in short runs (1460 to 1570 TFLOP/s
+// of the operations above; the launch of the products 0.83 ms), 0.96 to 1.03 ms
+// kept up (1.6 GHz); 4096 x 14336 in 2.64 to 2.83 ms, eight of 4096 x 4096 in 7.4
+// ms.  Small ones are bound by the 15 dependent products, about
 // 6 us each from tile to tile: 256 x 256 89 to 96 us, 1024 x 1024 150 us.  Eight of
 // 1531 x 1000: 267 to 280 us, between the two.  PRECISE: 2.8 ms, 8.1 ms, 138 us,
 // 288 us and 553 us.
