@@ -1,4 +1,13 @@
-"""Layer norm at the ends of its arguments' ranges."""
+"""Layer norm at the ends of its arguments' ranges.
+
+The tolerances of the shared checks (32 and 64 units of 2^-24 a row, rows / 128 + 256
+a column) for the kernels' shapes.  A row: a thread holds up to 32 elements, whose
+squares are 16 additions of pairs and one of the two halves, and the sum over a team is up to
+10 levels; the mean's terms cancel, so its leading bits and rests are added apart.  27
+roundings in all; up to 40001 columns above the rings' widths: 40 and 10.  A column: its
+rows of a block one after the other, at least 128 blocks or 38 clusters of at most 900
+rows, 8 teams, and up to 512 blocks by 32 warps: 16 and 5 levels.
+"""
 import pytest
 import torch
 
