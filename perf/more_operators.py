@@ -350,7 +350,7 @@ def _run_own(s):
 def _plain_route(s):
     x, k, e = s["logits"].float(), s["topk"], s["experts"]
     order = torch.argsort(x, dim=1, descending=True, stable=True)[:, :k]
-    kept = (torch.gather(x, 1, order) > -math.inf) & s["mask"][:, None]
+    kept = (torch.gather(x, 1, order) != -math.inf) & s["mask"][:, None]
     on = kept[:, 0]  # tokens with an expert
     top = torch.where(on[:, None], x, torch.zeros_like(x))
     peak = top.amax(1, keepdim=True)
@@ -475,7 +475,7 @@ def exact(case, seed):
     if op.startswith("route"):
         # by the library's softmax and, for the gradient, by autograd
         x = s["logits"].to(f)
-        on = (s["mask"] & (x > -math.inf).any(1)) if op == "route" else s["ids"][:, 0] >= 0
+        on = (s["mask"] & (x != -math.inf).any(1)) if op == "route" else s["ids"][:, 0] >= 0
         rows = torch.nonzero(on)[:, 0]
         n, e, k = max(1, rows.numel()), case["experts"], case["topk"]
         ids = _plain_route(s)["ids"] if op == "route" else s["ids"]
