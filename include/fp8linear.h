@@ -597,6 +597,128 @@ fp8_status fp8_moe_combine_backward(const void *dy, int64_t lddy, const void *ro
                                     cudaStream_t s);
 
 /* ------------------------------------------------------------------------ */
+/* Router                                                                    */
+/* ------------------------------------------------------------------------ */
+/* Each token's topk experts from its logits [tokens, experts] (type lt, row
+ * stride ldl), p = softmax(logits of the token):
+ *   ids [tokens, topk] (int32): the experts of the largest logits, in falling
+ *     order, the lowest id first among equal ones (NaN counts as the largest);
+ *     what fp8_moe_sort takes;
+ *   weights [tokens, topk] (fp32): p of these experts, or, with renormalize !=
+ *     0, p over the sum of the chosen ones; what fp8_moe_combine takes;
+ *   counts [experts] (int32): tokens that chose each expert;
+ *   live [1] (int32): tokens that have an expert;
+ *   losses [2] (fp32, nullable): the balance loss
+ *     experts / (live^2 topk) * sum over e of counts[e] * sum over t of p[t, e]
+ *     (1 when both are even over the experts) and the mean over the live tokens
+ *     of the square of log(sum of exp(logits)).
+ * A logit of -inf closes its expert to the token: it is never chosen, and ids
+ * behind the last open expert are -1 with a weight of 0.  A token whose mask
+ * (uint8 [tokens], nullable) is 0 or whose experts are all closed has ids of -1
+ * and counts nowhere; no such token's logits reach another's results.  NaN and
+ * +inf logits make their token's weights and the losses NaN.
+ * tokens >= 0, 1 <= topk <= experts (FP8_ERR_SHAPE); experts <= 1024 and topk
+ * <= 32 (else FP8_ERR_UNSUPPORTED).  Sums over tokens are formed in a fixed
+ * order: the same call gives the same bits.  workspace:
+ * fp8_moe_route_workspace_bytes(tokens, experts) bytes (0 for bad arguments),
+ * overwritten. */
+size_t fp8_moe_route_workspace_bytes(int64_t tokens, int64_t experts);
+fp8_status fp8_moe_route(const void *logits, int64_t ldl, fp8_dtype lt, const uint8_t *mask,
+                         int64_t tokens, int64_t experts, int64_t topk, int32_t renormalize,
+                         int32_t *ids, float *weights, int32_t *counts, int32_t *live,
+                         float *losses, void *workspace, cudaStream_t s);
+
+/* dlogits [tokens, experts] (type lt, contiguous) = the gradient at the logits
+ * of <weights, dweights> + <losses, dlosses>, the counts taken as constants;
+ * dweights (fp32 [tokens, topk]) and dlosses (fp32 [2], on the device) are
+ * nullable (zeros).  logits, ids, counts and live as the forward call had and
+ * wrote them (a token's ids differ); a token whose first id is below 0 gets
+ * zeros.  dlogits may be the logits themselves where they are contiguous. */
+fp8_status fp8_moe_route_backward(const void *logits, int64_t ldl, fp8_dtype lt, int64_t tokens,
+                                  int64_t experts, int64_t topk, int32_t renormalize,
+                                  const int32_t *ids, const int32_t *counts, const int32_t *live,
+                                  const float *dweights, const float *dlosses, void *dlogits,
+                                  cudaStream_t s);
+
+/* ------------------------------------------------------------------------ */
+/* The experts' linears in one launch (block recipe)                         */
+/* ------------------------------------------------------------------------ */
+/* For rows sorted by expert (fp8_moe_sort): expert e's rows are offsets[e] to
+ * offsets[e + 1] - 1 (int32 [experts + 1], on the device: nothing waits for
+ * them), and its weight is W_e [N, K].  The products and scales are those of
+ * the block recipe (fp8_linear_fprop and its gradients), each expert's with
+ * its own weight.  N and K are multiples of 128 (FP8_ERR_ALIGNMENT); 1 <=
+ * experts <= 1024 (else FP8_ERR_UNSUPPORTED); experts * N, experts * K and
+ * capacity < 2^31 (FP8_ERR_SHAPE).  All pointers but offsets are 16-byte
+ * aligned.  Offsets outside 0..capacity are taken as the nearest that is in
+ * it.  Rows from offsets[experts] on are neither read into any result nor
+ * written. */
+
+/* y [capacity, N] (bf16): row r of expert e = xq[r] · Wq_e^T.  xq [capacity, K]
+ * and x_scale [capacity, K/128] as fp8_quantize(BLOCK) makes them of the sorted
+ * rows; wq [experts, N, K] and w_scale [experts, N/128, K/128] as
+ * fp8_quantize(BLOCK_2D) makes them of the stacked [experts * N, K].  Segments
+ * may start at any row. */
+fp8_status fp8_moe_linear_fprop(const uint8_t *xq, const float *x_scale, const uint8_t *wq,
+                                const float *w_scale, const int32_t *offsets, int64_t experts,
+                                int64_t capacity, int64_t N, int64_t K, uint16_t *y,
+                                cudaStream_t s);
+
+/* dx [capacity, K] (bf16): row r of expert e = gq[r] · Wq_e.  gq [capacity, N]
+ * and g_scale [capacity, N/128] as fp8_quantize(BLOCK) makes them; wqt
+ * [K, experts * N] and w_scale as fp8_quantize_transpose(BLOCK_2D) makes them
+ * of the stacked [experts * N, K]. */
+fp8_status fp8_moe_linear_dgrad(const uint8_t *gq, const float *g_scale, const uint8_t *wqt,
+                                const float *w_scale, const int32_t *offsets, int64_t experts,
+                                int64_t capacity, int64_t N, int64_t K, uint16_t *dx,
+                                cudaStream_t s);
+
+/* dw [experts, N, K] (bf16, overwritten): Gq_e^T · Xq_e over expert e's rows,
+ * zero for an expert without rows.  gqt [N, capacity], g_scale_t [capacity/128,
+ * N], xqt [K, capacity] and x_scale_t [capacity/128, K] as
+ * fp8_quantize_transpose(BLOCK) makes qt and scale_t of the sorted rows, padding
+ * rows included (fp8_moe_dispatch writes zeros there).  capacity is a multiple
+ * of 128, and segments start and end at multiples of 128 (fp8_moe_sort's
+ * multiple): the dw of an expert whose segment does not is NaN. */
+fp8_status fp8_moe_linear_wgrad(const uint8_t *gqt, const float *g_scale_t, const uint8_t *xqt,
+                                const float *x_scale_t, const int32_t *offsets, int64_t experts,
+                                int64_t capacity, int64_t N, int64_t K, uint16_t *dw,
+                                cudaStream_t s);
+
+/* ------------------------------------------------------------------------ */
+/* Gated activation, with its input kept in 8 bits                           */
+/* ------------------------------------------------------------------------ */
+/* h [rows, 2 cols] (type ht, row stride ldh): the gate's columns, then the
+ * up's.  With s = 1 / (1 + exp(-gate)), y = gate * s * up.  Outputs, not all
+ * NULL:
+ *   y [rows, cols] in h's type;
+ *   yq [rows, cols] (E4M3) with y_scale [rows, ceil(cols/128)]: y under a scale
+ *     for each 1x128 tile, as fp8_quantize(BLOCK) casts it, from the fp32 y
+ *     before its rounding (the operand of the linear that follows);
+ *   hq [rows, 2 cols] (E4M3) with h_scale [rows, 2 ceil(cols/128)]: h itself
+ *     under 1x128 tiles that begin at the first column of each half (the
+ *     gate's scales, then the up's): 8 bits an element to keep for the
+ *     backward pass.
+ * live (int32 [1] on the device, nullable): rows from *live on are left as they
+ * were (offsets + experts of fp8_moe_sort, for rows sorted by expert).
+ * rows >= 0, 0 <= cols < 2^30 (FP8_ERR_SHAPE). */
+fp8_status fp8_swiglu(const void *h, int64_t ldh, fp8_dtype ht, int64_t rows, int64_t cols,
+                      const int32_t *live, void *y, uint8_t *yq, float *y_scale, uint8_t *hq,
+                      float *h_scale, cudaStream_t s);
+
+/* dh [rows, 2 cols] (type t) = the gradient at h for dy [rows, cols] (type t,
+ * row stride lddy):
+ *   dgate = dy * up * (s + gate * s * (1 - s)), dup = dy * gate * s.
+ * With h_scale, h is the checkpoint hq above (E4M3 bytes, row stride ldh) and
+ * its values are those the bytes stand for; without, h has type t.  y (nullable,
+ * [rows, cols], type t): the forward's y again, from the same h, so that it need
+ * not be kept for the next linear's weight gradient.  dh may be h where both are
+ * contiguous and of type t.  live as above. */
+fp8_status fp8_swiglu_backward(const void *dy, int64_t lddy, fp8_dtype t, const void *h,
+                               int64_t ldh, const float *h_scale, int64_t rows, int64_t cols,
+                               const int32_t *live, void *dh, void *y, cudaStream_t s);
+
+/* ------------------------------------------------------------------------ */
 /* Orthogonalised updates                                                    */
 /* ------------------------------------------------------------------------ */
 /* out [batch, rows, cols] (bf16, contiguous) = scale * X after `steps` steps of

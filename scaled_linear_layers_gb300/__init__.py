@@ -36,6 +36,9 @@ __all__ = [
     "fp8_layer_norm", "fp8_layer_norm_backward", "fp8_layer_norm_workspace_bytes",
     "fp8_moe_capacity", "fp8_moe_sort", "fp8_moe_sort_workspace_bytes", "fp8_moe_dispatch",
     "fp8_moe_dispatch_backward", "fp8_moe_combine", "fp8_moe_combine_backward",
+    "fp8_moe_route", "fp8_moe_route_backward", "fp8_moe_route_workspace_bytes",
+    "fp8_moe_linear_fprop", "fp8_moe_linear_dgrad", "fp8_moe_linear_wgrad",
+    "fp8_swiglu", "fp8_swiglu_backward",
     "fp8_orthogonalize", "fp8_orthogonalize_workspace_bytes",
     "Fp8Error", "DELAYED", "DYNAMIC", "BLOCK", "BLOCK_2D", "SLOT_W", "SLOT_X", "SLOT_G",
     "library_path",
@@ -475,6 +478,8 @@ _I32 = (torch.int32,)
 _INTS = (torch.int32, torch.int64)
 _E4M3 = (torch.uint8, torch.float8_e4m3fn)
 _BF16 = (torch.bfloat16,)
+_MASK = (torch.bool, torch.uint8)
+BLOCK_COLS = 128  # columns of a row tile of the block recipe
 
 
 def _param_type(who, *params):
@@ -633,6 +638,153 @@ def fp8_moe_combine_backward(dy, rows, row_of, source, weights, drows, dweights=
         _dense(weights, who, "weights", _F32, (tokens, topk)),
         _dense(drows, who, "drows", (rows.dtype,), (cap, hidden)),
         _dense(dweights, who, "dweights", _F32, (tokens, topk)), _stream(stream)))
+
+
+@functools.lru_cache(maxsize=256)
+def fp8_moe_route_workspace_bytes(tokens: int, experts: int) -> int:
+    return int(_LIB.fp8_moe_route_workspace_bytes(tokens, experts))
+
+
+def fp8_moe_route(logits, ids, weights, counts, live, losses, workspace, mask=None,
+                  renormalize=True, stream=None):
+    """Each token's experts and their weights from logits [tokens, experts]
+    (bf16 or fp32, any row stride) into ids (int32) and weights (fp32) [tokens,
+    topk]; counts (int32 [experts]), live (int32 [1]) and losses (fp32 [2] or
+    None: balance, mean square of the log-sums) as in the C header.  ``mask``:
+    bool or uint8 [tokens], 0 for padding."""
+    who = "fp8_moe_route"
+    lp, ldl = _rows(logits, who, "logits")
+    tokens, experts = logits.shape
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        _refuse(_lib.FP8_ERR_SHAPE, f"{who}: ids must be [tokens, topk]")
+    route = (tokens, ids.shape[1])
+    _check(_LIB.fp8_moe_route(
+        lp, ldl, _DTYPES[logits.dtype], _dense(mask, who, "mask", _MASK, (tokens,)), tokens,
+        experts, route[1], bool(renormalize), _dense(ids, who, "ids", _I32, route),
+        _dense(weights, who, "weights", _F32, route), _dense(counts, who, "counts", _I32, (experts,)),
+        _dense(live, who, "live", _I32, (1,)), _dense(losses, who, "losses", _F32, (2,)),
+        _workspace(workspace, who, fp8_moe_route_workspace_bytes(tokens, experts)),
+        _stream(stream)))
+
+
+def fp8_moe_route_backward(logits, ids, counts, live, dlogits, dweights=None, dlosses=None,
+                           renormalize=True, stream=None):
+    """dlogits: the gradient of fp8_moe_route's weights and losses at the
+    logits; ids, counts and live are the forward's, dlosses (fp32 [2]) is on
+    the device."""
+    who = "fp8_moe_route_backward"
+    lp, ldl = _rows(logits, who, "logits")
+    shape = logits.shape
+    tokens, experts = shape
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        _refuse(_lib.FP8_ERR_SHAPE, f"{who}: ids must be [tokens, topk]")
+    route = (tokens, ids.shape[1])
+    _check(_LIB.fp8_moe_route_backward(
+        lp, ldl, _DTYPES[logits.dtype], tokens, experts, route[1], bool(renormalize),
+        _dense(ids, who, "ids", _I32, route), _dense(counts, who, "counts", _I32, (experts,)),
+        _dense(live, who, "live", _I32, (1,)), _dense(dweights, who, "dweights", _F32, route),
+        _dense(dlosses, who, "dlosses", _F32, (2,)),
+        _dense(dlogits, who, "dlogits", (logits.dtype,), shape), _stream(stream)))
+
+
+def _matrix(t, who, name, dims=2):
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        _refuse(_lib.FP8_ERR_SHAPE, f"{who}: {name} must have {dims} dimensions")
+    return t.shape
+
+
+def _experts(who, offsets):
+    return _matrix(offsets, who, "offsets", 1)[0] - 1
+
+
+def fp8_moe_linear_fprop(xq, x_scale, wq, w_scale, offsets, y, stream=None):
+    """y [capacity, N] (bf16): the rows xq [capacity, K] of each expert's
+    segment times its wq [experts, N, K]^T (E4M3, block recipe; see the C
+    header); offsets is fp8_moe_sort's."""
+    who = "fp8_moe_linear_fprop"
+    experts = _experts(who, offsets)
+    cap, k = _matrix(xq, who, "xq")
+    n = _matrix(y, who, "y")[1]
+    _check(_LIB.fp8_moe_linear_fprop(
+        _dense(xq, who, "xq", _E4M3, (cap, k)),
+        _dense(x_scale, who, "x_scale", _F32, (cap, k // BLOCK_COLS)),
+        _dense(wq, who, "wq", _E4M3, (experts, n, k)),
+        _dense(w_scale, who, "w_scale", _F32, (experts, n // BLOCK_COLS, k // BLOCK_COLS)),
+        _dense(offsets, who, "offsets", _I32, (experts + 1,)), experts, cap, n, k,
+        _dense(y, who, "y", _BF16, (cap, n)), _stream(stream)))
+
+
+def fp8_moe_linear_dgrad(gq, g_scale, wqt, w_scale, offsets, dx, stream=None):
+    """dx [capacity, K] (bf16): the rows gq [capacity, N] of each expert's
+    segment times its weight; wqt [K, experts * N]."""
+    who = "fp8_moe_linear_dgrad"
+    experts = _experts(who, offsets)
+    cap, n = _matrix(gq, who, "gq")
+    k = _matrix(dx, who, "dx")[1]
+    _check(_LIB.fp8_moe_linear_dgrad(
+        _dense(gq, who, "gq", _E4M3, (cap, n)),
+        _dense(g_scale, who, "g_scale", _F32, (cap, n // BLOCK_COLS)),
+        _dense(wqt, who, "wqt", _E4M3, (k, experts * n)),
+        _dense(w_scale, who, "w_scale", _F32, (experts, n // BLOCK_COLS, k // BLOCK_COLS)),
+        _dense(offsets, who, "offsets", _I32, (experts + 1,)), experts, cap, n, k,
+        _dense(dx, who, "dx", _BF16, (cap, k)), _stream(stream)))
+
+
+def fp8_moe_linear_wgrad(gqt, g_scale_t, xqt, x_scale_t, offsets, dw, stream=None):
+    """dw [experts, N, K] (bf16): gqt [N, capacity] times xqt [K, capacity]^T
+    over each expert's rows (segments in whole blocks of 128 rows)."""
+    who = "fp8_moe_linear_wgrad"
+    experts = _experts(who, offsets)
+    n, cap = _matrix(gqt, who, "gqt")
+    k = _matrix(xqt, who, "xqt")[0]
+    blocks = -(-cap // BLOCK_COLS)
+    _check(_LIB.fp8_moe_linear_wgrad(
+        _dense(gqt, who, "gqt", _E4M3, (n, cap)),
+        _dense(g_scale_t, who, "g_scale_t", _F32, (blocks, n)),
+        _dense(xqt, who, "xqt", _E4M3, (k, cap)),
+        _dense(x_scale_t, who, "x_scale_t", _F32, (blocks, k)),
+        _dense(offsets, who, "offsets", _I32, (experts + 1,)), experts, cap, n, k,
+        _dense(dw, who, "dw", _BF16, (experts, n, k)), _stream(stream)))
+
+
+def fp8_swiglu(h, y=None, yq=None, y_scale=None, hq=None, h_scale=None, live=None, stream=None):
+    """The gated activation y = silu(gate) * up of h = (gate | up) [rows, 2
+    cols] (bf16 or fp32, any row stride): rows y in h's type, E4M3 yq with
+    y_scale [rows, ceil(cols/128)], and h itself as E4M3 hq with h_scale [rows,
+    2 ceil(cols/128)].  ``live`` (int32 [1]): rows from there on are left as
+    they were."""
+    who = "fp8_swiglu"
+    hp, ldh = _rows(h, who, "h")
+    rows, width = h.shape
+    cols = width // 2
+    if width % 2:
+        _refuse(_lib.FP8_ERR_SHAPE, f"{who}: h has {width} columns, which are not two halves")
+    tiles = -(-cols // BLOCK_COLS)
+    _check(_LIB.fp8_swiglu(
+        hp, ldh, _DTYPES[h.dtype], rows, cols, _dense(live, who, "live", _I32, (1,)),
+        _dense(y, who, "y", (h.dtype,), (rows, cols)), _dense(yq, who, "yq", _E4M3, (rows, cols)),
+        _dense(y_scale, who, "y_scale", _F32, (rows, tiles)),
+        _dense(hq, who, "hq", _E4M3, (rows, width)),
+        _dense(h_scale, who, "h_scale", _F32, (rows, 2 * tiles)), _stream(stream)))
+
+
+def fp8_swiglu_backward(dy, h, dh, h_scale=None, y=None, live=None, stream=None):
+    """dh [rows, 2 cols] for dy [rows, cols]: h is the forward's input in dy's
+    type or, with h_scale, its E4M3 checkpoint.  ``y``: the forward's output
+    again."""
+    who = "fp8_swiglu_backward"
+    dp, lddy = _rows(dy, who, "dy")
+    rows, cols = dy.shape
+    if h_scale is None:
+        hp, ldh = _rows(h, who, "h", dy.dtype, (rows, 2 * cols))
+    else:
+        hp, ldh = _dense(h, who, "h", _E4M3, (rows, 2 * cols)), 2 * cols
+    tiles = -(-cols // BLOCK_COLS)
+    _check(_LIB.fp8_swiglu_backward(
+        dp, lddy, _DTYPES[dy.dtype], hp, ldh, _dense(h_scale, who, "h_scale", _F32, (rows, 2 * tiles)),
+        rows, cols, _dense(live, who, "live", _I32, (1,)),
+        _dense(dh, who, "dh", (dy.dtype,), (rows, 2 * cols)),
+        _dense(y, who, "y", (dy.dtype,), (rows, cols)), _stream(stream)))
 
 
 @functools.lru_cache(maxsize=256)

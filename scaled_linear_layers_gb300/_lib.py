@@ -99,6 +99,14 @@ SIGNATURES = {
     "fp8_moe_dispatch_backward": (S, [P, I64, S, I64, I64, I64, P, I64, P, P]),
     "fp8_moe_combine": (S, [P, I64, S, I64, I64, I64, P, I64, P, P, P]),
     "fp8_moe_combine_backward": (S, [P, I64, P, I64, S, I64, I64, I64, P, P, I64, P, P, P, P]),
+    "fp8_moe_route_workspace_bytes": (ctypes.c_size_t, [I64, I64]),
+    "fp8_moe_route": (S, [P, I64, S, P, I64, I64, I64, I32, P, P, P, P, P, P, P]),
+    "fp8_moe_route_backward": (S, [P, I64, S, I64, I64, I64, I32, P, P, P, P, P, P, P]),
+    "fp8_moe_linear_fprop": (S, [P, P, P, P, P, I64, I64, I64, I64, P, P]),
+    "fp8_moe_linear_dgrad": (S, [P, P, P, P, P, I64, I64, I64, I64, P, P]),
+    "fp8_moe_linear_wgrad": (S, [P, P, P, P, P, I64, I64, I64, I64, P, P]),
+    "fp8_swiglu": (S, [P, I64, S, I64, I64, P, P, P, P, P, P, P]),
+    "fp8_swiglu_backward": (S, [P, I64, S, P, I64, P, I64, I64, P, P, P, P]),
     "fp8_orthogonalize_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64]),
     "fp8_orthogonalize": (S, [P, I64, I64, S, I64, I64, I64, I32, ctypes.POINTER(F32), F32, F32,
                               P, P, P]),

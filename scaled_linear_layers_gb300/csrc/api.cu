@@ -1304,6 +1304,233 @@ fp8_status orthogonalize(const char *who, bool precise, const void *g, int64_t l
 
 }  // namespace
 
+size_t fp8_moe_route_workspace_bytes(int64_t tokens, int64_t experts) {
+    if (tokens < 0 || experts < 1 || experts > kMoeMaxExperts) return 0;
+    return (size_t)moe_route_workspace_bytes(tokens, experts);
+}
+
+namespace {
+
+fp8_status check_route(const char *who, fp8_dtype t, int64_t ldl, int64_t tokens, int64_t experts,
+                       int64_t topk) {
+    FP8_TRY(check_dtype(who, t));
+    if (tokens < 0 || experts < 1 || topk < 1 || topk > experts || ldl < 0)
+        return fail(FP8_ERR_SHAPE, "%s: tokens=%lld experts=%lld topk=%lld row stride=%lld", who,
+                    (long long)tokens, (long long)experts, (long long)topk, (long long)ldl);
+    if (experts > kMoeMaxExperts || topk > kRouteMaxTopk)
+        return fail(FP8_ERR_UNSUPPORTED, "%s: experts=%lld topk=%lld, at most %d and %d", who,
+                    (long long)experts, (long long)topk, kMoeMaxExperts, kRouteMaxTopk);
+    if (tokens > 0x7FFFFFFF / topk)
+        return fail(FP8_ERR_SHAPE, "%s: assignments must be below 2^31", who);
+    return FP8_OK;
+}
+
+}  // namespace
+
+fp8_status fp8_moe_route(const void *logits, int64_t ldl, fp8_dtype lt, const uint8_t *mask,
+                         int64_t tokens, int64_t experts, int64_t topk, int32_t renormalize,
+                         int32_t *ids, float *weights, int32_t *counts, int32_t *live,
+                         float *losses, void *workspace, cudaStream_t s) {
+    const char *who = "fp8_moe_route";
+    FP8_TRY(check_route(who, lt, ldl, tokens, experts, topk));
+    if (tokens > 0) {
+        FP8_NEED(logits, who);
+        FP8_NEED(ids, who);
+        FP8_NEED(weights, who);
+    }
+    FP8_NEED(counts, who);
+    FP8_NEED(live, who);
+    FP8_NEED(workspace, who);
+    FP8_ELEM(logits, lt, who);
+    FP8_ELEM(ids, FP8_DT_F32, who);
+    FP8_ELEM(weights, FP8_DT_F32, who);
+    FP8_ELEM(counts, FP8_DT_F32, who);
+    FP8_ELEM(live, FP8_DT_F32, who);
+    FP8_ELEM(losses, FP8_DT_F32, who);
+    FP8_ELEM(workspace, FP8_DT_F32, who);
+    FP8_TRY(check_device(who));
+    const Route a = {logits, ldl, lt == FP8_DT_F32, mask, tokens, (int)experts, (int)topk,
+                     renormalize != 0, ids, weights, counts, live, losses,
+                     reinterpret_cast<float *>(workspace)};
+    return cuda_status(launch_moe_route(a, s), who);
+}
+
+fp8_status fp8_moe_route_backward(const void *logits, int64_t ldl, fp8_dtype lt, int64_t tokens,
+                                  int64_t experts, int64_t topk, int32_t renormalize,
+                                  const int32_t *ids, const int32_t *counts, const int32_t *live,
+                                  const float *dweights, const float *dlosses, void *dlogits,
+                                  cudaStream_t s) {
+    const char *who = "fp8_moe_route_backward";
+    FP8_TRY(check_route(who, lt, ldl, tokens, experts, topk));
+    if (tokens > 0) {
+        FP8_NEED(logits, who);
+        FP8_NEED(ids, who);
+        FP8_NEED(dlogits, who);
+    }
+    FP8_NEED(counts, who);
+    FP8_NEED(live, who);
+    FP8_ELEM(logits, lt, who);
+    FP8_ELEM(dlogits, lt, who);
+    FP8_ELEM(ids, FP8_DT_F32, who);
+    FP8_ELEM(counts, FP8_DT_F32, who);
+    FP8_ELEM(live, FP8_DT_F32, who);
+    FP8_ELEM(dweights, FP8_DT_F32, who);
+    FP8_ELEM(dlosses, FP8_DT_F32, who);
+    FP8_TRY(check_device(who));
+    const RouteBackward a = {logits, ldl, lt == FP8_DT_F32, tokens, (int)experts, (int)topk,
+                             renormalize != 0, ids, counts, live, dweights, dlosses, dlogits};
+    return cuda_status(launch_moe_route_backward(a, s), who);
+}
+
+namespace {
+
+// The arguments that the experts' three products share, and the launch.
+fp8_status moe_linear(const char *who, const MoeGemm &m, int64_t capacity_multiple,
+                      cudaError_t (*launch)(const MoeGemm &, cudaStream_t, const char **),
+                      cudaStream_t s) {
+    if (m.experts < 1 || m.capacity < 0 || m.N < 1 || m.K < 1)
+        return fail(FP8_ERR_SHAPE, "%s: experts=%lld capacity=%lld N=%lld K=%lld", who,
+                    (long long)m.experts, (long long)m.capacity, (long long)m.N, (long long)m.K);
+    if (m.experts > kMoeMaxExperts)
+        return fail(FP8_ERR_UNSUPPORTED, "%s: experts=%lld, at most %d", who,
+                    (long long)m.experts, kMoeMaxExperts);
+    FP8_TRY(check_dim16(who, "N", m.N, 128));
+    FP8_TRY(check_dim16(who, "K", m.K, 128));
+    FP8_TRY(check_dim16(who, "capacity", m.capacity, capacity_multiple));
+    const int64_t top = 0x7FFFFFFF;
+    if (m.capacity > top || m.N > top / m.experts || m.K > top / m.experts)
+        return fail(FP8_ERR_SHAPE, "%s: capacity, experts * N and experts * K must be below 2^31",
+                    who);
+    FP8_ELEM(m.offsets, FP8_DT_F32, who);
+    FP8_TRY(check_device(who));
+    const char *why = nullptr;
+    return cuda_status(launch(m, s, &why), who, why);
+}
+
+}  // namespace
+
+fp8_status fp8_moe_linear_fprop(const uint8_t *xq, const float *x_scale, const uint8_t *wq,
+                                const float *w_scale, const int32_t *offsets, int64_t experts,
+                                int64_t capacity, int64_t N, int64_t K, uint16_t *y,
+                                cudaStream_t s) {
+    const char *who = "fp8_moe_linear_fprop";
+    if (capacity != 0) {
+        FP8_NEED(xq, who);
+        FP8_NEED(x_scale, who);
+        FP8_NEED(y, who);
+    }
+    FP8_NEED(wq, who);
+    FP8_NEED(w_scale, who);
+    FP8_NEED(offsets, who);
+    FP8_ALIGN(xq, who);
+    FP8_ALIGN(x_scale, who);
+    FP8_ALIGN(wq, who);
+    FP8_ALIGN(w_scale, who);
+    FP8_ALIGN(y, who);
+    return moe_linear(who, {xq, x_scale, wq, w_scale, offsets, experts, capacity, N, K, y}, 1,
+                      launch_moe_fprop, s);
+}
+
+fp8_status fp8_moe_linear_dgrad(const uint8_t *gq, const float *g_scale, const uint8_t *wqt,
+                                const float *w_scale, const int32_t *offsets, int64_t experts,
+                                int64_t capacity, int64_t N, int64_t K, uint16_t *dx,
+                                cudaStream_t s) {
+    const char *who = "fp8_moe_linear_dgrad";
+    if (capacity != 0) {
+        FP8_NEED(gq, who);
+        FP8_NEED(g_scale, who);
+        FP8_NEED(dx, who);
+    }
+    FP8_NEED(wqt, who);
+    FP8_NEED(w_scale, who);
+    FP8_NEED(offsets, who);
+    FP8_ALIGN(gq, who);
+    FP8_ALIGN(g_scale, who);
+    FP8_ALIGN(wqt, who);
+    FP8_ALIGN(w_scale, who);
+    FP8_ALIGN(dx, who);
+    return moe_linear(who, {gq, g_scale, wqt, w_scale, offsets, experts, capacity, N, K, dx}, 1,
+                      launch_moe_dgrad, s);
+}
+
+fp8_status fp8_moe_linear_wgrad(const uint8_t *gqt, const float *g_scale_t, const uint8_t *xqt,
+                                const float *x_scale_t, const int32_t *offsets, int64_t experts,
+                                int64_t capacity, int64_t N, int64_t K, uint16_t *dw,
+                                cudaStream_t s) {
+    const char *who = "fp8_moe_linear_wgrad";
+    if (capacity != 0) {
+        FP8_NEED(gqt, who);
+        FP8_NEED(g_scale_t, who);
+        FP8_NEED(xqt, who);
+        FP8_NEED(x_scale_t, who);
+    }
+    FP8_NEED(offsets, who);
+    FP8_NEED(dw, who);
+    FP8_ALIGN(gqt, who);
+    FP8_ALIGN(g_scale_t, who);
+    FP8_ALIGN(xqt, who);
+    FP8_ALIGN(x_scale_t, who);
+    FP8_ALIGN(dw, who);
+    return moe_linear(who, {gqt, g_scale_t, xqt, x_scale_t, offsets, experts, capacity, N, K, dw},
+                      128, launch_moe_wgrad, s);
+}
+
+namespace {
+
+fp8_status check_swiglu(const char *who, fp8_dtype t, int64_t rows, int64_t cols, int64_t ld,
+                        int64_t ld2) {
+    FP8_TRY(check_dtype(who, t));
+    if (rows < 0 || cols < 0 || cols >= (1 << 30) || ld < 0 || ld2 < 0)
+        return fail(FP8_ERR_SHAPE, "%s: rows=%lld cols=%lld, row strides %lld, %lld", who,
+                    (long long)rows, (long long)cols, (long long)ld, (long long)ld2);
+    return FP8_OK;
+}
+
+}  // namespace
+
+fp8_status fp8_swiglu(const void *h, int64_t ldh, fp8_dtype ht, int64_t rows, int64_t cols,
+                      const int32_t *live, void *y, uint8_t *yq, float *y_scale, uint8_t *hq,
+                      float *h_scale, cudaStream_t s) {
+    const char *who = "fp8_swiglu";
+    FP8_TRY(check_swiglu(who, ht, rows, cols, ldh, 0));
+    if (rows > 0 && cols > 0) {
+        FP8_NEED(h, who);
+        if (yq == nullptr && hq == nullptr) FP8_NEED(y, who);
+        if (yq != nullptr) FP8_NEED(y_scale, who);
+        if (hq != nullptr) FP8_NEED(h_scale, who);
+    }
+    FP8_ELEM(h, ht, who);
+    FP8_ELEM(y, ht, who);
+    FP8_ELEM(live, FP8_DT_F32, who);
+    FP8_ELEM(y_scale, FP8_DT_F32, who);
+    FP8_ELEM(h_scale, FP8_DT_F32, who);
+    FP8_TRY(check_device(who));
+    const SwigluForward a = {h, ldh, ht == FP8_DT_F32, rows, cols, live, y, yq, y_scale, hq,
+                             h_scale};
+    return cuda_status(launch_swiglu(a, s), who);
+}
+
+fp8_status fp8_swiglu_backward(const void *dy, int64_t lddy, fp8_dtype t, const void *h,
+                               int64_t ldh, const float *h_scale, int64_t rows, int64_t cols,
+                               const int32_t *live, void *dh, void *y, cudaStream_t s) {
+    const char *who = "fp8_swiglu_backward";
+    FP8_TRY(check_swiglu(who, t, rows, cols, lddy, ldh));
+    if (rows > 0 && cols > 0) {
+        FP8_NEED(dy, who);
+        FP8_NEED(h, who);
+        FP8_NEED(dh, who);
+    }
+    FP8_ELEM(dy, t, who);
+    if (h_scale == nullptr) FP8_ELEM(h, t, who);
+    FP8_ELEM(dh, t, who);
+    FP8_ELEM(y, t, who);
+    FP8_ELEM(live, FP8_DT_F32, who);
+    FP8_ELEM(h_scale, FP8_DT_F32, who);
+    FP8_TRY(check_device(who));
+    const SwigluBackward a = {dy, lddy, t == FP8_DT_F32, h, ldh, h_scale, rows, cols, live, dh, y};
+    return cuda_status(launch_swiglu_backward(a, s), who);
+}
+
 size_t fp8_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
     return orthogonalize_bytes(batch, rows, cols, false);
 }

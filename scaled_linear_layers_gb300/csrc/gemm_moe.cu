@@ -1,0 +1,567 @@
+// The FP8 linears of all experts in one launch, block recipe: rows sorted by
+// expert in segments offsets[e] .. offsets[e + 1] - 1 (on the device), and for
+// the rows r of expert e
+//
+//   fprop: y[r, n]  = sum_kb xs(r, kb) ws(e, n/128, kb) sum_{k in kb} x[r, k] w[e, n, k]
+//   dgrad: dx[r, k] = sum_nb gs(r, nb) ws(e, nb, k/128) sum_{n in nb} g[r, n] w[e, n, k]
+//   wgrad: dw[e, n, k] = sum_b gs(b, n) xs(b, k) sum_{r in b} g[r, n] x[r, k],
+//          b the 128-row blocks of e's segment
+//
+// The pipeline is that of the single block-scaled GEMM (one persistent CTA an
+// SM, 128 x 256 output tiles; TMA ring, an MMA warp that writes each 128-deep
+// partial into one of two TMEM slots, eight epilogue warps that fold it into
+// fp32 registers with its scales).  What differs is that a tile's rows,
+// weights and contraction depend on offsets that only the device knows: every
+// CTA reads them once, counts the row tiles of each expert into shared memory
+// and finds a tile's expert by bisection, so the host launches without waiting
+// for the sort.  Tiles go expert by expert, so that an expert's weights are in
+// L2 while its rows pass.  Rows of a tile past its segment are computed from
+// what lies there and not stored.
+#include <cuda.h>
+
+#include <atomic>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "rowops.cuh"
+#include "tmap.h"
+
+namespace fp8 {
+
+extern std::atomic<uint64_t> g_wait_limit_ns;
+
+namespace {
+
+constexpr int BM = 128, BN = 256, BK = 128;
+constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int STAGES = 4;
+constexpr int SLOTS = 2;  // TMEM slots of BN columns
+constexpr int EPI_WARPS = 8, EPI0 = 4;
+constexpr int THREADS = 32 * (EPI0 + EPI_WARPS);
+constexpr int COLS = BN * 4 / EPI_WARPS;  // accumulator columns of a one-row thread
+constexpr int REGS_LOW = 40, REGS_HIGH = 232;
+constexpr uint32_t IDESC = idesc_f8_f32(BM, BN);
+constexpr int SCALES = 2 * EPI_WARPS * COLS;  // wgrad: staged column scales, two blocks a warp
+constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + SCALES * sizeof(float) + 256 +
+                        (kMoeMaxExperts + 1) * sizeof(int32_t);
+static_assert(SLOTS * BN == 512, "the slots fill TMEM");
+static_assert(SMEM <= 227 * 1024, "smem");
+
+struct Args {
+    const int32_t *offsets;
+    int experts;
+    int capacity;
+    int rows_out, cols_out;  // wgrad: rows of an expert's dw; columns of the output
+    int depth;               // contraction blocks (fprop, dgrad)
+    int by, bx;              // per expert: where its rows and its columns of B begin
+    const float *sa, *sb;
+    int64_t sa_row, sa_k;          // scale of A's row i, block kb: sa[i sa_row + kb sa_k]
+    int64_t sb_expert, sb_col, sb_k;  // of B's 128-column tile j: sb[e sb_expert + j sb_col + kb sb_k]
+    uint16_t *d;
+    uint64_t wait_limit_ns;
+    unsigned int *status;
+};
+
+// One output tile.
+struct Tile {
+    int expert, m, n;  // n: first output column
+    int row0, rows;    // A's first row (fprop, dgrad: in the sorted order), rows to store
+    int kb0, nk;       // contraction blocks (kb0: the first, wgrad)
+    bool bad;          // wgrad: a segment that does not lie on 128-row blocks
+};
+
+__device__ __forceinline__ void segment(const Args &p, int e, int &lo, int &hi) {
+    // whatever the offsets hold, a segment lies in the rows that exist
+    lo = min(max(p.offsets[e], 0), p.capacity);
+    hi = min(max(p.offsets[e + 1], lo), p.capacity);
+}
+
+// first[e]: row tiles of the experts before e.
+template <bool kWgrad>
+__device__ __forceinline__ int total_tiles(const Args &p, const int32_t *first) {
+    const int n_tiles = (p.cols_out + BN - 1) / BN;
+    if (kWgrad) return p.experts * (p.rows_out / BM) * n_tiles;
+    return first[p.experts] * n_tiles;
+}
+
+template <bool kWgrad>
+__device__ __forceinline__ Tile find_tile(const Args &p, const int32_t *first, int index) {
+    const int n_tiles = (p.cols_out + BN - 1) / BN;
+    Tile t;
+    int m_tiles, lo, hi, in;
+    if (kWgrad) {
+        m_tiles = p.rows_out / BM;
+        const int per = m_tiles * n_tiles;
+        t.expert = index / per;
+        in = index - t.expert * per;
+    } else {
+        int a = 0, b = p.experts;  // first[a] n_tiles <= index < first[b] n_tiles
+        const int at = index / n_tiles;
+        while (b - a > 1) {
+            const int mid = (a + b) >> 1;
+            if (first[mid] <= at) a = mid;
+            else b = mid;
+        }
+        t.expert = a;
+        m_tiles = first[a + 1] - first[a];
+        in = index - first[a] * n_tiles;
+    }
+    segment(p, t.expert, lo, hi);
+    int tn;
+    grouped_tile(in, m_tiles, n_tiles, 16, t.m, tn);
+    t.n = tn * BN;
+    if (kWgrad) {
+        t.bad = ((lo | hi) & (BK - 1)) != 0;
+        t.row0 = t.m * BM;
+        t.rows = BM;
+        t.kb0 = lo / BK;
+        t.nk = t.bad ? 0 : (hi - lo) / BK;
+    } else {
+        t.bad = false;
+        t.row0 = lo + t.m * BM;
+        t.rows = min(BM, hi - t.row0);
+        t.kb0 = 0;
+        t.nk = p.depth;
+    }
+    return t;
+}
+
+// acc += p * f on a pair of neighbouring columns
+__device__ __forceinline__ void fold(uint64_t &acc, uint32_t p0, uint32_t p1, uint64_t f) {
+    uint64_t pv;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(pv) : "r"(p0), "r"(p1));
+    acc = pair_fma(pv, f, acc);
+}
+
+template <bool kWgrad>
+__global__ void __launch_bounds__(THREADS, 1)
+    moe_gemm_kernel(const __grid_constant__ CUtensorMap tma_a,
+                    const __grid_constant__ CUtensorMap tma_b, const Args p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~uintptr_t(1023));
+    uint8_t *sA = smem;
+    uint8_t *sB = smem + STAGES * A_BYTES;
+    float *sbuf = reinterpret_cast<float *>(smem + STAGES * STAGE_BYTES);
+    uint64_t *full = reinterpret_cast<uint64_t *>(sbuf + SCALES);  // [STAGES] TMA -> MMA
+    uint64_t *empty = full + STAGES;                               // [STAGES] MMA -> TMA
+    uint64_t *sfull = empty + STAGES;                              // [SLOTS] MMA -> epilogue
+    uint64_t *sempty = sfull + SLOTS;                              // [SLOTS] epilogue -> MMA
+    uint64_t *drain = sempty + SLOTS;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+    int32_t *first = reinterpret_cast<int32_t *>(full) + 64;  // [experts + 1]
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < SLOTS; ++s) {
+            mbar_init(&sfull[s], 1);
+            mbar_init(&sempty[s], EPI_WARPS);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&tma_a);
+        tma_prefetch_desc(&tma_b);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_holder, SLOTS * BN);
+        tmem_relinquish();
+    }
+    pdl_wait_prior();  // the offsets are the previous kernels' result
+    pdl_allow_next();
+    if (!kWgrad && warp == 2) {
+        // row tiles of the experts before each, 32 experts at a time
+        int before = 0;
+        for (int e0 = 0; e0 < p.experts; e0 += 32) {
+            int lo = 0, hi = 0;
+            if (e0 + lane < p.experts) segment(p, e0 + lane, lo, hi);
+            int sum = (hi - lo + BM - 1) / BM;
+            const int own = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            if (e0 + lane < p.experts) first[e0 + lane] = before + sum - own;
+            before += __shfl_sync(0xFFFFFFFFu, sum, 31);
+        }
+        if (lane == 0) first[p.experts] = before;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    const int num_tiles = total_tiles<kWgrad>(p, first);
+    // each warp of the first warpgroup gives registers back as it enters its
+    // role, each epilogue warp takes more
+    auto regs_low = [] { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_LOW)); };
+
+    if (warp == 0) {
+        regs_low();
+        if (lane == 0) {
+            // ------------------------------------------------ TMA producer
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int index = blockIdx.x; index < num_tiles && ok; index += gridDim.x) {
+                const Tile t = find_tile<kWgrad>(p, first, index);
+                const int ax = t.kb0 * BK, bx = t.expert * p.bx + t.kb0 * BK;
+                const int brow = t.expert * p.by + t.n;
+                for (int q = 0; q < t.nk; ++q) {
+                    if (!mbar_wait_bounded<true>(&empty[stage], phase ^ 1u, abort_flag,
+                                                 p.wait_limit_ns, kStatusTimeoutTma, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&full[stage], STAGE_BYTES);
+                    tma_load_2d(sA + stage * A_BYTES, &tma_a, &full[stage], ax + q * BK, t.row0);
+                    tma_load_2d(sB + stage * B_BYTES, &tma_b, &full[stage], bx + q * BK, brow);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok) {
+                // wait (bounded) for the copies still in flight before teardown
+                for (int s = 0; s < STAGES; ++s) {
+                    stage = stage == 0 ? STAGES - 1 : stage - 1;
+                    if (stage == STAGES - 1) phase ^= 1u;
+                    volatile int no_abort = 0;
+                    mbar_wait_bounded(&full[stage], phase, &no_abort, 10000000ull,
+                                      kStatusTimeoutTma, p.status);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        regs_low();
+        if (lane == 0) {
+            // ------------------------------------------------- MMA issuer
+            int stage = 0;
+            uint32_t phase = 0;
+            uint32_t g = 0;  // blocks issued so far (across tiles)
+            bool ok = true;
+            for (int index = blockIdx.x; index < num_tiles && ok; index += gridDim.x) {
+                const Tile t = find_tile<kWgrad>(p, first, index);
+                for (int q = 0; q < t.nk; ++q, ++g) {
+                    const uint32_t slot = g % SLOTS, sphase = (g / SLOTS) & 1u;
+                    if (!mbar_wait_bounded<true>(&sempty[slot], sphase ^ 1u, abort_flag,
+                                                 p.wait_limit_ns, kStatusTimeoutMma, p.status) ||
+                        !mbar_wait_bounded<true>(&full[stage], phase, abort_flag, p.wait_limit_ns,
+                                                 kStatusTimeoutMma, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a0 = smem_u32(sA + stage * A_BYTES);
+                    const uint32_t b0 = smem_u32(sB + stage * B_BYTES);
+#pragma unroll
+                    for (int k = 0; k < BK / 32; ++k)
+                        mma_f8(tmem_base + slot * BN, smem_desc_sw128(a0 + 32 * k),
+                               smem_desc_sw128(b0 + 32 * k), IDESC, k != 0);
+                    mma_commit(&empty[stage]);
+                    mma_commit(&sfull[slot]);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            mma_commit(drain);
+            volatile int no_abort = 0;
+            mbar_wait_bounded(drain, 0, &no_abort, p.wait_limit_ns, kStatusTimeoutMma, p.status);
+        }
+    } else if (warp < EPI0) {
+        regs_low();  // idle warps of the first warpgroup
+    } else {
+        // ------------------------------------------------- epilogue (8 warps)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_HIGH));
+        const int quarter = warp & 3;          // TMEM lanes 32*quarter .. +31
+        const int half = (warp - EPI0) >> 2;   // columns half*COLS .. +COLS-1 of the tile
+        bool ok = true;
+        uint32_t g = 0;
+        auto wait_block = [&](uint32_t slot, uint32_t sphase) {
+            if (ok)
+                ok = mbar_wait_bounded<true>(&sfull[slot], sphase, abort_flag, p.wait_limit_ns,
+                                             kStatusTimeoutEpilogue, p.status);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (ok) tc_fence_after();
+        };
+        auto hand_back = [&](uint32_t slot) {  // the block's partial is in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sempty[slot]);
+        };
+        if constexpr (kWgrad) {
+            // Four rows x 32 columns a thread (16-lane TMEM loads): thread l
+            // holds rows 8i + l/4 (i = 0..3) of its lane quarter and, of every
+            // 8 columns, 2(l%4) and +1, so it needs 32 column scales a block
+            // instead of 128; they are staged by cp.async, one block ahead.
+            float *wbuf = sbuf + (warp - EPI0) * 2 * COLS;
+            const int fr = lane >> 2, fc = lane & 3;
+            for (int index = blockIdx.x; index < num_tiles; index += gridDim.x) {
+                const Tile t = find_tile<kWgrad>(p, first, index);
+                const int row0 = t.row0 + quarter * 32 + fr, j0 = t.n + half * COLS;
+                const float *sa = p.sa + (int64_t)t.kb0 * p.sa_k + row0;
+                const float *sb = p.sb + (int64_t)t.kb0 * p.sb_k + min(j0 + 4 * lane, p.cols_out - 4);
+                float acc[4][COLS / 4];  // [i][2 j + c]: columns 8 j + 2 fc + c
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < COLS / 4; ++j)
+                        acc[i][j] = t.bad ? __uint_as_float(0x7FFFFFFFu) : 0.f;
+                float next[4] = {};
+                auto fetch = [&](int q) {
+                    if (q < t.nk) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) next[i] = sa[(int64_t)q * p.sa_k + 8 * i];
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(
+                                         smem_u32(wbuf + (q & 1) * COLS + 4 * lane)),
+                                     "l"(sb + (int64_t)q * p.sb_k)
+                                     : "memory");
+                    }
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                };
+                fetch(0);
+                for (int q = 0; q < t.nk; ++q, ++g) {
+                    const uint32_t slot = g % SLOTS, sphase = (g / SLOTS) & 1u;
+                    float cur[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) cur[i] = next[i];
+                    asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    __syncwarp();
+                    fetch(q + 1);
+                    wait_block(slot, sphase);
+                    if (!ok) continue;
+                    const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) +
+                                           slot * BN + (uint32_t)(half * COLS);
+                    const float *buf = wbuf + (q & 1) * COLS + 2 * fc;
+                    // 16 columns a load, the next load in flight while one is folded in
+                    constexpr int NC = COLS / 16;
+                    uint32_t ra[2][8], rb[2][8];
+                    tmem_ld_16x256b_x2(taddr, ra[0]);
+                    tmem_ld_16x256b_x2(taddr + (16u << 16), rb[0]);
+                    tmem_ld_wait();
+                    tmem_regs_ready(ra[0]);
+                    tmem_regs_ready(rb[0]);
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        if (c + 1 < NC) {
+                            tmem_ld_16x256b_x2(taddr + 16 * (c + 1), ra[(c + 1) & 1]);
+                            tmem_ld_16x256b_x2(taddr + (16u << 16) + 16 * (c + 1), rb[(c + 1) & 1]);
+                        }
+                        const uint32_t(&r0)[8] = ra[c & 1], (&r1)[8] = rb[c & 1];
+#pragma unroll
+                        for (int jj = 0; jj < 2; ++jj) {
+                            const int j = 2 * c + jj;
+                            const float2 s = *reinterpret_cast<const float2 *>(buf + 8 * j);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t v0 = i < 2 ? r0[4 * jj + 2 * i] : r1[4 * jj + 2 * i - 4];
+                                const uint32_t v1 =
+                                    i < 2 ? r0[4 * jj + 2 * i + 1] : r1[4 * jj + 2 * i - 3];
+                                acc[i][2 * j] = __fmaf_rn(__uint_as_float(v0),
+                                                          __fmul_rn(s.x, cur[i]), acc[i][2 * j]);
+                                acc[i][2 * j + 1] = __fmaf_rn(__uint_as_float(v1),
+                                                              __fmul_rn(s.y, cur[i]), acc[i][2 * j + 1]);
+                            }
+                        }
+                        if (c + 1 < NC) {
+                            tmem_ld_wait();
+                            tmem_regs_ready(ra[(c + 1) & 1]);
+                            tmem_regs_ready(rb[(c + 1) & 1]);
+                            if (c + 2 == NC) hand_back(slot);
+                        }
+                    }
+                }
+                if (ok && j0 < p.cols_out) {
+                    uint16_t *d = p.d + (int64_t)t.expert * p.rows_out * p.cols_out;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t *dst = reinterpret_cast<uint32_t *>(
+                            d + (int64_t)(row0 + 8 * i) * p.cols_out + j0 + 2 * fc);
+#pragma unroll
+                        for (int j = 0; j < COLS / 8; ++j)
+                            dst[4 * j] = pack_bf16x2(acc[i][2 * j], acc[i][2 * j + 1]);
+                    }
+                }
+            }
+        } else {
+            // one row x 128 columns a thread: a block's scale is one product
+            for (int index = blockIdx.x; index < num_tiles; index += gridDim.x) {
+                const Tile t = find_tile<kWgrad>(p, first, index);
+                const int in = quarter * 32 + lane, j0 = t.n + half * COLS;
+                const float *sa = p.sa + (int64_t)min(t.row0 + in, p.capacity - 1) * p.sa_row;
+                const float *sb = p.sb + t.expert * p.sb_expert +
+                                  (int64_t)(min(j0, p.cols_out - 1) / BK) * p.sb_col;
+                uint64_t acc[COLS / 2];
+#pragma unroll
+                for (int j = 0; j < COLS / 2; ++j) acc[j] = 0ull;
+                float sa_next = sa[0], sb_next = sb[0];
+                for (int q = 0; q < t.nk; ++q, ++g) {
+                    const uint32_t slot = g % SLOTS, sphase = (g / SLOTS) & 1u;
+                    const float f = sa_next * sb_next;
+                    const uint64_t ff = pair_of(f, f);
+                    const int qn = min(q + 1, t.nk - 1);
+                    sa_next = sa[(int64_t)qn * p.sa_k];
+                    sb_next = sb[(int64_t)qn * p.sb_k];
+                    wait_block(slot, sphase);
+                    if (!ok) continue;
+                    const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) +
+                                           slot * BN + (uint32_t)(half * COLS);
+                    constexpr int NC = COLS / 32;
+                    uint32_t r[2][32];
+                    tmem_ld_32x32b_x32(taddr, r[0]);
+                    tmem_ld_wait();
+                    tmem_regs_ready(r[0]);
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        if (c + 1 < NC) tmem_ld_32x32b_x32(taddr + 32 * (c + 1), r[(c + 1) & 1]);
+#pragma unroll
+                        for (int a = 0; a < 16; ++a)
+                            fold(acc[16 * c + a], r[c & 1][2 * a], r[c & 1][2 * a + 1], ff);
+                        if (c + 1 < NC) {
+                            tmem_ld_wait();
+                            tmem_regs_ready(r[(c + 1) & 1]);
+                            if (c + 2 == NC) hand_back(slot);
+                        }
+                    }
+                }
+                if (ok && in < t.rows && j0 < p.cols_out) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.d + (int64_t)(t.row0 + in) * p.cols_out + j0);
+#pragma unroll
+                    for (int c = 0; c < COLS / 8; ++c) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 v = pair_split(acc[4 * c + e]);
+                            w[e] = pack_bf16x2(v.x, v.y);
+                        }
+                        dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+        }
+    }
+
+    __syncwarp();  // lanes that skipped a role wait here for their warp's lane 0
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        tmem_dealloc(tmem_base, SLOTS * BN);
+    }
+}
+
+template <bool kWgrad>
+cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const Args &args, int64_t tiles,
+                   cudaStream_t s, const char **why) {
+    static std::atomic<bool> attr_done[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64 || !attr_done[dev]) {
+        // setmaxnreg.inc waits until the launch's own registers can supply the
+        // raised counts: a build with fewer than the split needs is refused
+        cudaFuncAttributes fa;
+        cudaError_t e = cudaFuncGetAttributes(&fa, moe_gemm_kernel<kWgrad>);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs * THREADS < 128 * REGS_LOW + (THREADS - 128) * REGS_HIGH) {
+            *why = "the register split does not fit the kernel's launch allocation";
+            return cudaErrorInvalidConfiguration;
+        }
+        e = cudaFuncSetAttribute(moe_gemm_kernel<kWgrad>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) attr_done[dev] = true;
+    }
+    const int64_t sms = num_sms();
+    return launch_pdl(moe_gemm_kernel<kWgrad>, (unsigned)(tiles < sms ? tiles : sms), THREADS, SMEM,
+                      s, ta, tb, args);
+}
+
+Args common_args(const MoeGemm &m) {
+    Args a = {};
+    a.offsets = m.offsets;
+    a.experts = (int)m.experts;
+    a.capacity = (int)m.capacity;
+    a.sa = m.sa;
+    a.sb = m.sb;
+    a.d = m.d;
+    a.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+    a.status = device_status_word();
+    return a;
+}
+
+// Output tiles of fprop and dgrad at most: every expert may end in a tile of its own.
+int64_t most_tiles(const MoeGemm &m, int64_t cols) {
+    const int64_t ends = m.experts < m.capacity ? m.experts : m.capacity;
+    return (m.capacity / BM + ends) * ((cols + BN - 1) / BN);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_fprop(const MoeGemm &m, cudaStream_t s, const char **why) {
+    if (m.capacity == 0) return cudaSuccess;
+    CUtensorMap ta, tb;
+    if (!make_tmap_k128(&ta, m.a, m.capacity, m.K, BM) ||
+        !make_tmap_k128(&tb, m.b, m.experts * m.N, m.K, BN)) {
+        *why = "cuTensorMapEncodeTiled failed";
+        return cudaErrorInvalidValue;
+    }
+    Args a = common_args(m);
+    a.cols_out = (int)m.N;
+    a.depth = (int)(m.K / BK);
+    a.by = (int)m.N;
+    a.sa_row = m.K / BK;
+    a.sa_k = 1;
+    a.sb_expert = (m.N / BK) * (m.K / BK);
+    a.sb_col = m.K / BK;
+    a.sb_k = 1;
+    return launch<false>(ta, tb, a, most_tiles(m, m.N), s, why);
+}
+
+cudaError_t launch_moe_dgrad(const MoeGemm &m, cudaStream_t s, const char **why) {
+    if (m.capacity == 0) return cudaSuccess;
+    CUtensorMap ta, tb;
+    if (!make_tmap_k128(&ta, m.a, m.capacity, m.N, BM) ||
+        !make_tmap_k128(&tb, m.b, m.K, m.experts * m.N, BN)) {
+        *why = "cuTensorMapEncodeTiled failed";
+        return cudaErrorInvalidValue;
+    }
+    Args a = common_args(m);
+    a.cols_out = (int)m.K;
+    a.depth = (int)(m.N / BK);
+    a.bx = (int)m.N;
+    a.sa_row = m.N / BK;
+    a.sa_k = 1;
+    a.sb_expert = (m.N / BK) * (m.K / BK);
+    a.sb_col = 1;
+    a.sb_k = m.K / BK;
+    return launch<false>(ta, tb, a, most_tiles(m, m.K), s, why);
+}
+
+cudaError_t launch_moe_wgrad(const MoeGemm &m, cudaStream_t s, const char **why) {
+    if (m.capacity == 0)
+        return cudaMemsetAsync(m.d, 0, (size_t)(m.experts * m.N * m.K) * sizeof(uint16_t), s);
+    CUtensorMap ta, tb;
+    if (!make_tmap_k128(&ta, m.a, m.N, m.capacity, BM) ||
+        !make_tmap_k128(&tb, m.b, m.K, m.capacity, BN)) {
+        *why = "cuTensorMapEncodeTiled failed";
+        return cudaErrorInvalidValue;
+    }
+    Args a = common_args(m);
+    a.rows_out = (int)m.N;
+    a.cols_out = (int)m.K;
+    a.sa_k = m.N;
+    a.sb_k = m.K;
+    const int64_t tiles = m.experts * (m.N / BM) * ((m.K + BN - 1) / BN);
+    return launch<true>(ta, tb, a, tiles, s, why);
+}
+
+}  // namespace fp8

@@ -214,6 +214,79 @@ cudaError_t launch_moe_combine_backward(const MoeRows &m, const void *dy, int64_
                                         const void *rows, int64_t ldr, const float *weights,
                                         void *drows, float *dweights, cudaStream_t s);
 
+// The router (moe_route.cu).  mask, losses nullable.
+constexpr int kRouteMaxTopk = 32, kRouteMaxBlocks = 512;
+struct Route {
+    const void *logits;
+    int64_t ldl;
+    int f32;
+    const uint8_t *mask;
+    int64_t tokens;
+    int experts, topk, renormalize;
+    int32_t *ids;
+    float *weights;
+    int32_t *counts, *live;
+    float *losses, *workspace;
+};
+int64_t moe_route_workspace_bytes(int64_t tokens, int64_t experts);
+cudaError_t launch_moe_route(const Route &a, cudaStream_t s);
+// Its gradient; nullable: dweights, dlosses.
+struct RouteBackward {
+    const void *logits;
+    int64_t ldl;
+    int f32;
+    int64_t tokens;
+    int experts, topk, renormalize;
+    const int32_t *ids, *counts, *live;
+    const float *dweights, *dlosses;
+    void *dlogits;
+};
+cudaError_t launch_moe_route_backward(const RouteBackward &a, cudaStream_t s);
+
+// The experts' block-scaled products (gemm_moe.cu); a, b, sa, sb, d as the
+// entry points of the same names describe them.
+struct MoeGemm {
+    const uint8_t *a;
+    const float *sa;
+    const uint8_t *b;
+    const float *sb;
+    const int32_t *offsets;
+    int64_t experts, capacity, N, K;
+    uint16_t *d;
+};
+cudaError_t launch_moe_fprop(const MoeGemm &m, cudaStream_t s, const char **why);
+cudaError_t launch_moe_dgrad(const MoeGemm &m, cudaStream_t s, const char **why);
+cudaError_t launch_moe_wgrad(const MoeGemm &m, cudaStream_t s, const char **why);
+
+// The gated activation (swiglu.cu).  Nullable: live; y; yq with y_scale; hq
+// with h_scale.
+struct SwigluForward {
+    const void *h;
+    int64_t ldh;
+    int f32;
+    int64_t rows, cols;
+    const int32_t *live;
+    void *y;
+    uint8_t *yq;
+    float *y_scale;
+    uint8_t *hq;
+    float *h_scale;
+};
+cudaError_t launch_swiglu(const SwigluForward &a, cudaStream_t s);
+// Its gradient; h is E4M3 with h_scale, else dy's type.  Nullable: live, y.
+struct SwigluBackward {
+    const void *dy;
+    int64_t lddy;
+    int f32;
+    const void *h;
+    int64_t ldh;
+    const float *h_scale;
+    int64_t rows, cols;
+    const int32_t *live;
+    void *dh, *y;
+};
+cudaError_t launch_swiglu_backward(const SwigluBackward &a, cudaStream_t s);
+
 // Newton-Schulz orthogonalisation of a batch of [rows, cols] matrices
 // (orthogonalize.cu).
 struct Orthogonalize {
