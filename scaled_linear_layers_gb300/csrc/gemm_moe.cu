@@ -12,8 +12,9 @@
 // partial into one of two TMEM slots, eight epilogue warps that fold it into
 // fp32 registers with its scales).  What differs is that a tile's rows,
 // weights and contraction depend on offsets that only the device knows: every
-// CTA reads them once, counts the row tiles of each expert into shared memory
-// and finds a tile's expert by bisection, so the host launches without waiting
+// CTA reads them once, keeps them in shared memory with the row tiles before
+// each expert, and a warp of its own finds the tiles' experts by bisection, a
+// few tiles ahead of the producer, MMA and epilogue warps: the host launches without waiting
 // for the sort.  Tiles go expert by expert, so that an expert's weights are in
 // L2 while its rows pass.  Rows of a tile past its segment are computed from
 // what lies there and not stored.
@@ -42,8 +43,10 @@ constexpr int COLS = BN * 4 / EPI_WARPS;  // accumulator columns of a one-row th
 constexpr int REGS_LOW = 40, REGS_HIGH = 232;
 constexpr uint32_t IDESC = idesc_f8_f32(BM, BN);
 constexpr int SCALES = 2 * EPI_WARPS * COLS;  // wgrad: staged column scales, two blocks a warp
-constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + SCALES * sizeof(float) + 256 +
-                        (kMoeMaxExperts + 1) * sizeof(int32_t);
+constexpr int TILES = 4;  // tiles found ahead of their use
+constexpr int READERS = 2 + EPI_WARPS;
+constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + SCALES * sizeof(float) + 512 +
+                        (3 * kMoeMaxExperts + 1) * sizeof(int32_t);
 static_assert(SLOTS * BN == 512, "the slots fill TMEM");
 static_assert(SMEM <= 227 * 1024, "smem");
 
@@ -63,12 +66,13 @@ struct Args {
 };
 
 // One output tile.
-struct Tile {
-    int expert, m, n;  // n: first output column
-    int row0, rows;    // A's first row (fprop, dgrad: in the sorted order), rows to store
-    int kb0, nk;       // contraction blocks (kb0: the first, wgrad)
-    bool bad;          // wgrad: a segment that does not lie on 128-row blocks
+struct __align__(16) Tile {
+    int expert, n;   // n: first output column
+    int row0, rows;  // A's first row (fprop, dgrad: in the sorted order), rows to store
+    int kb0, nk;     // contraction blocks (kb0: the first, wgrad); nk < 0: no tile is left
+    int bad, unused;  // bad (wgrad): a segment that does not lie on 128-row blocks
 };
+static_assert(sizeof(Tile) == 32, "two 16-byte loads");
 
 __device__ __forceinline__ void segment(const Args &p, int e, int &lo, int &hi) {
     // whatever the offsets hold, a segment lies in the rows that exist
@@ -76,16 +80,45 @@ __device__ __forceinline__ void segment(const Args &p, int e, int &lo, int &hi) 
     hi = min(max(p.offsets[e + 1], lo), p.capacity);
 }
 
-// first[e]: row tiles of the experts before e.
-template <bool kWgrad>
-__device__ __forceinline__ int total_tiles(const Args &p, const int32_t *first) {
-    const int n_tiles = (p.cols_out + BN - 1) / BN;
-    if (kWgrad) return p.experts * (p.rows_out / BM) * n_tiles;
-    return first[p.experts] * n_tiles;
+// The experts' segments and the row tiles before each, in shared memory: a
+// tile is found without a load from global memory.
+struct Segments {
+    int32_t *first, *lo, *hi;  // [experts + 1], [experts], [experts]
+};
+
+// By one warp.
+__device__ __forceinline__ void count_tiles(const Args &p, const Segments &g, int lane) {
+    int before = 0;
+    for (int e0 = 0; e0 < p.experts; e0 += 32) {
+        int lo = 0, hi = 0;
+        const int e = e0 + lane;
+        if (e < p.experts) segment(p, e, lo, hi);
+        int sum = (hi - lo + BM - 1) / BM;
+        const int own = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        if (e < p.experts) {
+            g.first[e] = before + sum - own;
+            g.lo[e] = lo;
+            g.hi[e] = hi;
+        }
+        before += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    }
+    if (lane == 0) g.first[p.experts] = before;
 }
 
 template <bool kWgrad>
-__device__ __forceinline__ Tile find_tile(const Args &p, const int32_t *first, int index) {
+__device__ __forceinline__ int total_tiles(const Args &p, const Segments &g) {
+    const int n_tiles = (p.cols_out + BN - 1) / BN;
+    if (kWgrad) return p.experts * (p.rows_out / BM) * n_tiles;
+    return g.first[p.experts] * n_tiles;
+}
+
+template <bool kWgrad>
+__device__ __forceinline__ Tile find_tile(const Args &p, const Segments &g, int index) {
     const int n_tiles = (p.cols_out + BN - 1) / BN;
     Tile t;
     int m_tiles, lo, hi, in;
@@ -99,26 +132,28 @@ __device__ __forceinline__ Tile find_tile(const Args &p, const int32_t *first, i
         const int at = index / n_tiles;
         while (b - a > 1) {
             const int mid = (a + b) >> 1;
-            if (first[mid] <= at) a = mid;
+            if (g.first[mid] <= at) a = mid;
             else b = mid;
         }
         t.expert = a;
-        m_tiles = first[a + 1] - first[a];
-        in = index - first[a] * n_tiles;
+        m_tiles = g.first[a + 1] - g.first[a];
+        in = index - g.first[a] * n_tiles;
     }
-    segment(p, t.expert, lo, hi);
-    int tn;
-    grouped_tile(in, m_tiles, n_tiles, 16, t.m, tn);
+    lo = g.lo[t.expert];
+    hi = g.hi[t.expert];
+    int tm, tn;
+    grouped_tile(in, m_tiles, n_tiles, 16, tm, tn);
     t.n = tn * BN;
+    t.unused = 0;
     if (kWgrad) {
         t.bad = ((lo | hi) & (BK - 1)) != 0;
-        t.row0 = t.m * BM;
+        t.row0 = tm * BM;
         t.rows = BM;
         t.kb0 = lo / BK;
         t.nk = t.bad ? 0 : (hi - lo) / BK;
     } else {
-        t.bad = false;
-        t.row0 = lo + t.m * BM;
+        t.bad = 0;
+        t.row0 = lo + tm * BM;
         t.rows = min(BM, hi - t.row0);
         t.kb0 = 0;
         t.nk = p.depth;
@@ -147,10 +182,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint64_t *empty = full + STAGES;                               // [STAGES] MMA -> TMA
     uint64_t *sfull = empty + STAGES;                              // [SLOTS] MMA -> epilogue
     uint64_t *sempty = sfull + SLOTS;                              // [SLOTS] epilogue -> MMA
-    uint64_t *drain = sempty + SLOTS;
+    uint64_t *tfull = sempty + SLOTS;                              // [TILES] search -> readers
+    uint64_t *tempty = tfull + TILES;                              // [TILES] readers -> search
+    uint64_t *drain = tempty + TILES;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
-    int32_t *first = reinterpret_cast<int32_t *>(full) + 64;  // [experts + 1]
+    Tile *tiles = reinterpret_cast<Tile *>(full + 32);  // [TILES]
+    Segments seg;
+    seg.first = reinterpret_cast<int32_t *>(full) + 128;
+    seg.lo = seg.first + p.experts + 1;
+    seg.hi = seg.lo + p.experts;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -161,6 +202,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int s = 0; s < SLOTS; ++s) {
             mbar_init(&sfull[s], 1);
             mbar_init(&sempty[s], EPI_WARPS);
+        }
+        for (int s = 0; s < TILES; ++s) {
+            mbar_init(&tfull[s], 1);
+            mbar_init(&tempty[s], READERS);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -174,29 +219,21 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     pdl_wait_prior();  // the offsets are the previous kernels' result
     pdl_allow_next();
-    if (!kWgrad && warp == 2) {
-        // row tiles of the experts before each, 32 experts at a time
-        int before = 0;
-        for (int e0 = 0; e0 < p.experts; e0 += 32) {
-            int lo = 0, hi = 0;
-            if (e0 + lane < p.experts) segment(p, e0 + lane, lo, hi);
-            int sum = (hi - lo + BM - 1) / BM;
-            const int own = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-                if (lane >= o) sum += v;
-            }
-            if (e0 + lane < p.experts) first[e0 + lane] = before + sum - own;
-            before += __shfl_sync(0xFFFFFFFFu, sum, 31);
-        }
-        if (lane == 0) first[p.experts] = before;
-    }
+    if (warp == 2) count_tiles(p, seg, lane);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
-    const int num_tiles = total_tiles<kWgrad>(p, first);
+    // The i-th tile of this CTA for one reader; false when there is none left or
+    // the wait for it gave up.
+    auto read_tile = [&](uint32_t i, Tile &t) {
+        const uint32_t at = i % TILES;
+        if (!mbar_wait_bounded<true>(&tfull[at], (i / TILES) & 1u, abort_flag, p.wait_limit_ns,
+                                     kStatusTimeoutTma, p.status))
+            return false;
+        t = tiles[at];
+        return true;
+    };
     // each warp of the first warpgroup gives registers back as it enters its
     // role, each epilogue warp takes more
     auto regs_low = [] { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_LOW)); };
@@ -208,34 +245,33 @@ __global__ void __launch_bounds__(THREADS, 1)
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int index = blockIdx.x; index < num_tiles && ok; index += gridDim.x) {
-                const Tile t = find_tile<kWgrad>(p, first, index);
-                const int ax = t.kb0 * BK, bx = t.expert * p.bx + t.kb0 * BK;
-                const int brow = t.expert * p.by + t.n;
-                for (int q = 0; q < t.nk; ++q) {
+            Tile t;
+            for (uint32_t i = 0; ok && read_tile(i, t) && t.nk >= 0; ++i) {
+                mbar_arrive(&tempty[i % TILES]);
+                const int brow = t.expert * p.by + t.n, arow = t.row0, nk = t.nk;
+                int ax = t.kb0 * BK, bx = t.expert * p.bx + t.kb0 * BK;
+                for (int q = 0; q < nk; ++q, ax += BK, bx += BK) {
                     if (!mbar_wait_bounded<true>(&empty[stage], phase ^ 1u, abort_flag,
                                                  p.wait_limit_ns, kStatusTimeoutTma, p.status)) {
                         ok = false;
                         break;
                     }
                     mbar_arrive_expect_tx(&full[stage], STAGE_BYTES);
-                    tma_load_2d(sA + stage * A_BYTES, &tma_a, &full[stage], ax + q * BK, t.row0);
-                    tma_load_2d(sB + stage * B_BYTES, &tma_b, &full[stage], bx + q * BK, brow);
+                    tma_load_2d(sA + stage * A_BYTES, &tma_a, &full[stage], ax, arow);
+                    tma_load_2d(sB + stage * B_BYTES, &tma_b, &full[stage], bx, brow);
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
             }
-            if (!ok) {
-                // wait (bounded) for the copies still in flight before teardown
-                for (int s = 0; s < STAGES; ++s) {
-                    stage = stage == 0 ? STAGES - 1 : stage - 1;
-                    if (stage == STAGES - 1) phase ^= 1u;
-                    volatile int no_abort = 0;
-                    mbar_wait_bounded(&full[stage], phase, &no_abort, 10000000ull,
-                                      kStatusTimeoutTma, p.status);
-                }
+            // wait (bounded) for the copies still in flight before teardown
+            for (int s = 0; s < STAGES; ++s) {
+                stage = stage == 0 ? STAGES - 1 : stage - 1;
+                if (stage == STAGES - 1) phase ^= 1u;
+                volatile int no_abort = 0;
+                mbar_wait_bounded(&full[stage], phase, &no_abort, 10000000ull, kStatusTimeoutTma,
+                                  p.status);
             }
         }
     } else if (warp == 1) {
@@ -246,9 +282,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             uint32_t phase = 0;
             uint32_t g = 0;  // blocks issued so far (across tiles)
             bool ok = true;
-            for (int index = blockIdx.x; index < num_tiles && ok; index += gridDim.x) {
-                const Tile t = find_tile<kWgrad>(p, first, index);
-                for (int q = 0; q < t.nk; ++q, ++g) {
+            Tile t;
+            for (uint32_t i = 0; ok && read_tile(i, t) && t.nk >= 0; ++i) {
+                mbar_arrive(&tempty[i % TILES]);
+                const int nk = t.nk;
+                for (int q = 0; q < nk; ++q, ++g) {
                     const uint32_t slot = g % SLOTS, sphase = (g / SLOTS) & 1u;
                     if (!mbar_wait_bounded<true>(&sempty[slot], sphase ^ 1u, abort_flag,
                                                  p.wait_limit_ns, kStatusTimeoutMma, p.status) ||
@@ -276,8 +314,27 @@ __global__ void __launch_bounds__(THREADS, 1)
             volatile int no_abort = 0;
             mbar_wait_bounded(drain, 0, &no_abort, p.wait_limit_ns, kStatusTimeoutMma, p.status);
         }
+    } else if (warp == 2) {
+        regs_low();
+        if (lane == 0) {
+            // -------------------------------------------- search for tiles
+            const int num_tiles = total_tiles<kWgrad>(p, seg);
+            int index = blockIdx.x;
+            for (uint32_t i = 0;; ++i, index += gridDim.x) {
+                const uint32_t at = i % TILES;
+                Tile t;
+                t.nk = -1;
+                if (index < num_tiles) t = find_tile<kWgrad>(p, seg, index);
+                if (!mbar_wait_bounded<true>(&tempty[at], ((i / TILES) & 1u) ^ 1u, abort_flag,
+                                             p.wait_limit_ns, kStatusTimeoutTma, p.status))
+                    break;
+                tiles[at] = t;
+                mbar_arrive(&tfull[at]);
+                if (t.nk < 0) break;
+            }
+        }
     } else if (warp < EPI0) {
-        regs_low();  // idle warps of the first warpgroup
+        regs_low();  // an idle warp of the first warpgroup
     } else {
         // ------------------------------------------------- epilogue (8 warps)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_HIGH));
@@ -292,6 +349,19 @@ __global__ void __launch_bounds__(THREADS, 1)
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (ok) tc_fence_after();
         };
+        // A tile stays in its place until the warp is done with it, so that what
+        // the stores need is read again rather than kept in registers.
+        auto next_tile = [&](uint32_t i) {
+            if (ok)
+                ok = mbar_wait_bounded<true>(&tfull[i % TILES], (i / TILES) & 1u, abort_flag,
+                                             p.wait_limit_ns, kStatusTimeoutEpilogue, p.status);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            return ok && tiles[i % TILES].nk >= 0;
+        };
+        auto free_tile = [&](uint32_t i) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty[i % TILES]);
+        };
         auto hand_back = [&](uint32_t slot) {  // the block's partial is in registers
             tc_fence_before();
             __syncwarp();
@@ -304,40 +374,43 @@ __global__ void __launch_bounds__(THREADS, 1)
             // instead of 128; they are staged by cp.async, one block ahead.
             float *wbuf = sbuf + (warp - EPI0) * 2 * COLS;
             const int fr = lane >> 2, fc = lane & 3;
-            for (int index = blockIdx.x; index < num_tiles; index += gridDim.x) {
-                const Tile t = find_tile<kWgrad>(p, first, index);
-                const int row0 = t.row0 + quarter * 32 + fr, j0 = t.n + half * COLS;
-                const float *sa = p.sa + (int64_t)t.kb0 * p.sa_k + row0;
-                const float *sb = p.sb + (int64_t)t.kb0 * p.sb_k + min(j0 + 4 * lane, p.cols_out - 4);
+            for (uint32_t i = 0; next_tile(i); ++i) {
+                const Tile &t = tiles[i % TILES];
+                const int nk = t.nk;
+                const float *sa = p.sa + (int64_t)t.kb0 * p.sa_k + t.row0 + quarter * 32 + fr;
+                const float *sb = p.sb + (int64_t)t.kb0 * p.sb_k +
+                                  min(t.n + half * COLS + 4 * lane, p.cols_out - 4);
+                const float start = t.bad ? __uint_as_float(0x7FFFFFFFu) : 0.f;
                 float acc[4][COLS / 4];  // [i][2 j + c]: columns 8 j + 2 fc + c
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int j = 0; j < COLS / 4; ++j)
-                        acc[i][j] = t.bad ? __uint_as_float(0x7FFFFFFFu) : 0.f;
+                    for (int j = 0; j < COLS / 4; ++j) acc[i][j] = start;
                 float next[4] = {};
                 auto fetch = [&](int q) {
-                    if (q < t.nk) {
+                    if (q < nk) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) next[i] = sa[(int64_t)q * p.sa_k + 8 * i];
+                        for (int i = 0; i < 4; ++i) next[i] = sa[8 * i];
                         asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(
                                          smem_u32(wbuf + (q & 1) * COLS + 4 * lane)),
-                                     "l"(sb + (int64_t)q * p.sb_k)
+                                     "l"(sb)
                                      : "memory");
+                        sa += p.sa_k;
+                        sb += p.sb_k;
                     }
                     asm volatile("cp.async.commit_group;" ::: "memory");
                 };
                 fetch(0);
-                for (int q = 0; q < t.nk; ++q, ++g) {
+                for (int q = 0; q < nk; ++q, ++g) {
                     const uint32_t slot = g % SLOTS, sphase = (g / SLOTS) & 1u;
-                    float cur[4];
+                    uint64_t cur2[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) cur[i] = next[i];
+                    for (int i = 0; i < 4; ++i) cur2[i] = pair_of(next[i], next[i]);
                     asm volatile("cp.async.wait_group 0;" ::: "memory");
                     __syncwarp();
                     fetch(q + 1);
                     wait_block(slot, sphase);
-                    if (!ok) continue;
+                    if (!ok) break;
                     const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) +
                                            slot * BN + (uint32_t)(half * COLS);
                     const float *buf = wbuf + (q & 1) * COLS + 2 * fc;
@@ -360,15 +433,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                         for (int jj = 0; jj < 2; ++jj) {
                             const int j = 2 * c + jj;
                             const float2 s = *reinterpret_cast<const float2 *>(buf + 8 * j);
+                            const uint64_t ss = pair_of(s.x, s.y);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const uint32_t v0 = i < 2 ? r0[4 * jj + 2 * i] : r1[4 * jj + 2 * i - 4];
-                                const uint32_t v1 =
-                                    i < 2 ? r0[4 * jj + 2 * i + 1] : r1[4 * jj + 2 * i - 3];
-                                acc[i][2 * j] = __fmaf_rn(__uint_as_float(v0),
-                                                          __fmul_rn(s.x, cur[i]), acc[i][2 * j]);
-                                acc[i][2 * j + 1] = __fmaf_rn(__uint_as_float(v1),
-                                                              __fmul_rn(s.y, cur[i]), acc[i][2 * j + 1]);
+                                const uint32_t *v = i < 2 ? r0 + 4 * jj + 2 * i : r1 + 4 * jj + 2 * i - 4;
+                                const float2 f = pair_split(pair_mul(ss, cur2[i]));
+                                acc[i][2 * j] = __fmaf_rn(__uint_as_float(v[0]), f.x, acc[i][2 * j]);
+                                acc[i][2 * j + 1] =
+                                    __fmaf_rn(__uint_as_float(v[1]), f.y, acc[i][2 * j + 1]);
                             }
                         }
                         if (c + 1 < NC) {
@@ -379,6 +451,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     }
                 }
+                const int row0 = t.row0 + quarter * 32 + fr, j0 = t.n + half * COLS;
                 if (ok && j0 < p.cols_out) {
                     uint16_t *d = p.d + (int64_t)t.expert * p.rows_out * p.cols_out;
 #pragma unroll
@@ -390,41 +463,47 @@ __global__ void __launch_bounds__(THREADS, 1)
                             dst[4 * j] = pack_bf16x2(acc[i][2 * j], acc[i][2 * j + 1]);
                     }
                 }
+                free_tile(i);
             }
+            cp_async_wait_all();
         } else {
             // one row x 128 columns a thread: a block's scale is one product
-            for (int index = blockIdx.x; index < num_tiles; index += gridDim.x) {
-                const Tile t = find_tile<kWgrad>(p, first, index);
-                const int in = quarter * 32 + lane, j0 = t.n + half * COLS;
+            for (uint32_t i = 0; next_tile(i); ++i) {
+                const Tile &t = tiles[i % TILES];
+                const int nk = t.nk, in = quarter * 32 + lane;
                 const float *sa = p.sa + (int64_t)min(t.row0 + in, p.capacity - 1) * p.sa_row;
                 const float *sb = p.sb + t.expert * p.sb_expert +
-                                  (int64_t)(min(j0, p.cols_out - 1) / BK) * p.sb_col;
+                                  (int64_t)(min(t.n + half * COLS, p.cols_out - 1) / BK) * p.sb_col;
                 uint64_t acc[COLS / 2];
 #pragma unroll
                 for (int j = 0; j < COLS / 2; ++j) acc[j] = 0ull;
-                float sa_next = sa[0], sb_next = sb[0];
-                for (int q = 0; q < t.nk; ++q, ++g) {
+                float sa_next = *sa, sb_next = *sb;
+                for (int q = 0; q < nk; ++q, ++g) {
                     const uint32_t slot = g % SLOTS, sphase = (g / SLOTS) & 1u;
-                    const float f = sa_next * sb_next;
-                    const uint64_t ff = pair_of(f, f);
-                    const int qn = min(q + 1, t.nk - 1);
-                    sa_next = sa[(int64_t)qn * p.sa_k];
-                    sb_next = sb[(int64_t)qn * p.sb_k];
+                    const float sa_cur = sa_next, sb_cur = sb_next;
+                    if (q + 1 < nk) {
+                        sa += p.sa_k;
+                        sb += p.sb_k;
+                    }
+                    sa_next = *sa;
+                    sb_next = *sb;
                     wait_block(slot, sphase);
-                    if (!ok) continue;
+                    if (!ok) break;
+                    const float f = sa_cur * sb_cur;
+                    const uint64_t ff = pair_of(f, f);
                     const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) +
                                            slot * BN + (uint32_t)(half * COLS);
-                    constexpr int NC = COLS / 32;
-                    uint32_t r[2][32];
-                    tmem_ld_32x32b_x32(taddr, r[0]);
+                    constexpr int NC = COLS / 16;
+                    uint32_t r[2][16];
+                    tmem_ld_32x32b_x16(taddr, r[0]);
                     tmem_ld_wait();
                     tmem_regs_ready(r[0]);
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
-                        if (c + 1 < NC) tmem_ld_32x32b_x32(taddr + 32 * (c + 1), r[(c + 1) & 1]);
+                        if (c + 1 < NC) tmem_ld_32x32b_x16(taddr + 16 * (c + 1), r[(c + 1) & 1]);
 #pragma unroll
-                        for (int a = 0; a < 16; ++a)
-                            fold(acc[16 * c + a], r[c & 1][2 * a], r[c & 1][2 * a + 1], ff);
+                        for (int a = 0; a < 8; ++a)
+                            fold(acc[8 * c + a], r[c & 1][2 * a], r[c & 1][2 * a + 1], ff);
                         if (c + 1 < NC) {
                             tmem_ld_wait();
                             tmem_regs_ready(r[(c + 1) & 1]);
@@ -432,6 +511,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     }
                 }
+                const int j0 = t.n + half * COLS;
                 if (ok && in < t.rows && j0 < p.cols_out) {
                     uint4 *dst = reinterpret_cast<uint4 *>(p.d + (int64_t)(t.row0 + in) * p.cols_out + j0);
 #pragma unroll
@@ -445,6 +525,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
+                free_tile(i);
             }
         }
     }
