@@ -621,7 +621,7 @@ fp8_status fp8_moe_combine_backward(const void *dy, int64_t lddy, const void *ro
  * <= 32 (else FP8_ERR_UNSUPPORTED).  Sums over tokens are formed in a fixed
  * order: the same call gives the same bits.  workspace:
  * fp8_moe_route_workspace_bytes(tokens, experts) bytes (0 for bad arguments),
- * overwritten. */
+ * 16-byte aligned, overwritten. */
 size_t fp8_moe_route_workspace_bytes(int64_t tokens, int64_t experts);
 fp8_status fp8_moe_route(const void *logits, int64_t ldl, fp8_dtype lt, const uint8_t *mask,
                          int64_t tokens, int64_t experts, int64_t topk, int32_t renormalize,

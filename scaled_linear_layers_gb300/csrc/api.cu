@@ -1347,7 +1347,7 @@ fp8_status fp8_moe_route(const void *logits, int64_t ldl, fp8_dtype lt, const ui
     FP8_ELEM(counts, FP8_DT_F32, who);
     FP8_ELEM(live, FP8_DT_F32, who);
     FP8_ELEM(losses, FP8_DT_F32, who);
-    FP8_ELEM(workspace, FP8_DT_F32, who);
+    FP8_ALIGN(workspace, who);
     FP8_TRY(check_device(who));
     const Route a = {logits, ldl, lt == FP8_DT_F32, mask, tokens, (int)experts, (int)topk,
                      renormalize != 0, ids, weights, counts, live, losses,

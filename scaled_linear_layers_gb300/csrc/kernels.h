@@ -216,6 +216,7 @@ cudaError_t launch_moe_combine_backward(const MoeRows &m, const void *dy, int64_
 
 // The router (moe_route.cu).  mask, losses nullable.
 constexpr int kRouteMaxTopk = 32, kRouteMaxBlocks = 512;
+constexpr int kRouteOneBlock = 64;  // tokens that one block takes by itself
 struct Route {
     const void *logits;
     int64_t ldl;

@@ -15,62 +15,306 @@
 // gradient).  A logit of -inf closes its expert to the token; a token whose
 // mask is 0 or whose experts are all closed has ids of -1, and is in no sum.
 //
-// A warp takes a token, a lane every 32nd expert.  The order of logits is the
-// order of whole numbers made of their bits, so a round of the top-k is a
-// maximum over the lane's own, one over the warp, and a minimum over the ids
-// that have it.  Sums over tokens are formed per warp, then per block, then
-// over the blocks, always in the same order; the counts are whole numbers, so
-// their atomics are exact in any order.
+// A warp takes a token and its lanes share the experts.  A logit and its expert become
+// one whole number that orders as the logits do, the lowest expert first among
+// equal ones; a lane sorts its own, and a round of the top-k is a maximum over
+// the lanes' first ones, whose owner moves on to its next.  From 129 experts on
+// most logits are left out first: topk lanes have one that is at least the
+// topk-th largest of the lanes' largest, so only logits from there on can be
+// chosen; usually a few more than topk, they are dealt out to the lanes anew.
+// The chosen logits are read back from their numbers.  Sums over tokens
+// are formed per warp, per block and over the blocks (by a cluster of eight
+// blocks, a share of them each), always in the same order; the counts are whole
+// numbers, so their atomics are exact in any order.  Few tokens stay in one block
+// and one launch.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
+#include "occupancy.h"
 #include "rowops.cuh"
 
 namespace fp8 {
 
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kSumCtas = 8;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
+constexpr uint32_t kClosed = 0x007FFFFFu;  // the order of -inf
 
-// Logits in their order as whole numbers: 0 for -inf (closed), the largest for
-// NaN, equal ones for the two zeros.
-__device__ __forceinline__ uint32_t order_key(float l) {
-    if (l != l) return kAll;
-    const uint32_t b = __float_as_uint(l + 0.f);
-    if (b == 0xFF800000u) return 0u;
-    return b ^ ((b >> 31) != 0 ? kAll : 0x80000000u);
+// Logits in their order as whole numbers: NaN the largest (an addition makes
+// every NaN the same positive one), equal for the two zeros.
+__device__ __forceinline__ uint32_t order_of(float l) {
+    const uint32_t b = __float_as_uint(__fadd_rn(l, 0.f));
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
+__device__ __forceinline__ float logit_of(uint32_t order) {
+    return __uint_as_float((order >> 31) != 0 ? order ^ 0x80000000u : ~order);
+}
+
+// -inf, which stands behind the last expert: a closed one.
 template <typename T>
-__device__ __forceinline__ float logit_at(const T *row, int e, int experts) {
-    return e < experts ? elem_to_float(row[e]) : -INFINITY;
+__device__ __forceinline__ T closed_logit() {
+    if constexpr (std::is_same<T, float>::value) return -INFINITY;
+    else return T(0xFF80u);
 }
 
-__device__ __forceinline__ float warp_max(float v) {
+// How a warp shares a token's experts, R to a lane: every 32nd one, or, where a
+// row lies on groups of four (VEC), four neighbours of every 128.
+template <int R, bool VEC>
+__device__ __forceinline__ int expert_of(int r, int lane) {
+    return VEC ? (r >> 2) * 128 + lane * 4 + (r & 3) : r * 32 + lane;
+}
+
+template <typename T, int R, bool VEC>
+__device__ __forceinline__ void load_logits(const T *row, bool there, int experts, int lane,
+                                            T (&l)[R]) {
+    if constexpr (VEC) {
+        using Four = typename std::conditional<sizeof(T) == 4, float4, ushort4>::type;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-    return v;
+        for (int r = 0; r < R; r += 4) {
+            Four v = {closed_logit<T>(), closed_logit<T>(), closed_logit<T>(), closed_logit<T>()};
+            if (there && expert_of<R, VEC>(r, lane) < experts)
+                v = *reinterpret_cast<const Four *>(row + expert_of<R, VEC>(r, lane));
+            l[r] = v.x, l[r + 1] = v.y, l[r + 2] = v.z, l[r + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            l[r] = there && r * 32 + lane < experts ? row[r * 32 + lane] : closed_logit<T>();
+    }
 }
 
-// A block's part of the sums: probabilities [experts], then the sum of lse^2;
-// counts [experts], then the tokens.
-struct Parts {
-    float *sums;
-    int32_t *counts;
+template <typename T, int R, bool VEC>
+__device__ __forceinline__ void store_logits(T *row, int experts, int lane, const float (&l)[R]) {
+    if constexpr (VEC) {
+#pragma unroll
+        for (int r = 0; r < R; r += 4) {
+            if (expert_of<R, VEC>(r, lane) >= experts) continue;
+            T *at = row + expert_of<R, VEC>(r, lane);
+            if constexpr (sizeof(T) == 4)
+                *reinterpret_cast<float4 *>(at) = make_float4(l[r], l[r + 1], l[r + 2], l[r + 3]);
+            else
+                *reinterpret_cast<uint2 *>(at) = make_uint2(pack_bf16x2(l[r], l[r + 1]),
+                                                            pack_bf16x2(l[r + 2], l[r + 3]));
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (r * 32 + lane < experts) float_to_elem(row + r * 32 + lane, l[r]);
+    }
+}
+
+// 1/x for x >= 1 and log x, by the hardware's approximations (2^-23 and 2^-22).
+__device__ __forceinline__ float inverse(float x) { return __fdividef(1.f, x); }
+__device__ __forceinline__ float logarithm(float x) { return __logf(x); }
+
+// The order of a logit and its expert as one number; 0 orders behind all.
+// bf16 logits leave their order in 16 bits.
+template <typename T>
+struct Choice {  // fp32
+    using Key = uint64_t;
+    static __device__ __forceinline__ Key make(uint32_t order, int e) {
+        return ((uint64_t)order << 32) | (uint32_t)~e;
+    }
+    static __device__ __forceinline__ uint32_t order(Key k) { return (uint32_t)(k >> 32); }
+    static __device__ __forceinline__ int expert(Key k) { return (int)~(uint32_t)k; }
+    static __device__ __forceinline__ Key warp_max(Key k) {
+        const uint32_t hi = __reduce_max_sync(kAll, order(k));
+        const uint32_t lo = __reduce_max_sync(kAll, order(k) == hi ? (uint32_t)k : 0u);
+        return ((uint64_t)hi << 32) | lo;
+    }
+};
+template <>
+struct Choice<uint16_t> {
+    using Key = uint32_t;
+    static __device__ __forceinline__ Key make(uint32_t order, int e) {
+        return (order & 0xFFFF0000u) | (uint32_t)(0xFFFF - e);
+    }
+    // (the low half of a negative logit's order is all ones)
+    static __device__ __forceinline__ uint32_t order(Key k) {
+        return (k >> 31) != 0 ? k & 0xFFFF0000u : k | 0xFFFFu;
+    }
+    static __device__ __forceinline__ int expert(Key k) { return 0xFFFF - (int)(k & 0xFFFFu); }
+    static __device__ __forceinline__ Key warp_max(Key k) { return __reduce_max_sync(kAll, k); }
 };
 
-__device__ __forceinline__ Parts parts_of(const Route &a, int block) {
-    float *base = a.workspace + (int64_t)block * 2 * (a.experts + 1);
-    return {base, reinterpret_cast<int32_t *>(base + a.experts + 1)};
+// Falling order, by Batcher's odd-even merge network.
+template <typename K, int N>
+__device__ __forceinline__ void sort_falling(K (&k)[N]) {
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+            for (int j = q % p; j + q < N; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                        const K a = k[i + j], b = k[i + j + q];
+                        k[i + j] = a > b ? a : b;
+                        k[i + j + q] = a > b ? b : a;
+                    }
 }
 
-template <typename T, int R>
-__global__ void __launch_bounds__(kThreads) moe_route_kernel(const Route a) {
+// A lane's largest number that is left, and its removal.
+template <typename K, int R, bool SORTED = (R <= 4)>
+struct Left;
+template <typename K, int R>
+struct Left<K, R, true> {
+    K k[R];
+    __device__ __forceinline__ void begin() { sort_falling(k); }
+    __device__ __forceinline__ K first() const { return k[0]; }
+    __device__ __forceinline__ void remove(K top) {
+        const bool mine = k[0] == top;
+#pragma unroll
+        for (int r = 0; r + 1 < R; ++r) k[r] = mine ? k[r + 1] : k[r];
+        k[R - 1] = mine ? 0 : k[R - 1];
+    }
+};
+template <typename K, int R>
+struct Left<K, R, false> {
+    K k[R];
+    __device__ __forceinline__ void begin() {}
+    __device__ __forceinline__ K first() const {
+        K best = 0;
+#pragma unroll
+        for (int r = 0; r < R; ++r) best = k[r] > best ? k[r] : best;
+        return best;
+    }
+    __device__ __forceinline__ void remove(K top) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) k[r] = k[r] == top ? 0 : k[r];
+    }
+};
+
+// The topk largest in their order: lane j returns the j-th (0: none).
+template <typename C, typename K, int R, bool S>
+__device__ __forceinline__ K choose(Left<K, R, S> &left, int topk, int lane) {
+    K mine = 0;
+    for (int j = 0; j < topk; ++j) {
+        const K top = C::warp_max(left.first());
+        if (C::order(top) <= kClosed) break;
+        if (lane == j) mine = top;
+        left.remove(top);
+    }
+    return mine;
+}
+
+template <typename C, bool VEC, int R>
+__device__ __forceinline__ Left<typename C::Key, R> numbered(const uint32_t (&order)[R], int lane) {
+    Left<typename C::Key, R> left;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        left.k[r] = C::make(order[r], expert_of<R, VEC>(r, lane));
+    left.begin();
+    return left;
+}
+
+// The same from the logits' orders, by way of the few that can be among them;
+// best: the lane's largest, least: the warp's.  A number's place is the count of
+// larger ones.
+constexpr int kDealt = 64;
+template <typename C, bool VEC, int R>
+__device__ __forceinline__ typename C::Key choose_few(const uint32_t (&order)[R], uint32_t best,
+                                                      uint32_t least, int topk, int lane,
+                                                      typename C::Key *dealt) {
+    using K = typename C::Key;
+    for (int j = 1; j < topk && least > kClosed; ++j) {
+        best = best == least ? 0u : best;
+        least = __reduce_max_sync(kAll, best);
+    }
+    least = max(least, kClosed + 1);
+    int found = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const bool in = order[r] >= least;
+        const uint32_t lanes = __ballot_sync(kAll, in);
+        const int at = found + __popc(lanes & ((1u << lane) - 1u));
+        if (in && at < kDealt) dealt[at] = C::make(order[r], expert_of<R, VEC>(r, lane));
+        found += __popc(lanes);
+    }
+    __syncwarp();
+    K mine = 0;
+    if (found <= kDealt) {
+        const K one = lane < found ? dealt[lane] : K(0);
+        const K two = lane + 32 < found ? dealt[lane + 32] : K(0);
+        int place = 0, place2 = 0;
+        for (int i = 0; i < found; ++i) {
+            const K other = dealt[i];
+            place += other > one;
+            if (found > 32) place2 += other > two;
+        }
+        __syncwarp();
+        // back by their places
+        if (lane < found) dealt[place] = one;
+        if (lane + 32 < found) dealt[place2] = two;
+        __syncwarp();
+        if (lane < min(found, topk)) mine = dealt[lane];
+    } else {  // many equal logits
+        auto left = numbered<C, VEC>(order, lane);
+        mine = choose<C>(left, topk, lane);
+    }
+    __syncwarp();
+    return mine;
+}
+
+// e^x for x <= 0: the hardware's 2^y, relative error 2^-22 + |x| 2^-23.
+__device__ __forceinline__ float exp_falling(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
+    return y;
+}
+
+// The sum of probabilities (of lse^2) and the count of one expert (of tokens).
+using Part = float2;
+__device__ __forceinline__ Part part(float sum, int32_t count) {
+    return make_float2(sum, __int_as_float(count));
+}
+__device__ __forceinline__ int32_t count_of(const Part &p) { return __float_as_int(p.y); }
+
+// The counts and losses from the whole sums, parts(e) for e <= experts, by one
+// block; red: 2 + kWarps floats.
+template <typename F>
+__device__ __forceinline__ void finish(const Route &a, float *red, F parts) {
+    float balance = 0.f;
+    for (int e = threadIdx.x; e <= a.experts; e += kThreads) {
+        const Part p = parts(e);
+        if (e < a.experts) {
+            a.counts[e] = count_of(p);
+            balance += (float)count_of(p) * p.x;
+        } else {
+            red[0] = __int_as_float(count_of(p));
+            red[1] = p.x;
+        }
+    }
+    float v[1] = {balance};
+    row_sum<kThreads, 1>(v, red + 2);
+    if (threadIdx.x == 0) {
+        const int32_t tokens = __float_as_int(red[0]);
+        const float n = (float)max(tokens, 1);
+        *a.live = tokens;
+        if (a.losses != nullptr) {
+            a.losses[0] = v[0] / n / n * ((float)a.experts / (float)a.topk);
+            a.losses[1] = red[1] / n;
+        }
+    }
+}
+
+template <typename T, int R, bool VEC>
+__global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) moe_route_kernel(const Route a) {
+    using C = Choice<T>;
+    using K = typename C::Key;
     extern __shared__ float smem[];
-    float *sums = smem;                                                   // [kWarps][experts + 1]
-    int32_t *counts = reinterpret_cast<int32_t *>(sums + kWarps * (a.experts + 1));  // [experts + 1]
+    const int width = a.experts + 1;
+    float *sums = smem;                                                     // [kWarps / 2][width]
+    int32_t *counts = reinterpret_cast<int32_t *>(sums + kWarps / 2 * width);  // [width]
+    float *red = reinterpret_cast<float *>(counts + width);                 // [2 + kWarps]
+    __shared__ K dealt[R > 4 ? kWarps * kDealt : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int e = threadIdx.x; e <= a.experts; e += kThreads) counts[e] = 0;
+    for (int e = threadIdx.x; e < width; e += kThreads) counts[e] = 0;
     __syncthreads();
     pdl_wait_prior();
     pdl_allow_next();
@@ -78,136 +322,158 @@ __global__ void __launch_bounds__(kThreads) moe_route_kernel(const Route a) {
     int32_t tokens = 0;
 #pragma unroll
     for (int r = 0; r < R; ++r) psum[r] = 0.f;
-    for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.tokens;
-         t += (int64_t)gridDim.x * kWarps) {
-        const T *row = reinterpret_cast<const T *>(a.logits) + t * a.ldl;
-        const bool masked = a.mask != nullptr && a.mask[t] == 0;
+    const int64_t step = (int64_t)gridDim.x * kWarps;
+    int64_t t = (int64_t)blockIdx.x * kWarps + warp;
+    constexpr bool kAhead = R <= 8;  // the next token's logits come while one is worked on
+    T next[R];
+    bool next_masked = false;
+    auto fetch = [&](int64_t at) {
+        const bool there = at < a.tokens;
+        load_logits<T, R, VEC>(reinterpret_cast<const T *>(a.logits) + at * a.ldl, there, a.experts,
+                               lane, next);
+        next_masked = there && a.mask != nullptr && a.mask[at] == 0;
+    };
+    if (kAhead) fetch(t);
+    for (; t < a.tokens; t += step) {
+        if (!kAhead) fetch(t);
+        const bool masked = next_masked;
         float l[R];
-        uint32_t key[R];
-        float peak = -INFINITY;
-        bool open = false;
-#pragma unroll
-        for (int r = 0; r < R; ++r) l[r] = logit_at(row, r * 32 + lane, a.experts);
+        uint32_t order[R], best = 0;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            key[r] = order_key(l[r]);
-            open |= key[r] != 0;
-            peak = fmaxf(peak, l[r]);
+            l[r] = elem_to_float(next[r]);
+            order[r] = order_of(l[r]);
+            best = max(best, order[r]);
         }
-        const bool on = !masked && __any_sync(kAll, open);
+        if (kAhead) fetch(t + step);
+        const uint32_t top = __reduce_max_sync(kAll, best);
         int my_id = -1;
         float my_w = 0.f;
-        if (on) {
-            peak = warp_max(peak);
+        if (!masked && top > kClosed) {
+            const float peak = logit_of(top);
             float total = 0.f;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                l[r] = r * 32 + lane < a.experts ? expf(l[r] - peak) : 0.f;
+                l[r] = exp_falling(l[r] - peak);
                 total += l[r];
             }
             total = warp_sum(total);
-            const float lse = peak + logf(total);
+            const float inv = inverse(total);
+            const float lse = peak + logarithm(total);
             zsum += lse * lse;
             ++tokens;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                l[r] = __fdiv_rn(l[r], total);
-                psum[r] += l[r];
+            for (int r = 0; r < R; ++r) psum[r] = fmaf(l[r], inv, psum[r]);
+            K mine;
+            if constexpr (R > 4) {
+                mine = choose_few<C, VEC>(order, best, top, a.topk, lane, dealt + warp * kDealt);
+            } else {
+                auto left = numbered<C, VEC>(order, lane);
+                mine = choose<C>(left, a.topk, lane);
             }
-            for (int j = 0; j < a.topk; ++j) {
-                uint32_t best = 0;
-                int at = 0;
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-                    if (key[r] > best) best = key[r], at = r;
-                const uint32_t top = __reduce_max_sync(kAll, best);
-                if (top == 0) break;
-                const uint32_t id =
-                    __reduce_min_sync(kAll, best == top ? (uint32_t)(at * 32 + lane) : kAll);
-                float w = 0.f;
-                const bool mine = lane == (int)(id & 31u);
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-                    if (mine && r == (int)(id >> 5)) {
-                        key[r] = 0;
-                        w = l[r];
-                    }
-                w = __shfl_sync(kAll, w, id & 31u);
-                if (lane == j) {
-                    my_id = (int)id;
-                    my_w = w;
-                }
+            if (mine != 0) {
+                my_id = C::expert(mine);
+                my_w = exp_falling(logit_of(C::order(mine)) - peak);
+                atomicAdd(&counts[my_id], 1);
             }
-            if (a.renormalize) {
-                const float chosen = warp_sum(my_w);
-                if (my_id >= 0) my_w = __fdiv_rn(my_w, chosen);
-            }
-            if (my_id >= 0) atomicAdd(&counts[my_id], 1);
+            const float chosen = a.renormalize ? inverse(warp_sum(my_w)) : inv;
+            my_w = my_id >= 0 ? my_w * chosen : 0.f;
         }
         if (lane < a.topk) {
             a.ids[t * a.topk + lane] = my_id;
             a.weights[t * a.topk + lane] = my_w;
         }
     }
+    // the warps' sums: the upper half's first, the lower half's added to them
+    float *own = sums + (warp % (kWarps / 2)) * width;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-        if (r * 32 + lane < a.experts) sums[warp * (a.experts + 1) + r * 32 + lane] = psum[r];
-    if (lane == 0) {
-        sums[warp * (a.experts + 1) + a.experts] = zsum;
-        atomicAdd(&counts[a.experts], tokens);
+    for (int upper = 1; upper >= 0; --upper) {
+        if (warp / (kWarps / 2) == upper) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int e = expert_of<R, VEC>(r, lane);
+                if (e < a.experts) own[e] = upper ? psum[r] : own[e] + psum[r];
+            }
+            if (lane == 0) {
+                own[a.experts] = upper ? zsum : own[a.experts] + zsum;
+                atomicAdd(&counts[a.experts], tokens);
+            }
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    const Parts out = parts_of(a, blockIdx.x);
-    for (int e = threadIdx.x; e <= a.experts; e += kThreads) {
+    auto block_part = [&](int e) {
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += sums[w * (a.experts + 1) + e];
-        out.sums[e] = v;
-        out.counts[e] = counts[e];
+        for (int w = 0; w < kWarps / 2; ++w) v += sums[w * width + e];
+        return part(v, counts[e]);
+    };
+    if (gridDim.x == 1) {
+        finish(a, red, block_part);
+    } else {
+        Part *out = reinterpret_cast<Part *>(a.workspace) + (int64_t)blockIdx.x * width;
+        for (int e = threadIdx.x; e < width; e += kThreads) out[e] = block_part(e);
     }
 }
 
-// The blocks' parts added in order; one block.
-__global__ void __launch_bounds__(1024) moe_route_sum_kernel(const Route a, int blocks) {
-    __shared__ float red[64];
-    __shared__ int32_t tokens;
-    __shared__ float zsum;
+// The blocks' parts added up: every CTA of one cluster takes each eighth of
+// them, the first adds the CTAs' sums.
+__global__ void __cluster_dims__(kSumCtas, 1, 1) __launch_bounds__(kThreads)
+    moe_route_sum_kernel(const Route a, int blocks) {
+    __shared__ Part share[kMoeMaxExperts + 1];
+    __shared__ float red[2 + kWarps];
+    const int width = a.experts + 1, rank = (int)cluster_ctarank();
     pdl_wait_prior();
     pdl_allow_next();
-    float balance = 0.f;
-    for (int e = threadIdx.x; e <= a.experts; e += 1024) {
+    const Part *parts = reinterpret_cast<const Part *>(a.workspace);
+    for (int e = threadIdx.x; e < width; e += kThreads) {
         float sum = 0.f, err = 0.f;
         int32_t n = 0;
-        for (int b = 0; b < blocks; ++b) {
-            const Parts p = parts_of(a, b);
-            add_exact(sum, err, p.sums[e]);
-            n += p.counts[e];
+        constexpr int kBatch = 20;  // loads in flight
+        for (int b0 = rank; b0 < blocks; b0 += kSumCtas * kBatch) {
+            Part p[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int b = b0 + kSumCtas * i;
+                p[i] = b < blocks ? parts[(int64_t)b * width + e] : part(0.f, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                add_exact(sum, err, p[i].x);
+                n += count_of(p[i]);
+            }
         }
-        if (e < a.experts) {
-            a.counts[e] = n;
-            balance += (float)n * (sum + err);
-        } else {
-            tokens = n;
-            zsum = sum + err;
-        }
+        share[e] = part(sum + err, n);
     }
-    float v[1] = {balance};
-    row_sum<1024, 1>(v, red);
-    if (threadIdx.x == 0) {
-        const float n = (float)max(tokens, 1);
-        *a.live = tokens;
-        if (a.losses != nullptr) {
-            a.losses[0] = v[0] / n / n * ((float)a.experts / (float)a.topk);
-            a.losses[1] = zsum / n;
-        }
-    }
+    cluster_sync_all();
+    if (rank == 0)
+        finish(a, red, [&](int e) {
+            Part p[kSumCtas];
+#pragma unroll
+            for (int c = 0; c < kSumCtas; ++c)
+                asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                             : "=f"(p[c].x), "=f"(p[c].y)
+                             : "r"(mapa_shared(smem_u32(&share[e]), c)));
+            float sum = 0.f;
+            int32_t n = 0;
+#pragma unroll
+            for (int c = 0; c < kSumCtas; ++c) {
+                sum += p[c].x;
+                n += count_of(p[c]);
+            }
+            return part(sum, n);
+        });
+    cluster_sync_all();  // the others' sums stay until they have been read
 }
 
-template <typename T, int R>
-__global__ void __launch_bounds__(kThreads) moe_route_backward_kernel(const RouteBackward a) {
+template <typename T, int R, bool VEC>
+__global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1)
+    moe_route_backward_kernel(const RouteBackward a) {
     extern __shared__ float smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float *chosen = smem + warp * R * 32;  // the weights' path, by expert
+    float *chosen = smem + warp * R * 32;  // the weights' path by expert, zero between tokens
+#pragma unroll
+    for (int r = 0; r < R; ++r) chosen[r * 32 + lane] = 0.f;
+    __syncwarp();
     pdl_wait_prior();
     pdl_allow_next();
     const float n = (float)max(*a.live, 1);
@@ -215,128 +481,149 @@ __global__ void __launch_bounds__(kThreads) moe_route_backward_kernel(const Rout
     const float dz = a.dlosses == nullptr ? 0.f : 2.f * a.dlosses[1] / n;
     float c[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-        c[r] = r * 32 + lane < a.experts
-                   ? db * ((float)a.experts / (float)a.topk) * ((float)a.counts[r * 32 + lane] / n) / n
+    for (int r = 0; r < R; ++r) {
+        const int e = expert_of<R, VEC>(r, lane);
+        c[r] = e < a.experts
+                   ? db * ((float)a.experts / (float)a.topk) * ((float)a.counts[e] / n) / n
                    : 0.f;
-    for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.tokens;
-         t += (int64_t)gridDim.x * kWarps) {
-        const T *row = reinterpret_cast<const T *>(a.logits) + t * a.ldl;
+    }
+    const int64_t step = (int64_t)gridDim.x * kWarps;
+    int64_t t = (int64_t)blockIdx.x * kWarps + warp;
+    T next[R];
+    int next_id = -1;
+    float next_dw = 0.f;
+    auto fetch = [&](int64_t at) {
+        const bool there = at < a.tokens;
+        load_logits<T, R, VEC>(reinterpret_cast<const T *>(a.logits) + at * a.ldl, there, a.experts,
+                               lane, next);
+        next_id = there && lane < a.topk ? a.ids[at * a.topk + lane] : -1;
+        next_dw = there && lane < a.topk && a.dweights != nullptr ? a.dweights[at * a.topk + lane] : 0.f;
+    };
+    constexpr bool kAhead = R <= 8;
+    if (kAhead) fetch(t);
+    for (; t < a.tokens; t += step) {
+        if (!kAhead) fetch(t);
         T *out = reinterpret_cast<T *>(a.dlogits) + t * a.experts;
-        int id = -1;
-        float dw = 0.f;
-        if (lane < a.topk) {
-            id = a.ids[t * a.topk + lane];
-            if (id >= a.experts) id = -1;
-            if (id >= 0 && a.dweights != nullptr) dw = a.dweights[t * a.topk + lane];
-        }
-        const bool on = __shfl_sync(kAll, lane < a.topk ? a.ids[t * a.topk + lane] : -1, 0) >= 0;
         float l[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) l[r] = elem_to_float(next[r]);
+        const bool on = __shfl_sync(kAll, next_id, 0) >= 0;
+        const int id = next_id < a.experts ? next_id : -1;
+        const float dw = id >= 0 ? next_dw : 0.f;
+        if (kAhead) fetch(t + step);
         if (on) {
-            float peak = -INFINITY;
+            uint32_t peak_order = 0;
 #pragma unroll
-            for (int r = 0; r < R; ++r) l[r] = logit_at(row, r * 32 + lane, a.experts);
-#pragma unroll
-            for (int r = 0; r < R; ++r) peak = fmaxf(peak, l[r]);
-            peak = warp_max(peak);
-            const float mine = id >= 0 ? expf(elem_to_float(row[id]) - peak) : 0.f;
+            for (int r = 0; r < R; ++r) peak_order = max(peak_order, order_of(l[r]));
+            const float peak = logit_of(__reduce_max_sync(kAll, peak_order));
             float total = 0.f, pc = 0.f;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                l[r] = r * 32 + lane < a.experts ? expf(l[r] - peak) : 0.f;
+                l[r] = exp_falling(l[r] - peak);
                 total += l[r];
-                pc += l[r] * c[r];
+                pc = fmaf(l[r], c[r], pc);
             }
+            const float mine = id >= 0 ? exp_falling(elem_to_float(
+                reinterpret_cast<const T *>(a.logits)[t * a.ldl + id]) - peak) : 0.f;
             total = warp_sum(total);
-            const float inv = __fdiv_rn(1.f, total);
-            float common = dz * (peak + logf(total)) - warp_sum(pc) * inv;
-            float w, d;
-            if (a.renormalize) {
-                const float sum = warp_sum(mine);
-                w = id >= 0 ? __fdiv_rn(mine, sum) : 0.f;
-                d = w * (dw - warp_sum(w * dw));
-            } else {
-                w = mine * inv;
-                common -= warp_sum(w * dw);
-                d = w * dw;
-            }
-#pragma unroll
-            for (int r = 0; r < R; ++r) chosen[r * 32 + lane] = 0.f;
-            __syncwarp();
-            if (id >= 0) atomicAdd(&chosen[id], d);
+            pc = warp_sum(pc);
+            const float inv = inverse(total);
+            float common = dz * (peak + logarithm(total)) - pc * inv;
+            const float w = mine * (a.renormalize ? inverse(warp_sum(mine)) : inv);
+            const float dot = warp_sum(id >= 0 ? w * dw : 0.f);
+            if (!a.renormalize) common -= dot;
+            if (id >= 0) chosen[id] = a.renormalize ? w * (dw - dot) : w * dw;
             __syncwarp();
 #pragma unroll
             for (int r = 0; r < R; ++r)
-                l[r] = l[r] * inv * (c[r] + common) + chosen[r * 32 + lane];
+                l[r] = fmaf(l[r] * inv, c[r] + common, chosen[expert_of<R, VEC>(r, lane)]);
+            __syncwarp();
+            if (id >= 0) chosen[id] = 0.f;
             __syncwarp();
         } else {
 #pragma unroll
             for (int r = 0; r < R; ++r) l[r] = 0.f;
         }
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            if (r * 32 + lane < a.experts) float_to_elem(out + r * 32 + lane, l[r]);
+        store_logits<T, R, VEC>(out, a.experts, lane, l);
     }
 }
 
-template <typename T, int R>
-cudaError_t route(const Route &a, int blocks, cudaStream_t s) {
-    const size_t smem = (size_t)(kWarps + 1) * (a.experts + 1) * sizeof(float);
-    cudaError_t e = launch_pdl(moe_route_kernel<T, R>, blocks, kThreads, smem, s, a);
+// Blocks of a warp to a token, as many as stay on the device at once.
+template <auto KERNEL>
+cudaError_t route_blocks(int64_t tokens, int most, int *blocks) {
+    int per_sm = 0;
+    cudaError_t e = blocks_per_sm<KERNEL>(kThreads, &per_sm);
     if (e != cudaSuccess) return e;
-    return launch_pdl(moe_route_sum_kernel, 1, 1024, 0, s, a, blocks);
+    const int64_t want = (tokens + kWarps - 1) / kWarps, room = (int64_t)per_sm * num_sms();
+    *blocks = (int)min(min(want, room), (int64_t)most);
+    return cudaSuccess;
 }
 
-template <typename T, int R>
-cudaError_t route_backward(const RouteBackward &a, int blocks, cudaStream_t s) {
+template <typename T, int R, bool VEC>
+cudaError_t route(const Route &a, cudaStream_t s) {
+    int blocks = 1;  // at least: the counts of no tokens are zeros
+    if (a.tokens > kRouteOneBlock) {
+        cudaError_t e = route_blocks<moe_route_kernel<T, R, VEC>>(a.tokens, kRouteMaxBlocks, &blocks);
+        if (e != cudaSuccess) return e;
+    }
+    const size_t smem = ((kWarps / 2 + 1) * (a.experts + 1) + 2 + kWarps) * sizeof(float);
+    cudaError_t e = launch_pdl(moe_route_kernel<T, R, VEC>, blocks, kThreads, smem, s, a);
+    if (e != cudaSuccess || blocks == 1) return e;
+    return launch_pdl(moe_route_sum_kernel, kSumCtas, kThreads, 0, s, a, blocks);
+}
+
+template <typename T, int R, bool VEC>
+cudaError_t route_backward(const RouteBackward &a, cudaStream_t s) {
+    int blocks = 0;
+    cudaError_t e = route_blocks<moe_route_backward_kernel<T, R, VEC>>(a.tokens, 1 << 20, &blocks);
+    if (e != cudaSuccess) return e;
     const size_t smem = (size_t)kWarps * R * 32 * sizeof(float);
-    return launch_pdl(moe_route_backward_kernel<T, R>, blocks, kThreads, smem, s, a);
+    if (smem > 48 * 1024) {
+        e = cudaFuncSetAttribute(moe_route_backward_kernel<T, R, VEC>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(moe_route_backward_kernel<T, R, VEC>, blocks, kThreads, smem, s, a);
 }
 
-int route_blocks(int64_t tokens, int per_sm) {
-    const int64_t blocks = (tokens + kWarps - 1) / kWarps, most = (int64_t)per_sm * num_sms();
-    return (int)(blocks < most ? blocks : most);
-}
-
-// f<R>(): the smallest R with 32 R >= experts
-#define FP8_BY_EXPERTS(experts, f)                \
-    ((experts) <= 32    ? f<T, 1>(a, blocks, s)   \
-     : (experts) <= 64  ? f<T, 2>(a, blocks, s)   \
-     : (experts) <= 128 ? f<T, 4>(a, blocks, s)   \
-     : (experts) <= 256 ? f<T, 8>(a, blocks, s)   \
-     : (experts) <= 512 ? f<T, 16>(a, blocks, s)  \
-                        : f<T, 32>(a, blocks, s))
+// f<T, R, VEC>(a, s) with the smallest R that holds the experts, 32 to a
+// register; `four` says that rows lie on groups of four logits.
+#define FP8_BY_EXPERTS(f, four)                                                   \
+    (a.experts <= 32    ? f<T, 1, false>(a, s)                                    \
+     : a.experts <= 64  ? f<T, 2, false>(a, s)                                    \
+     : a.experts <= 128 ? (four ? f<T, 4, true>(a, s) : f<T, 4, false>(a, s))     \
+     : a.experts <= 256 ? (four ? f<T, 8, true>(a, s) : f<T, 8, false>(a, s))     \
+     : a.experts <= 512 ? (four ? f<T, 16, true>(a, s) : f<T, 16, false>(a, s))   \
+                        : (four ? f<T, 32, true>(a, s) : f<T, 32, false>(a, s)))
 
 template <typename T>
-cudaError_t route_by_type(const Route &a, int blocks, cudaStream_t s) {
-    return FP8_BY_EXPERTS(a.experts, route);
+cudaError_t route_by_type(const Route &a, cudaStream_t s) {
+    const bool four = a.experts % 4 == 0 && a.ldl % 4 == 0 && aligned_to(a.logits, 4 * sizeof(T));
+    return FP8_BY_EXPERTS(route, four);
 }
 
 template <typename T>
-cudaError_t backward_by_type(const RouteBackward &a, int blocks, cudaStream_t s) {
-    return FP8_BY_EXPERTS(a.experts, route_backward);
+cudaError_t backward_by_type(const RouteBackward &a, cudaStream_t s) {
+    const bool four = a.experts % 4 == 0 && a.ldl % 4 == 0 && aligned_to(a.logits, 4 * sizeof(T)) &&
+                      aligned_to(a.dlogits, 4 * sizeof(T));
+    return FP8_BY_EXPERTS(route_backward, four);
 }
 
 }  // namespace
 
 int64_t moe_route_workspace_bytes(int64_t tokens, int64_t experts) {
     const int64_t blocks = (tokens + kWarps - 1) / kWarps;
-    return (blocks < kRouteMaxBlocks ? (blocks > 0 ? blocks : 1) : kRouteMaxBlocks) * 2 *
-           (experts + 1) * (int64_t)sizeof(float);
+    return (blocks > kRouteMaxBlocks ? kRouteMaxBlocks : blocks > 0 ? blocks : 1) *
+           (experts + 1) * (int64_t)sizeof(Part);
 }
 
 cudaError_t launch_moe_route(const Route &a, cudaStream_t s) {
-    // a block at least: the counts of no tokens are zeros
-    int blocks = route_blocks(a.tokens, 2);
-    blocks = blocks < 1 ? 1 : blocks < kRouteMaxBlocks ? blocks : kRouteMaxBlocks;
-    return a.f32 ? route_by_type<float>(a, blocks, s) : route_by_type<uint16_t>(a, blocks, s);
+    return a.f32 ? route_by_type<float>(a, s) : route_by_type<uint16_t>(a, s);
 }
 
 cudaError_t launch_moe_route_backward(const RouteBackward &a, cudaStream_t s) {
     if (a.tokens == 0) return cudaSuccess;
-    const int blocks = route_blocks(a.tokens, 8);
-    return a.f32 ? backward_by_type<float>(a, blocks, s)
-                 : backward_by_type<uint16_t>(a, blocks, s);
+    return a.f32 ? backward_by_type<float>(a, s) : backward_by_type<uint16_t>(a, s);
 }
 
 }  // namespace fp8
