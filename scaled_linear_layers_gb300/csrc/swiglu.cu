@@ -19,6 +19,8 @@
 // a tile, eight neighbouring columns each, so that a tile's maximum is four
 // shuffles and a bf16 lane's loads are 16 bytes; rows that do not lie on 16
 // bytes go element by element, a tile's columns dealt out to the lanes in turn.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "occupancy.h"
@@ -31,8 +33,20 @@ namespace {
 constexpr int kTile = 128, kLanes = 16, kPer = kTile / kLanes;
 constexpr int kThreads = 256, kTeams = kThreads / kLanes;
 
+// Blocks an SM, so that the next item's loads are held in registers beside the
+// one at work.  16384 x 14336 bf16, two, three and four blocks: forward 330, 291
+// and 310 us, backward 417, 371 and 361; fp32 rows of odd width, backward of 3001
+// x 1001: 11.9, 13.6 and 22.6.
+template <typename T, bool VECTOR>
+constexpr int blocks_for(bool forward) {
+    return !VECTOR ? 2 : forward || sizeof(T) == 4 ? 3 : 4;
+}
+
 __device__ __forceinline__ float sigmoid(float x, uint16_t) {
-    return __fdividef(1.f, 1.f + __expf(-x));
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+    return s;
 }
 __device__ __forceinline__ float sigmoid(float x, float) { return __fdiv_rn(1.f, 1.f + expf(-x)); }
 
@@ -48,26 +62,48 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t two) {
 }
 
 // A lane's eight columns of one tile: neighbours when VECTOR, else every 16th
-// from `lane` on, those below `left` (the tile's columns).
+// from `lane` on, those below `left` (the tile's columns).  Loaded and then
+// unpacked, so that all loads of an item are under way before the first is used.
 template <typename T, bool VECTOR>
-__device__ __forceinline__ void load_cols(const T *p, int lane, int left, float (&f)[kPer]) {
-    if constexpr (VECTOR) {
-        using R = RowVec<T, true>;
-#pragma unroll
-        for (int i = 0; i < kPer; i += R::V) {
-            typename R::Raw raw = R::zero();
-            if (kPer * lane < left) raw = R::load(p + kPer * lane + i);
-            float v[R::V];
-            R::unpack(raw, v);
-#pragma unroll
-            for (int k = 0; k < R::V; ++k) f[i + k] = v[k];
-        }
-    } else {
+struct Cols;
+template <>
+struct Cols<uint16_t, true> {
+    uint4 raw;
+    __device__ __forceinline__ void load(const uint16_t *p, int lane, int left) {
+        raw = kPer * lane < left ? *reinterpret_cast<const uint4 *>(p + kPer * lane)
+                                 : make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void unpack(float (&f)[kPer]) const {
+        RowVec<uint16_t, true>::unpack(raw, f);
+    }
+};
+template <>
+struct Cols<float, true> {
+    float4 raw[2];
+    __device__ __forceinline__ void load(const float *p, int lane, int left) {
+        const float4 *q = reinterpret_cast<const float4 *>(p + kPer * lane);
+        const bool on = kPer * lane < left;
+        raw[0] = on ? q[0] : make_float4(0.f, 0.f, 0.f, 0.f);
+        raw[1] = on ? q[1] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __device__ __forceinline__ void unpack(float (&f)[kPer]) const {
+        f[0] = raw[0].x, f[1] = raw[0].y, f[2] = raw[0].z, f[3] = raw[0].w;
+        f[4] = raw[1].x, f[5] = raw[1].y, f[6] = raw[1].z, f[7] = raw[1].w;
+    }
+};
+template <typename T>
+struct Cols<T, false> {
+    T raw[kPer];
+    __device__ __forceinline__ void load(const T *p, int lane, int left) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
-            f[i] = lane + kLanes * i < left ? elem_to_float(p[lane + kLanes * i]) : 0.f;
+            raw[i] = lane + kLanes * i < left ? p[lane + kLanes * i] : T(0);
     }
-}
+    __device__ __forceinline__ void unpack(float (&f)[kPer]) const {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) f[i] = elem_to_float(raw[i]);
+    }
+};
 
 template <typename T, bool VECTOR>
 __device__ __forceinline__ void store_cols(T *p, int lane, int left, const float (&f)[kPer]) {
@@ -107,62 +143,73 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, int lane, int left, const
     }
 }
 
-template <bool VECTOR>
-__device__ __forceinline__ void load_e4m3(const uint8_t *p, int lane, int left, float scale,
-                                          float (&f)[kPer]) {
-    uint32_t two[kPer / 2] = {};
-    if constexpr (VECTOR) {
-        if (kPer * lane < left) {
-            const uint2 w = *reinterpret_cast<const uint2 *>(p + kPer * lane);
-            two[0] = w.x & 0xFFFFu, two[1] = w.x >> 16, two[2] = w.y & 0xFFFFu, two[3] = w.y >> 16;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (lane + kLanes * i < left)
-                two[i / 2] |= (uint32_t)p[lane + kLanes * i] << (8 * (i & 1));
-    }
-#pragma unroll
-    for (int i = 0; i < kPer / 2; ++i) {
-        const float2 v = e4m3x2_to_float2(two[i]);
-        f[2 * i] = v.x * scale;
-        f[2 * i + 1] = v.y * scale;
-    }
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 
-// The largest |v| of a tile, as a bit pattern, in all of its sixteen lanes.
-__device__ __forceinline__ uint32_t tile_amax(const float (&f)[kPer]) {
-    uint32_t m = 0;
+// The larger of a lane's and the other lanes' of its tile.
+__device__ __forceinline__ float team_max(float m) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) m = max(m, abs_bits(f[i]));
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    for (int o = kLanes / 2; o > 0; o >>= 1)
+        m = max_abs_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     return m;
 }
 
-// Walks the tiles of [rows, tiles] in steps of the grid's teams: a division at
-// the start, then whole rows and the rest of a step at a time.
-struct TileWalk {
-    int64_t row;
-    int tile;
-    __device__ __forceinline__ TileWalk(int tiles) {
-        const int64_t first = (int64_t)blockIdx.x * kTeams + threadIdx.x / kLanes;
-        row = first / tiles;
-        tile = (int)(first - row * tiles);
-    }
-    __device__ __forceinline__ void next(int tiles, int64_t step_rows, int step_tiles) {
-        row += step_rows;
-        tile += step_tiles;
-        if (tile >= tiles) {
-            tile -= tiles;
-            ++row;
-        }
-    }
+// The largest |v| of a tile in all of its sixteen lanes (NaN if any is).
+__device__ __forceinline__ float tile_amax(const float (&f)[kPer]) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) m = max_abs_nan(m, f[i]);
+    return team_max(m);
+}
+
+// Those of the gate's and the up's tile.
+template <typename T, bool VECTOR>
+__device__ __forceinline__ void tile_amax2(const Cols<T, VECTOR> &, const Cols<T, VECTOR> &,
+                                           const float (&g)[kPer], const float (&u)[kPer],
+                                           float &mg, float &mu) {
+    mg = tile_amax(g);
+    mu = tile_amax(u);
+}
+// bf16 magnitudes order as 16-bit whole numbers: both maxima in one register
+template <>
+__device__ __forceinline__ void tile_amax2<uint16_t, true>(const Cols<uint16_t, true> &g,
+                                                           const Cols<uint16_t, true> &u,
+                                                           const float (&)[kPer],
+                                                           const float (&)[kPer], float &mg,
+                                                           float &mu) {
+    constexpr uint32_t kAbs = 0x7FFF7FFFu;
+    const uint32_t a = max_u16x2(max_u16x2(g.raw.x & kAbs, g.raw.y & kAbs),
+                                max_u16x2(g.raw.z & kAbs, g.raw.w & kAbs));
+    const uint32_t b = max_u16x2(max_u16x2(u.raw.x & kAbs, u.raw.y & kAbs),
+                                max_u16x2(u.raw.z & kAbs, u.raw.w & kAbs));
+    uint32_t m = max_u16x2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1)
+        m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    mg = bf16_lo(m);
+    mu = bf16_hi(m);
+}
+
+// Every team of sixteen lanes keeps a tile's columns and goes down the rows, so
+// that its addresses move by constants: `width` teams side by side (a tile each,
+// or each width-th of more tiles than there are teams), `row_step` rows of them.
+struct Walk {
+    int tiles, width;
+    int64_t row_step;
 };
 
-struct Walk {
-    int tiles, step_tiles;
-    int64_t step_rows;
+struct Team {
+    int lane;
+    int64_t tile, row0;
+    __device__ __forceinline__ explicit Team(const Walk &w) {
+        const int64_t team = (int64_t)blockIdx.x * kTeams + threadIdx.x / kLanes;
+        lane = threadIdx.x % kLanes;
+        row0 = team / w.width;
+        tile = team - row0 * w.width;
+    }
 };
 
 __device__ __forceinline__ int64_t live_rows(const int32_t *live, int64_t rows) {
@@ -170,85 +217,178 @@ __device__ __forceinline__ int64_t live_rows(const int32_t *live, int64_t rows) 
 }
 
 template <typename T, bool VECTOR>
-__global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluForward a, const Walk w) {
+__global__ void __launch_bounds__(kThreads, blocks_for<T, VECTOR>(true)) swiglu_kernel(const SwigluForward a, const Walk w) {
     pdl_wait_prior();
     pdl_allow_next();
-    const int lane = threadIdx.x % kLanes, lane32 = threadIdx.x & 31;
+    Team at(w);
+    const int lane = at.lane, first = threadIdx.x & 16;  // the team's first lane of the warp
     const int64_t rows = live_rows(a.live, a.rows);
-    const T *h = reinterpret_cast<const T *>(a.h);
-    T *y = reinterpret_cast<T *>(a.y);
-    TileWalk at(w.tiles);
-    // both halves of a warp go on until neither has a tile left
-    while (__any_sync(0xFFFFFFFFu, at.row < rows)) {
-        const bool on = at.row < rows;
-        const int64_t c0 = (int64_t)at.tile * kTile;
-        const int left = on ? (int)min((int64_t)kTile, a.cols - c0) : 0;
-        float g[kPer], u[kPer], v[kPer];
-        load_cols<T, VECTOR>(h + at.row * a.ldh + c0, lane, left, g);
-        load_cols<T, VECTOR>(h + at.row * a.ldh + a.cols + c0, lane, left, u);
+    const int64_t h_step = w.row_step * a.ldh, y_step = w.row_step * a.cols;
+    // Lanes 0..2 form and store the scales of the gate's, the up's and y's tile,
+    // lanes 3..5 their inverses: one division a lane.
+    const bool of_gate = lane % 3 == 0, of_up = lane % 3 == 1, forward = lane < 3;
+    const bool has_scale = lane == 2 ? a.yq != nullptr : lane < 2 && a.hq != nullptr;
+    const int64_t s_step = w.row_step * w.tiles * (lane == 2 ? 1 : 2);
+    // both teams of a warp go on until neither has anything left
+    for (; __any_sync(0xFFFFFFFFu, at.tile < w.tiles); at.tile += w.width) {
+        const int64_t c0 = at.tile * kTile, row = at.row0;
+        const int left = (int)max((int64_t)0, min((int64_t)kTile, a.cols - c0));
+        const int own = at.row0 < w.row_step && left > 0 && row < rows
+                            ? (int)((rows - row + w.row_step - 1) / w.row_step) : 0;
+        const int most = max(own, __shfl_xor_sync(0xFFFFFFFFu, own, 16));
+        const T *h = reinterpret_cast<const T *>(a.h) + row * a.ldh + c0;
+        T *y = reinterpret_cast<T *>(a.y) + row * a.cols + c0;
+        uint8_t *yq = a.yq + row * a.cols + c0, *hq = a.hq + 2 * row * a.cols + c0;
+        float *scale = lane == 2 ? a.y_scale + row * w.tiles + at.tile
+                                 : a.h_scale + (2 * row + lane) * w.tiles + at.tile;
+        Cols<T, VECTOR> next_gate, next_up;
+        next_gate.load(h, lane, 0 < own ? left : 0);
+        next_up.load(h + a.cols, lane, 0 < own ? left : 0);
+        for (int i = 0; i < most; ++i) {
+            const Cols<T, VECTOR> gate = next_gate, up = next_up;
+            const int cols = i < own ? left : 0;
+            h += h_step;
+            next_gate.load(h, lane, i + 1 < own ? left : 0);
+            next_up.load(h + a.cols, lane, i + 1 < own ? left : 0);
+            float g[kPer], u[kPer], v[kPer];
+            gate.unpack(g);
+            up.unpack(u);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) v[i] = g[i] * sigmoid(g[i], T()) * u[i];
-        if (y != nullptr) store_cols<T, VECTOR>(y + at.row * a.cols + c0, lane, left, v);
-        // the three tiles' scales are formed by three lanes side by side
-        const uint32_t mg = a.hq != nullptr ? tile_amax(g) : 0u;
-        const uint32_t mu = a.hq != nullptr ? tile_amax(u) : 0u;
-        const uint32_t mv = a.yq != nullptr ? tile_amax(v) : 0u;
-        float s, inv;
-        scales_from_amax(__uint_as_float(lane == 0 ? mg : lane == 1 ? mu : mv), s, inv);
-        const float ig = __shfl_sync(0xFFFFFFFFu, inv, lane32 & 16);
-        const float iu = __shfl_sync(0xFFFFFFFFu, inv, (lane32 & 16) + 1);
-        const float iv = __shfl_sync(0xFFFFFFFFu, inv, (lane32 & 16) + 2);
-        if (a.hq != nullptr) {
-            uint8_t *q = a.hq + at.row * 2 * a.cols + c0;
-            store_e4m3<VECTOR>(q, lane, left, g, ig);
-            store_e4m3<VECTOR>(q + a.cols, lane, left, u, iu);
-            if (on && lane < 2) a.h_scale[(at.row * 2 + lane) * w.tiles + at.tile] = s;
+            for (int k = 0; k < kPer; ++k) v[k] = g[k] * sigmoid(g[k], T()) * u[k];
+            if (a.y != nullptr) {
+                store_cols<T, VECTOR>(y, lane, cols, v);
+                y += y_step;
+            }
+            float mg = 0.f, mu = 0.f, mv = 0.f;
+            if (a.hq != nullptr) tile_amax2<T, VECTOR>(gate, up, g, u, mg, mu);
+            if (a.yq != nullptr) mv = tile_amax(v);
+            // scales_from_amax
+            const float m = of_gate ? mg : of_up ? mu : mv, top = m < 1e-12f ? 1e-12f : m;
+            const float s = __fdiv_rn(forward ? top : 448.f, forward ? 448.f : top);
+            if (has_scale && i < own) *scale = s;
+            scale += s_step;
+            if (a.hq != nullptr) {
+                store_e4m3<VECTOR>(hq, lane, cols, g, __shfl_sync(0xFFFFFFFFu, s, first + 3));
+                store_e4m3<VECTOR>(hq + a.cols, lane, cols, u,
+                                   __shfl_sync(0xFFFFFFFFu, s, first + 4));
+                hq += 2 * y_step;
+            }
+            if (a.yq != nullptr) {
+                store_e4m3<VECTOR>(yq, lane, cols, v, __shfl_sync(0xFFFFFFFFu, s, first + 5));
+                yq += y_step;
+            }
         }
-        if (a.yq != nullptr) {
-            store_e4m3<VECTOR>(a.yq + at.row * a.cols + c0, lane, left, v, iv);
-            if (on && lane == 2) a.y_scale[at.row * w.tiles + at.tile] = s;
-        }
-        at.next(w.tiles, w.step_rows, w.step_tiles);
     }
 }
 
+// The bytes of a lane's columns of one checkpoint tile.
+template <bool VECTOR>
+struct Bytes;
+template <>
+struct Bytes<true> {
+    uint2 raw;
+    __device__ __forceinline__ void load(const uint8_t *p, int lane, int left) {
+        raw = kPer * lane < left ? *reinterpret_cast<const uint2 *>(p + kPer * lane)
+                                 : make_uint2(0, 0);
+    }
+    __device__ __forceinline__ uint32_t two(int i) const {
+        return ((i & 2) ? raw.y : raw.x) >> (16 * (i & 1));
+    }
+};
+template <>
+struct Bytes<false> {
+    uint8_t raw[kPer];
+    __device__ __forceinline__ void load(const uint8_t *p, int lane, int left) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            raw[i] = lane + kLanes * i < left ? p[lane + kLanes * i] : (uint8_t)0;
+    }
+    __device__ __forceinline__ uint32_t two(int i) const {
+        return raw[2 * i] | ((uint32_t)raw[2 * i + 1] << 8);
+    }
+};
+template <bool VECTOR>
+__device__ __forceinline__ void decode(const Bytes<VECTOR> &b, float scale, float (&f)[kPer]) {
+#pragma unroll
+    for (int i = 0; i < kPer / 2; ++i) {
+        const float2 v = e4m3x2_to_float2(b.two(i));
+        f[2 * i] = v.x * scale;
+        f[2 * i + 1] = v.y * scale;
+    }
+}
+
+// One team's input of the backward pass: dy, and h from its bytes or as it is.
 template <typename T, bool VECTOR, bool SAVED>
-__global__ void __launch_bounds__(kThreads)
+struct BackwardInput {
+    Cols<T, VECTOR> grad;
+    typename std::conditional<SAVED, Bytes<VECTOR>, Cols<T, VECTOR>>::type gate, up;
+    float gate_scale, up_scale;
+    template <typename H>
+    __device__ __forceinline__ void load(const T *dy, const H *h, const float *scale, int64_t cols,
+                                         int tiles, int lane, int left) {
+        grad.load(dy, lane, left);
+        gate.load(h, lane, left);
+        up.load(h + cols, lane, left);
+        if constexpr (SAVED) {
+            gate_scale = left > 0 ? scale[0] : 0.f;
+            up_scale = left > 0 ? scale[tiles] : 0.f;
+        }
+    }
+    __device__ __forceinline__ void unpack(float (&d)[kPer], float (&g)[kPer], float (&u)[kPer]) const {
+        grad.unpack(d);
+        if constexpr (SAVED) {
+            decode(gate, gate_scale, g);
+            decode(up, up_scale, u);
+        } else {
+            gate.unpack(g);
+            up.unpack(u);
+        }
+    }
+};
+
+template <typename T, bool VECTOR, bool SAVED>
+__global__ void __launch_bounds__(kThreads, blocks_for<T, VECTOR>(false))
     swiglu_backward_kernel(const SwigluBackward a, const Walk w) {
+    using H = typename std::conditional<SAVED, uint8_t, T>::type;
     pdl_wait_prior();
     pdl_allow_next();
-    const int lane = threadIdx.x % kLanes;
+    Team at(w);
+    const int lane = at.lane;
     const int64_t rows = live_rows(a.live, a.rows);
-    const T *dy = reinterpret_cast<const T *>(a.dy);
-    T *dh = reinterpret_cast<T *>(a.dh), *y = reinterpret_cast<T *>(a.y);
-    TileWalk at(w.tiles);
-    for (; at.row < rows; at.next(w.tiles, w.step_rows, w.step_tiles)) {
-        const int64_t c0 = (int64_t)at.tile * kTile;
+    const int64_t h_step = w.row_step * a.ldh, dy_step = w.row_step * a.lddy;
+    const int64_t y_step = w.row_step * a.cols, s_step = w.row_step * 2 * w.tiles;
+    if (at.row0 >= w.row_step) return;
+    for (; at.tile < w.tiles; at.tile += w.width) {
+        const int64_t c0 = at.tile * kTile;
         const int left = (int)min((int64_t)kTile, a.cols - c0);
-        float g[kPer], u[kPer], d[kPer];
-        load_cols<T, VECTOR>(dy + at.row * a.lddy + c0, lane, left, d);
-        if constexpr (SAVED) {
-            const uint8_t *q = reinterpret_cast<const uint8_t *>(a.h) + at.row * a.ldh + c0;
-            const float *s = a.h_scale + at.row * 2 * w.tiles + at.tile;
-            load_e4m3<VECTOR>(q, lane, left, s[0], g);
-            load_e4m3<VECTOR>(q + a.cols, lane, left, s[w.tiles], u);
-        } else {
-            const T *h = reinterpret_cast<const T *>(a.h) + at.row * a.ldh + c0;
-            load_cols<T, VECTOR>(h, lane, left, g);
-            load_cols<T, VECTOR>(h + a.cols, lane, left, u);
-        }
-        float v[kPer];
+        int64_t row = at.row0, to = row * a.cols + c0;
+        const T *dy = reinterpret_cast<const T *>(a.dy) + row * a.lddy + c0;
+        const H *h = reinterpret_cast<const H *>(a.h) + row * a.ldh + c0;
+        const float *scale = a.h_scale + row * 2 * w.tiles + at.tile;
+        BackwardInput<T, VECTOR, SAVED> next;
+        next.load(dy, h, scale, a.cols, w.tiles, lane, row < rows ? left : 0);
+        for (; row < rows; to += y_step) {
+            const BackwardInput<T, VECTOR, SAVED> in = next;
+            row += w.row_step;
+            dy += dy_step;
+            h += h_step;
+            scale += s_step;
+            next.load(dy, h, scale, a.cols, w.tiles, lane, row < rows ? left : 0);
+            float d[kPer], g[kPer], u[kPer], v[kPer];
+            in.unpack(d, g, u);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const float s = sigmoid(g[i], T()), act = g[i] * s;
-            v[i] = act * u[i];
-            g[i] = d[i] * u[i] * (s + act * (1.f - s));
-            u[i] = d[i] * act;
+            for (int i = 0; i < kPer; ++i) {
+                const float s = sigmoid(g[i], T()), act = g[i] * s;
+                v[i] = act * u[i];
+                g[i] = d[i] * u[i] * (s + act * (1.f - s));
+                u[i] = d[i] * act;
+            }
+            T *out = reinterpret_cast<T *>(a.dh) + 2 * to - c0;
+            store_cols<T, VECTOR>(out, lane, left, g);
+            store_cols<T, VECTOR>(out + a.cols, lane, left, u);
+            if (a.y != nullptr)
+                store_cols<T, VECTOR>(reinterpret_cast<T *>(a.y) + to, lane, left, v);
         }
-        T *out = dh + at.row * 2 * a.cols + c0;
-        store_cols<T, VECTOR>(out, lane, left, g);
-        store_cols<T, VECTOR>(out + a.cols, lane, left, u);
-        if (y != nullptr) store_cols<T, VECTOR>(y + at.row * a.cols + c0, lane, left, v);
     }
 }
 
@@ -259,12 +399,12 @@ cudaError_t plan(int64_t rows, int64_t cols, Walk *w, int *grid) {
     cudaError_t e = blocks_per_sm<KERNEL>(kThreads, &per_sm);
     if (e != cudaSuccess) return e;
     w->tiles = (int)((cols + kTile - 1) / kTile);
-    const int64_t blocks = (rows * w->tiles + kTeams - 1) / kTeams;
+    const int64_t want = (rows * w->tiles + kTeams - 1) / kTeams;
     const int64_t most = (int64_t)per_sm * num_sms();
-    *grid = (int)(blocks < most ? blocks : most);
-    const int64_t step = (int64_t)*grid * kTeams;
-    w->step_rows = step / w->tiles;
-    w->step_tiles = (int)(step % w->tiles);
+    *grid = (int)(want < most ? want : most);
+    const int64_t teams = (int64_t)*grid * kTeams;
+    w->width = (int)(w->tiles < teams ? w->tiles : teams);
+    w->row_step = teams / w->width;
     return cudaSuccess;
 }
 
