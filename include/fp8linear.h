@@ -652,7 +652,10 @@ fp8_status fp8_moe_route_backward(const void *logits, int64_t ldl, fp8_dtype lt,
  * capacity < 2^31 (FP8_ERR_SHAPE).  All pointers but offsets are 16-byte
  * aligned.  Offsets outside 0..capacity are taken as the nearest that is in
  * it.  Rows from offsets[experts] on are neither read into any result nor
- * written. */
+ * written.  fprop and dgrad run on one of two kernels, for many or for few rows
+ * an expert, that give the same bits; the environment variable
+ * FP8LINEAR_MOE_FEW=0/1, read at each call, overrides the choice (for tests and
+ * tuning). */
 
 /* y [capacity, N] (bf16): row r of expert e = xq[r] · Wq_e^T.  xq [capacity, K]
  * and x_scale [capacity, K/128] as fp8_quantize(BLOCK) makes them of the sorted

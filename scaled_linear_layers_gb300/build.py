@@ -18,7 +18,8 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libfp8linear.so")
 SOURCES = ["api.cu", "quantize.cu", "quantize_fused.cu", "gemm.cu", "gemm_pair.cu",
            "gemm_block.cu", "meta.cu", "multi.cu", "linear_small.cu",
-           "layer_norm.cu", "moe.cu", "orthogonalize.cu", "moe_route.cu", "gemm_moe.cu", "swiglu.cu"]
+           "layer_norm.cu", "moe.cu", "orthogonalize.cu", "moe_route.cu", "gemm_moe.cu",
+           "gemm_moe_few.cu", "swiglu.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-Xptxas", "-v", "--expt-relaxed-constexpr"]

@@ -21,9 +21,11 @@
 #include <cuda.h>
 
 #include <atomic>
+#include <cstdlib>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "moe_tiles.cuh"
 #include "rowops.cuh"
 #include "tmap.h"
 
@@ -33,7 +35,7 @@ extern std::atomic<uint64_t> g_wait_limit_ns;
 
 namespace {
 
-constexpr int BM = 128, BN = 256, BK = 128;
+constexpr int BM = kMoeBlock, BN = 256, BK = kMoeBlock;
 constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int STAGES = 4;
 constexpr int SLOTS = 2;  // TMEM slots of BN columns
@@ -46,79 +48,22 @@ constexpr int SCALES = 2 * EPI_WARPS * COLS;  // wgrad: staged column scales, tw
 constexpr int TILES = 4;  // tiles found ahead of their use
 constexpr int READERS = 2 + EPI_WARPS;
 constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + SCALES * sizeof(float) + 512 +
-                        (3 * kMoeMaxExperts + 1) * sizeof(int32_t);
+                        kMoeSegmentBytes;
 static_assert(SLOTS * BN == 512, "the slots fill TMEM");
 static_assert(SMEM <= 227 * 1024, "smem");
 
-struct Args {
-    const int32_t *offsets;
-    int experts;
-    int capacity;
-    int rows_out, cols_out;  // wgrad: rows of an expert's dw; columns of the output
-    int depth;               // contraction blocks (fprop, dgrad)
-    int by, bx;              // per expert: where its rows and its columns of B begin
-    const float *sa, *sb;
-    int64_t sa_row, sa_k;          // scale of A's row i, block kb: sa[i sa_row + kb sa_k]
-    int64_t sb_expert, sb_col, sb_k;  // of B's 128-column tile j: sb[e sb_expert + j sb_col + kb sb_k]
-    uint16_t *d;
-    uint64_t wait_limit_ns;
-    unsigned int *status;
-};
-
-// One output tile.
-struct __align__(16) Tile {
-    int expert, n;   // n: first output column
-    int row0, rows;  // A's first row (fprop, dgrad: in the sorted order), rows to store
-    int kb0, nk;     // contraction blocks (kb0: the first, wgrad); nk < 0: no tile is left
-    int bad, unused;  // bad (wgrad): a segment that does not lie on 128-row blocks
-};
-static_assert(sizeof(Tile) == 32, "two 16-byte loads");
-
-__device__ __forceinline__ void segment(const Args &p, int e, int &lo, int &hi) {
-    // whatever the offsets hold, a segment lies in the rows that exist
-    lo = min(max(p.offsets[e], 0), p.capacity);
-    hi = min(max(p.offsets[e + 1], lo), p.capacity);
-}
-
-// The experts' segments and the row tiles before each, in shared memory: a
-// tile is found without a load from global memory.
-struct Segments {
-    int32_t *first, *lo, *hi;  // [experts + 1], [experts], [experts]
-};
-
-// By one warp.
-__device__ __forceinline__ void count_tiles(const Args &p, const Segments &g, int lane) {
-    int before = 0;
-    for (int e0 = 0; e0 < p.experts; e0 += 32) {
-        int lo = 0, hi = 0;
-        const int e = e0 + lane;
-        if (e < p.experts) segment(p, e, lo, hi);
-        int sum = (hi - lo + BM - 1) / BM;
-        const int own = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-            if (lane >= o) sum += v;
-        }
-        if (e < p.experts) {
-            g.first[e] = before + sum - own;
-            g.lo[e] = lo;
-            g.hi[e] = hi;
-        }
-        before += __shfl_sync(0xFFFFFFFFu, sum, 31);
-    }
-    if (lane == 0) g.first[p.experts] = before;
-}
+using Args = MoeArgs;
+using Tile = MoeTile;
 
 template <bool kWgrad>
-__device__ __forceinline__ int total_tiles(const Args &p, const Segments &g) {
+__device__ __forceinline__ int total_tiles(const Args &p, const MoeSegments &g) {
     const int n_tiles = (p.cols_out + BN - 1) / BN;
     if (kWgrad) return p.experts * (p.rows_out / BM) * n_tiles;
     return g.first[p.experts] * n_tiles;
 }
 
 template <bool kWgrad>
-__device__ __forceinline__ Tile find_tile(const Args &p, const Segments &g, int index) {
+__device__ __forceinline__ Tile find_tile(const Args &p, const MoeSegments &g, int index) {
     const int n_tiles = (p.cols_out + BN - 1) / BN;
     Tile t;
     int m_tiles, lo, hi, in;
@@ -128,23 +73,16 @@ __device__ __forceinline__ Tile find_tile(const Args &p, const Segments &g, int 
         t.expert = index / per;
         in = index - t.expert * per;
     } else {
-        int a = 0, b = p.experts;  // first[a] n_tiles <= index < first[b] n_tiles
-        const int at = index / n_tiles;
-        while (b - a > 1) {
-            const int mid = (a + b) >> 1;
-            if (g.first[mid] <= at) a = mid;
-            else b = mid;
-        }
-        t.expert = a;
-        m_tiles = g.first[a + 1] - g.first[a];
-        in = index - g.first[a] * n_tiles;
+        t.expert = moe_expert_of(g, p.experts, index / n_tiles);
+        m_tiles = g.first[t.expert + 1] - g.first[t.expert];
+        in = index - g.first[t.expert] * n_tiles;
     }
     lo = g.lo[t.expert];
     hi = g.hi[t.expert];
     int tm, tn;
     grouped_tile(in, m_tiles, n_tiles, 16, tm, tn);
     t.n = tn * BN;
-    t.unused = 0;
+    t.w_rows = BN;
     if (kWgrad) {
         t.bad = ((lo | hi) & (BK - 1)) != 0;
         t.row0 = tm * BM;
@@ -188,10 +126,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     Tile *tiles = reinterpret_cast<Tile *>(full + 32);  // [TILES]
-    Segments seg;
-    seg.first = reinterpret_cast<int32_t *>(full) + 128;
-    seg.lo = seg.first + p.experts + 1;
-    seg.hi = seg.lo + p.experts;
+    const MoeSegments seg(reinterpret_cast<int32_t *>(full) + 128, p.experts);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -219,7 +154,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     pdl_wait_prior();  // the offsets are the previous kernels' result
     pdl_allow_next();
-    if (warp == 2) count_tiles(p, seg, lane);
+    if (warp == 2) moe_count_tiles<BM>(p, seg, lane);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -374,8 +309,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             // instead of 128; they are staged by cp.async, one block ahead.
             float *wbuf = sbuf + (warp - EPI0) * 2 * COLS;
             const int fr = lane >> 2, fc = lane & 3;
-            for (uint32_t i = 0; next_tile(i); ++i) {
-                const Tile &t = tiles[i % TILES];
+            for (uint32_t at = 0; next_tile(at); ++at) {
+                const Tile &t = tiles[at % TILES];
                 const int nk = t.nk;
                 const float *sa = p.sa + (int64_t)t.kb0 * p.sa_k + t.row0 + quarter * 32 + fr;
                 const float *sb = p.sb + (int64_t)t.kb0 * p.sb_k +
@@ -428,7 +363,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             tmem_ld_16x256b_x2(taddr + 16 * (c + 1), ra[(c + 1) & 1]);
                             tmem_ld_16x256b_x2(taddr + (16u << 16) + 16 * (c + 1), rb[(c + 1) & 1]);
                         }
-                        const uint32_t(&r0)[8] = ra[c & 1], (&r1)[8] = rb[c & 1];
+                        const uint32_t *r0 = ra[c & 1], *r1 = rb[c & 1];
 #pragma unroll
                         for (int jj = 0; jj < 2; ++jj) {
                             const int j = 2 * c + jj;
@@ -463,13 +398,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                             dst[4 * j] = pack_bf16x2(acc[i][2 * j], acc[i][2 * j + 1]);
                     }
                 }
-                free_tile(i);
+                free_tile(at);
             }
             cp_async_wait_all();
         } else {
             // one row x 128 columns a thread: a block's scale is one product
-            for (uint32_t i = 0; next_tile(i); ++i) {
-                const Tile &t = tiles[i % TILES];
+            for (uint32_t at = 0; next_tile(at); ++at) {
+                const Tile &t = tiles[at % TILES];
                 const int nk = t.nk, in = quarter * 32 + lane;
                 const float *sa = p.sa + (int64_t)min(t.row0 + in, p.capacity - 1) * p.sa_row;
                 const float *sb = p.sb + t.expert * p.sb_expert +
@@ -525,7 +460,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
-                free_tile(i);
+                free_tile(at);
             }
         }
     }
@@ -579,6 +514,14 @@ Args common_args(const MoeGemm &m) {
     return a;
 }
 
+// Whether the kernel that puts the weights on the tensor cores' rows takes a
+// call: up to one of its tiles an expert on average (what the host knows of the
+// routing is the capacity).  FP8LINEAR_MOE_FEW=0/1 overrides.
+bool few_rows(const MoeGemm &m) {
+    const char *env = getenv("FP8LINEAR_MOE_FEW");
+    return env != nullptr ? atoi(env) == 1 : m.capacity <= kMoeFewRows * m.experts;
+}
+
 // Output tiles of fprop and dgrad at most: every expert may end in a tile of its own.
 int64_t most_tiles(const MoeGemm &m, int64_t cols) {
     const int64_t ends = m.experts < m.capacity ? m.experts : m.capacity;
@@ -587,14 +530,26 @@ int64_t most_tiles(const MoeGemm &m, int64_t cols) {
 
 }  // namespace
 
-cudaError_t launch_moe_fprop(const MoeGemm &m, cudaStream_t s, const char **why) {
-    if (m.capacity == 0) return cudaSuccess;
+namespace {
+
+// fprop and dgrad: A [capacity, K] times each expert's K-deep rows of B
+// [b_rows, b_cols].
+cudaError_t launch_rows(const MoeGemm &m, const Args &p, int64_t K, int64_t b_rows, int64_t b_cols,
+                        cudaStream_t s, const char **why) {
+    if (few_rows(m)) return launch_moe_few(p, m.a, K, m.b, b_rows, b_cols, s, why);
     CUtensorMap ta, tb;
-    if (!make_tmap_k128(&ta, m.a, m.capacity, m.K, BM) ||
-        !make_tmap_k128(&tb, m.b, m.experts * m.N, m.K, BN)) {
+    if (!make_tmap_k128(&ta, m.a, m.capacity, K, BM) ||
+        !make_tmap_k128(&tb, m.b, b_rows, b_cols, BN)) {
         *why = "cuTensorMapEncodeTiled failed";
         return cudaErrorInvalidValue;
     }
+    return launch<false>(ta, tb, p, most_tiles(m, p.cols_out), s, why);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_fprop(const MoeGemm &m, cudaStream_t s, const char **why) {
+    if (m.capacity == 0) return cudaSuccess;
     Args a = common_args(m);
     a.cols_out = (int)m.N;
     a.depth = (int)(m.K / BK);
@@ -604,17 +559,11 @@ cudaError_t launch_moe_fprop(const MoeGemm &m, cudaStream_t s, const char **why)
     a.sb_expert = (m.N / BK) * (m.K / BK);
     a.sb_col = m.K / BK;
     a.sb_k = 1;
-    return launch<false>(ta, tb, a, most_tiles(m, m.N), s, why);
+    return launch_rows(m, a, m.K, m.experts * m.N, m.K, s, why);
 }
 
 cudaError_t launch_moe_dgrad(const MoeGemm &m, cudaStream_t s, const char **why) {
     if (m.capacity == 0) return cudaSuccess;
-    CUtensorMap ta, tb;
-    if (!make_tmap_k128(&ta, m.a, m.capacity, m.N, BM) ||
-        !make_tmap_k128(&tb, m.b, m.K, m.experts * m.N, BN)) {
-        *why = "cuTensorMapEncodeTiled failed";
-        return cudaErrorInvalidValue;
-    }
     Args a = common_args(m);
     a.cols_out = (int)m.K;
     a.depth = (int)(m.N / BK);
@@ -624,7 +573,7 @@ cudaError_t launch_moe_dgrad(const MoeGemm &m, cudaStream_t s, const char **why)
     a.sb_expert = (m.N / BK) * (m.K / BK);
     a.sb_col = 1;
     a.sb_k = m.K / BK;
-    return launch<false>(ta, tb, a, most_tiles(m, m.K), s, why);
+    return launch_rows(m, a, m.N, m.K, m.experts * m.N, s, why);
 }
 
 cudaError_t launch_moe_wgrad(const MoeGemm &m, cudaStream_t s, const char **why) {

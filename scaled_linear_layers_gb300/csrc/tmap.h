@@ -44,6 +44,22 @@ inline bool make_tmap_k128(CUtensorMap *m, const uint8_t *base, int64_t rows, in
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same matrix as blocks of 128 columns: dims (128, rows, K / 128), K a
+// multiple of 128, box = box_rows rows of `blocks` neighbouring blocks, each
+// block's rows together in shared memory (128-byte swizzle as above).
+inline bool make_tmap_k128_blocks(CUtensorMap *m, const uint8_t *base, int64_t rows, int64_t K,
+                                  int box_rows, int blocks) {
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[3] = {128u, (cuuint64_t)rows, (cuuint64_t)(K / 128)};
+    cuuint64_t strides[2] = {(cuuint64_t)K, 128u};
+    cuuint32_t box[3] = {128u, (cuuint32_t)box_rows, (cuuint32_t)blocks};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t *>(base), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 2D bf16 matrix [rows, cols] with row stride ld elements (ld * 2 a multiple
 // of 16 bytes) as the target of 32-row x 32-column box stores from shared
 // memory laid out with the 64-byte swizzle: the 16-byte chunk c of box row r

@@ -14,6 +14,14 @@ BF, F, D = torch.bfloat16, torch.float32, torch.float64
 B = 128
 
 
+@pytest.fixture(params=["chosen", "many", "few"])
+def kernel(request, monkeypatch):
+    """Runs a test on the kernel that the call chooses, and on both."""
+    if request.param != "chosen":
+        monkeypatch.setenv("FP8LINEAR_MOE_FEW", "1" if request.param == "few" else "0")
+    return request.param
+
+
 def rnd(*shape, seed, scale=1.0):
     g = torch.Generator(device="cuda").manual_seed(seed)
     return (scale * torch.randn(shape, generator=g, device="cuda")).to(BF)
@@ -85,7 +93,7 @@ def case(counts, multiple, seed, extra=0):
 
 @pytest.mark.parametrize("counts, multiple, N, K", SIZES)
 @pytest.mark.parametrize("extra", [0, 300])
-def test_fprop_and_dgrad(counts, multiple, N, K, extra):
+def test_fprop_and_dgrad(counts, multiple, N, K, extra, kernel):
     at, offsets, cap = case(counts, multiple, 1, extra)
     if cap == 0:
         cap = B
@@ -127,7 +135,7 @@ def test_wgrad(counts, N, K):
     fp8.fp8_check_device_status()
 
 
-def test_the_bits_of_one_call_an_expert():
+def test_the_bits_of_one_call_an_expert(kernel):
     counts, N, K = [128, 640, 0, 256], 512, 768
     at, offsets, cap = case(counts, B, 7)
     w, x, g = rnd(4, N, K, seed=8), rnd(cap, K, seed=9), rnd(cap, N, seed=10, scale=1e-3)
@@ -158,7 +166,7 @@ def test_the_bits_of_one_call_an_expert():
         assert torch.equal(one, dw[i])
 
 
-def test_nan_outside_the_segments_reaches_nothing():
+def test_nan_outside_the_segments_reaches_nothing(kernel):
     counts, N, K = [40, 0, 200, 3], 256, 256
     at, offsets, cap = case(counts, B, 11, 130)
     wq, ws, wqt = square_tiles(rnd(4, N, K, seed=12))
@@ -197,7 +205,7 @@ def test_wgrad_of_segments_off_the_blocks_is_nan():
     assert dw[0].isfinite().all() and dw[1].isnan().all() and dw[2].isnan().all()
 
 
-def test_offsets_outside_the_rows_are_held_inside():
+def test_offsets_outside_the_rows_are_held_inside(kernel):
     N, K, cap = 128, 128, 256
     wq, ws, _ = square_tiles(rnd(3, N, K, seed=17))
     xq, xs, xqt, xst = row_tiles(rnd(cap, K, seed=18))
@@ -228,7 +236,7 @@ def test_no_rows_at_all():
     assert (dw == 0).all()
 
 
-def test_two_streams_and_a_replayed_graph_with_new_offsets():
+def test_two_streams_and_a_replayed_graph_with_new_offsets(kernel):
     N, K, cap = 384, 512, 512
     wq, ws, _ = square_tiles(rnd(4, N, K, seed=20))
     xq, xs, _, _ = row_tiles(rnd(cap, K, seed=21))
@@ -262,7 +270,7 @@ def test_two_streams_and_a_replayed_graph_with_new_offsets():
         assert torch.equal(out, w)
 
 
-def test_a_wait_that_runs_out_is_reported():
+def test_a_wait_that_runs_out_is_reported(kernel):
     N, K, cap = 512, 1024, 1024
     wq, ws, _ = square_tiles(rnd(4, N, K, seed=22))
     xq, xs, _, _ = row_tiles(rnd(cap, K, seed=23))
