@@ -82,7 +82,7 @@ __device__ __forceinline__ Tile find_tile(const Args &p, const MoeSegments &g, i
     int tm, tn;
     grouped_tile(in, m_tiles, n_tiles, 16, tm, tn);
     t.n = tn * BN;
-    t.w_rows = BN;
+    t.unused = 0;
     if (kWgrad) {
         t.bad = ((lo | hi) & (BK - 1)) != 0;
         t.row0 = tm * BM;
@@ -159,15 +159,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
-    // The i-th tile of this CTA for one reader; false when there is none left or
-    // the wait for it gave up.
-    auto read_tile = [&](uint32_t i, Tile &t) {
-        const uint32_t at = i % TILES;
-        if (!mbar_wait_bounded<true>(&tfull[at], (i / TILES) & 1u, abort_flag, p.wait_limit_ns,
-                                     kStatusTimeoutTma, p.status))
-            return false;
-        t = tiles[at];
-        return true;
+    // The i-th tile of this CTA is in its place; false when none is left or the
+    // wait gave up.
+    auto have_tile = [&](uint32_t i) {
+        return mbar_wait_bounded<true>(&tfull[i % TILES], (i / TILES) & 1u, abort_flag,
+                                       p.wait_limit_ns, kStatusTimeoutTma, p.status) &&
+               tiles[i % TILES].nk >= 0;
     };
     // each warp of the first warpgroup gives registers back as it enters its
     // role, each epilogue warp takes more
@@ -175,80 +172,86 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     if (warp == 0) {
         regs_low();
-        if (lane == 0) {
-            // ------------------------------------------------ TMA producer
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            Tile t;
-            for (uint32_t i = 0; ok && read_tile(i, t) && t.nk >= 0; ++i) {
-                mbar_arrive(&tempty[i % TILES]);
-                const int brow = t.expert * p.by + t.n, arow = t.row0, nk = t.nk;
-                int ax = t.kb0 * BK, bx = t.expert * p.bx + t.kb0 * BK;
-                for (int q = 0; q < nk; ++q, ax += BK, bx += BK) {
-                    if (!mbar_wait_bounded<true>(&empty[stage], phase ^ 1u, abort_flag,
-                                                 p.wait_limit_ns, kStatusTimeoutTma, p.status)) {
-                        ok = false;
-                        break;
-                    }
+        // ---------------------------------------------------- TMA producer
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        const bool leader = elect_one();
+        for (uint32_t i = 0; ok && __all_sync(0xFFFFFFFFu, have_tile(i)); ++i) {
+            const Tile &t = tiles[i % TILES];
+            const int nk = __shfl_sync(0xFFFFFFFFu, t.nk, 0);
+            const int arow = __shfl_sync(0xFFFFFFFFu, t.row0, 0);
+            const int brow = __shfl_sync(0xFFFFFFFFu, t.expert * p.by + t.n, 0);
+            int ax = __shfl_sync(0xFFFFFFFFu, t.kb0 * BK, 0);
+            int bx = ax + __shfl_sync(0xFFFFFFFFu, t.expert * p.bx, 0);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty[i % TILES]);
+            for (int q = 0; q < nk; ++q, ax += BK, bx += BK) {
+                ok = __all_sync(0xFFFFFFFFu,
+                                mbar_wait_bounded<true>(&empty[stage], phase ^ 1u, abort_flag,
+                                                        p.wait_limit_ns, kStatusTimeoutTma, p.status));
+                if (!ok) break;
+                if (leader) {
                     mbar_arrive_expect_tx(&full[stage], STAGE_BYTES);
                     tma_load_2d(sA + stage * A_BYTES, &tma_a, &full[stage], ax, arow);
                     tma_load_2d(sB + stage * B_BYTES, &tma_b, &full[stage], bx, brow);
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                }
+                __syncwarp();
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
-            // wait (bounded) for the copies still in flight before teardown
-            for (int s = 0; s < STAGES; ++s) {
-                stage = stage == 0 ? STAGES - 1 : stage - 1;
-                if (stage == STAGES - 1) phase ^= 1u;
-                volatile int no_abort = 0;
-                mbar_wait_bounded(&full[stage], phase, &no_abort, 10000000ull, kStatusTimeoutTma,
-                                  p.status);
-            }
+        }
+        // wait (bounded) for the copies still in flight before teardown
+        for (int s = 0; s < STAGES; ++s) {
+            stage = stage == 0 ? STAGES - 1 : stage - 1;
+            if (stage == STAGES - 1) phase ^= 1u;
+            volatile int no_abort = 0;
+            mbar_wait_bounded(&full[stage], phase, &no_abort, 10000000ull, kStatusTimeoutTma,
+                              p.status);
         }
     } else if (warp == 1) {
         regs_low();
-        if (lane == 0) {
-            // ------------------------------------------------- MMA issuer
-            int stage = 0;
-            uint32_t phase = 0;
-            uint32_t g = 0;  // blocks issued so far (across tiles)
-            bool ok = true;
-            Tile t;
-            for (uint32_t i = 0; ok && read_tile(i, t) && t.nk >= 0; ++i) {
-                mbar_arrive(&tempty[i % TILES]);
-                const int nk = t.nk;
-                for (int q = 0; q < nk; ++q, ++g) {
-                    const uint32_t slot = g % SLOTS, sphase = (g / SLOTS) & 1u;
-                    if (!mbar_wait_bounded<true>(&sempty[slot], sphase ^ 1u, abort_flag,
-                                                 p.wait_limit_ns, kStatusTimeoutMma, p.status) ||
-                        !mbar_wait_bounded<true>(&full[stage], phase, abort_flag, p.wait_limit_ns,
-                                                 kStatusTimeoutMma, p.status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t a0 = smem_u32(sA + stage * A_BYTES);
-                    const uint32_t b0 = smem_u32(sB + stage * B_BYTES);
+        // ------------------------------------------------------ MMA issuer
+        int stage = 0;
+        uint32_t phase = 0;
+        uint32_t g = 0;  // blocks issued so far (across tiles)
+        bool ok = true;
+        const bool leader = elect_one();
+        const uint64_t a_desc = smem_desc_sw128(smem_u32(sA)), b_desc = smem_desc_sw128(smem_u32(sB));
+        for (uint32_t i = 0; ok && __all_sync(0xFFFFFFFFu, have_tile(i)); ++i) {
+            const int nk = __shfl_sync(0xFFFFFFFFu, tiles[i % TILES].nk, 0);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty[i % TILES]);
+            for (int q = 0; q < nk; ++q, ++g) {
+                const uint32_t slot = g % SLOTS, sphase = (g / SLOTS) & 1u;
+                ok = __all_sync(0xFFFFFFFFu,
+                                mbar_wait_bounded<true>(&sempty[slot], sphase ^ 1u, abort_flag,
+                                                        p.wait_limit_ns, kStatusTimeoutMma, p.status) &&
+                                    mbar_wait_bounded<true>(&full[stage], phase, abort_flag,
+                                                            p.wait_limit_ns, kStatusTimeoutMma, p.status));
+                if (!ok) break;
+                tc_fence_after();
+                if (leader) {
+                    const uint64_t a0 = a_desc + (stage * A_BYTES >> 4);
+                    const uint64_t b0 = b_desc + (stage * B_BYTES >> 4);
 #pragma unroll
                     for (int k = 0; k < BK / 32; ++k)
-                        mma_f8(tmem_base + slot * BN, smem_desc_sw128(a0 + 32 * k),
-                               smem_desc_sw128(b0 + 32 * k), IDESC, k != 0);
+                        mma_f8(tmem_base + slot * BN, a0 + 2 * k, b0 + 2 * k, IDESC, k != 0);
                     mma_commit(&empty[stage]);
                     mma_commit(&sfull[slot]);
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                }
+                __syncwarp();
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
-            mma_commit(drain);
-            volatile int no_abort = 0;
-            mbar_wait_bounded(drain, 0, &no_abort, p.wait_limit_ns, kStatusTimeoutMma, p.status);
         }
+        if (leader) mma_commit(drain);
+        volatile int no_abort = 0;
+        mbar_wait_bounded(drain, 0, &no_abort, p.wait_limit_ns, kStatusTimeoutMma, p.status);
     } else if (warp == 2) {
         regs_low();
         if (lane == 0) {
@@ -287,11 +290,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         // A tile stays in its place until the warp is done with it, so that what
         // the stores need is read again rather than kept in registers.
         auto next_tile = [&](uint32_t i) {
-            if (ok)
-                ok = mbar_wait_bounded<true>(&tfull[i % TILES], (i / TILES) & 1u, abort_flag,
-                                             p.wait_limit_ns, kStatusTimeoutEpilogue, p.status);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            return ok && tiles[i % TILES].nk >= 0;
+            ok = __all_sync(0xFFFFFFFFu, ok && have_tile(i));
+            return ok;
         };
         auto free_tile = [&](uint32_t i) {
             __syncwarp();

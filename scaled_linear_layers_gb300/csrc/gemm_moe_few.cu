@@ -33,7 +33,6 @@ namespace {
 constexpr int BW = kMoeBlock, BT = kMoeFewRows, BK = kMoeBlock;  // weight rows, tokens, depth of a block
 constexpr int KG = 4;  // blocks of a group
 constexpr int TOKENS = 16;  // of a step of the instruction's width
-constexpr int W_PART = 32;  // weight rows of an epilogue warp and of the smallest tile part
 constexpr int W_BYTES = BW * BK, T_BYTES = BT * BK;
 constexpr int STAGE_BYTES = KG * (W_BYTES + T_BYTES), STAGES = 2;
 constexpr int SLOTS = 2;  // TMEM slots of a group, KG * BT columns
@@ -48,45 +47,24 @@ static_assert(SLOTS * KG * BT == 512, "the slots fill TMEM");
 static_assert(PANEL % KG == 0, "a group lies in one panel");
 static_assert(SMEM <= 227 * 1024, "smem");
 
-// The tiles of all experts, the last of them split over their weight rows where
-// that evens out the CTAs' shares: tiles from `whole` on come in `parts` parts.
-struct Plan {
-    int w_tiles, whole, parts, items;
-    __device__ __forceinline__ Plan(const MoeArgs &p, const MoeSegments &g, int ctas) {
-        w_tiles = p.cols_out / BW;
-        const int tiles = g.first[p.experts] * w_tiles, rest = tiles % ctas;
-        whole = tiles - rest;
-        parts = 1;
-        int best = 4 * (rest != 0);  // time of the last wave, in quarters
-        for (int s = 2; s <= BW / W_PART; s *= 2) {
-            const int time = (rest * s + ctas - 1) / ctas * (4 / s);
-            if (time < best) best = time, parts = s;
-        }
-        items = whole + rest * parts;
-    }
-};
-
-__device__ __forceinline__ MoeTile find_tile(const MoeArgs &p, const MoeSegments &g,
-                                             const Plan &plan, int item) {
+__device__ __forceinline__ MoeTile find_tile(const MoeArgs &p, const MoeSegments &g, int index) {
+    const int w_tiles = p.cols_out / BW;
     MoeTile t;
-    t.w_rows = item < plan.whole ? BW : BW / plan.parts;
-    const int past = item - plan.whole;
-    const int index = past < 0 ? item : plan.whole + past / plan.parts;
-    t.expert = moe_expert_of(g, p.experts, index / plan.w_tiles);
+    t.expert = moe_expert_of(g, p.experts, index / w_tiles);
     const int t_tiles = g.first[t.expert + 1] - g.first[t.expert];
-    const int in = index - g.first[t.expert] * plan.w_tiles;
+    const int in = index - g.first[t.expert] * w_tiles;
     // an expert's tokens one after the other against the same weights
-    t.n = in / t_tiles * BW + (past < 0 ? 0 : past % plan.parts * t.w_rows);
+    t.n = in / t_tiles * BW;
     t.row0 = g.lo[t.expert] + in % t_tiles * BT;
     t.rows = min(BT, g.hi[t.expert] - t.row0);
-    t.kb0 = t.bad = 0;
+    t.kb0 = t.bad = t.unused = 0;
     t.nk = p.depth;
     return t;
 }
 
-// Copies of a group: of 128 or 32 weight rows, of 16, 32 or 64 tokens.
+// Copies of a group: of 128 weight rows, and of 16, 32 or 64 tokens.
 struct Maps {
-    CUtensorMap w[2], t[3];
+    CUtensorMap w, t[3];
 };
 
 __global__ void __launch_bounds__(THREADS, 1)
@@ -132,7 +110,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbarrier_init();
-        tma_prefetch_desc(&maps.w[0]);
+        tma_prefetch_desc(&maps.w);
         tma_prefetch_desc(&maps.t[0]);
     }
     if (warp == 1) {
@@ -164,30 +142,21 @@ __global__ void __launch_bounds__(THREADS, 1)
         const bool leader = elect_one();
         for (uint32_t i = 0; ok && __all_sync(0xFFFFFFFFu, have_tile(i)); ++i) {
             const MoeTile &t = tiles[i % TILES];
-            const int nk = __shfl_sync(0xFFFFFFFFu, t.nk, 0), rows = t.rows, w_rows = t.w_rows;
+            const int nk = __shfl_sync(0xFFFFFFFFu, t.nk, 0), rows = t.rows;
             const int size = __shfl_sync(0xFFFFFFFFu, rows > 32 ? 2 : rows > 16 ? 1 : 0, 0);
             const int w_row = __shfl_sync(0xFFFFFFFFu, t.expert * p.by + t.n, 0);
             const int w_k = __shfl_sync(0xFFFFFFFFu, t.expert * p.bx / BK, 0);
             const int row0 = __shfl_sync(0xFFFFFFFFu, t.row0, 0);
-            const int parts = __shfl_sync(0xFFFFFFFFu, w_rows == BW ? 0 : w_rows / W_PART, 0);
             __syncwarp();
             if (lane == 0) mbar_arrive(&tempty[i % TILES]);
-            const uint32_t bytes = KG * BK * ((parts == 0 ? BW : parts * W_PART) + (TOKENS << size));
+            const uint32_t bytes = KG * BK * (BW + (TOKENS << size));
             for (int q = 0; q < nk; q += KG) {
                 ok = __all_sync(0xFFFFFFFFu, wait(&empty[stage], phase ^ 1u, kStatusTimeoutTma));
                 if (!ok) break;
-                uint8_t *w = sW + stage * KG * W_BYTES, *tok = sT + stage * KG * T_BYTES;
                 if (leader) {
                     mbar_arrive_expect_tx(&full[stage], bytes);
-                    if (parts == 0) {
-                        tma_load_3d(w, &maps.w[0], &full[stage], 0, w_row, w_k + q);
-                    } else {  // the parts' rows lie block by block, like whole ones
-                        for (int r = 0; r < parts; ++r)
-                            for (int j = 0; j < KG; ++j)
-                                tma_load_3d(w + j * W_BYTES + r * W_PART * BK, &maps.w[1],
-                                            &full[stage], 0, w_row + r * W_PART, w_k + q + j);
-                    }
-                    tma_load_3d(tok, &maps.t[size], &full[stage], 0, row0, q);
+                    tma_load_3d(sW + stage * KG * W_BYTES, &maps.w, &full[stage], 0, w_row, w_k + q);
+                    tma_load_3d(sT + stage * KG * T_BYTES, &maps.t[size], &full[stage], 0, row0, q);
                 }
                 __syncwarp();
                 if (++stage == STAGES) {
@@ -252,12 +221,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp == 2) {
         if (lane == 0) {
             // -------------------------------------------- search for tiles
-            const Plan plan(p, seg, gridDim.x);
+            const int num_tiles = seg.first[p.experts] * (p.cols_out / BW);
             int index = blockIdx.x;
             for (uint32_t i = 0;; ++i, index += gridDim.x) {
                 MoeTile t;
                 t.nk = -1;
-                if (index < plan.items) t = find_tile(p, seg, plan, index);
+                if (index < num_tiles) t = find_tile(p, seg, index);
                 if (!wait(&tempty[i % TILES], ((i / TILES) & 1u) ^ 1u, kStatusTimeoutTma)) break;
                 tiles[i % TILES] = t;
                 mbar_arrive(&tfull[i % TILES]);
@@ -302,10 +271,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             ok = __all_sync(0xFFFFFFFFu, ok && have_tile(i));
             if (!ok) break;
             const MoeTile &t = tiles[i % TILES];
-            // (rows of a partial product behind the tile's weight rows are of what
-            // lay in shared memory: nobody reads them)
-            const bool mine = quarter * W_PART < t.w_rows;
-            const int nk = t.nk, rows = mine ? t.rows : 0, chunks = (rows + 15) / 16;
+            const int nk = t.nk, rows = t.rows, chunks = (rows + 15) / 16;
             float acc[BT];
 #pragma unroll
             for (int j = 0; j < BT; ++j) acc[j] = 0.f;
@@ -385,8 +351,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 cudaError_t launch_moe_few(const MoeArgs &p, const uint8_t *a, int64_t a_cols, const uint8_t *b,
                            int64_t b_rows, int64_t b_cols, cudaStream_t s, const char **why) {
     Maps maps;
-    bool made = make_tmap_k128_blocks(&maps.w[0], b, b_rows, b_cols, BW, KG) &&
-                make_tmap_k128_blocks(&maps.w[1], b, b_rows, b_cols, W_PART, 1);
+    bool made = make_tmap_k128_blocks(&maps.w, b, b_rows, b_cols, BW, KG);
     for (int i = 0; i < 3; ++i)
         made = made && make_tmap_k128_blocks(&maps.t[i], a, p.capacity, a_cols, TOKENS << i, KG);
     if (!made) {
@@ -404,7 +369,7 @@ cudaError_t launch_moe_few(const MoeArgs &p, const uint8_t *a, int64_t a_cols, c
     }
     // every expert may end in a tile of its own
     const int64_t ends = p.experts < p.capacity ? p.experts : p.capacity;
-    const int64_t most = (p.capacity / BT + ends) * (p.cols_out / W_PART), sms = num_sms();
+    const int64_t most = (p.capacity / BT + ends) * (p.cols_out / BW), sms = num_sms();
     return launch_pdl(moe_few_kernel, (unsigned)(most < sms ? most : sms), THREADS, SMEM, s, maps, p);
 }
 

@@ -30,8 +30,7 @@ struct __align__(16) MoeTile {
     int expert, n;   // n: first output column
     int row0, rows;  // A's first row (fprop, dgrad: in the sorted order), rows to store
     int kb0, nk;     // contraction blocks (kb0: the first, wgrad); nk < 0: no tile is left
-    int bad;         // wgrad: a segment that does not lie on 128-row blocks
-    int w_rows;      // gemm_moe_few.cu: rows of B
+    int bad, unused;  // bad (wgrad): a segment that does not lie on 128-row blocks
 };
 static_assert(sizeof(MoeTile) == 32, "two 16-byte loads");
 
