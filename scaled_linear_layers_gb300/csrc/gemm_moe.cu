@@ -44,10 +44,13 @@ constexpr int THREADS = 32 * (EPI0 + EPI_WARPS);
 constexpr int COLS = BN * 4 / EPI_WARPS;  // accumulator columns of a one-row thread
 constexpr int REGS_LOW = 40, REGS_HIGH = 232;
 constexpr uint32_t IDESC = idesc_f8_f32(BM, BN);
-constexpr int SCALES = 2 * EPI_WARPS * COLS;  // wgrad: staged column scales, two blocks a warp
+// Shared memory of an epilogue warp: the box that a tile's output goes through
+// (wgrad: half of it; the other half holds column scales, two blocks of them).
+constexpr int WARP_BYTES = 2048;
+static_assert(2 * COLS * sizeof(float) == WARP_BYTES / 2, "two blocks' column scales");
 constexpr int TILES = 4;  // tiles found ahead of their use
 constexpr int READERS = 2 + EPI_WARPS;
-constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + SCALES * sizeof(float) + 512 +
+constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + EPI_WARPS * WARP_BYTES + 512 +
                         kMoeSegmentBytes;
 static_assert(SLOTS * BN == 512, "the slots fill TMEM");
 static_assert(SMEM <= 227 * 1024, "smem");
@@ -115,8 +118,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                                                 ~uintptr_t(1023));
     uint8_t *sA = smem;
     uint8_t *sB = smem + STAGES * A_BYTES;
-    float *sbuf = reinterpret_cast<float *>(smem + STAGES * STAGE_BYTES);
-    uint64_t *full = reinterpret_cast<uint64_t *>(sbuf + SCALES);  // [STAGES] TMA -> MMA
+    uint8_t *boxes = smem + STAGES * STAGE_BYTES;  // [EPI_WARPS]
+    uint64_t *full = reinterpret_cast<uint64_t *>(boxes + EPI_WARPS * WARP_BYTES);  // [STAGES] TMA -> MMA
     uint64_t *empty = full + STAGES;                               // [STAGES] MMA -> TMA
     uint64_t *sfull = empty + STAGES;                              // [SLOTS] MMA -> epilogue
     uint64_t *sempty = sfull + SLOTS;                              // [SLOTS] epilogue -> MMA
@@ -257,6 +260,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) {
             // -------------------------------------------- search for tiles
             const int num_tiles = total_tiles<kWgrad>(p, seg);
+            // a place is free once the tile before is done: far from its end where
+            // the contraction is long
+            const uint64_t limit_ns =
+                p.wait_limit_ns + moe_tile_ns(kWgrad ? p.capacity / BK : p.depth);
             int index = blockIdx.x;
             for (uint32_t i = 0;; ++i, index += gridDim.x) {
                 const uint32_t at = i % TILES;
@@ -264,7 +271,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 t.nk = -1;
                 if (index < num_tiles) t = find_tile<kWgrad>(p, seg, index);
                 if (!mbar_wait_bounded<true>(&tempty[at], ((i / TILES) & 1u) ^ 1u, abort_flag,
-                                             p.wait_limit_ns, kStatusTimeoutTma, p.status))
+                                             limit_ns, kStatusTimeoutTma, p.status))
                     break;
                 tiles[at] = t;
                 mbar_arrive(&tfull[at]);
@@ -302,40 +309,48 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&sempty[slot]);
         };
+        uint8_t *box = boxes + (warp - EPI0) * WARP_BYTES;
         if constexpr (kWgrad) {
             // Four rows x 32 columns a thread (16-lane TMEM loads): thread l
             // holds rows 8i + l/4 (i = 0..3) of its lane quarter and, of every
             // 8 columns, 2(l%4) and +1, so it needs 32 column scales a block
             // instead of 128; they are staged by cp.async, one block ahead.
-            float *wbuf = sbuf + (warp - EPI0) * 2 * COLS;
+            float *wbuf = reinterpret_cast<float *>(box + WARP_BYTES / 2);
             const int fr = lane >> 2, fc = lane & 3;
-            for (uint32_t at = 0; next_tile(at); ++at) {
+            const float *sa = nullptr, *sb = nullptr;
+            float next[4] = {};
+            // block h of all: its scales into its half of wbuf
+            auto fetch = [&](uint32_t h, bool there) {
+                if (there) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) next[i] = sa[8 * i];
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(
+                                     smem_u32(wbuf + (h & 1) * COLS + 4 * lane)),
+                                 "l"(sb)
+                                 : "memory");
+                    sa += p.sa_k;
+                    sb += p.sb_k;
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            };
+            auto begin = [&](uint32_t at) {
+                const Tile &t = tiles[at % TILES];
+                sa = p.sa + (int64_t)t.kb0 * p.sa_k + t.row0 + quarter * 32 + fr;
+                sb = p.sb + (int64_t)t.kb0 * p.sb_k +
+                     min(t.n + half * COLS + 4 * lane, p.cols_out - 4);
+                fetch(g, t.nk > 0);
+            };
+            bool more = next_tile(0);
+            if (more) begin(0);
+            for (uint32_t at = 0; more; ++at) {
                 const Tile &t = tiles[at % TILES];
                 const int nk = t.nk;
-                const float *sa = p.sa + (int64_t)t.kb0 * p.sa_k + t.row0 + quarter * 32 + fr;
-                const float *sb = p.sb + (int64_t)t.kb0 * p.sb_k +
-                                  min(t.n + half * COLS + 4 * lane, p.cols_out - 4);
                 const float start = t.bad ? __uint_as_float(0x7FFFFFFFu) : 0.f;
                 float acc[4][COLS / 4];  // [i][2 j + c]: columns 8 j + 2 fc + c
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int j = 0; j < COLS / 4; ++j) acc[i][j] = start;
-                float next[4] = {};
-                auto fetch = [&](int q) {
-                    if (q < nk) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) next[i] = sa[8 * i];
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(
-                                         smem_u32(wbuf + (q & 1) * COLS + 4 * lane)),
-                                     "l"(sb)
-                                     : "memory");
-                        sa += p.sa_k;
-                        sb += p.sb_k;
-                    }
-                    asm volatile("cp.async.commit_group;" ::: "memory");
-                };
-                fetch(0);
                 for (int q = 0; q < nk; ++q, ++g) {
                     const uint32_t slot = g % SLOTS, sphase = (g / SLOTS) & 1u;
                     uint64_t cur2[4];
@@ -343,12 +358,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int i = 0; i < 4; ++i) cur2[i] = pair_of(next[i], next[i]);
                     asm volatile("cp.async.wait_group 0;" ::: "memory");
                     __syncwarp();
-                    fetch(q + 1);
+                    fetch(g + 1, q + 1 < nk);
                     wait_block(slot, sphase);
                     if (!ok) break;
                     const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) +
                                            slot * BN + (uint32_t)(half * COLS);
-                    const float *buf = wbuf + (q & 1) * COLS + 2 * fc;
+                    const float *buf = wbuf + (g & 1) * COLS + 2 * fc;
                     // 16 columns a load, the next load in flight while one is folded in
                     constexpr int NC = COLS / 16;
                     uint32_t ra[2][8], rb[2][8];
@@ -386,33 +401,60 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     }
                 }
-                const int row0 = t.row0 + quarter * 32 + fr, j0 = t.n + half * COLS;
-                if (ok && j0 < p.cols_out) {
-                    uint16_t *d = p.d + (int64_t)t.expert * p.rows_out * p.cols_out;
+                const bool done = ok;
+                more = next_tile(at + 1);
+                if (more) begin(at + 1);
+                const int j0 = t.n + half * COLS;
+                if (done && j0 < p.cols_out) {
+                    // eight rows of 64 columns at a time through the box (16-byte
+                    // groups, group j of row r at j ^ r): 128 bytes of a row a store
+                    uint16_t *d = p.d +
+                                  ((int64_t)t.expert * p.rows_out + t.row0 + quarter * 32 + (lane >> 3)) *
+                                      p.cols_out +
+                                  j0 + 8 * (lane & 7);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t *dst = reinterpret_cast<uint32_t *>(
-                            d + (int64_t)(row0 + 8 * i) * p.cols_out + j0 + 2 * fc);
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
-                        for (int j = 0; j < COLS / 8; ++j)
-                            dst[4 * j] = pack_bf16x2(acc[i][2 * j], acc[i][2 * j + 1]);
-                    }
+                        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                *reinterpret_cast<uint32_t *>(box + fr * 128 + ((j ^ fr) * 16) + 4 * fc) =
+                                    pack_bf16x2(acc[i][16 * h + 2 * j], acc[i][16 * h + 2 * j + 1]);
+                            __syncwarp();
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const int r = 4 * k + (lane >> 3);
+                                const uint4 v = *reinterpret_cast<const uint4 *>(
+                                    box + r * 128 + (((lane & 7) ^ r) * 16));
+                                *reinterpret_cast<uint4 *>(d + (int64_t)(8 * i + 4 * k) * p.cols_out +
+                                                           64 * h) = v;
+                            }
+                            __syncwarp();
+                        }
                 }
                 free_tile(at);
             }
             cp_async_wait_all();
         } else {
             // one row x 128 columns a thread: a block's scale is one product
-            for (uint32_t at = 0; next_tile(at); ++at) {
+            const float *sa = nullptr, *sb = nullptr;
+            float sa_next = 0.f, sb_next = 0.f;
+            auto begin = [&](uint32_t at) {
                 const Tile &t = tiles[at % TILES];
-                const int nk = t.nk, in = quarter * 32 + lane;
-                const float *sa = p.sa + (int64_t)min(t.row0 + in, p.capacity - 1) * p.sa_row;
-                const float *sb = p.sb + t.expert * p.sb_expert +
-                                  (int64_t)(min(t.n + half * COLS, p.cols_out - 1) / BK) * p.sb_col;
+                sa = p.sa + (int64_t)min(t.row0 + quarter * 32 + lane, p.capacity - 1) * p.sa_row;
+                sb = p.sb + t.expert * p.sb_expert +
+                     (int64_t)(min(t.n + half * COLS, p.cols_out - 1) / BK) * p.sb_col;
+                sa_next = *sa;
+                sb_next = *sb;
+            };
+            bool more = next_tile(0);
+            if (more) begin(0);
+            for (uint32_t at = 0; more; ++at) {
+                const Tile &t = tiles[at % TILES];
+                const int nk = t.nk;
                 uint64_t acc[COLS / 2];
 #pragma unroll
                 for (int j = 0; j < COLS / 2; ++j) acc[j] = 0ull;
-                float sa_next = *sa, sb_next = *sb;
                 for (int q = 0; q < nk; ++q, ++g) {
                     const uint32_t slot = g % SLOTS, sphase = (g / SLOTS) & 1u;
                     const float sa_cur = sa_next, sb_cur = sb_next;
@@ -446,18 +488,38 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     }
                 }
-                const int j0 = t.n + half * COLS;
-                if (ok && in < t.rows && j0 < p.cols_out) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.d + (int64_t)(t.row0 + in) * p.cols_out + j0);
+                const bool done = ok;
+                more = next_tile(at + 1);
+                if (more) begin(at + 1);
+                const int j0 = t.n + half * COLS, there = t.rows - quarter * 32;
+                if (done && there > 0 && j0 < p.cols_out) {
+                    // 32 columns at a time through the box (16-byte groups, group c
+                    // of row r at c ^ r/2): 64 bytes of eight rows a store
+                    uint16_t *d = p.d + (int64_t)(t.row0 + quarter * 32 + (lane >> 2)) * p.cols_out + j0 +
+                                  8 * (lane & 3);
 #pragma unroll
-                    for (int c = 0; c < COLS / 8; ++c) {
-                        uint32_t w[4];
+                    for (int c = 0; c < COLS / 32; ++c) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 v = pair_split(acc[4 * c + e]);
-                            w[e] = pack_bf16x2(v.x, v.y);
+                        for (int b = 0; b < 4; ++b) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float2 v = pair_split(acc[16 * c + 4 * b + e]);
+                                w[e] = pack_bf16x2(v.x, v.y);
+                            }
+                            *reinterpret_cast<uint4 *>(box + lane * 64 + ((b ^ ((lane >> 1) & 3)) * 16)) =
+                                make_uint4(w[0], w[1], w[2], w[3]);
                         }
-                        dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
+                        __syncwarp();
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int r = 8 * k + (lane >> 2);
+                            const uint4 v = *reinterpret_cast<const uint4 *>(
+                                box + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) * 16));
+                            if (r < there)
+                                *reinterpret_cast<uint4 *>(d + (int64_t)(8 * k) * p.cols_out + 32 * c) = v;
+                        }
+                        __syncwarp();
                     }
                 }
                 free_tile(at);

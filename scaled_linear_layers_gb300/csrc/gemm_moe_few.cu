@@ -227,7 +227,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 MoeTile t;
                 t.nk = -1;
                 if (index < num_tiles) t = find_tile(p, seg, index);
-                if (!wait(&tempty[i % TILES], ((i / TILES) & 1u) ^ 1u, kStatusTimeoutTma)) break;
+                if (!mbar_wait_bounded<true>(&tempty[i % TILES], ((i / TILES) & 1u) ^ 1u, abort_flag,
+                                             p.wait_limit_ns + moe_tile_ns(p.depth),
+                                             kStatusTimeoutTma, p.status))
+                    break;
                 tiles[i % TILES] = t;
                 mbar_arrive(&tfull[i % TILES]);
                 if (t.nk < 0) break;

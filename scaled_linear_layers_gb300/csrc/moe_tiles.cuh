@@ -83,6 +83,10 @@ __device__ __forceinline__ int moe_expert_of(const MoeSegments &g, int experts, 
     return a;
 }
 
+// What the search for tiles allows a tile of `blocks` contraction blocks beside
+// the limit of a wait, at 10 us a block (they take 0.3 to 1).
+__device__ __forceinline__ uint64_t moe_tile_ns(int blocks) { return 10000ull * (uint64_t)blocks; }
+
 // fprop and dgrad of few rows an expert (gemm_moe_few.cu); a, b as in MoeGemm.
 cudaError_t launch_moe_few(const MoeArgs &p, const uint8_t *a, int64_t a_cols, const uint8_t *b,
                            int64_t b_rows, int64_t b_cols, cudaStream_t s, const char **why);

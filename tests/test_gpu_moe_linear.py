@@ -291,3 +291,42 @@ def test_a_wait_that_runs_out_is_reported(kernel):
     fp8.fp8_moe_linear_fprop(xq, xs, wq, ws, offsets, y)
     fp8.fp8_check_device_status()
     assert torch.equal(y, want)
+
+
+def test_a_tile_that_takes_longer_than_a_wait():
+    """The search for tiles runs ahead of a tile of 2^14 blocks (9 ms or so),
+    further than the 3 ms that every other wait is held to."""
+    N, K, cap, experts = 128, 128, 1 << 21, 1024
+    g = torch.Generator(device="cuda").manual_seed(24)
+    gqt, xqt = (torch.randint(0, 120, (n, cap), generator=g, dtype=torch.uint8, device="cuda")
+                for n in (N, K))
+    gst, xst = (torch.rand(cap // B, n, generator=g, device="cuda") for n in (N, K))
+    offsets = torch.full((experts + 1,), cap, dtype=torch.int32, device="cuda")
+    offsets[0] = 0
+    dw, one = empty(BF, experts, N, K), empty(BF, N, K)
+    fp8.fp8_linear_wgrad(gqt, gst, xqt, xst, cap, N, K, fp8.BLOCK, one)
+    torch.cuda.synchronize()
+    old = fp8.fp8_set_wait_limit_ns(3000000)
+    try:
+        fp8.fp8_moe_linear_wgrad(gqt, gst, xqt, xst, offsets, dw)
+        torch.cuda.synchronize()
+    finally:
+        fp8.fp8_set_wait_limit_ns(old)
+    fp8.fp8_check_device_status()
+    assert torch.equal(dw[0], one) and (dw[1:] == 0).all()
+
+
+@pytest.mark.parametrize("N, K", [(384, 640), (128, 128), (256, 1152)])
+def test_every_row_count_of_the_last_tile(N, K):
+    """Outputs leave through boxes of eight rows: none behind a segment."""
+    counts = [1, 7, 8, 9, 31, 32, 33, 63, 65, 96, 97, 127, 129, 161]
+    at, offsets, cap = case(counts, 1, 25, 200)
+    wq, ws, _ = square_tiles(rnd(len(counts), N, K, seed=26))
+    xq, xs, _, _ = row_tiles(rnd(cap, K, seed=27))
+    y = {}
+    for few in "01":
+        with pytest.MonkeyPatch.context() as env:
+            env.setenv("FP8LINEAR_MOE_FEW", few)
+            y[few] = torch.full((cap, N), 7.0, dtype=BF, device="cuda")
+            fp8.fp8_moe_linear_fprop(xq, xs, wq, ws, offsets, y[few])
+    assert torch.equal(y["0"], y["1"]) and (y["0"][at[-1]:] == 7.0).all()
