@@ -109,6 +109,11 @@ __device__ __forceinline__ void fold(uint64_t &acc, uint32_t p0, uint32_t p1, ui
     acc = pair_fma(pv, f, acc);
 }
 
+__device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
+    const float2 f = pair_split(v);
+    return pack_bf16x2(f.x, f.y);
+}
+
 template <bool kWgrad>
 __global__ void __launch_bounds__(THREADS, 1)
     moe_gemm_kernel(const __grid_constant__ CUtensorMap tma_a,
@@ -287,9 +292,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int half = (warp - EPI0) >> 2;   // columns half*COLS .. +COLS-1 of the tile
         bool ok = true;
         uint32_t g = 0;
-        auto wait_block = [&](uint32_t slot, uint32_t sphase) {
+        auto wait_block = [&](uint32_t h) {  // block h of all
             if (ok)
-                ok = mbar_wait_bounded<true>(&sfull[slot], sphase, abort_flag, p.wait_limit_ns,
+                ok = mbar_wait_bounded<true>(&sfull[h % SLOTS], (h / SLOTS) & 1u, abort_flag, p.wait_limit_ns,
                                              kStatusTimeoutEpilogue, p.status);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (ok) tc_fence_after();
@@ -319,6 +324,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int fr = lane >> 2, fc = lane & 3;
             const float *sa = nullptr, *sb = nullptr;
             float next[4] = {};
+            constexpr int NC = COLS / 16;  // 16 columns a load
+            // Chunk c of the block in work: the partials of rows 0..15 and 16..31
+            // and the scales of this thread's columns, with those of chunk c + 1
+            // under way while it is folded in.
+            uint32_t ra[2][8], rb[2][8];
+            uint64_t sc[2][2];
             // block h of all: its scales into its half of wbuf
             auto fetch = [&](uint32_t h, bool there) {
                 if (there) {
@@ -333,6 +344,22 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
             };
+            auto scales = [&](uint32_t h, int c) {
+                const float *buf = wbuf + (h & 1) * COLS + 2 * fc + 16 * c;
+                sc[c & 1][0] = *reinterpret_cast<const uint64_t *>(buf);
+                sc[c & 1][1] = *reinterpret_cast<const uint64_t *>(buf + 8);
+            };
+            auto load = [&](uint32_t h, int c) {
+                const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) +
+                                       (h % SLOTS) * BN + (uint32_t)(half * COLS) + 16 * c;
+                tmem_ld_16x256b_x2(taddr, ra[c & 1]);
+                tmem_ld_16x256b_x2(taddr + (16u << 16), rb[c & 1]);
+            };
+            auto loaded = [&](int c) {
+                tmem_ld_wait();
+                tmem_regs_ready(ra[c & 1]);
+                tmem_regs_ready(rb[c & 1]);
+            };
             auto begin = [&](uint32_t at) {
                 const Tile &t = tiles[at % TILES];
                 sa = p.sa + (int64_t)t.kb0 * p.sa_k + t.row0 + quarter * 32 + fr;
@@ -346,58 +373,39 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const Tile &t = tiles[at % TILES];
                 const int nk = t.nk;
                 const float start = t.bad ? __uint_as_float(0x7FFFFFFFu) : 0.f;
-                float acc[4][COLS / 4];  // [i][2 j + c]: columns 8 j + 2 fc + c
+                uint64_t acc[4][COLS / 8];  // [i][j]: columns 8 j + 2 fc and + 1
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int j = 0; j < COLS / 4; ++j) acc[i][j] = start;
+                    for (int j = 0; j < COLS / 8; ++j) acc[i][j] = pair_of(start, start);
                 for (int q = 0; q < nk; ++q, ++g) {
-                    const uint32_t slot = g % SLOTS, sphase = (g / SLOTS) & 1u;
-                    uint64_t cur2[4];
+                    uint64_t cur[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) cur2[i] = pair_of(next[i], next[i]);
+                    for (int i = 0; i < 4; ++i) cur[i] = pair_of(next[i], next[i]);
                     asm volatile("cp.async.wait_group 0;" ::: "memory");
                     __syncwarp();
                     fetch(g + 1, q + 1 < nk);
-                    wait_block(slot, sphase);
+                    wait_block(g);
                     if (!ok) break;
-                    const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) +
-                                           slot * BN + (uint32_t)(half * COLS);
-                    const float *buf = wbuf + (g & 1) * COLS + 2 * fc;
-                    // 16 columns a load, the next load in flight while one is folded in
-                    constexpr int NC = COLS / 16;
-                    uint32_t ra[2][8], rb[2][8];
-                    tmem_ld_16x256b_x2(taddr, ra[0]);
-                    tmem_ld_16x256b_x2(taddr + (16u << 16), rb[0]);
-                    tmem_ld_wait();
-                    tmem_regs_ready(ra[0]);
-                    tmem_regs_ready(rb[0]);
+                    scales(g, 0);
+                    load(g, 0);
+                    loaded(0);
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
                         if (c + 1 < NC) {
-                            tmem_ld_16x256b_x2(taddr + 16 * (c + 1), ra[(c + 1) & 1]);
-                            tmem_ld_16x256b_x2(taddr + (16u << 16) + 16 * (c + 1), rb[(c + 1) & 1]);
+                            load(g, c + 1);
+                            scales(g, c + 1);
                         }
-                        const uint32_t *r0 = ra[c & 1], *r1 = rb[c & 1];
 #pragma unroll
-                        for (int jj = 0; jj < 2; ++jj) {
-                            const int j = 2 * c + jj;
-                            const float2 s = *reinterpret_cast<const float2 *>(buf + 8 * j);
-                            const uint64_t ss = pair_of(s.x, s.y);
+                        for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const uint32_t *v = i < 2 ? r0 + 4 * jj + 2 * i : r1 + 4 * jj + 2 * i - 4;
-                                const float2 f = pair_split(pair_mul(ss, cur2[i]));
-                                acc[i][2 * j] = __fmaf_rn(__uint_as_float(v[0]), f.x, acc[i][2 * j]);
-                                acc[i][2 * j + 1] =
-                                    __fmaf_rn(__uint_as_float(v[1]), f.y, acc[i][2 * j + 1]);
+                                const uint32_t *v = (i < 2 ? ra : rb)[c & 1] + 4 * jj + 2 * (i & 1);
+                                fold(acc[i][2 * c + jj], v[0], v[1], pair_mul(sc[c & 1][jj], cur[i]));
                             }
-                        }
                         if (c + 1 < NC) {
-                            tmem_ld_wait();
-                            tmem_regs_ready(ra[(c + 1) & 1]);
-                            tmem_regs_ready(rb[(c + 1) & 1]);
-                            if (c + 2 == NC) hand_back(slot);
+                            loaded(c + 1);
+                            if (c + 2 == NC) hand_back(g % SLOTS);
                         }
                     }
                 }
@@ -419,7 +427,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
                                 *reinterpret_cast<uint32_t *>(box + fr * 128 + ((j ^ fr) * 16) + 4 * fc) =
-                                    pack_bf16x2(acc[i][16 * h + 2 * j], acc[i][16 * h + 2 * j + 1]);
+                                    pack_pair(acc[i][8 * h + j]);
                             __syncwarp();
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
@@ -439,6 +447,17 @@ __global__ void __launch_bounds__(THREADS, 1)
             // one row x 128 columns a thread: a block's scale is one product
             const float *sa = nullptr, *sb = nullptr;
             float sa_next = 0.f, sb_next = 0.f;
+            constexpr int NC = COLS / 16;
+            uint32_t r[2][16];  // chunk c of the block in work and, under way, c + 1
+            auto load = [&](uint32_t h, int c) {
+                tmem_ld_32x32b_x16(tmem_base + ((uint32_t)(quarter * 32) << 16) + (h % SLOTS) * BN +
+                                       (uint32_t)(half * COLS) + 16 * c,
+                                   r[c & 1]);
+            };
+            auto loaded = [&](int c) {
+                tmem_ld_wait();
+                tmem_regs_ready(r[c & 1]);
+            };
             auto begin = [&](uint32_t at) {
                 const Tile &t = tiles[at % TILES];
                 sa = p.sa + (int64_t)min(t.row0 + quarter * 32 + lane, p.capacity - 1) * p.sa_row;
@@ -456,35 +475,27 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int j = 0; j < COLS / 2; ++j) acc[j] = 0ull;
                 for (int q = 0; q < nk; ++q, ++g) {
-                    const uint32_t slot = g % SLOTS, sphase = (g / SLOTS) & 1u;
-                    const float sa_cur = sa_next, sb_cur = sb_next;
+                    const float f = sa_next * sb_next;
+                    const uint64_t ff = pair_of(f, f);
                     if (q + 1 < nk) {
                         sa += p.sa_k;
                         sb += p.sb_k;
                     }
                     sa_next = *sa;
                     sb_next = *sb;
-                    wait_block(slot, sphase);
+                    wait_block(g);
                     if (!ok) break;
-                    const float f = sa_cur * sb_cur;
-                    const uint64_t ff = pair_of(f, f);
-                    const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) +
-                                           slot * BN + (uint32_t)(half * COLS);
-                    constexpr int NC = COLS / 16;
-                    uint32_t r[2][16];
-                    tmem_ld_32x32b_x16(taddr, r[0]);
-                    tmem_ld_wait();
-                    tmem_regs_ready(r[0]);
+                    load(g, 0);
+                    loaded(0);
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
-                        if (c + 1 < NC) tmem_ld_32x32b_x16(taddr + 16 * (c + 1), r[(c + 1) & 1]);
+                        if (c + 1 < NC) load(g, c + 1);
 #pragma unroll
                         for (int a = 0; a < 8; ++a)
                             fold(acc[8 * c + a], r[c & 1][2 * a], r[c & 1][2 * a + 1], ff);
                         if (c + 1 < NC) {
-                            tmem_ld_wait();
-                            tmem_regs_ready(r[(c + 1) & 1]);
-                            if (c + 2 == NC) hand_back(slot);
+                            loaded(c + 1);
+                            if (c + 2 == NC) hand_back(g % SLOTS);
                         }
                     }
                 }
@@ -503,10 +514,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         for (int b = 0; b < 4; ++b) {
                             uint32_t w[4];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float2 v = pair_split(acc[16 * c + 4 * b + e]);
-                                w[e] = pack_bf16x2(v.x, v.y);
-                            }
+                            for (int e = 0; e < 4; ++e) w[e] = pack_pair(acc[16 * c + 4 * b + e]);
                             *reinterpret_cast<uint4 *>(box + lane * 64 + ((b ^ ((lane >> 1) & 3)) * 16)) =
                                 make_uint4(w[0], w[1], w[2], w[3]);
                         }
