@@ -24,7 +24,7 @@
 // chosen; usually a few more than topk, they are dealt out to the lanes anew.
 // The chosen logits are read back from their numbers.  Sums over tokens
 // are formed per warp, per block and over the blocks (by a cluster of eight
-// blocks, a share of them each), always in the same order; the counts are whole
+// blocks, a share of the experts each), always in the same order; the counts are whole
 // numbers, so their atomics are exact in any order.  Few tokens stay in one block
 // and one launch.
 #include <type_traits>
@@ -275,6 +275,16 @@ __device__ __forceinline__ Part part(float sum, int32_t count) {
 }
 __device__ __forceinline__ int32_t count_of(const Part &p) { return __float_as_int(p.y); }
 
+// balance: the sum of counts times probabilities; z: of lse^2.
+__device__ __forceinline__ void write_losses(const Route &a, int32_t tokens, float balance, float z) {
+    const float n = (float)max(tokens, 1);
+    *a.live = tokens;
+    if (a.losses != nullptr) {
+        a.losses[0] = balance / n / n * ((float)a.experts / (float)a.topk);
+        a.losses[1] = z / n;
+    }
+}
+
 // The counts and losses from the whole sums, parts(e) for e <= experts, by one
 // block; red: 2 + kWarps floats.
 template <typename F>
@@ -292,15 +302,7 @@ __device__ __forceinline__ void finish(const Route &a, float *red, F parts) {
     }
     float v[1] = {balance};
     row_sum<kThreads, 1>(v, red + 2);
-    if (threadIdx.x == 0) {
-        const int32_t tokens = __float_as_int(red[0]);
-        const float n = (float)max(tokens, 1);
-        *a.live = tokens;
-        if (a.losses != nullptr) {
-            a.losses[0] = v[0] / n / n * ((float)a.experts / (float)a.topk);
-            a.losses[1] = red[1] / n;
-        }
-    }
+    if (threadIdx.x == 0) write_losses(a, __float_as_int(red[0]), v[0], red[1]);
 }
 
 template <typename T, int R, bool VEC>
@@ -415,26 +417,31 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) moe_route_kernel(con
     }
 }
 
-// The blocks' parts added up: every CTA of one cluster takes each eighth of
-// them, the first adds the CTAs' sums.
+// The blocks' parts added up by one cluster: a CTA takes 32 of every 256 columns
+// of parts (experts, then the tokens), a lane each, and its warps each 16th block;
+// the CTAs' shares of the balance meet in the first.
 __global__ void __cluster_dims__(kSumCtas, 1, 1) __launch_bounds__(kThreads)
     moe_route_sum_kernel(const Route a, int blocks) {
-    __shared__ Part share[kMoeMaxExperts + 1];
-    __shared__ float red[2 + kWarps];
+    __shared__ Part share[kWarps][32];
+    __shared__ float balances;
+    __shared__ Part all_tokens;
     const int width = a.experts + 1, rank = (int)cluster_ctarank();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait_prior();
     pdl_allow_next();
     const Part *parts = reinterpret_cast<const Part *>(a.workspace);
-    for (int e = threadIdx.x; e < width; e += kThreads) {
+    float balance = 0.f;
+    for (int e0 = 32 * rank; e0 < width; e0 += 32 * kSumCtas) {
+        const int e = e0 + lane;
         float sum = 0.f, err = 0.f;
         int32_t n = 0;
         constexpr int kBatch = 20;  // loads in flight
-        for (int b0 = rank; b0 < blocks; b0 += kSumCtas * kBatch) {
+        for (int b0 = warp; b0 < blocks; b0 += kWarps * kBatch) {
             Part p[kBatch];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                const int b = b0 + kSumCtas * i;
-                p[i] = b < blocks ? parts[(int64_t)b * width + e] : part(0.f, 0);
+                const int b = b0 + kWarps * i;
+                p[i] = b < blocks && e < width ? parts[(int64_t)b * width + e] : part(0.f, 0);
             }
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
@@ -442,26 +449,45 @@ __global__ void __cluster_dims__(kSumCtas, 1, 1) __launch_bounds__(kThreads)
                 n += count_of(p[i]);
             }
         }
-        share[e] = part(sum + err, n);
+        share[warp][lane] = part(isinf(sum) ? sum : sum + err, n);  // (inf's err is NaN)
+        __syncthreads();
+        if (warp == 0 && e < width) {
+            sum = 0.f;
+            n = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                sum += share[w][lane].x;
+                n += count_of(share[w][lane]);
+            }
+            if (e < a.experts) {
+                a.counts[e] = n;
+                balance += (float)n * sum;
+            } else {
+                all_tokens = part(sum, n);
+            }
+        }
+        __syncthreads();
+    }
+    if (warp == 0) {
+        balance = warp_sum(balance);
+        if (lane == 0) balances = balance;
     }
     cluster_sync_all();
-    if (rank == 0)
-        finish(a, red, [&](int e) {
-            Part p[kSumCtas];
+    if (rank == 0 && threadIdx.x == 0) {
+        float sum = 0.f, z, tokens;
+        float v[kSumCtas];
 #pragma unroll
-            for (int c = 0; c < kSumCtas; ++c)
-                asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
-                             : "=f"(p[c].x), "=f"(p[c].y)
-                             : "r"(mapa_shared(smem_u32(&share[e]), c)));
-            float sum = 0.f;
-            int32_t n = 0;
+        for (int c = 0; c < kSumCtas; ++c)
+            asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                         : "=f"(v[c])
+                         : "r"(mapa_shared(smem_u32(&balances), c)));
+        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                     : "=f"(z), "=f"(tokens)
+                     : "r"(mapa_shared(smem_u32(&all_tokens), a.experts / 32 % kSumCtas)));
 #pragma unroll
-            for (int c = 0; c < kSumCtas; ++c) {
-                sum += p[c].x;
-                n += count_of(p[c]);
-            }
-            return part(sum, n);
-        });
+        for (int c = 0; c < kSumCtas; ++c) sum += v[c];
+        write_losses(a, __float_as_int(tokens), sum, z);
+    }
     cluster_sync_all();  // the others' sums stay until they have been read
 }
 

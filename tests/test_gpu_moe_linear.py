@@ -330,3 +330,27 @@ def test_every_row_count_of_the_last_tile(N, K):
             y[few] = torch.full((cap, N), 7.0, dtype=BF, device="cuda")
             fp8.fp8_moe_linear_fprop(xq, xs, wq, ws, offsets, y[few])
     assert torch.equal(y["0"], y["1"]) and (y["0"][at[-1]:] == 7.0).all()
+
+
+@pytest.mark.parametrize("cap", [1, 5, 16, 17, 63, 100, 131])
+def test_capacities_smaller_than_a_copy(cap, kernel):
+    """Any number of rows: copies of 16 to 128 rows reach past the last."""
+    N, K = 256, 640
+    offsets = torch.tensor([0, cap // 3, cap // 3, cap], dtype=torch.int32, device="cuda")
+    w = rnd(3, N, K, seed=28, scale=K ** -0.5)
+    wq, ws, wqt = square_tiles(w)
+    for which, wide, out in (("fprop", K, N), ("dgrad", N, K)):
+        full = row_tiles(rnd(2 * B, wide, seed=29))
+        # exactly cap rows, in memory of their own
+        q, s = full[0][:cap].clone(), full[1][:cap].clone()
+        y = torch.full((cap + 8, out), 7.0, dtype=BF, device="cuda")
+        if which == "fprop":
+            fp8.fp8_moe_linear_fprop(q, s, wq, ws, offsets, y[:cap])
+        else:
+            fp8.fp8_moe_linear_dgrad(q, s, wqt, ws, offsets, y[:cap])
+        x = values(q, s)
+        for i, (lo, hi) in enumerate(((0, cap // 3), (cap // 3, cap // 3), (cap // 3, cap))):
+            wv = values(wq[i], ws[i], B)
+            near(y[lo:hi], x[lo:hi], wv if which == "fprop" else wv.t(), wide)
+        assert (y[cap:] == 7.0).all()
+    fp8.fp8_check_device_status()

@@ -305,3 +305,13 @@ def test_a_launch_that_fails_is_reported():
             route(x, 2)
         _LIB.fp8_inject_launch_failures(0)
     check(route(x, 2), plain(x, 2), x)
+
+
+@pytest.mark.parametrize("tokens", [40, 700])
+def test_a_squared_log_sum_past_fp32_is_infinite(tokens):
+    """(3e19)^2 is past fp32's 3.4e38: the loss is the infinity that rounding
+    gives, in one block and over many, and the balance stays finite."""
+    x = logits_of(tokens, 24, seed=30)
+    x[tokens // 2] = 3e19
+    got = route(x, 3)
+    assert got["losses"][1].item() == math.inf and got["losses"][0].isfinite()
