@@ -14,10 +14,27 @@
 // weights and contraction depend on offsets that only the device knows: every
 // CTA reads them once, keeps them in shared memory with the row tiles before
 // each expert, and a warp of its own finds the tiles' experts by bisection, a
-// few tiles ahead of the producer, MMA and epilogue warps: the host launches without waiting
-// for the sort.  Tiles go expert by expert, so that an expert's weights are in
-// L2 while its rows pass.  Rows of a tile past its segment are computed from
-// what lies there and not stored.
+// few tiles ahead of the producer, MMA and epilogue warps: the host launches
+// without waiting for the sort.  Tiles go expert by expert, so that an expert's
+// weights are in L2 while its rows pass.  Rows of a tile past its segment are
+// computed from what lies there and not stored.
+//
+// What bounds it is the promotion, as in the single GEMM: a block's 32768
+// partials an SM take one packed multiply-add for two of them (fprop, dgrad), or
+// a packed product of scales besides (wgrad), by two warps a scheduler that wait
+// for each 16 columns' load from TMEM.  Measured, us: 16384 rows of 8 experts to
+// 28672 columns, 4096 deep; dgrad of 65536 rows of 64 experts to 4096 columns,
+// 2048 deep; wgrad 14336 x 4096 of 8 experts' 32768 rows:
+//   16 (fprop) or 4 bytes of a row stored at a time, first scales read as a
+//   tile begins                                               1705   632   2715
+//   outputs through a box in shared memory, the next tile's first scales read
+//   before them                                               1596   534   2644
+//   wgrad in pairs: accumulators, partials and scales in register pairs, a
+//   chunk's scales read a chunk ahead                         1547   501   2468
+// and, not taken: loads of 32 columns 1989, 599, 3168 (registers spilled) and for
+// wgrad alone 2783; the next block's first load asked for before the last chunk's
+// products 1845, 602, 3340; two products of 128 columns a block, each with TMEM
+// slots of its own, 1842, 585, 2461 (A is read twice from shared memory).
 #include <cuda.h>
 
 #include <atomic>
@@ -585,11 +602,18 @@ Args common_args(const MoeGemm &m) {
 }
 
 // Whether the kernel that puts the weights on the tensor cores' rows takes a
-// call: up to one of its tiles an expert on average (what the host knows of the
-// routing is the capacity).  FP8LINEAR_MOE_FEW=0/1 overrides.
+// call: up to 24 rows an expert on average (what the host knows of the routing is
+// the capacity, padding included).  This kernel and that one, us, fprop: T tokens
+// to 8 of 64 experts, 2048 x 4096, T = 1, 4, 8, 32, 64 (8 rows an expert): 19.5 and
+// 16.4, 42.6 and 36.9, 58.0 and 54.1, 88.5 and 81.3, 89.9 and 84.8; to 2 of 8, 28672
+// x 4096, T = 1, 8, 64 (16 rows): 43.6 and 39.6, 128.9 and 119.8, 145.2 and 143.7;
+// its narrower tiles fill the last wave better.  Even segments of 24, 32, 48, 64 and
+// 128 rows, 64 x 2048 x 4096: 91.6 and 88.5, 92.5 and 89.8, 94.1 and 98.4, 95.5 and
+// 112, 102 and 213; 8 x 4096 x 14336: 76.8 and 79.3, 76.9 and 79.9, 77.7 and 87.3,
+// 78.1 and 98, 80.7 and 185.  FP8LINEAR_MOE_FEW=0/1 overrides.
 bool few_rows(const MoeGemm &m) {
     const char *env = getenv("FP8LINEAR_MOE_FEW");
-    return env != nullptr ? atoi(env) == 1 : m.capacity <= kMoeFewRows * m.experts;
+    return env != nullptr ? atoi(env) == 1 : m.capacity <= 24 * m.experts;
 }
 
 // Output tiles of fprop and dgrad at most: every expert may end in a tile of its own.

@@ -11,7 +11,7 @@
 // A tile's scales are those of fp8_quantize's block recipe (amax/448, taken as
 // a multiply by 448/amax); y is quantised before its rounding to rows, so the
 // cast adds the only rounding.  All arithmetic is fp32; bf16 rows take the
-// hardware's exponential and division (2^-21 or so, far below bf16's 2^-9),
+// hardware's exponential and division (2^-21 or so, far below bf16's 2^-8),
 // fp32 rows the exact ones.
 //
 // Everything moves once and is bound by HBM: 7.1 bytes an element forward to
