@@ -24,9 +24,16 @@
 // chosen; usually a few more than topk, they are dealt out to the lanes anew.
 // The chosen logits are read back from their numbers.  Sums over tokens
 // are formed per warp, per block and over the blocks (by a cluster of eight
-// blocks, a share of the experts each), always in the same order; the counts are whole
-// numbers, so their atomics are exact in any order.  Few tokens stay in one block
-// and one launch.
+// blocks, a share of the experts each), always in the same order; the counts are
+// whole numbers, so their atomics are exact in any order.  Few tokens stay in one
+// block and one launch.
+//
+// Issue slots bound it, not the 16 bytes of a lane's loads: 16384 tokens of 256 fp32
+// logits, top 8, 15.6 us (2.6 for the bytes), 620 instructions a token and the second
+// launch, whose blocks find room only as the first's leave.  With each round of the
+// top-k over all logits and a logit a load it was 68 us, with the sums over the
+// blocks by parts instead of by experts 16.2.  Its gradient, 9.5 us (5.1), was 16
+// with a logit a load and no token ahead.
 #include <type_traits>
 
 #include "common.cuh"

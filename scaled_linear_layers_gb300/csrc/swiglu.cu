@@ -19,6 +19,9 @@
 // a tile, eight neighbouring columns each, so that a tile's maximum is four
 // shuffles and a bf16 lane's loads are 16 bytes; rows that do not lie on 16
 // bytes go element by element, a tile's columns dealt out to the lanes in turn.
+// 16384 x 14336 bf16: forward to E4M3 with the checkpoint 282 us, 0.87 of the
+// measured bandwidth (376 when a team took one tile after another, a division for
+// each scale and its inverse in every lane); backward with y again 363 us, 0.96.
 #include <type_traits>
 
 #include "common.cuh"
