@@ -224,6 +224,10 @@ __device__ __forceinline__ Left<typename C::Key, R> numbered(const uint32_t (&or
 // best: the lane's largest, least: the warp's.  A number's place is the count of
 // larger ones.
 constexpr int kDealt = 64;
+template <typename K>
+struct __align__(4 * sizeof(K) > 16 ? 16 : 4 * sizeof(K)) Four {
+    K a, b, c, d;
+};
 template <typename C, bool VEC, int R>
 __device__ __forceinline__ typename C::Key choose_few(const uint32_t (&order)[R], uint32_t best,
                                                       uint32_t least, int topk, int lane,
@@ -234,26 +238,35 @@ __device__ __forceinline__ typename C::Key choose_few(const uint32_t (&order)[R]
         least = __reduce_max_sync(kAll, best);
     }
     least = max(least, kClosed + 1);
-    int found = 0;
+    int count = 0;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const bool in = order[r] >= least;
-        const uint32_t lanes = __ballot_sync(kAll, in);
-        const int at = found + __popc(lanes & ((1u << lane) - 1u));
-        if (in && at < kDealt) dealt[at] = C::make(order[r], expert_of<R, VEC>(r, lane));
-        found += __popc(lanes);
+    for (int r = 0; r < R; ++r) count += order[r] >= least;
+    int at = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kAll, at, o);
+        if (lane >= o) at += v;
     }
-    __syncwarp();
+    const int found = __shfl_sync(kAll, at, 31);
     K mine = 0;
     if (found <= kDealt) {
+        at -= count;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (order[r] >= least) dealt[at++] = C::make(order[r], expert_of<R, VEC>(r, lane));
+        if (lane < 3) dealt[found + lane] = 0;  // places are counted four numbers at a time
+        __syncwarp();
         const K one = lane < found ? dealt[lane] : K(0);
         const K two = lane + 32 < found ? dealt[lane + 32] : K(0);
-        int place = 0, place2 = 0;
-        for (int i = 0; i < found; ++i) {
-            const K other = dealt[i];
-            place += other > one;
-            if (found > 32) place2 += other > two;
-        }
+        auto larger = [&](K than) {
+            int n = 0;
+            for (int i = 0; i < found; i += 4) {
+                const Four<K> f = *reinterpret_cast<const Four<K> *>(dealt + i);
+                n += (f.a > than) + (f.b > than) + (f.c > than) + (f.d > than);
+            }
+            return n;
+        };
+        const int place = larger(one), place2 = found > 32 ? larger(two) : 0;
         __syncwarp();
         // back by their places
         if (lane < found) dealt[place] = one;
@@ -321,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) moe_route_kernel(con
     float *sums = smem;                                                     // [kWarps / 2][width]
     int32_t *counts = reinterpret_cast<int32_t *>(sums + kWarps / 2 * width);  // [width]
     float *red = reinterpret_cast<float *>(counts + width);                 // [2 + kWarps]
-    __shared__ K dealt[R > 4 ? kWarps * kDealt : 1];
+    __shared__ __align__(16) K dealt[R > 4 ? kWarps * (kDealt + 4) : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int e = threadIdx.x; e < width; e += kThreads) counts[e] = 0;
     __syncthreads();
@@ -375,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) moe_route_kernel(con
             for (int r = 0; r < R; ++r) psum[r] = fmaf(l[r], inv, psum[r]);
             K mine;
             if constexpr (R > 4) {
-                mine = choose_few<C, VEC>(order, best, top, a.topk, lane, dealt + warp * kDealt);
+                mine = choose_few<C, VEC>(order, best, top, a.topk, lane, dealt + warp * (kDealt + 4));
             } else {
                 auto left = numbered<C, VEC>(order, lane);
                 mine = choose<C>(left, a.topk, lane);
