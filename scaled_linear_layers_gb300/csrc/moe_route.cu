@@ -28,12 +28,12 @@
 // whole numbers, so their atomics are exact in any order.  Few tokens stay in one
 // block and one launch.
 //
-// Issue slots bound it, not the 16 bytes of a lane's loads: 16384 tokens of 256 fp32
-// logits, top 8, 15.6 us (2.6 for the bytes), 620 instructions a token and the second
-// launch, whose blocks find room only as the first's leave.  With each round of the
-// top-k over all logits and a logit a load it was 68 us, with the sums over the
-// blocks by parts instead of by experts 16.2.  Its gradient, 9.5 us (5.1), was 16
-// with a logit a load and no token ahead.
+// Issue slots bound it, not the bytes: 16384 tokens of 256 fp32 logits, top 8, 14.7 us
+// (2.6 for the bytes), 570 instructions a token and the second launch, whose blocks
+// find room only as the first's leave.  With each round of the top-k over all logits
+// and a logit a load it was 68 us, with the few logits dealt out by a vote a register
+// 15.6, with the sums over the blocks by parts instead of by experts 16.2.  Its
+// gradient, 9.3 us (5.1), was 16 with a logit a load.
 #include <type_traits>
 
 #include "common.cuh"
@@ -558,10 +558,11 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1)
         const float dw = id >= 0 ? next_dw : 0.f;
         if (kAhead) fetch(t + step);
         if (on) {
-            uint32_t peak_order = 0;
+            // (a NaN is no maximum, but makes the total NaN)
+            float best = l[0];
 #pragma unroll
-            for (int r = 0; r < R; ++r) peak_order = max(peak_order, order_of(l[r]));
-            const float peak = logit_of(__reduce_max_sync(kAll, peak_order));
+            for (int r = 1; r < R; ++r) best = fmaxf(best, l[r]);
+            const float peak = logit_of(__reduce_max_sync(kAll, order_of(best)));
             float total = 0.f, pc = 0.f;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
@@ -580,9 +581,21 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1)
             if (!a.renormalize) common -= dot;
             if (id >= 0) chosen[id] = a.renormalize ? w * (dw - dot) : w * dw;
             __syncwarp();
+            common *= inv;
+            if constexpr (VEC) {
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-                l[r] = fmaf(l[r] * inv, c[r] + common, chosen[expert_of<R, VEC>(r, lane)]);
+                for (int r = 0; r < R; r += 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(chosen + expert_of<R, VEC>(r, lane));
+                    l[r] = fmaf(l[r], fmaf(c[r], inv, common), v.x);
+                    l[r + 1] = fmaf(l[r + 1], fmaf(c[r + 1], inv, common), v.y);
+                    l[r + 2] = fmaf(l[r + 2], fmaf(c[r + 2], inv, common), v.z);
+                    l[r + 3] = fmaf(l[r + 3], fmaf(c[r + 3], inv, common), v.w);
+                }
+            } else {
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    l[r] = fmaf(l[r], fmaf(c[r], inv, common), chosen[r * 32 + lane]);
+            }
             __syncwarp();
             if (id >= 0) chosen[id] = 0.f;
             __syncwarp();
