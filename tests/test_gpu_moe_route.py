@@ -315,3 +315,55 @@ def test_a_squared_log_sum_past_fp32_is_infinite(tokens):
     x[tokens // 2] = 3e19
     got = route(x, 3)
     assert got["losses"][1].item() == math.inf and got["losses"][0].isfinite()
+
+
+@pytest.mark.parametrize("tokens, experts, topk", [(3000, 96, 6), (5000, 300, 8), (64, 64, 8)])
+def test_replayed_with_new_logits_beside_other_streams(tokens, experts, topk):
+    """One captured call (a launch, or two over many blocks) replayed with other
+    logits and masks, while the same calls run on two more streams."""
+    inputs = [(logits_of(tokens, experts, seed=40 + i),
+               torch.rand(tokens, device="cuda") < (0.9, 0.1, 0.0)[i]) for i in range(3)]
+    want = [route(x, topk, mask=m) for x, m in inputs]
+    x, m = inputs[0][0].clone(), inputs[0][1].clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = route(x, topk, mask=m)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for i, w in enumerate(want):
+        x.copy_(inputs[i][0])
+        m.copy_(inputs[i][1])
+        torch.cuda.synchronize()
+        others = []
+        for s in streams:
+            with torch.cuda.stream(s):
+                others.append([route(*inputs[j][:1], topk, mask=inputs[j][1]) for j in range(3)])
+        graph.replay()
+        torch.cuda.synchronize()
+        for name, value in w.items():
+            assert torch.equal(held[name], value), name
+            for got in others:
+                assert torch.equal(got[i][name], value), name
+
+
+def test_nan_rows_have_nan_gradients_and_no_other():
+    """A NaN or +inf logit makes its token's gradient NaN, whichever lane and
+    register holds it; a closed logit beside finite ones gets zero."""
+    tokens, experts, topk = 200, 260, 4
+    x = logits_of(tokens, experts, seed=50)
+    bad = torch.arange(0, tokens, 7, device="cuda")
+    x[bad, (bad * 13) % experts] = math.nan
+    x[3, 5], x[4, 9] = math.inf, -math.inf
+    clean = torch.nan_to_num(x, nan=0.0, posinf=0.0, neginf=-math.inf)
+    ids = torch.argsort(clean, 1, descending=True)[:, :topk].int().contiguous()
+    counts = torch.bincount(ids.reshape(-1), minlength=experts).int()
+    live = torch.tensor([tokens], dtype=torch.int32, device="cuda")
+    dw = torch.randn(tokens, topk, device="cuda")
+    dl = torch.tensor([0.5, 0.25], device="cuda")
+    d, ok = torch.empty_like(x), torch.empty_like(x)
+    fp8.fp8_moe_route_backward(x, ids, counts, live, d, dw, dl)
+    fp8.fp8_moe_route_backward(clean, ids, counts, live, ok, dw, dl)
+    rows = torch.zeros(tokens, dtype=torch.bool, device="cuda")
+    rows[bad], rows[3] = True, True
+    assert d[rows].isnan().all() and torch.equal(d[~rows], ok[~rows])
+    assert d[4, 9] == 0 and ok.isfinite().all()
