@@ -307,7 +307,7 @@ def test_a_launch_that_fails_is_reported():
     check(route(x, 2), plain(x, 2), x)
 
 
-@pytest.mark.parametrize("tokens", [40, 700])
+@pytest.mark.parametrize("tokens", [20, 40, 700])
 def test_a_squared_log_sum_past_fp32_is_infinite(tokens):
     """(3e19)^2 is past fp32's 3.4e38: the loss is the infinity that rounding
     gives, in one block and over many, and the balance stays finite."""
@@ -317,7 +317,7 @@ def test_a_squared_log_sum_past_fp32_is_infinite(tokens):
     assert got["losses"][1].item() == math.inf and got["losses"][0].isfinite()
 
 
-@pytest.mark.parametrize("tokens, experts, topk", [(3000, 96, 6), (5000, 300, 8), (64, 64, 8)])
+@pytest.mark.parametrize("tokens, experts, topk", [(3000, 96, 6), (5000, 300, 8), (64, 64, 8), (32, 64, 8)])
 def test_replayed_with_new_logits_beside_other_streams(tokens, experts, topk):
     """One captured call (a launch, or two over many blocks) replayed with other
     logits and masks, while the same calls run on two more streams."""
