@@ -655,7 +655,9 @@ fp8_status fp8_moe_route_backward(const void *logits, int64_t ldl, fp8_dtype lt,
  * written.  fprop and dgrad run on one of two kernels, for many or for few rows
  * an expert, that give the same bits; the environment variable
  * FP8LINEAR_MOE_FEW=0/1, read at each call, overrides the choice (for tests and
- * tuning). */
+ * tuning).  Every wait in them is bounded by fp8_set_wait_limit_ns; that of the
+ * search for tiles, which runs ahead, by 10 us more for each 128-deep block of a
+ * tile. */
 
 /* y [capacity, N] (bf16): row r of expert e = xq[r] · Wq_e^T.  xq [capacity, K]
  * and x_scale [capacity, K/128] as fp8_quantize(BLOCK) makes them of the sorted
