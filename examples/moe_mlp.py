@@ -165,7 +165,7 @@ class MoeMlp:
         return x + total
 
 
-def main(tokens=2048, hidden=1024, width=2048, experts=8, topk=2, steps=5, lr=0.5):
+def main(tokens=2048, hidden=1024, width=2048, experts=8, topk=2, steps=5, lr=0.05):
     g = torch.Generator(device="cuda").manual_seed(1)
     layer = MoeMlp(hidden, width, experts, topk)
     x, target = (torch.randn(tokens, hidden, generator=g, device="cuda").to(BF) for _ in range(2))
