@@ -37,13 +37,15 @@ constexpr int kTile = 128, kLanes = 16, kPer = kTile / kLanes;
 constexpr int kThreads = 256, kTeams = kThreads / kLanes;
 
 // Blocks an SM, so that the next item's loads are held in registers beside the
-// one at work.  16384 x 14336 bf16, two, three and four blocks: forward 330, 291
-// and 310 us, backward 417, 371 and 361; fp32 rows of odd width, backward of 3001
-// x 1001: 11.9, 13.6 and 22.6.
-template <typename T, bool VECTOR>
-constexpr int blocks_for(bool forward) {
-    return !VECTOR ? 2 : forward || sizeof(T) == 4 ? 3 : 4;
-}
+// one at work.  Two, three and four blocks, us: 16384 x 14336 bf16 forward 330, 291
+// and 310, backward from the checkpoint 417, 371 and 361; 8192 x 8192, forward fp32
+// 125, 111 and 129, backward fp32 from the checkpoint 185, 245 and 226, bf16 from h
+// 136, 120 and 135; fp32 rows of odd width, backward of 3001 x 1001: 11.9, 13.6 and
+// 22.6.
+template <bool VECTOR>
+constexpr int kForwardBlocks = VECTOR ? 3 : 2;
+template <typename T, bool VECTOR, bool SAVED>
+constexpr int kBackwardBlocks = !VECTOR || sizeof(T) == 4 ? 2 : SAVED ? 4 : 3;
 
 __device__ __forceinline__ float sigmoid(float x, uint16_t) {
     float e, s;
@@ -220,7 +222,8 @@ __device__ __forceinline__ int64_t live_rows(const int32_t *live, int64_t rows) 
 }
 
 template <typename T, bool VECTOR>
-__global__ void __launch_bounds__(kThreads, blocks_for<T, VECTOR>(true)) swiglu_kernel(const SwigluForward a, const Walk w) {
+__global__ void __launch_bounds__(kThreads, kForwardBlocks<VECTOR>)
+    swiglu_kernel(const SwigluForward a, const Walk w) {
     pdl_wait_prior();
     pdl_allow_next();
     Team at(w);
@@ -350,7 +353,7 @@ struct BackwardInput {
 };
 
 template <typename T, bool VECTOR, bool SAVED>
-__global__ void __launch_bounds__(kThreads, blocks_for<T, VECTOR>(false))
+__global__ void __launch_bounds__(kThreads, kBackwardBlocks<T, VECTOR, SAVED>)
     swiglu_backward_kernel(const SwigluBackward a, const Walk w) {
     using H = typename std::conditional<SAVED, uint8_t, T>::type;
     pdl_wait_prior();
@@ -451,7 +454,9 @@ cudaError_t launch_swiglu_backward(const SwigluBackward &a, cudaStream_t s) {
                         aligned_to(a.dh, 16) && aligned_to(a.y, 16);
     if (a.f32) {
         if (saved) return vector ? backward<float, true, true>(a, s) : backward<float, false, true>(a, s);
-        return vector ? backward<float, true, false>(a, s) : backward<float, false, false>(a, s);
+        // columns dealt out in turn are whole lines at each load: 8192 x 8192 246 us,
+        // by eight neighbouring columns a lane 280
+        return backward<float, false, false>(a, s);
     }
     if (saved)
         return vector ? backward<uint16_t, true, true>(a, s) : backward<uint16_t, false, true>(a, s);
