@@ -194,8 +194,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
             // all MMAs issued by this thread complete before TMEM is freed
             mma_commit(drain);
-            volatile int no_abort = 0;
-            mbar_wait_bounded(drain, 0, &no_abort, p.wait_limit_ns, kStatusTimeoutMma, p.status);
+            volatile int no_abort = 0;  // a short limit must not cut this wait short
+            mbar_wait_bounded(drain, 0, &no_abort, kDefaultWaitLimitNs, kStatusTimeoutMma, p.status);
         }
     } else {
         // ---------------------------------------------------- epilogue

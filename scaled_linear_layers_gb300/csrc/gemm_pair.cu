@@ -297,8 +297,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                 if (ok) mma_commit_pair(&tfull[acc], 0x3);
             }
             mma_commit_pair(drain, 0x1);
-            volatile int no_abort = 0;
-            mbar_wait_bounded(drain, 0, &no_abort, p.wait_limit_ns, kStatusTimeoutMma, p.status);
+            volatile int no_abort = 0;  // a short limit must not cut this wait short
+            mbar_wait_bounded(drain, 0, &no_abort, kDefaultWaitLimitNs, kStatusTimeoutMma, p.status);
         }
     } else {
         // ---------------------------------------------- epilogue (both CTAs)
