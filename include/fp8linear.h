@@ -782,9 +782,11 @@ fp8_status fp8_check_device_status(cudaStream_t s);
 fp8_status fp8_inject_launch_failures(int32_t n);
 
 /* Test hook: in the calling thread's next n layer-norm calls (forward or
- * backward) the rows that come by bulk copies are waited for but not copied, so
- * these waits run out (fp8_set_wait_limit_ns; a copy that is under way arrives
- * long before a wait looks at the clock).  The kernels end by themselves with
+ * backward) the rows that come by bulk copies, and in its next n products of the
+ * experts (fp8_moe_linear_*, counted together) the third copies of each block's
+ * first tile, are waited for but not copied, so these waits run out
+ * (fp8_set_wait_limit_ns; a copy that is under way arrives long before a wait
+ * looks at the clock).  The kernels end by themselves with
  * the status word set and invalid outputs; n = 0 clears it. */
 fp8_status fp8_inject_lost_copies(int32_t n);
 

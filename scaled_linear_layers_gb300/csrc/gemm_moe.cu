@@ -221,8 +221,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!ok) break;
                 if (leader) {
                     mbar_arrive_expect_tx(&full[stage], STAGE_BYTES);
-                    tma_load_2d(sA + stage * A_BYTES, &tma_a, &full[stage], ax, arow);
-                    tma_load_2d(sB + stage * B_BYTES, &tma_b, &full[stage], bx, brow);
+                    if (!(p.lose && i == 0 && q == 2)) {
+                        tma_load_2d(sA + stage * A_BYTES, &tma_a, &full[stage], ax, arow);
+                        tma_load_2d(sB + stage * B_BYTES, &tma_b, &full[stage], bx, brow);
+                    }
                 }
                 __syncwarp();
                 if (++stage == STAGES) {
@@ -601,6 +603,7 @@ Args common_args(const MoeGemm &m) {
     a.d = m.d;
     a.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
     a.status = device_status_word();
+    a.lose = take_lost_copies();
     return a;
 }
 

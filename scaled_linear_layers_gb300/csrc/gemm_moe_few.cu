@@ -155,8 +155,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!ok) break;
                 if (leader) {
                     mbar_arrive_expect_tx(&full[stage], bytes);
-                    tma_load_3d(sW + stage * KG * W_BYTES, &maps.w, &full[stage], 0, w_row, w_k + q);
-                    tma_load_3d(sT + stage * KG * T_BYTES, &maps.t[size], &full[stage], 0, row0, q);
+                    if (!(p.lose && i == 0 && q == 2 * KG)) {
+                        tma_load_3d(sW + stage * KG * W_BYTES, &maps.w, &full[stage], 0, w_row, w_k + q);
+                        tma_load_3d(sT + stage * KG * T_BYTES, &maps.t[size], &full[stage], 0, row0, q);
+                    }
                 }
                 __syncwarp();
                 if (++stage == STAGES) {

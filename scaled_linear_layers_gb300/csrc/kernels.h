@@ -13,9 +13,14 @@ int num_sms();  // SM count of the current device (cached per device)
 // calling thread's next n launches through launch_pdl return
 // cudaErrorLaunchFailure without launching anything.
 extern thread_local int tl_fail_launches;
-// (fp8_inject_lost_copies) the thread's next n layer-norm calls wait for rows
-// that no copy brings.
+// (fp8_inject_lost_copies) the thread's next n calls that take it wait for copies
+// that nothing brings.
 extern thread_local int tl_lose_copies;
+inline int take_lost_copies() {
+    if (tl_lose_copies == 0) return 0;
+    --tl_lose_copies;
+    return 1;
+}
 
 // Launches `kernel` on `s` with programmatic stream serialisation allowed: it
 // may begin while the previous kernel on the stream drains, and must wait

@@ -1313,12 +1313,6 @@ cudaError_t norm_bwd_type(const NormBwdArgs &a, int *parts, cudaStream_t s) {
     return vec ? pick_bwd<T, true>(a, parts, s) : pick_bwd<T, false>(a, parts, s);
 }
 
-int take_lost_copies() {
-    if (tl_lose_copies == 0) return 0;
-    --tl_lose_copies;
-    return 1;
-}
-
 }  // namespace
 
 cudaError_t launch_layer_norm(const NormForward &n, cudaStream_t s) {

@@ -23,6 +23,7 @@ struct MoeArgs {
     uint16_t *d;
     uint64_t wait_limit_ns;
     unsigned int *status;
+    int lose;  // (tests) a CTA's third hand-off of copies is waited for but not copied
 };
 
 // One output tile.
