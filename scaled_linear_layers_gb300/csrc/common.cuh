@@ -102,8 +102,8 @@ __device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t *bar, uint32_t pari
 // Wait for the phase with the given parity to complete.  Gives up after
 // limit_ns (or as soon as *abort is set by another thread of the block),
 // recording `code` in the device status word.  Returns false on give-up.
-// kSleep selects the hinted try_wait (each poll then lasts up to 1 ms, so the
-// limit is checked at least every 64 ms).
+// kSleep selects the hinted try_wait: each poll then lasts up to 1 ms, so the
+// flag and the clock are looked at after every one.
 template <bool kSleep = false>
 __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity,
                                                   volatile int *abort, uint64_t limit_ns,
@@ -113,7 +113,7 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
     const uint64_t t0 = global_timer_ns();
     for (uint32_t i = 1;; ++i) {
         if (poll()) return true;
-        if ((i & 63u) == 0) {
+        if (kSleep || (i & 63u) == 0) {
             if (*abort) return false;
             if (global_timer_ns() - t0 > limit_ns) {
                 *abort = 1;

@@ -84,3 +84,13 @@ def test_a_copy_that_never_arrives_is_reported(which, few, monkeypatch):
         call()
         fp8.fp8_check_device_status()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("which, few", KINDS)
+def test_a_lost_copy_is_reported_soon(which, few, monkeypatch):
+    """A wait ends within two polls (1 ms each) of its limit of 1 ms, and the last
+    wait for the copy that is lost after 10 ms more; 64 polls between two looks at
+    the clock took 62 ms and more."""
+    call, _ = products(which, few, monkeypatch)
+    call()
+    assert lose_a_call(call) < 40
