@@ -608,18 +608,26 @@ Args common_args(const MoeGemm &m) {
 }
 
 // Whether the kernel that puts the weights on the tensor cores' rows takes a
-// call: up to 24 rows an expert on average (what the host knows of the routing is
-// the capacity, padding included).  This kernel and that one, us, fprop: T tokens
-// to 8 of 64 experts, 2048 x 4096, T = 1, 4, 8, 32, 64 (8 rows an expert): 19.5 and
-// 16.4, 42.6 and 36.9, 58.0 and 54.1, 88.5 and 81.3, 89.9 and 84.8; to 2 of 8, 28672
-// x 4096, T = 1, 8, 64 (16 rows): 43.6 and 39.6, 128.9 and 119.8, 145.2 and 143.7;
-// its narrower tiles fill the last wave better.  Even segments of 24, 32, 48, 64 and
-// 128 rows, 64 x 2048 x 4096: 91.6 and 88.5, 92.5 and 89.8, 94.1 and 98.4, 95.5 and
-// 112, 102 and 213; 8 x 4096 x 14336: 76.8 and 79.3, 76.9 and 79.9, 77.7 and 87.3,
-// 78.1 and 98, 80.7 and 185.  FP8LINEAR_MOE_FEW=0/1 overrides.
-bool few_rows(const MoeGemm &m) {
+// call, by the rows an expert on average (what the host knows of the routing is
+// the capacity, padding included) and the contraction's blocks.  That kernel's time
+// over this one's, mean of 8 to 256 experts and 512 to 8192 columns, rows routed at
+// random (fprop / dgrad):
+//   rows            0.25          1            4            8           16           24
+//    4 blocks      - / 1.27    - / 1.72    - / 1.86     - / 1.88     - / 1.94     - / 2.01
+//    8 blocks   0.99 / 0.97  1.10 / 1.05  1.15 / 1.11  1.17 / 1.13  1.26 / 1.22  1.37 / 1.33
+//   10          0.88 / 0.89  0.94 / 0.97  1.00 / 1.02                1.16 / 1.15
+//   14          0.81 / 0.83  0.87 / 0.89  0.97 / 0.98                1.06 / 1.07
+//   16          0.87 / 0.85  0.93 / 0.95  0.99 / 1.00  1.01 / 1.01  1.05 / 1.04  1.11 / 1.10
+//   32          0.80 / 0.80  0.91 / 0.90  0.98 / 0.97  0.99 / 0.98  1.02 / 1.01  1.06 / 1.05
+//   64             - / 0.76    - / 0.87    - / 0.95     - / 0.96     - / 0.98     - / 1.03
+// Single shapes lie up to a fifth to either side; the limit of 16 leaves room for the
+// padding.  With 24 rows at any depth as the rule, 832 calls took 1.08 times the
+// better kernel's time on average and 2.2 at most; so, 1.01 and 1.23.
+// FP8LINEAR_MOE_FEW=0/1 overrides.
+bool few_rows(const MoeGemm &m, int depth) {
     const char *env = getenv("FP8LINEAR_MOE_FEW");
-    return env != nullptr ? atoi(env) == 1 : m.capacity <= 24 * m.experts;
+    if (env != nullptr) return atoi(env) == 1;
+    return m.capacity <= (depth >= 16 ? 16 : depth >= 10 ? 1 : 0) * m.experts;
 }
 
 // Output tiles of fprop and dgrad at most: every expert may end in a tile of its own.
@@ -636,7 +644,7 @@ namespace {
 // [b_rows, b_cols].
 cudaError_t launch_rows(const MoeGemm &m, const Args &p, int64_t K, int64_t b_rows, int64_t b_cols,
                         cudaStream_t s, const char **why) {
-    if (few_rows(m)) return launch_moe_few(p, m.a, K, m.b, b_rows, b_cols, s, why);
+    if (few_rows(m, p.depth)) return launch_moe_few(p, m.a, K, m.b, b_rows, b_cols, s, why);
     CUtensorMap ta, tb;
     if (!make_tmap_k128(&ta, m.a, m.capacity, K, BM) ||
         !make_tmap_k128(&tb, m.b, b_rows, b_cols, BN)) {
