@@ -781,6 +781,10 @@ fp8_status fp8_check_device_status(cudaStream_t s);
  * kernels may have enqueued the earlier ones before the failing launch. */
 fp8_status fp8_inject_launch_failures(int32_t n);
 
+/* The same for one launch: `after` launches of the calling thread are made, the
+ * next one fails.  fp8_inject_launch_failures(0) clears it. */
+fp8_status fp8_inject_later_launch_failure(int32_t after);
+
 /* Test hook: in the calling thread's next n layer-norm calls (forward or
  * backward) the rows that come by bulk copies, and in its next n products of the
  * experts (fp8_moe_linear_*, counted together) the third copies of each block's

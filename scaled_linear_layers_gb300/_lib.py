@@ -115,6 +115,7 @@ SIGNATURES = {
                                       F32, P, P, P]),
     "fp8_check_device_status": (S, [P]),
     "fp8_inject_launch_failures": (S, [I32]),
+    "fp8_inject_later_launch_failure": (S, [I32]),
     "fp8_inject_lost_copies": (S, [I32]),
     "fp8_selftest_wait_timeout": (S, [U32, P]),
     "fp8_set_wait_limit_ns": (ctypes.c_uint64, [ctypes.c_uint64]),

@@ -39,7 +39,7 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 }  // namespace
 
-thread_local int tl_fail_launches = 0;
+thread_local int tl_fail_launches = 0, tl_pass_launches = 0;
 thread_local int tl_lose_copies = 0;
 
 namespace {
@@ -995,6 +995,14 @@ fp8_status fp8_pad_tokens(const uint16_t *x, int64_t rows, int64_t cols, int64_t
 fp8_status fp8_inject_launch_failures(int32_t n) {
     if (n < 0) return fail(FP8_ERR_SHAPE, "fp8_inject_launch_failures: n=%d", n);
     tl_fail_launches = n;
+    tl_pass_launches = 0;
+    return FP8_OK;
+}
+
+fp8_status fp8_inject_later_launch_failure(int32_t after) {
+    if (after < 0) return fail(FP8_ERR_SHAPE, "fp8_inject_later_launch_failure: after=%d", after);
+    tl_fail_launches = 1;
+    tl_pass_launches = after;
     return FP8_OK;
 }
 

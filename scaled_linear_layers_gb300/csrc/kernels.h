@@ -10,9 +10,18 @@ namespace fp8 {
 int num_sms();  // SM count of the current device (cached per device)
 
 // Host-side fault injection for the tests (fp8_inject_launch_failures): the
-// calling thread's next n launches through launch_pdl return
+// calling thread's next n launches, after tl_pass_launches that are made, return
 // cudaErrorLaunchFailure without launching anything.
-extern thread_local int tl_fail_launches;
+extern thread_local int tl_fail_launches, tl_pass_launches;
+inline bool launch_is_to_fail() {
+    if (tl_fail_launches == 0) return false;
+    if (tl_pass_launches > 0) {
+        --tl_pass_launches;
+        return false;
+    }
+    --tl_fail_launches;
+    return true;
+}
 // (fp8_inject_lost_copies) the thread's next n calls that take it wait for copies
 // that nothing brings.
 extern thread_local int tl_lose_copies;
@@ -28,10 +37,7 @@ inline int take_lost_copies() {
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                        cudaStream_t s, Args &&...args) {
-    if (tl_fail_launches > 0) {
-        --tl_fail_launches;
-        return cudaErrorLaunchFailure;
-    }
+    if (launch_is_to_fail()) return cudaErrorLaunchFailure;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;

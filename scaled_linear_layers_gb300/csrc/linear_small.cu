@@ -338,10 +338,7 @@ cudaError_t launch_linear_small_dynamic(const uint16_t *x, const uint16_t *w, in
                                         int64_t K, const uint16_t *bias, float *scales,
                                         float *amax, uint8_t *xq, uint8_t *wq, uint16_t *y,
                                         cudaStream_t s) {
-    if (tl_fail_launches > 0) {
-        --tl_fail_launches;
-        return cudaErrorLaunchFailure;
-    }
+    if (launch_is_to_fail()) return cudaErrorLaunchFailure;
     const int C = small_cluster(N);
     const int nkb = (int)((K + 127) / 128);
     const size_t smem = 1024 + (size_t)nkb * (kBoxA + (N / C) * 128) + 64;

@@ -1197,10 +1197,7 @@ cudaError_t ns_resident(int *workers) {
 // Cooperative: the CTAs wait for one another's tiles.
 cudaError_t ns_launch(void (*kernel)(NsMaps, NsPlan), int grid, cudaStream_t s, const NsMaps &maps,
                       const NsPlan &p) {
-    if (tl_fail_launches > 0) {
-        --tl_fail_launches;
-        return cudaErrorLaunchFailure;
-    }
+    if (launch_is_to_fail()) return cudaErrorLaunchFailure;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = NS_THREADS;
