@@ -605,7 +605,8 @@ fp8_status fp8_moe_combine_backward(const void *dy, int64_t lddy, const void *ro
  *     order, the lowest id first among equal ones (NaN counts as the largest);
  *     what fp8_moe_sort takes;
  *   weights [tokens, topk] (fp32): p of these experts, or, with renormalize !=
- *     0, p over the sum of the chosen ones; what fp8_moe_combine takes;
+ *     0, p over the sum of the chosen ones (0 where exp(logit - the token's
+ *     largest) is below 2^-126); what fp8_moe_combine takes;
  *   counts [experts] (int32): tokens that chose each expert;
  *   live [1] (int32): tokens that have an expert;
  *   losses [2] (fp32, nullable): the balance loss
@@ -655,9 +656,9 @@ fp8_status fp8_moe_route_backward(const void *logits, int64_t ldl, fp8_dtype lt,
  * written.  fprop and dgrad run on one of two kernels, for many or for few rows
  * an expert, that give the same bits; the environment variable
  * FP8LINEAR_MOE_FEW=0/1, read at each call, overrides the choice (for tests and
- * tuning).  Every wait in them is bounded by fp8_set_wait_limit_ns; that of the
- * search for tiles, which runs ahead, by 10 us more for each 128-deep block of a
- * tile. */
+ * tuning).  Every wait in them for another part of the kernel is bounded by
+ * fp8_set_wait_limit_ns; that of the search for tiles, which runs ahead, by 10 us
+ * more for each 128-deep block of a tile. */
 
 /* y [capacity, N] (bf16): row r of expert e = xq[r] · Wq_e^T.  xq [capacity, K]
  * and x_scale [capacity, K/128] as fp8_quantize(BLOCK) makes them of the sorted
@@ -694,8 +695,8 @@ fp8_status fp8_moe_linear_wgrad(const uint8_t *gqt, const float *g_scale_t, cons
 /* Gated activation, with its input kept in 8 bits                           */
 /* ------------------------------------------------------------------------ */
 /* h [rows, 2 cols] (type ht, row stride ldh): the gate's columns, then the
- * up's.  With s = 1 / (1 + exp(-gate)), y = gate * s * up.  Outputs, not all
- * NULL:
+ * up's.  With s = 1 / (1 + exp(-gate)), y = gate * s * up, in fp32 (s is zero for
+ * gates below -87.3 of bf16 and -88.7 of fp32 rows).  Outputs, not all NULL:
  *   y [rows, cols] in h's type;
  *   yq [rows, cols] (E4M3) with y_scale [rows, ceil(cols/128)]: y under a scale
  *     for each 1x128 tile, as fp8_quantize(BLOCK) casts it, from the fp32 y

@@ -19,10 +19,12 @@
 // weights are in L2 while its rows pass.  Rows of a tile past its segment are
 // computed from what lies there and not stored.
 //
-// What bounds it is the promotion, as in the single GEMM: a block's 32768
-// partials an SM take one packed multiply-add for two of them (fprop, dgrad), or
-// a packed product of scales besides (wgrad), by two warps a scheduler that wait
-// for each 16 columns' load from TMEM.  Measured, us: 16384 rows of 8 experts to
+// wgrad is bound by the promotion: a block's 32768 partials an SM take a packed
+// multiply-add and a packed product of scales for two of them, by two warps a scheduler
+// that wait for each 16 columns' load from TMEM.  fprop and dgrad, whose partials take
+// the multiply-add alone, are bound by the tensor cores' feed and the hand-offs (a copy
+// of fprop without the promotion's arithmetic takes 1414 us of 1541) and by a tile's
+// end, in which nothing is folded.  Measured, us: 16384 rows of 8 experts to
 // 28672 columns, 4096 deep; dgrad of 65536 rows of 64 experts to 4096 columns,
 // 2048 deep; wgrad 14336 x 4096 of 8 experts' 32768 rows:
 //   16 (fprop) or 4 bytes of a row stored at a time, first scales read as a

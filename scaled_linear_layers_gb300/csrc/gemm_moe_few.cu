@@ -9,8 +9,10 @@
 // a copy of the weights and one of the tokens, and a hand-off each.  With a block
 // a hand-off the single threads that issue copies and products bound it, at 600
 // to 850 cycles a block where the bandwidth leaves 700 (8 tokens to 8 of 64
-// experts, 4096 x 2048: 71 us); warps that issue as a whole, by an elected lane,
-// and a copy for four blocks leave them time: 60 us, 52 of them the weights' bytes.  The MMA warp writes the blocks'
+// experts, each expert's rows padded to 16, 4096 x 2048: 71 us); warps that issue as a
+// whole, by an elected lane, and a copy for four blocks leave them time: 60 us, 52 of
+// them the weights' bytes.  Contractions of few groups do not fill that pipeline
+// (few_rows in gemm_moe.cu chooses by them).  The MMA warp writes the blocks'
 // partial products into TMEM slots, and four epilogue warps fold them into fp32
 // registers, each column with its token's scale times the weights'.  A warp of
 // its own brings those scales into shared memory, 16 blocks at a time and ahead

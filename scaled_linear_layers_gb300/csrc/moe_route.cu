@@ -21,19 +21,24 @@
 // the lanes' first ones, whose owner moves on to its next.  Of more experts
 // most logits are left out first: topk lanes have one that is at least the
 // topk-th largest of the lanes' largest, so only logits from there on can be
-// chosen; usually a few more than topk, they are dealt out to the lanes anew.
-// The chosen logits are read back from their numbers.  Sums over tokens
+// chosen.  Up to a topk of 16 or so they are a few more than topk and are dealt out
+// to the lanes anew; near 32 that bar is the least of the lanes' largest, most
+// tokens have more above it than are dealt out, and all logits go through the
+// rounds.  The chosen logits are read back from their numbers.  Sums over tokens
 // are formed per warp, per block and over the blocks (by a cluster of eight
 // blocks, a share of the experts each), always in the same order; the counts are
 // whole numbers, so their atomics are exact in any order.  Few tokens stay in one
 // block and one launch.
 //
-// Issue slots bound it, not the bytes: 16384 tokens of 256 fp32 logits, top 8, 14.7 us
-// (2.6 for the bytes), 570 instructions a token and the second launch, whose blocks
-// find room only as the first's leave.  With each round of the top-k over all logits
+// Not the bytes bound it: 16384 tokens of 256 fp32 logits, top 8, 14.7 us (2.6 for the
+// bytes; bf16 15.0).  The second launch, whose blocks find room only as the first's
+// leave, is 3.2 of them, and 570 instructions a token are 8 us of issue slots, which
+// bound it while all warps have a token; 304 blocks take the tokens in four passes, the
+// last for a third of the warps, so that the SMs issue at 54 % of their rate.  Other
+// topk, fp32: 16 16.9, 24 24, 28 43, 32 77; 1024 experts 37 at 8, 40 at 16, 258 at 32.  With each round of the top-k over all logits
 // and a logit a load it was 68 us, with the few logits dealt out by a vote a register
 // 15.6, with the sums over the blocks by parts instead of by experts 16.2.  Its
-// gradient, 9.3 us (5.1), was 16 with a logit a load.
+// gradient, 9.3 us (5.1; bf16 7.9), was 16 with a logit a load.
 #include <type_traits>
 
 #include "common.cuh"
@@ -114,7 +119,10 @@ __device__ __forceinline__ void store_logits(T *row, int experts, int lane, cons
     }
 }
 
-// 1/x for x >= 1 and log x, by the hardware's approximations (2^-23 and 2^-22).
+// 1/x and log x for x >= 1, by the hardware's approximations: two units in the last
+// place; 2^-21.4 of an absolute error up to 2, three units above.  With logf and a
+// division 15.5 us and 9.8 for the gradient (14.7 and 9.3); errors against 64 bits as
+// before: weights 6e-8 in the 2-norm (6e-8), log-sums' gradient 7e-8 (7e-8).
 __device__ __forceinline__ float inverse(float x) { return __fdividef(1.f, x); }
 __device__ __forceinline__ float logarithm(float x) { return __logf(x); }
 
@@ -221,7 +229,8 @@ __device__ __forceinline__ Left<typename C::Key, R> numbered(const uint32_t (&or
 }
 
 // Whether the topk go by way of the few logits that can be among them: 64-bit
-// numbers cost a round more.  Without and with, 16384 tokens, top 8, us: fp32 64
+// numbers cost a round more.  Without and with, 16384 tokens, top 8 (more than 16
+// gains less: see the fallback), us: fp32 64
 // experts 11.1 and 10.5, 128 13.5 and 11.6, 256 25.9 and 14.6; bf16 128 10.7 and 11.4,
 // 256 17.0 and 14.8.
 template <typename T, int R>
@@ -280,7 +289,7 @@ __device__ __forceinline__ typename C::Key choose_few(const uint32_t (&order)[R]
         if (lane + 32 < found) dealt[place2] = two;
         __syncwarp();
         if (lane < min(found, topk)) mine = dealt[lane];
-    } else {  // many equal logits
+    } else {  // a topk near 32, or many equal logits
         auto left = numbered<C, VEC>(order, lane);
         mine = choose<C>(left, topk, lane);
     }
@@ -288,7 +297,9 @@ __device__ __forceinline__ typename C::Key choose_few(const uint32_t (&order)[R]
     return mine;
 }
 
-// e^x for x <= 0: the hardware's 2^y, relative error 2^-22 + |x| 2^-23.
+// e^x for x <= 0: the hardware's 2^y, relative error 2^-22 + |x| 2^-23, zero below
+// 2^-126.  expf takes 16.4 us where this takes 14.7, and gives the same errors in the
+// 2-norm of weights and gradients (6e-8, 8e-8).
 __device__ __forceinline__ float exp_falling(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));

@@ -11,8 +11,12 @@
 // A tile's scales are those of fp8_quantize's block recipe (amax/448, taken as
 // a multiply by 448/amax); y is quantised before its rounding to rows, so the
 // cast adds the only rounding.  All arithmetic is fp32; bf16 rows take the
-// hardware's exponential and division (2^-21 or so, far below bf16's 2^-8),
-// fp32 rows the exact ones.
+// hardware's exponential and reciprocal, whose error in s is 2^-21 (1 + |gate|/8), far
+// below bf16's 2^-8, and whose s is zero for gates below -87.3; fp32 rows take expf
+// and a division (zero below -88.7).  Of 2.9e7 E4M3 values of y, 14 take the other
+// neighbour of a border than with expf and a division, which bring scales and bytes no
+// nearer to 64 bits (scales 5e-8 either way) and take 370 us where this takes 281 (expf
+// alone 290).
 //
 // Everything moves once and is bound by HBM: 7.1 bytes an element forward to
 // E4M3 with the checkpoint, 10.1 backward from it (bf16).  Sixteen lanes share
@@ -454,8 +458,8 @@ cudaError_t launch_swiglu_backward(const SwigluBackward &a, cudaStream_t s) {
                         aligned_to(a.dh, 16) && aligned_to(a.y, 16);
     if (a.f32) {
         if (saved) return vector ? backward<float, true, true>(a, s) : backward<float, false, true>(a, s);
-        // columns dealt out in turn are whole lines at each load: 8192 x 8192 246 us,
-        // by eight neighbouring columns a lane 280
+        // columns dealt out in turn are whole lines at each load: 8192 x 8192 with y
+        // again 255 us, by eight neighbouring columns a lane 280
         return backward<float, false, false>(a, s);
     }
     if (saved)
