@@ -803,9 +803,9 @@ fp8_status fp8_inject_lost_copies(int32_t n);
  * runs out sets the device status word (FP8_ERR_TIMEOUT from
  * fp8_check_device_status) and its kernel returns without finishing its
  * outputs; before that it waits, under limits of its own (10 ms a copy, 2 s),
- * for its copies and products still in flight.  For callers that want faster failure detection, and for tests
- * that drive a wait into its timeout path without faulting or hanging the
- * GPU.  Host only, no GPU work. */
+ * for its copies and products still in flight.  For callers that want faster
+ * failure detection, and for tests that drive a wait into its timeout path
+ * without faulting or hanging the GPU.  Host only, no GPU work. */
 uint64_t fp8_set_wait_limit_ns(uint64_t limit_ns);
 
 /* Diagnostic: launches one block that waits on a barrier nothing will ever

@@ -35,10 +35,11 @@
 // leave, is 3.2 of them, and 570 instructions a token are 8 us of issue slots, which
 // bound it while all warps have a token; 304 blocks take the tokens in four passes, the
 // last for a third of the warps, so that the SMs issue at 54 % of their rate.  Other
-// topk, fp32: 16 16.9, 24 24, 28 43, 32 77; 1024 experts 37 at 8, 40 at 16, 258 at 32.  With each round of the top-k over all logits
-// and a logit a load it was 68 us, with the few logits dealt out by a vote a register
-// 15.6, with the sums over the blocks by parts instead of by experts 16.2.  Its
-// gradient, 9.3 us (5.1; bf16 7.9), was 16 with a logit a load.
+// topk, fp32: 16 16.9, 24 24, 28 43, 32 77; 1024 experts 37 at 8, 40 at 16, 258 at 32.
+// With each round of the top-k over all logits and a logit a load it was 68 us, with
+// the few logits dealt out by a vote a register 15.6, with the sums over the blocks by
+// parts instead of by experts 16.2.  Its gradient, 9.3 us (5.1; bf16 7.9), was 16 with
+// a logit a load.
 #include <type_traits>
 
 #include "common.cuh"
